@@ -94,7 +94,8 @@ enum gfr_dtype {
     GFR_DT_I64 = 7,
     GFR_DT_I32 = 8,
     GFR_DT_I8 = 9,
-    GFR_DT_INT4X2 = 10       /* signed 4-bit (two's complement) elements, packed */
+    GFR_DT_INT4X2 = 10,      /* signed 4-bit (two's complement) elements, packed */
+    GFR_DT_F16 = 11          /* IEEE half (gfr_linear, gfr_moe_route's x) */
 };
 
 /* A tensor argument: device pointer to contiguous row-major storage of
@@ -122,6 +123,8 @@ enum gfr_group_list_type { GFR_GROUP_LIST_CUMSUM = 0, GFR_GROUP_LIST_COUNT = 1 }
 #define GFR_DEV_BAD_GROUP_LIST 0x1 /* negative count, decreasing prefix, or total > M:
                                       ranges are clamped to [0, M) */
 #define GFR_DEV_BAD_ROW_INDEX 0x2  /* row_index outside [0, batch): token skipped */
+
+#define GFR_DEV_BAD_EXPERT 0x4    /* a top-k id below -1 or not below E: pair skipped */
 
 /* Limits of this implementation. */
 #define GFR_MAX_EXPERTS 1024       /* [P3] Atlas 350 notes: e <= 1024 */
@@ -350,6 +353,172 @@ int gmm_finalize_routing_det_noalloc(const gfr_tensor *x1, const gfr_tensor *x2,
                                      int64_t shared_input_offset, const gfr_tensor *out,
                                      int transpose_x2, int fp8_kind, void *stream,
                                      int32_t *status_dev);
+
+/* ======================================================================== *
+ * The rest of the MoE block: router and dense products, the router's choice *
+ * and the tokens in expert order, the experts for a few tokens.  Descriptor *
+ * calls with the conventions above.                                         *
+ * ======================================================================== */
+
+/* Activations of gfr_linear. */
+enum gfr_activation {
+    GFR_ACT_NONE = 0,
+    GFR_ACT_RELU = 1,       /* max(v, 0); NaN stays NaN */
+    GFR_ACT_SILU = 2,       /* v / (1 + exp(-v)) */
+    GFR_ACT_GELU = 3,       /* v (1 + erf(v / sqrt 2)) / 2 */
+    GFR_ACT_GELU_TANH = 4,  /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2 */
+    GFR_ACT_SWIGLU = 5      /* silu(gate) * up: w holds the N gate rows, then the N up rows */
+};
+
+/*
+ * gfr_linear — dense product with its epilogue:
+ *
+ *   out[m, n] = act(sum_k x[m, k] * w[n, k] + bias[n]) + residual[m, n]
+ *
+ * accumulated in FP32, rounded once to out's type.  The router's logits, the
+ * shared expert's products (its bf16 result is gmm_finalize_routing's
+ * shared_input) and any other dense layer of the block.
+ *
+ *  x         BF16 or F16 [M, K].
+ *  w         x's dtype, [N, K]; [2N, K] with GFR_ACT_SWIGLU.
+ *  bias      x's dtype or F32, [rows of w], or NULL.
+ *  residual  x's dtype [M, N], or NULL; may be out itself (each element is
+ *            read before it is written), but not overlap it otherwise.
+ *  activation  gfr_activation.
+ *  out       x's dtype or F32 [M, N]; overwritten, must not overlap x or w.
+ *  opts      NULL, or a workspace of gfr_linear_workspace_size() bytes
+ *            (256-byte aligned); the other fields are ignored.
+ *
+ * Any M, N >= 0 and K >= 1 (K a multiple of 8 is the fast path).  M = 0 or
+ * N = 0 is a no-op.  The sizes fix the summation order: two calls give the
+ * same bits.  Errors:
+ * GFR_ERR_NULL_ARG, GFR_ERR_BAD_DTYPE, GFR_ERR_BAD_RANK, GFR_ERR_BAD_SHAPE,
+ * GFR_ERR_BAD_ARG (activation), GFR_ERR_UNSUPPORTED (M, N or K >= 2^31, or K >
+ * 2^22), GFR_ERR_BAD_ALIGNMENT (x or w not 16-byte, bias, residual or out not
+ * 8-byte aligned, workspace not 256), GFR_ERR_WORKSPACE_TOO_SMALL, GFR_ERR_HIP.
+ */
+int gfr_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *bias,
+               const gfr_tensor *residual, int activation, const gfr_tensor *out,
+               void *stream, const gfr_options *opts);
+
+/* Workspace bytes of gfr_linear on these descriptors (0 for most sizes).
+ * Checks the arguments as the call does. */
+int gfr_linear_workspace_size(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *bias,
+                              const gfr_tensor *residual, int activation,
+                              const gfr_tensor *out, size_t *bytes);
+
+/* Limits of gfr_moe_decode. */
+#define GFR_DECODE_MAX_TOKENS 64
+#define GFR_MAX_TOPK 32
+
+/*
+ * gfr_moe_decode — the expert part of a MoE block for at most
+ * GFR_DECODE_MAX_TOKENS tokens, in two launches:
+ *
+ *   gate, up  = x[t] @ w13[e]                      e = topk_ids[t, j]
+ *   out[t]    = sum_j topk_weights[t, j] * ((silu(gate) * up) @ w2[e])
+ *               + shared_input_weight * shared_input[t]
+ *
+ * gfr_gemm1_swiglu_quant's and gmm_finalize_routing's products on the same
+ * weights, but with bf16 activations (nothing is quantised: silu(gate) * up
+ * stays at 16 mantissa bits, the only rounding to bf16 is out's), and reading
+ * only the chosen experts' weights.  Longer batches take the grouped calls.
+ *
+ *  x             BF16 [T, H], T <= GFR_DECODE_MAX_TOKENS.
+ *  w13           FP8_E4M3FN or FP8_E5M2 [E, H, 2I] (gate columns, then up),
+ *                or [E, 2I, H] when transpose_w13.
+ *  scale13       E8M0 (or U8) [H/64, 2I, 2], or [2I, H/64, 2] when
+ *                transpose_w13; 4-D with a leading E extent: per expert.
+ *  w2            w13's dtype [E, I, N], or [E, N, I] when transpose_w2.
+ *  scale2        E8M0 (or U8) [I/64, N, 2], or [N, I/64, 2]; or 4-D.
+ *  topk_ids      I32 [T, k], 1 <= k <= GFR_MAX_TOPK, each in [0, E), or -1 for
+ *                no expert.  Other values are skipped and set
+ *                GFR_DEV_BAD_EXPERT.  An expert named twice counts twice.
+ *  topk_weights  F32 [T, k]; those of skipped pairs are not read.
+ *  shared_input  BF16 [T, N], or NULL; shared_input_weight its factor.
+ *  out           BF16 or F32 [T, N]; overwritten (a token without an expert
+ *                gets the shared term, or zero).
+ *  opts          workspace and workspace_bytes (gfr_moe_decode_workspace_size,
+ *                256-byte aligned), status_dev; the other fields are ignored.
+ *
+ * The summation order is fixed: two calls give the same bits.  Calls that
+ * overlap in time need workspaces of their own.  Needs H, I and N multiples of
+ * 64, E <= GFR_MAX_EXPERTS and T * k <= 1024 (GFR_ERR_UNSUPPORTED); data
+ * 16-byte aligned (GFR_ERR_BAD_ALIGNMENT).  Other errors as gfr_linear.
+ */
+int gfr_moe_decode(const gfr_tensor *x, const gfr_tensor *w13, const gfr_tensor *scale13,
+                   const gfr_tensor *w2, const gfr_tensor *scale2, const gfr_tensor *topk_ids,
+                   const gfr_tensor *topk_weights, const gfr_tensor *shared_input,
+                   float shared_input_weight, const gfr_tensor *out, int transpose_w13,
+                   int transpose_w2, void *stream, const gfr_options *opts);
+
+/* Workspace bytes of gfr_moe_decode for T tokens of k experts out of E,
+ * w2 [I, N] per expert in the given layout.  Pure host arithmetic. */
+int gfr_moe_decode_workspace_size(int64_t T, int64_t k, int64_t E, int64_t I, int64_t N,
+                                  int transpose_w2, size_t *bytes);
+
+/* Scores of gfr_moe_route. */
+enum gfr_scoring { GFR_SCORE_SOFTMAX = 0, GFR_SCORE_SIGMOID = 1 };
+
+/*
+ * gfr_moe_route — a router's choice from its logits, and the inputs of the
+ * grouped calls in expert order.
+ *
+ *   s[t, e]   softmax over e, or sigmoid, of logits[t, e]
+ *   v[t, e]   s[t, e] + bias[e]: what experts are chosen by (the weights are s)
+ *   groups    with n_group > 1, experts fall into n_group equal runs; a run's
+ *             value is the sum of its two largest v (the one, if it has one
+ *             live expert), and only the topk_group best runs stay
+ *   choice    the k = topk_ids.shape[1] largest v; equal values, runs' too, go
+ *             to the lower index; ordered by falling v
+ *   weight    s[t, e], divided by the sum over the choice when renormalize (0
+ *             if that sum is 0), times scaling
+ *
+ * An expert whose logit is -inf or NaN, or whose v is, is not live: it is never
+ * chosen, and where fewer than k are left the rest of the row is id -1,
+ * weight 0.  +inf logits give NaN weights under softmax, as the formula does.
+ * Without bias and runs the choice goes by the logits themselves; otherwise v
+ * is computed in FP64, so that neighbouring values are not confused.
+ *
+ *  logits        F32 or BF16 [T, E].
+ *  bias          F32 [E], or NULL.
+ *  topk_ids      I32 [T, k], topk_weights F32 [T, k]: written.
+ *
+ * and, when x is given (else all six are NULL), the pairs (t, j) ordered by
+ * expert, then t, then j, pairs without an expert last:
+ *
+ *  x             BF16 or F16 [T, H], H a multiple of 32.
+ *  xin           FP8_E4M3FN or FP8_E5M2 [T k, H]: each pair's token row in MX
+ *                blocks of 32; zeros for pairs without an expert.  Infinities
+ *                saturate, a NaN element gets a NaN code and does not enter its
+ *                block's maximum.
+ *  xin_scale     E8M0 or U8 [T k, ceil(H/64), 2]: block exponent
+ *                floor(log2(amax)) - emax + 127 (emax 8 / 15), 0 for a block
+ *                of zeros, for the half block behind an odd number of blocks
+ *                and for pairs without an expert.
+ *  group_list    I64 [E]: pairs per expert (GFR_GROUP_LIST_COUNT).
+ *  row_index     I32 [T k]: each row's token t.
+ *  logit         F32 [T k]: its weight.
+ *
+ *  opts          workspace (gfr_moe_route_workspace_size, 256-byte aligned),
+ *                the other fields are ignored.
+ *
+ * Needs 1 <= k <= GFR_MAX_TOPK, k <= E <= GFR_MAX_EXPERTS, E divisible by
+ * n_group, 1 <= topk_group <= n_group <= 64, T k < 2^31 (GFR_ERR_BAD_ARG or
+ * GFR_ERR_UNSUPPORTED); x, xin 16-byte aligned, logits, topk_ids, topk_weights,
+ * row_index, logit 4-byte, group_list 8-byte (GFR_ERR_BAD_ALIGNMENT).  T = 0 clears group_list and does nothing
+ * else.  Other errors as gfr_linear.
+ */
+int gfr_moe_route(const gfr_tensor *logits, const gfr_tensor *bias, int scoring, int n_group,
+                  int topk_group, int renormalize, float scaling, const gfr_tensor *topk_ids,
+                  const gfr_tensor *topk_weights, const gfr_tensor *x, const gfr_tensor *xin,
+                  const gfr_tensor *xin_scale, const gfr_tensor *group_list,
+                  const gfr_tensor *row_index, const gfr_tensor *logit, void *stream,
+                  const gfr_options *opts);
+
+/* Workspace bytes of gfr_moe_route with x for T tokens and E experts (0
+ * without x, and for few tokens).  Pure host arithmetic. */
+int gfr_moe_route_workspace_size(int64_t T, int64_t E, int64_t k, size_t *bytes);
 
 /* ======================================================================== *
  * Raw calls: device pointers plus sizes, semantics as the descriptor calls *

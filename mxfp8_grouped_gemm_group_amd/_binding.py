@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgfr.so")
 GFR_OK = 0
 DEV_BAD_GROUP_LIST = 0x1
 DEV_BAD_ROW_INDEX = 0x2
+DEV_BAD_EXPERT = 0x4
 
 _FP8_KIND = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1, torch.float4_e2m1fn_x2: 2}
 _PACKED = torch.float4_e2m1fn_x2   # two E2M1 elements per byte along the last axis
@@ -44,7 +45,7 @@ class GfrTensor(ctypes.Structure):
 # torch dtype -> gfr_dtype (include/gfr.h)
 DTYPES = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1, torch.float4_e2m1fn_x2: 2,
           torch.float8_e8m0fnu: 3, torch.uint8: 4, torch.bfloat16: 5, torch.float32: 6,
-          torch.int64: 7, torch.int32: 8, torch.int8: 9}
+          torch.int64: 7, torch.int32: 8, torch.int8: 9, torch.float16: 11}
 
 
 def tensor_desc(t: Optional[torch.Tensor]):

@@ -1,0 +1,96 @@
+// Device helpers of the dense product, the few-token experts and the router.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gfr {
+namespace {
+
+typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
+typedef float f4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
+
+// Raw buffer over [base, base + bytes): the base and the step's offset live in
+// scalar registers, a lane keeps one 32-bit offset.  Reads past the end give 0;
+// the end is that of the last aligned word that holds a valid byte, so that a
+// 16-bit element alone in it can be read as a word.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t buffer(const void *base, int64_t bytes) {
+    const int n = bytes > 0x7ffffffc ? 0x7ffffffc : static_cast<int>((bytes + 3) & ~int64_t{3});
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, n, 0x00020000);
+}
+constexpr int kNt = 2;   // non-temporal: read-once data leaves the caches alone
+template <int AUX>
+__device__ __forceinline__ u4_t load16(rsrc_t r, int lane_off, int off) {
+    return __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off, off, AUX));
+}
+template <int AUX>
+__device__ __forceinline__ u2_t load8(rsrc_t r, int lane_off, int off) {
+    return __builtin_bit_cast(u2_t, __builtin_amdgcn_raw_buffer_load_b64(r, lane_off, off, AUX));
+}
+__device__ __forceinline__ uint32_t load1(rsrc_t r, int lane_off, int off) {
+    return __builtin_amdgcn_raw_buffer_load_b8(r, lane_off, off, 0);
+}
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+template <class T>
+__device__ __forceinline__ T load(const void *p) {
+    return *static_cast<const T *>(p);
+}
+
+__device__ __forceinline__ float bf16_f32(uint32_t bits) {
+    return __uint_as_float(bits << 16);
+}
+// Two floats rounded to bf16 (to nearest, ties to even), first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const bf2_t v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+    return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    const h2_t v = {static_cast<_Float16>(a), static_cast<_Float16>(b)};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+template <int CTRL, int ROWS, int BANKS, bool BOUND>
+__device__ __forceinline__ uint32_t dpp(uint32_t old, uint32_t x) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+        static_cast<int>(old), static_cast<int>(x), CTRL, ROWS, BANKS, BOUND));
+}
+
+// Inclusive prefix sum over the 64 lanes: DPP row shifts, then the row totals
+// broadcast into the rows behind them.
+__device__ __forceinline__ uint32_t wave_prefix(uint32_t v) {
+    uint32_t x = v + dpp<0x111, 0xf, 0xf, true>(0, v);
+    x += dpp<0x112, 0xf, 0xf, true>(0, v);
+    x += dpp<0x113, 0xf, 0xf, true>(0, v);
+    x += dpp<0x114, 0xf, 0xe, false>(0, x);
+    x += dpp<0x118, 0xf, 0xc, false>(0, x);
+    x += dpp<0x142, 0xa, 0xf, false>(0, x);
+    x += dpp<0x143, 0xc, 0xf, false>(0, x);
+    return x;
+}
+
+__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
+
+// The current device's CU count, looked up once per device.
+inline int cu_count() {
+    static int cached[64] = {0};
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+    if (!cached[dev]) {
+        int n = 0;
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+            n <= 0)
+            n = 256;
+        cached[dev] = n;
+    }
+    return cached[dev];
+}
+
+}  // namespace
+}  // namespace gfr

@@ -1,0 +1,444 @@
+// Dense product with bias, activation and residual in its epilogue.
+// include/gfr.h states the operator.
+//
+// Both kernels run v_mfma_f32_16x16x32 on bf16 or f16 with FP32 sums, and apply
+// the epilogue to the sums in registers or LDS, so nothing but the result goes
+// to memory.
+//
+//   row kernel   up to 64 rows.  The weights' bytes bound it: a block takes
+//                16 or 32 columns (a gate and an up fragment for swiglu), its
+//                waves split K, and the sums meet in LDS; a lane reads 16
+//                bytes along K, straight into MFMA operands.
+//   tile kernel  more rows: BM x BN tiles, 64-K steps through LDS in two
+//                stages (the next step's loads are in flight in registers
+//                while the present one is multiplied).
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "gfr.h"
+#include "gfr_device.h"
+#include "gfr_layer.h"
+
+namespace gfr {
+namespace {
+
+template <bool F16>
+__device__ __forceinline__ f4_t mfma(u4_t a, u4_t b, f4_t c) {
+    if (F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8_t, a),
+                                                      __builtin_bit_cast(h8_t, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8_t, a),
+                                                   __builtin_bit_cast(bf8_t, b), c, 0, 0, 0);
+}
+
+// Eight elements at lane_off + off bytes.  With K a multiple of 8 they are 16
+// aligned bytes; otherwise rows begin at any even byte, and the four or five
+// aligned words that hold them are shifted into place (no word is read that
+// holds none of them).
+template <bool ALIGNED, int AUX>
+__device__ __forceinline__ u4_t eight(rsrc_t r, int lane_off, int off) {
+    if (ALIGNED) return load16<AUX>(r, lane_off, off);
+    const int at = lane_off & ~3;
+    const bool odd = lane_off & 2;
+    const u4_t q = load16<AUX>(r, at, off);
+    const uint32_t last = __builtin_amdgcn_raw_buffer_load_b32(r, at + (odd ? 16 : 12), off, AUX);
+    u4_t s;
+    s[0] = __builtin_amdgcn_alignbyte(q[1], q[0], 2);
+    s[1] = __builtin_amdgcn_alignbyte(q[2], q[1], 2);
+    s[2] = __builtin_amdgcn_alignbyte(q[3], q[2], 2);
+    s[3] = __builtin_amdgcn_alignbyte(last, q[3], 2);
+    return odd ? s : q;
+}
+
+// The same with only the first `valid` elements, and zeros behind them.
+template <bool ALIGNED>
+__device__ __forceinline__ u4_t eight_tail(rsrc_t r, int lane_off, int off, int valid) {
+    u4_t s = {0, 0, 0, 0};
+    if (ALIGNED) {
+        if (valid > 0) s = load16<0>(r, lane_off, off);
+        return s;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < valid)
+            s[i >> 1] |= static_cast<uint32_t>(
+                             __builtin_amdgcn_raw_buffer_load_b16(r, lane_off + 2 * i, off, 0))
+                         << (16 * (i & 1));
+    return s;
+}
+
+// Buffer over weight rows [first, first + rows).  Its base has to be a whole
+// word's address, which the first row's is not where first and K are odd:
+// returns the bytes from the base to the row.
+template <bool ALIGNED>
+__device__ __forceinline__ int weight_rows(const LinearParams &p, int64_t first, int64_t rows,
+                                           rsrc_t &r) {
+    const int skew = ALIGNED ? 0 : static_cast<int>(first * p.K & 1);
+    r = buffer(p.w + (first * p.K - skew), rows * p.K * 2 + 2 * skew);
+    return 2 * skew;
+}
+
+__device__ __forceinline__ float activate(float v, int act) {
+    switch (act) {
+    case GFR_ACT_RELU: return v < 0.0f ? 0.0f : v;
+    case GFR_ACT_SILU: return silu(v);
+    case GFR_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case GFR_ACT_GELU_TANH: {
+        // (1 + tanh u) / 2 = 1 / (1 + exp(-2u)): no cancellation for negative u
+        const float u = 0.79788456080286536f * (v + 0.044715f * v * v * v);
+        return v / (1.0f + expf(-2.0f * u));
+    }
+    default: return v;
+    }
+}
+
+__device__ __forceinline__ float element(const void *p, int64_t i, bool f32, bool f16) {
+    if (f32) return static_cast<const float *>(p)[i];
+    const uint16_t h = static_cast<const uint16_t *>(p)[i];
+    return f16 ? static_cast<float>(__builtin_bit_cast(_Float16, h)) : bf16_f32(h);
+}
+
+// Four columns n .. n + 3 of row m: activation (gate rows of swiglu in `gate`),
+// residual, rounding, store.  v already holds the sums; columns past N are
+// dropped.
+template <bool SWIGLU, bool F16>
+__device__ __forceinline__ void finish(const LinearParams &p, int m, int n, f4_t v, f4_t gate) {
+    const int64_t at = static_cast<int64_t>(m) * p.N + n;
+    const int cols = min(p.N - n, 4);
+    float y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (p.bias && j < cols) {
+            v[j] += element(p.bias, n + j + (SWIGLU ? p.N : 0), p.bias_f32, F16);
+            if (SWIGLU) gate[j] += element(p.bias, n + j, p.bias_f32, F16);
+        }
+        y[j] = SWIGLU ? silu(gate[j]) * v[j] : activate(v[j], p.act);
+    }
+    if (cols == 4 && (p.N & 3) == 0) {     // rows of whole, aligned fours
+        if (p.residual) {
+            const u2_t h = load<u2_t>(p.residual + at);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint16_t b = h[j >> 1] >> (16 * (j & 1));
+                y[j] += F16 ? static_cast<float>(__builtin_bit_cast(_Float16, b)) : bf16_f32(b);
+            }
+        }
+        if (p.out_f32) {
+            *reinterpret_cast<u2_t *>(static_cast<float *>(p.out) + at) =
+                u2_t{__float_as_uint(y[0]), __float_as_uint(y[1])};
+            *reinterpret_cast<u2_t *>(static_cast<float *>(p.out) + at + 2) =
+                u2_t{__float_as_uint(y[2]), __float_as_uint(y[3])};
+        } else {
+            *reinterpret_cast<u2_t *>(static_cast<uint16_t *>(p.out) + at) =
+                F16 ? u2_t{pack_f16(y[0], y[1]), pack_f16(y[2], y[3])}
+                    : u2_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j >= cols) break;
+        if (p.residual) y[j] += element(p.residual, at + j, false, F16);
+        if (p.out_f32)
+            static_cast<float *>(p.out)[at + j] = y[j];
+        else
+            static_cast<uint16_t *>(p.out)[at + j] =
+                F16 ? static_cast<uint16_t>(pack_f16(y[j], 0.0f))
+                    : static_cast<uint16_t>(pack_bf16(y[j], 0.0f));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Row kernel
+// ---------------------------------------------------------------------------
+constexpr int kRowThreads = 512;
+constexpr int kRowWaves = kRowThreads / 64;
+
+// RG fragments of 16 rows, NF of 16 weight rows (swiglu: NF = 2, gate and up).
+template <bool F16, bool ALIGNED, bool SWIGLU, int RG, int NF>
+__global__ __launch_bounds__(kRowThreads) void row_kernel(LinearParams p) {
+    constexpr int kTile = 16 * NF, kDepth = RG == 1 ? 4 : RG == 2 ? 3 : 2;
+    __shared__ float tiles[kRowWaves][16 * RG][kTile];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const int n0 = blockIdx.x * (SWIGLU ? 16 : kTile);
+    const int64_t bytes = 2 * static_cast<int64_t>(p.K);   // of a row
+    rsrc_t wr[NF];
+    int w_off[NF], x_off[RG];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+        // the fragment's rows; rows past the end read the last one
+        const int first = SWIGLU ? n0 : n0 + 16 * f, last = p.N - 1;
+        const int at = min(first, last);
+        const int skew = weight_rows<ALIGNED>(p, SWIGLU && f ? p.N + at : at, last - at + 1,
+                                              wr[f]);
+        w_off[f] = min(c, last - at) * static_cast<int>(bytes) + 16 * g + skew;
+    }
+    const rsrc_t xr = buffer(p.x, p.M * bytes);
+#pragma unroll
+    for (int q = 0; q < RG; ++q)
+        x_off[q] = min(16 * q + c, p.M - 1) * static_cast<int>(bytes) + 16 * g;
+
+    struct Stage {
+        u4_t w[NF][2], x[RG][2];
+    } st[kDepth];
+    f4_t acc[RG][NF] = {};
+    const int steps = p.K / 64;
+    const int s0 = steps * wave / kRowWaves, s1 = steps * (wave + 1) / kRowWaves;
+    auto fetch = [&](Stage &s, int step) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                s.w[f][h] = eight<ALIGNED, kNt>(wr[f], w_off[f], step * 128 + 64 * h);
+#pragma unroll
+            for (int q = 0; q < RG; ++q)
+                s.x[q][h] = eight<ALIGNED, 0>(xr, x_off[q], step * 128 + 64 * h);
+        }
+    };
+    auto use = [&](const Stage &s) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+                for (int q = 0; q < RG; ++q)
+                    acc[q][f] = mfma<F16>(s.x[q][h], s.w[f][h], acc[q][f]);
+    };
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d)
+        if (s0 + d < s1) fetch(st[d], s0 + d);
+    for (int s = s0; s < s1; s += kDepth)
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d)
+            if (s + d < s1) {
+                use(st[d]);
+                if (s + d + kDepth < s1) fetch(st[d], s + d + kDepth);
+            }
+    if (wave == kRowWaves - 1 && p.K % 64 != 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int valid = p.K - (64 * steps + 32 * h + 8 * g);
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                st[0].w[f][h] = eight_tail<ALIGNED>(wr[f], w_off[f], steps * 128 + 64 * h, valid);
+#pragma unroll
+            for (int q = 0; q < RG; ++q)
+                st[0].x[q][h] = eight_tail<ALIGNED>(xr, x_off[q], steps * 128 + 64 * h, valid);
+        }
+        use(st[0]);
+    }
+#pragma unroll
+    for (int q = 0; q < RG; ++q)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                tiles[wave][16 * q + 4 * g + i][16 * f + c] = acc[q][f][i];
+    __syncthreads();
+    constexpr int kFours = SWIGLU ? 4 : kTile / 4;
+    const int rows = min(p.M, 16 * RG);
+    for (int i = threadIdx.x; i < rows * kFours; i += kRowThreads) {
+        const int m = i / kFours, col = i % kFours * 4;
+        if (n0 + col >= p.N) continue;
+        f4_t v = {0, 0, 0, 0}, gate = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < kRowWaves; ++w) {
+            v += *reinterpret_cast<const f4_t *>(&tiles[w][m][SWIGLU ? 16 + col : col]);
+            if (SWIGLU) gate += *reinterpret_cast<const f4_t *>(&tiles[w][m][col]);
+        }
+        finish<SWIGLU, F16>(p, m, n0 + col, v, gate);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Tile kernel
+// ---------------------------------------------------------------------------
+
+// BM rows of x by BN weight rows (swiglu: BN / 2 output columns, their gate and
+// up rows in turn by fragments of 16), waves of WM x WN.  In LDS a row of 64
+// elements is eight 16-byte pieces, piece j of row r at j ^ (r & 7), so that the
+// 16 lanes that read one piece of 16 rows reach all banks.
+template <bool F16, bool ALIGNED, bool SWIGLU, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void tile_kernel(LinearParams p,
+                                                                          int tiles_m,
+                                                                          int tiles_n) {
+    constexpr int kThreads = (BM / WM) * (BN / WN) * 64;
+    constexpr int kNX = BM * 8 / kThreads, kNW = BN * 8 / kThreads;   // pieces per thread
+    constexpr int FM = WM / 16, FN = WN / 16;
+    extern __shared__ u4_t lds[];                  // [2][BM + BN][8]
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    // Blocks go round the eight XCDs; each XCD takes a run of tiles, eight
+    // tile rows deep, so that its L2 serves their shared operands.
+    const int total = tiles_m * tiles_n, per = (total + 7) / 8;
+    const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if (id >= total) return;
+    const int band = id / (8 * tiles_n), in_band = id - band * 8 * tiles_n;
+    const int depth = min(8, tiles_m - band * 8);
+    const int m0 = (band * 8 + in_band % depth) * BM;
+    const int n0 = in_band / depth * (SWIGLU ? BN / 2 : BN);
+
+    const int64_t bytes = 2 * static_cast<int64_t>(p.K);
+    const rsrc_t xr = buffer(p.x + m0 * static_cast<int64_t>(p.K), min(BM, p.M - m0) * bytes);
+    rsrc_t wr, ur;
+    const int rows = min(SWIGLU ? BN / 2 : BN, p.N - n0);
+    weight_rows<ALIGNED>(p, n0, rows, wr);          // n0 is even: no skew
+    const int skew = weight_rows<ALIGNED>(p, SWIGLU ? int64_t{n0} + p.N : n0, rows, ur);
+    int x_off[kNX], w_off[kNW], x_lds[kNX], w_lds[kNW];
+    const int piece = threadIdx.x & 7;
+#pragma unroll
+    for (int i = 0; i < kNX; ++i) {
+        const int r = (threadIdx.x >> 3) + i * (kThreads / 8);
+        x_off[i] = min(r, p.M - 1 - m0) * static_cast<int>(bytes) + 16 * piece;
+        x_lds[i] = r * 8 + (piece ^ (r & 7));
+    }
+#pragma unroll
+    for (int i = 0; i < kNW; ++i) {
+        const int r = (threadIdx.x >> 3) + i * (kThreads / 8);
+        const int row = SWIGLU ? (r >> 5) * 16 + (r & 15) : r;
+        w_off[i] = min(row, p.N - 1 - n0) * static_cast<int>(bytes) + 16 * piece +
+                   (SWIGLU && (r & 16) ? skew : 0);
+        w_lds[i] = (BM + r) * 8 + (piece ^ (r & 7));
+    }
+    u4_t xs[kNX], ws[kNW];
+    const int steps = (p.K + 63) / 64;
+    auto fetch = [&](int step) {
+        const int off = step * 128;
+        if (step * 64 + 64 <= p.K) {
+#pragma unroll
+            for (int i = 0; i < kNX; ++i) xs[i] = eight<ALIGNED, 0>(xr, x_off[i], off);
+#pragma unroll
+            for (int i = 0; i < kNW; ++i) {
+                if (!SWIGLU) {
+                    ws[i] = eight<ALIGNED, 0>(wr, w_off[i], off);
+                } else {
+                    // 64 lanes hold eight rows: all gate or all up
+                    const int r = uniform((threadIdx.x >> 3) + i * (kThreads / 8));
+                    ws[i] = r & 16 ? eight<ALIGNED, 0>(ur, w_off[i], off)
+                                   : eight<ALIGNED, 0>(wr, w_off[i], off);
+                }
+            }
+        } else {
+            const int valid = p.K - step * 64 - 8 * piece;
+#pragma unroll
+            for (int i = 0; i < kNX; ++i) xs[i] = eight_tail<ALIGNED>(xr, x_off[i], off, valid);
+#pragma unroll
+            for (int i = 0; i < kNW; ++i) {
+                const int r = uniform((threadIdx.x >> 3) + i * (kThreads / 8));
+                ws[i] = SWIGLU && (r & 16) ? eight_tail<ALIGNED>(ur, w_off[i], off, valid)
+                                           : eight_tail<ALIGNED>(wr, w_off[i], off, valid);
+            }
+        }
+    };
+    auto put = [&](int stage) {
+        u4_t *s = lds + stage * (BM + BN) * 8;
+#pragma unroll
+        for (int i = 0; i < kNX; ++i) s[x_lds[i]] = xs[i];
+#pragma unroll
+        for (int i = 0; i < kNW; ++i) s[w_lds[i]] = ws[i];
+    };
+    const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
+    f4_t acc[FM][FN] = {};
+    fetch(0);
+    put(0);
+    __syncthreads();
+    for (int step = 0; step < steps; ++step) {
+        const bool more = step + 1 < steps;
+        if (more) fetch(step + 1);
+        const u4_t *s = lds + (step & 1) * (BM + BN) * 8;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            u4_t a[FM], b[FN];
+#pragma unroll
+            for (int f = 0; f < FM; ++f)
+                a[f] = s[(wm + 16 * f + c) * 8 + ((4 * k + g) ^ (c & 7))];
+#pragma unroll
+            for (int f = 0; f < FN; ++f)
+                b[f] = s[(BM + wn + 16 * f + c) * 8 + ((4 * k + g) ^ (c & 7))];
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) acc[i][j] = mfma<F16>(b[j], a[i], acc[i][j]);
+        }
+        if (more) put((step + 1) & 1);
+        __syncthreads();
+    }
+    // lane (c, g) holds row 16 i + c, columns 16 j + 4 g .. + 3
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int m = m0 + wm + 16 * i + c;
+        if (m >= p.M) continue;
+#pragma unroll
+        for (int j = 0; j < FN; j += SWIGLU ? 2 : 1) {
+            const int n = n0 + (SWIGLU ? wn / 2 + 8 * j : wn + 16 * j) + 4 * g;
+            if (n < p.N)
+                finish<SWIGLU, F16>(p, m, n, acc[i][SWIGLU ? j + 1 : j], acc[i][j]);
+        }
+    }
+}
+
+template <bool F16, bool ALIGNED, bool SWIGLU, int RG>
+hipError_t launch_rows(const LinearParams &p, hipStream_t stream) {
+    constexpr int NF = SWIGLU ? 2 : 1;
+    const int cols = 16;
+    hipLaunchKernelGGL((row_kernel<F16, ALIGNED, SWIGLU, RG, NF>),
+                       dim3((p.N + cols - 1) / cols), dim3(kRowThreads), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <bool F16, bool ALIGNED, bool SWIGLU, int BM, int BN, int WM, int WN>
+hipError_t launch_tiles(const LinearParams &p, hipStream_t stream) {
+    constexpr int lds = 2 * (BM + BN) * 8 * 16;
+    constexpr int cols = SWIGLU ? BN / 2 : BN;
+    auto kernel = &tile_kernel<F16, ALIGNED, SWIGLU, BM, BN, WM, WN>;
+    if (lds > (64 << 10)) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+    }
+    const int tm = (p.M + BM - 1) / BM, tn = (p.N + cols - 1) / cols;
+    const int64_t grid = (static_cast<int64_t>(tm) * tn + 7) / 8 * 8;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)),
+                       dim3((BM / WM) * (BN / WN) * 64), lds, stream, p, tm, tn);
+    return hipGetLastError();
+}
+
+template <bool F16, bool ALIGNED, bool SWIGLU>
+hipError_t launch_linear_t(const LinearParams &p, hipStream_t stream) {
+    if (p.M <= 16) return launch_rows<F16, ALIGNED, SWIGLU, 1>(p, stream);
+    if (p.M <= 32) return launch_rows<F16, ALIGNED, SWIGLU, 2>(p, stream);
+    if (p.M <= 64) return launch_rows<F16, ALIGNED, SWIGLU, 4>(p, stream);
+    const int64_t cols = SWIGLU ? 128 : 256;
+    const int64_t big = ((p.M + 255) / 256) * ((p.N + cols - 1) / cols);
+    if (ALIGNED && big >= 192)
+        return launch_tiles<F16, ALIGNED, SWIGLU, 256, 256, 128, 64>(p, stream);
+    const int64_t mid = ((p.M + 127) / 128) * ((p.N + cols / 2 - 1) / (cols / 2));
+    if (mid >= 128) return launch_tiles<F16, ALIGNED, SWIGLU, 128, 128, 64, 64>(p, stream);
+    return launch_tiles<F16, ALIGNED, SWIGLU, 64, 64, 32, 32>(p, stream);
+}
+
+template <bool F16, bool ALIGNED>
+hipError_t launch_linear_a(const LinearParams &p, hipStream_t stream) {
+    return p.act == GFR_ACT_SWIGLU ? launch_linear_t<F16, ALIGNED, true>(p, stream)
+                                   : launch_linear_t<F16, ALIGNED, false>(p, stream);
+}
+
+}  // namespace
+
+int linear_split(int64_t M, int64_t N, int64_t K, int act) {
+    (void)M, (void)N, (void)K, (void)act;
+    return 1;
+}
+
+hipError_t launch_linear(const LinearParams &p, hipStream_t stream) {
+    const bool aligned = p.K % 8 == 0;
+    if (p.f16)
+        return aligned ? launch_linear_a<true, true>(p, stream)
+                       : launch_linear_a<true, false>(p, stream);
+    return aligned ? launch_linear_a<false, true>(p, stream)
+                   : launch_linear_a<false, false>(p, stream);
+}
+
+}  // namespace gfr
