@@ -413,7 +413,7 @@ int gfr_linear_workspace_size(const gfr_tensor *x, const gfr_tensor *w, const gf
 
 /*
  * gfr_moe_decode — the expert part of a MoE block for at most
- * GFR_DECODE_MAX_TOKENS tokens, in two launches:
+ * GFR_DECODE_MAX_TOKENS tokens, in three launches:
  *
  *   gate, up  = x[t] @ w13[e]                      e = topk_ids[t, j]
  *   out[t]    = sum_j topk_weights[t, j] * ((silu(gate) * up) @ w2[e])
@@ -452,10 +452,10 @@ int gfr_moe_decode(const gfr_tensor *x, const gfr_tensor *w13, const gfr_tensor 
                    float shared_input_weight, const gfr_tensor *out, int transpose_w13,
                    int transpose_w2, void *stream, const gfr_options *opts);
 
-/* Workspace bytes of gfr_moe_decode for T tokens of k experts out of E,
- * w2 [I, N] per expert in the given layout.  Pure host arithmetic. */
-int gfr_moe_decode_workspace_size(int64_t T, int64_t k, int64_t E, int64_t I, int64_t N,
-                                  int transpose_w2, size_t *bytes);
+/* Workspace bytes of gfr_moe_decode for T tokens of k experts out of E, w13 [H,
+ * 2I] and w2 [I, N] per expert in the given layouts.  Pure host arithmetic. */
+int gfr_moe_decode_workspace_size(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I,
+                                  int64_t N, int transpose_w13, int transpose_w2, size_t *bytes);
 
 /* Scores of gfr_moe_route. */
 enum gfr_scoring { GFR_SCORE_SOFTMAX = 0, GFR_SCORE_SIGMOID = 1 };

@@ -34,7 +34,8 @@ def _lib():
         lib.gfr_linear_workspace_size.argtypes = [_T] * 4 + [ctypes.c_int, _T, _SIZE]
         lib.gfr_moe_decode.argtypes = [_T] * 8 + [ctypes.c_float, _T, ctypes.c_int, ctypes.c_int,
                                                   _P, _O]
-        lib.gfr_moe_decode_workspace_size.argtypes = [ctypes.c_int64] * 5 + [ctypes.c_int, _SIZE]
+        lib.gfr_moe_decode_workspace_size.argtypes = [ctypes.c_int64] * 6 + \
+            [ctypes.c_int] * 2 + [_SIZE]
         lib.gfr_moe_route.argtypes = [_T, _T] + [ctypes.c_int] * 4 + [ctypes.c_float] + \
             [_T] * 8 + [_P, _O]
         lib.gfr_moe_route_workspace_size.argtypes = [ctypes.c_int64] * 3 + [_SIZE]
@@ -111,19 +112,19 @@ def linear(x, w, bias=None, *, activation="none", residual=None, out_dtype=None,
     return out
 
 
-def moe_decode_workspace_size(T: int, k: int, E: int, I: int, N: int,
-                              transpose_w2: bool = False) -> int:
+def moe_decode_workspace_size(T: int, k: int, E: int, H: int, I: int, N: int,
+                              transpose_w13: bool = False, transpose_w2: bool = False) -> int:
     """Workspace bytes of a moe_decode call of these sizes."""
     need = ctypes.c_size_t(0)
-    _check(_lib().gfr_moe_decode_workspace_size(T, k, E, I, N, int(bool(transpose_w2)),
-                                                ctypes.byref(need)))
+    _check(_lib().gfr_moe_decode_workspace_size(
+        T, k, E, H, I, N, int(bool(transpose_w13)), int(bool(transpose_w2)), ctypes.byref(need)))
     return need.value
 
 
 def moe_decode(x, w13, scale13, w2, scale2, topk_ids, topk_weights, *, transpose_w13=False,
                transpose_w2=False, shared_input=None, shared_input_weight=1.0,
                out_dtype=torch.bfloat16, out=None, workspace=None, status=None, stream=None):
-    """The experts of a MoE block for at most DECODE_MAX_TOKENS tokens, in two
+    """The experts of a MoE block for at most DECODE_MAX_TOKENS tokens, in three
     launches (include/gfr.h, gfr_moe_decode); returns out.
 
     out[t] = sum_j topk_weights[t, j] * swiglu(x[t] @ w13[e]) @ w2[e]
@@ -151,8 +152,8 @@ def moe_decode(x, w13, scale13, w2, scale2, topk_ids, topk_weights, *, transpose
         if out is None:
             out = torch.empty((x.shape[0], N), dtype=out_dtype, device=dev)
         if workspace is None:
-            workspace = _workspace(None, moe_decode_workspace_size(T, k, E, I, N, transpose_w2),
-                                   dev)
+            workspace = _workspace(None, moe_decode_workspace_size(
+                T, k, E, x.shape[1], I, N, transpose_w13, transpose_w2), dev)
         d = [tensor_desc(t) for t in (x, w13, scale13, w2, scale2, topk_ids, topk_weights,
                                       shared_input, out)]
         _check(lib.gfr_moe_decode(*map(_ref, d[:8]), float(shared_input_weight), _ref(d[8]),

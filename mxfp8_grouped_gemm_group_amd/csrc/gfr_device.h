@@ -75,7 +75,19 @@ __device__ __forceinline__ uint32_t wave_prefix(uint32_t v) {
     return x;
 }
 
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
+// exp(v) to about two units in the last place: v_exp_f32 (2^t) of the rounded
+// product t = v log2(e), times 1 + what the rounding left over.  Overflows to
+// infinity and underflows to 0 as exp does; NaN stays NaN.
+__device__ __forceinline__ float exp_f32(float v) {
+    constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596299112661746887e-8f;
+    const float b = __builtin_amdgcn_fmed3f(v, -200.0f, 200.0f);   // finite, for the remainder
+    const float r = fmaf(b, kLo, fmaf(b, kHi, -(b * kHi)));
+    return __builtin_amdgcn_exp2f(v * kHi) * fmaf(r, 0.693147182464599609375f, 1.0f);
+}
+// v / (1 + exp(-v))
+__device__ __forceinline__ float silu(float v) {
+    return v * __builtin_amdgcn_rcpf(1.0f + exp_f32(-v));
+}
 
 // The current device's CU count, looked up once per device.
 inline int cu_count() {

@@ -23,6 +23,12 @@ struct LinearParams {
 int linear_split(int64_t M, int64_t N, int64_t K, int act);
 hipError_t launch_linear(const LinearParams &p, hipStream_t stream);
 
+// One of moe_decode's two products: the K chunks whose partial sums are kept
+// apart, and the column tiles each wave of a block takes.
+struct DecodePart {
+    int32_t chunks, run;
+};
+
 struct DecodeParams {
     const uint16_t *x;         // [T, H] bf16
     const uint8_t *w13, *s13, *w2, *s2;
@@ -31,22 +37,23 @@ struct DecodeParams {
     const uint16_t *shared;    // [T, N] bf16 or null
     void *out;                 // [T, N]
     int32_t *status;           // may be null
-    uint16_t *h;               // [2][T k][I]: silu(gate) * up as two bf16 terms
-    float *y;                  // [split][T k][N]: weighted expert outputs
-    int32_t *counter;          // [column tiles]: finished units of a column tile
+    float *gu;                 // [gate_up.chunks][T k][2I]: partial sums of x w13
+    float *y;                  // [down.chunks][T k][N]: partial sums of h w2
     int64_t s13_e, s2_e;       // bytes between experts' scales (0: shared)
     float shared_w;
     int32_t out_f32;
-    int32_t T, k, E, H, I, N, split;
+    int32_t T, k, E, H, I, N;
+    DecodePart gate_up, down;
 };
 
-// Workspace layout of moe_decode (256-byte aligned regions) and the K splits
-// of its down product.
+// Workspace layout of moe_decode (256-byte aligned regions) and the products'
+// shapes.
 struct DecodeLayout {
-    size_t h, y, counter, total;
-    int split;
+    size_t gu, y, total;
+    DecodePart gate_up, down;
 };
-DecodeLayout decode_layout(int64_t T, int64_t k, int64_t E, int64_t I, int64_t N, int transpose_w2);
+DecodeLayout decode_layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int64_t N,
+                           int transpose_w13, int transpose_w2);
 hipError_t launch_decode(const DecodeParams &p, int transpose_w13, int transpose_w2, int e5m2,
                          hipStream_t stream);
 

@@ -66,13 +66,13 @@ size_t linear_bytes(const gfr::LinearParams &p) {
     return (sizeof(float) * p.split * p.M * rows + 255) & ~static_cast<size_t>(255);
 }
 
-int check_decode_sizes(int64_t T, int64_t k, int64_t E, int64_t I, int64_t N) {
-    if (T < 0 || k < 1 || E < 1 || I < 1 || N < 0) return GFR_ERR_BAD_SHAPE;
+int check_decode_sizes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int64_t N) {
+    if (T < 0 || k < 1 || E < 1 || H < 1 || I < 1 || N < 0) return GFR_ERR_BAD_SHAPE;
     if (T > GFR_DECODE_MAX_TOKENS || k > GFR_MAX_TOPK || T * k > 1024 || E > GFR_MAX_EXPERTS ||
-        I % 64 != 0 || N % 64 != 0)
+        H % 64 != 0 || I % 64 != 0 || N % 64 != 0)
         return GFR_ERR_UNSUPPORTED;
-    // an expert's weights, and silu(gate) * up of all pairs, by 32-bit offsets
-    if (I > kMaxRows || N > kMaxRows || I * N > kMaxRows || 4 * T * k * I > kMaxRows)
+    // an expert's weights are addressed by 32-bit offsets
+    if (H > kMaxRows || I > kMaxRows || N > kMaxRows || 2 * H * I > kMaxRows || I * N > kMaxRows)
         return GFR_ERR_UNSUPPORTED;
     return GFR_OK;
 }
@@ -119,12 +119,15 @@ int gfr_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *bias,
                                                                                  : GFR_ERR_HIP;
 }
 
-int gfr_moe_decode_workspace_size(int64_t T, int64_t k, int64_t E, int64_t I, int64_t N,
-                                  int transpose_w2, size_t *bytes) {
+int gfr_moe_decode_workspace_size(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I,
+                                  int64_t N, int transpose_w13, int transpose_w2, size_t *bytes) {
     if (!bytes) return GFR_ERR_NULL_ARG;
-    if (transpose_w2 != 0 && transpose_w2 != 1) return GFR_ERR_BAD_ARG;
-    GFR_TRY(check_decode_sizes(T, k, E, I, N));
-    *bytes = T > 0 && N > 0 ? gfr::decode_layout(T, k, E, I, N, transpose_w2).total : 0;
+    if ((transpose_w13 != 0 && transpose_w13 != 1) || (transpose_w2 != 0 && transpose_w2 != 1))
+        return GFR_ERR_BAD_ARG;
+    GFR_TRY(check_decode_sizes(T, k, E, H, I, N));
+    *bytes = T > 0 && N > 0
+                 ? gfr::decode_layout(T, k, E, H, I, N, transpose_w13, transpose_w2).total
+                 : 0;
     return GFR_OK;
 }
 
@@ -154,14 +157,13 @@ int gfr_moe_decode(const gfr_tensor *x, const gfr_tensor *w13, const gfr_tensor 
         GFR_TRY(check_desc(shared_input, {2}, {GFR_DT_BF16}));
         if (!shape_is(shared_input, {T, N})) return GFR_ERR_BAD_SHAPE;
     }
-    if (H < 1) return GFR_ERR_BAD_SHAPE;
-    GFR_TRY(check_decode_sizes(T, k, E, I, N));
-    if (H % 64 != 0 || H > int64_t{1} << 20 || H * N2 > kMaxRows) return GFR_ERR_UNSUPPORTED;
+    GFR_TRY(check_decode_sizes(T, k, E, H, I, N));
     if (T == 0 || N == 0) return GFR_OK;
     for (const gfr_tensor *t : {x, w13, scale13, w2, scale2, topk_ids, topk_weights, out})
         if (!aligned(t->data, 16)) return GFR_ERR_BAD_ALIGNMENT;
     if (present(shared_input) && !aligned(shared_input->data, 16)) return GFR_ERR_BAD_ALIGNMENT;
-    const gfr::DecodeLayout d = gfr::decode_layout(T, k, E, I, N, transpose_w2);
+    const gfr::DecodeLayout d =
+        gfr::decode_layout(T, k, E, H, I, N, transpose_w13, transpose_w2);
     GFR_TRY(check_workspace(opts, d.total));
     char *ws = static_cast<char *>(opts->workspace);
     p.x = static_cast<const uint16_t *>(x->data);
@@ -176,10 +178,10 @@ int gfr_moe_decode(const gfr_tensor *x, const gfr_tensor *w13, const gfr_tensor 
     p.out = out->data;
     p.out_f32 = out->dtype == GFR_DT_F32;
     p.status = opts->status_dev;
-    p.h = reinterpret_cast<uint16_t *>(ws + d.h);
+    p.gu = reinterpret_cast<float *>(ws + d.gu);
     p.y = reinterpret_cast<float *>(ws + d.y);
-    p.counter = reinterpret_cast<int32_t *>(ws + d.counter);
-    p.split = d.split;
+    p.gate_up = d.gate_up;
+    p.down = d.down;
     p.T = static_cast<int32_t>(T);
     p.k = static_cast<int32_t>(k);
     p.E = static_cast<int32_t>(E);

@@ -87,7 +87,7 @@ __device__ __forceinline__ float activate(float v, int act) {
     case GFR_ACT_GELU_TANH: {
         // (1 + tanh u) / 2 = 1 / (1 + exp(-2u)): no cancellation for negative u
         const float u = 0.79788456080286536f * (v + 0.044715f * v * v * v);
-        return v / (1.0f + expf(-2.0f * u));
+        return v * __builtin_amdgcn_rcpf(1.0f + exp_f32(-2.0f * u));
     }
     default: return v;
     }
@@ -365,17 +365,33 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void tile_kernel(Linear
         if (more) put((step + 1) & 1);
         __syncthreads();
     }
-    // lane (c, g) holds row 16 i + c, columns 16 j + 4 g .. + 3
+    // Lane (c, g) holds row 16 i + c, columns 16 j + 4 g .. + 3.  Sixteen rows at
+    // a time go through LDS (the wave's own part of the stages, which every wave
+    // is done with), so that the epilogue reads and writes whole runs of columns.
+    constexpr int kPitch = WN + 4;     // spreads the rows over the banks
+    constexpr int kCols = SWIGLU ? WN / 2 : WN;
+    float *slab = reinterpret_cast<float *>(lds) + wave * 16 * kPitch;
+    const int col0 = n0 + (SWIGLU ? wn / 2 : wn);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        const int m = m0 + wm + 16 * i + c;
-        if (m >= p.M) continue;
+        const int row0 = m0 + wm + 16 * i;
+        if (row0 >= p.M) break;
 #pragma unroll
-        for (int j = 0; j < FN; j += SWIGLU ? 2 : 1) {
-            const int n = n0 + (SWIGLU ? wn / 2 + 8 * j : wn + 16 * j) + 4 * g;
-            if (n < p.N)
-                finish<SWIGLU, F16>(p, m, n, acc[i][SWIGLU ? j + 1 : j], acc[i][j]);
+        for (int j = 0; j < FN; ++j)
+            *reinterpret_cast<f4_t *>(&slab[c * kPitch + 16 * j + 4 * g]) = acc[i][j];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int o = lane; o < 16 * (kCols / 4); o += 64) {
+            const int r = o / (kCols / 4), col = o % (kCols / 4) * 4;
+            if (row0 + r >= p.M || col0 + col >= p.N) continue;
+            const float *at = slab + r * kPitch + (SWIGLU ? (col >> 4) * 32 + (col & 15) : col);
+            const f4_t v = *reinterpret_cast<const f4_t *>(at + (SWIGLU ? 16 : 0));
+            const f4_t gate = *reinterpret_cast<const f4_t *>(at);
+            finish<SWIGLU, F16>(p, row0 + r, col0 + col, v, gate);
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
     }
 }
 

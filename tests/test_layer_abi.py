@@ -131,12 +131,13 @@ def test_decode_refusals(over, code):
 
 
 def test_decode_workspace_covers_its_regions():
-    for T, k, E, I, N, t in ((1, 8, 256, 512, 2048, False), (64, 3, 32, 8192, 4096, False),
-                             (64, 16, 4, 64, 64, True), (1, 1, 1, 4096, 64, True)):
-        need = gfr.moe_decode_workspace_size(T, k, E, I, N, t)
-        assert need >= 4 * T * k * I + 4 * T * k * N + 4 * (N // 16)
+    for T, k, E, H, I, N, t in ((1, 8, 256, 2048, 512, 2048, False),
+                                (64, 3, 32, 4096, 8192, 4096, False),
+                                (64, 16, 4, 64, 64, 64, True), (1, 1, 1, 64, 4096, 64, True)):
+        need = gfr.moe_decode_workspace_size(T, k, E, H, I, N, t, t)
+        assert need >= 4 * T * k * 2 * I + 4 * T * k * N
     with pytest.raises(gfr.GfrError):
-        gfr.moe_decode_workspace_size(65, 2, 8, 64, 64)
+        gfr.moe_decode_workspace_size(65, 2, 8, 64, 64, 64)
 
 
 # ---- moe_route --------------------------------------------------------------

@@ -180,7 +180,7 @@ def test_nan_token_reaches_no_other_token():
 @pytest.mark.parametrize("t", [False, True])
 def test_same_bits_twice_and_used_workspace(t):
     a = make(12, 4, 8, 256, 512, 256, "e5m2", t, t, shared=True)
-    need = gfr.moe_decode_workspace_size(12, 4, 8, 512, 256, t)
+    need = gfr.moe_decode_workspace_size(12, 4, 8, 256, 512, 256, t, t)
     ws = torch.randint(0, 256, (need + 256,), dtype=torch.uint8, device=DEV)
     one = call(a, workspace=ws[:need])
     guard = ws[need:].clone()
