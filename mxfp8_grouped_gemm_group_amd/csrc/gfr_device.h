@@ -33,8 +33,8 @@ template <int AUX>
 __device__ __forceinline__ u2_t load8(rsrc_t r, int lane_off, int off) {
     return __builtin_bit_cast(u2_t, __builtin_amdgcn_raw_buffer_load_b64(r, lane_off, off, AUX));
 }
-__device__ __forceinline__ uint32_t load1(rsrc_t r, int lane_off, int off) {
-    return __builtin_amdgcn_raw_buffer_load_b8(r, lane_off, off, 0);
+__device__ __forceinline__ uint32_t load2(rsrc_t r, int lane_off, int off) {
+    return __builtin_amdgcn_raw_buffer_load_b16(r, lane_off, off, 0);
 }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 

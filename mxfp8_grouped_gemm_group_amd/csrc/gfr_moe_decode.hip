@@ -48,32 +48,64 @@ constexpr int kOperandBytes = 64 << 10;    // of LDS for a chunk's operand rows
 // (a launch to make it once would cost more).  Within a group the order of the
 // pairs is left to the atomics: each is a row of its own, so no result depends
 // on it.  Which group of an expert a pair falls into must be the same in every
-// block, so where an expert has several groups the ranks are counted instead.
+// block, so where an expert has several groups its pairs are marked in a bit
+// mask, and a pair's rank is the count of the marks below its own.
 // ---------------------------------------------------------------------------
 struct Plan {
     int start[GFR_MAX_EXPERTS];        // counts, then first index into pairs
     uint16_t pairs[kMaxPairs];         // grouped by expert
-    uint16_t ids[kMaxPairs];           // only if an expert has several groups
     uint32_t totals[kWaves];
-    int several;
     int expert, first, count;          // this block's group
 };
+constexpr int kMaskWords = kMaxPairs / 32;
+constexpr int kMaskBytes = kMaxPairs / 16 * kMaskWords * 4;   // experts with over 16 pairs
 
-// Fills `s` for group `mine`; false if there are fewer groups.
+// The same for at most 64 pairs, one per lane, without a barrier: every wave
+// goes through the experts in the order of their first pairs until it reaches
+// group `mine`, and all write the same list.  (One token of 256 experts, three
+// launches: 29 -> 24 us with this and the weights' loads ahead of the operand.)
 template <int R>
-__device__ __forceinline__ bool make_plan(const DecodeParams &p, Plan &s, int mine) {
+__device__ __forceinline__ bool make_small_plan(const DecodeParams &p, Plan &s, int mine, int &e,
+                                                int &first, int &count) {
+    const int lane = threadIdx.x & 63;
+    int id = lane < p.T * p.k ? p.ids[lane] : -1;
+    if (id >= p.E || id < -1) {
+        if (p.status) atomicOr(p.status, GFR_DEV_BAD_EXPERT);
+        id = -1;
+    }
+    uint64_t left = __ballot(id >= 0);
+    while (left) {
+        e = __builtin_amdgcn_readlane(id, __ffsll(static_cast<unsigned long long>(left)) - 1);
+        const uint64_t same = __ballot(id == e);
+        const int pairs = __popcll(same), groups = (pairs + R - 1) / R;
+        if (mine < groups) {
+            first = mine * R;
+            count = min(pairs - first, R);
+            if (id == e) s.pairs[__popcll(same & ((uint64_t{1} << lane) - 1))] = lane;
+            return true;
+        }
+        mine -= groups;
+        left &= ~same;
+    }
+    return false;
+}
+
+// Fills `s` for group `mine`; false if there are fewer groups.  `mask`: kMaskBytes
+// of LDS that nothing else uses meanwhile.
+template <int R>
+__device__ __forceinline__ bool make_plan(const DecodeParams &p, Plan &s, uint32_t *mask,
+                                          int mine) {
     constexpr int kPer = kMaxPairs / kThreads, kExperts = GFR_MAX_EXPERTS / kThreads;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n = p.T * p.k;
-    for (int e = tid; e < p.E; e += kThreads) s.start[e] = 0;
-    if (tid == 0) s.several = 0;
-    __syncthreads();
     int id[kPer], rank[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int q = tid + i * kThreads;
         id[i] = q < n ? p.ids[q] : -1;
     }
+    for (int e = tid; e < p.E; e += kThreads) s.start[e] = 0;
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         if (id[i] >= p.E || id[i] < -1) {
@@ -83,15 +115,14 @@ __device__ __forceinline__ bool make_plan(const DecodeParams &p, Plan &s, int mi
         rank[i] = id[i] >= 0 ? atomicAdd(&s.start[id[i]], 1) : 0;
     }
     __syncthreads();
-    // consecutive experts per thread; pairs and groups scanned together (both
-    // at most 1024)
+    // Consecutive experts per thread.  Pairs (at most 1024), groups (1024) and
+    // experts of several groups (64) are scanned together: 11, 11 and 7 bits.
     uint32_t c[kExperts], v = 0;
 #pragma unroll
     for (int h = 0; h < kExperts; ++h) {
         const int e = kExperts * tid + h;
         c[h] = e < p.E ? s.start[e] : 0;
-        v += c[h] | ((c[h] + R - 1) / R) << 16;
-        if (c[h] > R) s.several = 1;
+        v += c[h] | ((c[h] + R - 1) / R) << 11 | (c[h] > R ? 1u << 22 : 0);
     }
     const uint32_t incl = wave_prefix(v);
     if (lane == 63) s.totals[wave] = incl;
@@ -102,38 +133,43 @@ __device__ __forceinline__ bool make_plan(const DecodeParams &p, Plan &s, int mi
         if (w < wave) at += s.totals[w];
         all += s.totals[w];
     }
-    if (mine >= static_cast<int>(all >> 16)) return false;
-    uint32_t pair = at & 0xffff;
-    int group = at >> 16;
+    if (mine >= static_cast<int>(all >> 11 & 0x7ff)) return false;
+    const int several = all >> 22;
 #pragma unroll
     for (int h = 0; h < kExperts; ++h) {
         const int e = kExperts * tid + h;
-        if (e < p.E) s.start[e] = pair;
-        const int groups = (c[h] + R - 1) / R;
+        const int pair = at & 0x7ff, group = at >> 11 & 0x7ff, groups = (c[h] + R - 1) / R;
+        // first index; mask + 1 above it
+        if (e < p.E) s.start[e] = pair | (c[h] > R ? (at >> 22) + 1 : 0) << 16;
         if (mine >= group && mine < group + groups) {
             const int r = (mine - group) * R;
             s.expert = e;
             s.first = pair + r;
             s.count = min(static_cast<int>(c[h]) - r, R);
         }
-        group += groups;
-        pair += c[h];
+        at += c[h] | groups << 11 | (c[h] > R ? 1u << 22 : 0);
     }
-    const bool several = s.several;
-    if (several)
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) s.ids[tid + i * kThreads] = static_cast<uint16_t>(id[i]);
+    for (int i = tid; i < several * kMaskWords; i += kThreads) mask[i] = 0;
     __syncthreads();
-    if (several)
+    if (several) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            rank[i] = 0;
-            if (id[i] >= 0)
-                for (int q = 0; q < tid + i * kThreads; ++q) rank[i] += s.ids[q] == id[i];
+            const int q = tid + i * kThreads, m = id[i] >= 0 ? s.start[id[i]] >> 16 : 0;
+            if (m) atomicOr(&mask[(m - 1) * kMaskWords + (q >> 5)], 1u << (q & 31));
         }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int q = tid + i * kThreads, m = id[i] >= 0 ? s.start[id[i]] >> 16 : 0;
+            if (!m) continue;
+            const uint32_t *w = mask + (m - 1) * kMaskWords;
+            rank[i] = __popc(w[q >> 5] & ((1u << (q & 31)) - 1));
+            for (int j = 0; j < q >> 5; ++j) rank[i] += __popc(w[j]);
+        }
+    }
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-        if (id[i] >= 0) s.pairs[s.start[id[i]] + rank[i]] = tid + i * kThreads;
+        if (id[i] >= 0) s.pairs[(s.start[id[i]] & 0xffff) + rank[i]] = tid + i * kThreads;
     __syncthreads();
     return true;
 }
@@ -177,6 +213,7 @@ struct Operand {
 // past the end read the next row's bytes, or zeros; nothing keeps them.)
 template <int FMT>
 struct StreamKN {
+    static constexpr bool kKN = true;
     static constexpr int kTile = 128, kAcc = 8, kStep = 64, kDepth = 2;
     struct Stage {
         u2_t w[2][8];
@@ -196,8 +233,9 @@ struct StreamKN {
         f.s = load16<0>(a.sc, a.sc_off, (k0 >> 6) * 2 * a.ld + 2 * n0);
     }
     template <int RG, int TERMS>
-    static __device__ __forceinline__ void use(const Stage &f, const Operand &x, int k,
+    static __device__ __forceinline__ void use(Stage &f, const Operand &x, int k, int left,
                                                int live, f4_t (&acc)[RG][kAcc]) {
+        (void)left;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             u4_t o[RG][TERMS];
@@ -250,54 +288,98 @@ struct StreamKN {
     }
 };
 
-// Weights [N, K]: of a 128-byte step, lane (c, g) reads bytes 32g .. 32g + 31,
-// one scale block, of columns 16 f + c, f < 4; accumulator f holds columns 16 f
-// + r for fragment rows r.  Where K ends inside a step, lanes past it hold
-// zeros.
-template <int FMT>
+// Weights [N, K]: a step is KL 128-byte lines of columns 16 f + r, f < NF = 4 /
+// KL; accumulator f holds columns 16 f + r for fragment rows r.  The MFMA wants
+// 16-byte pieces g and 4 + g of column c's line in lane (c, g).  Loading them so
+// would touch 16 half lines at a time; instead one load takes columns 0-7's whole
+// lines and one columns 8-15's, and the lanes with c < 8 swap what is not theirs
+// with those eight further (one DPP move per word).  The step's scales of column
+// c, eight 16-bit pairs, are read two to a lane and handed round, for the same
+// reason.
+// KL = 2 with one row fragment (16 experts of 4096 x 6144, 8 tokens: 156 us;
+// KL = 1 185, KL = 4 170), 1 with two, whose operand reads a wider tile shares.
+template <int FMT, int KL>
 struct StreamNK {
-    static constexpr int kTile = 64, kAcc = 4, kStep = 128, kDepth = 3;
+    static constexpr bool kKN = false;
+    static constexpr int NF = 4 / KL;
+    static constexpr int kTile = 16 * NF, kAcc = NF, kStep = 128 * KL, kDepth = 3;
     struct Stage {
-        u4_t w[4][2];
-        uint32_t s[4];
+        u4_t w[NF][KL][2];
+        uint32_t s[2];
     };
     static __device__ __forceinline__ void place(Weights &a, int c, int g) {
-        a.w_off = c * a.ld + 32 * g;
-        a.sc_off = c * (a.ld >> 5) + g;
+        a.w_off = (c & 7) * a.ld + 16 * (g + 4 * (c >> 3));
+        // pairs v = 2g, 2g + 1 of column c: fragment v / (2 KL), half v % (2 KL)
+        a.sc_off = (16 * (g / KL) + c) * (a.ld >> 5) + 4 * (g % KL);
     }
-    static __device__ __forceinline__ int lane_k(int g) { return 32 * g; }
+    static __device__ __forceinline__ int lane_k(int g) { return 16 * g; }
     static __device__ __forceinline__ void fetch(Stage &f, const Weights &a, int n0, int k0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < NF; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                f.w[i][h] = load16<kNt>(a.w, a.w_off, (n0 + 16 * i) * a.ld + k0 + 16 * h);
+            for (int l = 0; l < KL; ++l)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            f.s[i] = load1(a.sc, a.sc_off, (n0 + 16 * i) * (a.ld >> 5) + (k0 >> 5));
-        if (k0 + kStep > a.ld && (threadIdx.x & 32))   // g >= 2; K is a multiple of 64
+                for (int b = 0; b < 2; ++b)
+                    f.w[i][l][b] =
+                        load16<kNt>(a.w, a.w_off, (n0 + 16 * i + 8 * b) * a.ld + k0 + 128 * l);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f.w[i][0] = f.w[i][1] = u4_t{0, 0, 0, 0}, f.s[i] = 127;
+        for (int v = 0; v < 2; ++v)
+            f.s[v] = load2(a.sc, a.sc_off, n0 * (a.ld >> 5) + (k0 >> 5) + 2 * v);
+    }
+    // Swaps lanes c < 8's second words with lanes c + 8's first.
+    static __device__ __forceinline__ void swap_halves(u4_t &a, u4_t &b) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t x = a[j], y = b[j];
+            a[j] = dpp<0x128, 0xf, 0xc, false>(x, y);
+            b[j] = dpp<0x128, 0xf, 0x3, false>(y, x);
+        }
     }
     template <int RG, int TERMS>
-    static __device__ __forceinline__ void use(const Stage &f, const Operand &x, int k,
+    static __device__ __forceinline__ void use(Stage &f, const Operand &x, int k, int left,
                                                int live, f4_t (&acc)[RG][kAcc]) {
+        const int shift = threadIdx.x & 32 ? 8 : 0;    // g >= 2: the half's second block
+        const uint32_t pair = f.s[0] | f.s[1] << 16;
+        uint32_t s[4];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int j = 0; j < 4; ++j)
+            s[j] = __shfl(pair, (threadIdx.x & 15) + 16 * j) >> shift;
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+#pragma unroll
+            for (int l = 0; l < KL; ++l) swap_halves(f.w[i][l][0], f.w[i][l][1]);
+        if (left < kStep) {
+            // halves behind K's end are zeros (K is a multiple of 64), and their
+            // scales, another column's, one
+#pragma unroll
+            for (int h = 1; h < 2 * KL; ++h)
+                if (64 * h >= left)
+#pragma unroll
+                    for (int i = 0; i < NF; ++i) {
+                        f.w[i][h >> 1][h & 1] = u4_t{0, 0, 0, 0};
+                        const int v = i * 2 * KL + h;
+                        s[v >> 1] = v & 1 ? (s[v >> 1] & 0xffff) | 0x7f0000
+                                          : (s[v >> 1] & 0xffff0000u) | 0x7f;
+                    }
+        }
+#pragma unroll
+        for (int h = 0; h < 4 * KL; ++h) {             // 64-byte halves' 8-byte halves
             u4_t o[RG][TERMS];
 #pragma unroll
             for (int q = 0; q < RG; ++q)
                 if (q < live)
 #pragma unroll
                     for (int t = 0; t < TERMS; ++t)
-                        o[q][t] = load<u4_t>(x.lane + q * x.pitch + t * x.term + 2 * (k + 8 * h));
+                        o[q][t] = load<u4_t>(x.lane + q * x.pitch + t * x.term +
+                                             2 * (k + 64 * (h >> 1) + 8 * (h & 1)));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float scale = e8m0(f.s[i]);
+            for (int i = 0; i < NF; ++i) {
+                const int v = i * 2 * KL + (h >> 1);
+                const float scale = e8m0(s[v >> 1] >> (16 * (v & 1)) & 0xff);
                 u4_t m;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const uint32_t w = f.w[i][h >> 1][2 * (h & 1) + q];
+                    const uint32_t w = f.w[i][h >> 2][h >> 1 & 1][2 * (h & 1) + q];
                     m[2 * q] = to_bf16<FMT, false>(w, scale);
                     m[2 * q + 1] = to_bf16<FMT, true>(w, scale);
                 }
@@ -314,7 +396,7 @@ struct StreamNK {
                                                  const f4_t (&acc)[kAcc]) {
         (void)cols;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<f4_t *>(row + n0 + 16 * i + 4 * g) = acc[i];
+        for (int i = 0; i < NF; ++i) *reinterpret_cast<f4_t *>(row + n0 + 16 * i + 4 * g) = acc[i];
     }
 };
 
@@ -338,20 +420,59 @@ __device__ __forceinline__ void two_terms(f4_t gate, f4_t up, u2_t &hi, u2_t &lo
 // chunks, groups).
 template <class Stream, int RG, int TERMS>
 __global__ __launch_bounds__(kThreads, 2) void product_kernel(DecodeParams p) {
-    extern __shared__ uint8_t lds[];
-    __shared__ Plan plan;
+    // (aligned: 16-byte accesses to LDS at odd words take about twice as long)
+    extern __shared__ __align__(16) uint8_t lds[];
+    __shared__ __align__(16) Plan plan;
     constexpr int R = 16 * RG, kStep = Stream::kStep, kTile = Stream::kTile;
-    if (!make_plan<R>(p, plan, blockIdx.z)) return;
-    const int e = uniform(plan.expert), first = uniform(plan.first), count = uniform(plan.count);
+    int e = 0, first = 0, count = 0;
+    if (p.T * p.k <= 64) {
+        if (!make_small_plan<R>(p, plan, blockIdx.z, e, first, count)) return;
+    } else {
+        if (!make_plan<R>(p, plan, reinterpret_cast<uint32_t *>(lds), blockIdx.z)) return;
+        e = uniform(plan.expert), first = uniform(plan.first), count = uniform(plan.count);
+    }
     const DecodePart &d = TERMS == 1 ? p.gate_up : p.down;
     const int K = TERMS == 1 ? p.H : p.I, cols = TERMS == 1 ? 2 * p.I : p.N, n = p.T * p.k;
 
-    // The chunk's operand rows.  Rows past the group's are left as they are:
-    // a row's sums depend on its own operand alone.
     const int all = (K + kStep - 1) / kStep, chunk = blockIdx.y;
     const int s0 = all * chunk / d.chunks, steps = all * (chunk + 1) / d.chunks - s0;
     const int k0 = s0 * kStep, width = steps * kStep, real = min(width, K - k0);
     const int pitch = 2 * width + 16;       // spreads the rows over the banks
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const int64_t slice = static_cast<int64_t>(K) * cols;
+    Weights a;
+    a.w = buffer((TERMS == 1 ? p.w13 : p.w2) + e * slice, slice);
+    a.sc = buffer(TERMS == 1 ? p.s13 + e * p.s13_e : p.s2 + e * p.s2_e, slice / 32);
+    a.ld = Stream::kKN ? cols : K;
+    Stream::place(a, c, g);
+    Operand x;
+    x.lane = lds + c * pitch + 2 * Stream::lane_k(g);
+    x.pitch = 16 * pitch;
+    x.term = R * pitch;
+    const int live = (count + 15) >> 4;
+
+    // This wave's tiles: every kWaves-th of the block's run.
+    const int tiles = (cols + kTile - 1) / kTile;
+    int tile = blockIdx.x * d.run * kWaves + wave;
+    const int mine = max(min(d.run, (tiles - tile + kWaves - 1) / kWaves), 0);
+    // Blocks side by side begin at different steps and go round: rows and
+    // columns a power of two apart share memory channels.
+    const int turn = (blockIdx.x + blockIdx.z) % steps;
+    const int total = mine * steps;
+    int fetch_step = turn, fetch_n0 = tile * kTile, fetched = 0;
+    typename Stream::Stage f[Stream::kDepth];
+    auto fetch = [&](typename Stream::Stage &s) {
+        Stream::fetch(s, a, fetch_n0, k0 + fetch_step * kStep);
+        if (++fetch_step == steps) fetch_step = 0;
+        if (fetch_step == turn) fetch_n0 += kWaves * kTile;
+        ++fetched;
+    };
+#pragma unroll
+    for (int i = 0; i < Stream::kDepth; ++i)
+        if (i < total) fetch(f[i]);
+    // The chunk's operand rows.  Rows past the group's are left as they are: a
+    // row's sums depend on its own operand alone.
     if (TERMS == 1) {
         for (int i = threadIdx.x; i < count * (width / 8); i += kThreads) {
             const int r = i / (width / 8), k = i % (width / 8) * 8;
@@ -379,41 +500,6 @@ __global__ __launch_bounds__(kThreads, 2) void product_kernel(DecodeParams p) {
         }
     }
     __syncthreads();
-
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int c = lane & 15, g = lane >> 4;
-    const int64_t slice = static_cast<int64_t>(K) * cols;
-    Weights a;
-    a.w = buffer((TERMS == 1 ? p.w13 : p.w2) + e * slice, slice);
-    a.sc = buffer(TERMS == 1 ? p.s13 + e * p.s13_e : p.s2 + e * p.s2_e, slice / 32);
-    a.ld = kStep == 64 ? cols : K;
-    Stream::place(a, c, g);
-    Operand x;
-    x.lane = lds + c * pitch + 2 * Stream::lane_k(g);
-    x.pitch = 16 * pitch;
-    x.term = R * pitch;
-    const int live = (count + 15) >> 4;
-
-    // This wave's tiles: every kWaves-th of the block's run.
-    const int tiles = (cols + kTile - 1) / kTile;
-    int tile = blockIdx.x * d.run * kWaves + wave;
-    const int mine = min(d.run, (tiles - tile + kWaves - 1) / kWaves);
-    if (mine <= 0) return;
-    // Blocks side by side begin at different steps and go round: rows and
-    // columns a power of two apart share memory channels.
-    const int turn = (blockIdx.x + blockIdx.z) % steps;
-    const int total = mine * steps;
-    int fetch_step = turn, fetch_n0 = tile * kTile, fetched = 0;
-    typename Stream::Stage f[Stream::kDepth];
-    auto fetch = [&](typename Stream::Stage &s) {
-        Stream::fetch(s, a, fetch_n0, k0 + fetch_step * kStep);
-        if (++fetch_step == steps) fetch_step = 0;
-        if (fetch_step == turn) fetch_n0 += kWaves * kTile;
-        ++fetched;
-    };
-#pragma unroll
-    for (int i = 0; i < Stream::kDepth; ++i)
-        if (i < total) fetch(f[i]);
     f4_t acc[RG][Stream::kAcc] = {};
     int step = turn;
     float *out = (TERMS == 1 ? p.gu : p.y) + static_cast<int64_t>(chunk) * n * cols;
@@ -421,7 +507,7 @@ __global__ __launch_bounds__(kThreads, 2) void product_kernel(DecodeParams p) {
 #pragma unroll
         for (int j = 0; j < Stream::kDepth; ++j) {
             if (i + j >= total) break;
-            Stream::template use<RG, TERMS>(f[j], x, step * kStep, live, acc);
+            Stream::template use<RG, TERMS>(f[j], x, step * kStep, K - k0 - step * kStep, live, acc);
             if (fetched < total) fetch(f[j]);
             if (++step == steps) step = 0;
             if (step == turn) {
@@ -439,22 +525,39 @@ __global__ __launch_bounds__(kThreads, 2) void product_kernel(DecodeParams p) {
         }
 }
 
-// out[t, n .. n + 3] = sum_j weight[t, j] sum_s y[s][t k + j] + shared
+// out[t, n .. n + 3] = sum over t's pairs j and y's chunks s of weight[t, j]
+// y[s][t k + j], plus the shared term.  A block takes 128 columns of a token:
+// eight slices of the (j, s) terms at a time, so that the loads of one token's
+// few columns run side by side; then the slices in order.
+constexpr int kSlices = 8, kFours = kThreads / kSlices;
 __global__ __launch_bounds__(kThreads) void combine_kernel(DecodeParams p) {
-    const int n = p.T * p.k, fours = p.N / 4;
-    const int i = blockIdx.x * kThreads + threadIdx.x;
-    if (i >= p.T * fours) return;
-    const int t = i / fours, col = i % fours * 4;
-    f4_t v = {0, 0, 0, 0};
-    for (int j = 0; j < p.k; ++j) {
-        const int q = t * p.k + j, id = p.ids[q];
-        if (id < 0 || id >= p.E) continue;
-        const float *at = p.y + static_cast<int64_t>(q) * p.N + col;
-        f4_t u = load<f4_t>(at);
-        for (int s = 1; s < p.down.chunks; ++s)
-            u += load<f4_t>(at + static_cast<int64_t>(s) * n * p.N);
-        v += p.weights[q] * u;
+    __shared__ float weight[GFR_MAX_TOPK];
+    __shared__ int live[GFR_MAX_TOPK];
+    __shared__ f4_t part[kSlices][kFours];
+    const int t = blockIdx.y, slice = threadIdx.x / kFours, four = threadIdx.x % kFours;
+    const int col = (blockIdx.x * kFours + four) * 4;
+    if (threadIdx.x < p.k) {
+        const int id = p.ids[t * p.k + threadIdx.x];
+        live[threadIdx.x] = id >= 0 && id < p.E;
+        weight[threadIdx.x] = p.weights[t * p.k + threadIdx.x];
     }
+    __syncthreads();
+    f4_t v = {0, 0, 0, 0};
+    if (col < p.N) {
+        const int chunks = p.down.chunks, terms = p.k * chunks;
+        const float *at = p.y + static_cast<int64_t>(t) * p.k * p.N + col;
+        const int64_t plane = static_cast<int64_t>(p.T) * p.k * p.N;
+#pragma unroll 4
+        for (int i = slice; i < terms; i += kSlices) {
+            const int j = i / chunks, s = i - j * chunks;
+            if (live[j]) v += weight[j] * load<f4_t>(at + s * plane + static_cast<int64_t>(j) * p.N);
+        }
+    }
+    part[slice][four] = v;
+    __syncthreads();
+    if (slice != 0 || col >= p.N) return;
+#pragma unroll
+    for (int s = 1; s < kSlices; ++s) v += part[s][four];
     const int64_t at = static_cast<int64_t>(t) * p.N + col;
     if (p.shared) {
         const u2_t h = load<u2_t>(p.shared + at);
@@ -485,12 +588,19 @@ int64_t max_groups(int64_t pairs, int64_t E, int rg) {
     return g < pairs ? g : pairs;
 }
 
+// Lines of K per [N, K] step (StreamNK's KL).
+constexpr int lines(int rg) { return rg == 1 ? 2 : 1; }
+
 // Chunks and runs of one product.  As few chunks as the LDS allows; runs as
 // long as leaves kBlocks blocks; if even runs of one tile per wave are fewer,
 // more chunks, down to two steps.
 DecodePart part_shape(double groups, int64_t K, int64_t cols, int transpose, int rg, int terms) {
-    constexpr double kBlocks = 768;
-    const int64_t step = transpose ? 128 : 64, tile = transpose ? 64 : 128;
+#ifndef KBL
+#define KBL 768
+#endif
+    constexpr double kBlocks = KBL;
+    const int64_t step = transpose ? 128 * lines(rg) : 64;
+    const int64_t tile = transpose ? 64 / lines(rg) : 128;
     const int64_t steps = (K + step - 1) / step, tiles = (cols + tile - 1) / tile;
     const int64_t wide = kOperandBytes / (2 * terms * 16 * rg) / step;   // steps per chunk, most
     int64_t chunks = (steps + wide - 1) / wide;
@@ -498,7 +608,7 @@ DecodePart part_shape(double groups, int64_t K, int64_t cols, int transpose, int
     if (run < 1) {
         run = 1;
         const double blocks = groups * ((tiles + kWaves - 1) / kWaves);
-        while (blocks * chunks < kBlocks && steps / (chunks + 1) >= 2 && chunks < 8) ++chunks;
+        while (blocks * chunks < kBlocks && steps / (chunks + 1) >= (transpose ? 1 : 2) && chunks < 8) ++chunks;
     }
     const int64_t most = (tiles + kWaves - 1) / kWaves;
     if (run > most) run = most;
@@ -514,7 +624,8 @@ hipError_t launch_product(const DecodeParams &p, hipStream_t stream) {
     const int K = TERMS == 1 ? p.H : p.I, cols = TERMS == 1 ? 2 * p.I : p.N;
     const int steps = (K + Stream::kStep - 1) / Stream::kStep;
     const int width = (steps + d.chunks - 1) / d.chunks * Stream::kStep;
-    const int lds = TERMS * 16 * RG * (2 * width + 16);
+    const int operand = TERMS * 16 * RG * (2 * width + 16);
+    const int lds = operand > kMaskBytes ? operand : kMaskBytes;
     const int tiles = (cols + Stream::kTile - 1) / Stream::kTile;
     const int runs = (tiles + d.run * kWaves - 1) / (d.run * kWaves);
     auto kernel = &product_kernel<Stream, RG, TERMS>;
@@ -531,14 +642,15 @@ hipError_t launch_product(const DecodeParams &p, hipStream_t stream) {
 
 template <int FMT, int RG>
 hipError_t launch_decode_t(const DecodeParams &p, int t13, int t2, hipStream_t stream) {
-    hipError_t e = t13 ? launch_product<StreamNK<FMT>, RG, 1>(p, stream)
+    constexpr int KL = lines(RG);
+    hipError_t e = t13 ? launch_product<StreamNK<FMT, KL>, RG, 1>(p, stream)
                        : launch_product<StreamKN<FMT>, RG, 1>(p, stream);
     if (e != hipSuccess) return e;
-    e = t2 ? launch_product<StreamNK<FMT>, RG, 2>(p, stream)
+    e = t2 ? launch_product<StreamNK<FMT, KL>, RG, 2>(p, stream)
            : launch_product<StreamKN<FMT>, RG, 2>(p, stream);
     if (e != hipSuccess) return e;
-    const int blocks = (p.T * (p.N / 4) + kThreads - 1) / kThreads;
-    hipLaunchKernelGGL(combine_kernel, dim3(blocks), dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL(combine_kernel, dim3((p.N + 4 * kFours - 1) / (4 * kFours), p.T),
+                       dim3(kThreads), 0, stream, p);
     return hipGetLastError();
 }
 
