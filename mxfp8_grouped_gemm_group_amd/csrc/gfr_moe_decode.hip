@@ -474,6 +474,7 @@ __global__ __launch_bounds__(kThreads, 2) void product_kernel(DecodeParams p) {
     // The chunk's operand rows.  Rows past the group's are left as they are: a
     // row's sums depend on its own operand alone.
     if (TERMS == 1) {
+#pragma unroll 4
         for (int i = threadIdx.x; i < count * (width / 8); i += kThreads) {
             const int r = i / (width / 8), k = i % (width / 8) * 8;
             const int64_t t = plan.pairs[first + r] / p.k;
@@ -481,17 +482,27 @@ __global__ __launch_bounds__(kThreads, 2) void product_kernel(DecodeParams p) {
                 k < real ? load<u4_t>(p.x + t * p.H + k0 + k) : u4_t{0, 0, 0, 0};
         }
     } else {
+        const int64_t plane = static_cast<int64_t>(n) * 2 * p.I;
+        const int last = p.gate_up.chunks - 1;
+#pragma unroll 2
         for (int i = threadIdx.x; i < count * (width / 4); i += kThreads) {
             const int r = i / (width / 4), k = i % (width / 4) * 4;
             u2_t hi = {0, 0}, lo = {0, 0};
             if (k < real) {
                 const float *at =
                     p.gu + static_cast<int64_t>(plan.pairs[first + r]) * 2 * p.I + k0 + k;
-                f4_t gate = load<f4_t>(at), up = load<f4_t>(at + p.I);
-                for (int s = 1; s < p.gate_up.chunks; ++s) {
-                    at += static_cast<int64_t>(n) * 2 * p.I;
-                    gate += load<f4_t>(at);
-                    up += load<f4_t>(at + p.I);
+                f4_t gate = {0, 0, 0, 0}, up = {0, 0, 0, 0};
+                // four chunks' loads at a time, past the last one its own again
+                for (int s = 0; s <= last; s += 4) {
+                    f4_t v[4], u[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[j] = load<f4_t>(at + min(s + j, last) * plane);
+                        u[j] = load<f4_t>(at + min(s + j, last) * plane + p.I);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (s + j <= last) gate += v[j], up += u[j];
                 }
                 two_terms(gate, up, hi, lo);
             }
@@ -579,7 +590,10 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(DecodeParams p) {
 // enough for the second reading of its weights to matter; one otherwise.
 int row_fragments(int64_t T, int64_t k, int64_t E) {
     const int64_t mean = T * k / E;
-    return T <= 16 || mean <= 8 ? 1 : 2;
+#ifndef MEAN
+#define MEAN 8
+#endif
+    return T <= 16 || mean <= MEAN ? 1 : 2;
 }
 
 // Groups of the plan, at most.
@@ -596,9 +610,9 @@ constexpr int lines(int rg) { return rg == 1 ? 2 : 1; }
 // more chunks, down to two steps.
 DecodePart part_shape(double groups, int64_t K, int64_t cols, int transpose, int rg, int terms) {
 #ifndef KBL
-#define KBL 768
+#define KBL 448
 #endif
-    constexpr double kBlocks = KBL;
+    const double kBlocks = rg == 1 ? 768 : KBL;
     const int64_t step = transpose ? 128 * lines(rg) : 64;
     const int64_t tile = transpose ? 64 / lines(rg) : 128;
     const int64_t steps = (K + step - 1) / step, tiles = (cols + tile - 1) / tile;
