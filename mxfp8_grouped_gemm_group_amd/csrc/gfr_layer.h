@@ -16,6 +16,7 @@ struct LinearParams {
     void *out;                 // [M, N]
     float *partial;            // split K: [S][M][rows of w]
     int32_t bias_f32, out_f32, f16, act;
+    int32_t wide;              // rows of out and residual are whole, aligned 16 bytes
     int32_t M, N, K, split;
 };
 

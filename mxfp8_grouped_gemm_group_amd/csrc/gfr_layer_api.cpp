@@ -39,7 +39,7 @@ int resolve_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *b
         GFR_TRY(check_desc(residual, {2}, {x->dtype}));
         if (!shape_is(residual, {M, N})) return GFR_ERR_BAD_SHAPE;
     }
-    if (M > kMaxRows || rows > kMaxRows || K > int64_t{1} << 22) return GFR_ERR_UNSUPPORTED;
+    if (M > kMaxRows || rows > kMaxRows || K > int64_t{1} << 21) return GFR_ERR_UNSUPPORTED;
     if (!aligned(x->data, 16) || !aligned(w->data, 16) || !aligned(out->data, 8) ||
         (present(bias) && !aligned(bias->data, 8)) ||
         (present(residual) && !aligned(residual->data, 8)))
@@ -53,6 +53,8 @@ int resolve_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *b
     p.out_f32 = out->dtype == GFR_DT_F32;
     p.f16 = x->dtype == GFR_DT_F16;
     p.act = activation;
+    p.wide = N % 8 == 0 && aligned(out->data, 16) &&
+             (!present(residual) || aligned(residual->data, 16));
     p.M = static_cast<int32_t>(M);
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);

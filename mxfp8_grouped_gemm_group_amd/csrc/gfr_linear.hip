@@ -68,6 +68,9 @@ __device__ __forceinline__ u4_t eight_tail(rsrc_t r, int lane_off, int off, int 
     return s;
 }
 
+// Lane offset past every buffer's end (K <= 2^21): loads there give zeros.
+constexpr int kNowhere = 0x7f000000;
+
 // Buffer over weight rows [first, first + rows).  Its base has to be a whole
 // word's address, which the first row's is not where first and K are odd:
 // returns the bytes from the base to the row.
@@ -91,6 +94,21 @@ __device__ __forceinline__ float activate(float v, int act) {
     }
     default: return v;
     }
+}
+
+__device__ __forceinline__ void activate8(float (&y)[8], int act) {
+    if (act == GFR_ACT_NONE) return;
+#define GFR_ALL8(A)                                           \
+    case A:                                                   \
+        _Pragma("unroll") for (int j = 0; j < 8; ++j) y[j] = activate(y[j], A); \
+        return;
+    switch (act) {
+        GFR_ALL8(GFR_ACT_RELU)
+        GFR_ALL8(GFR_ACT_SILU)
+        GFR_ALL8(GFR_ACT_GELU)
+        GFR_ALL8(GFR_ACT_GELU_TANH)
+    }
+#undef GFR_ALL8
 }
 
 __device__ __forceinline__ float element(const void *p, int64_t i, bool f32, bool f16) {
@@ -255,26 +273,49 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(LinearParams p) {
 // ---------------------------------------------------------------------------
 // Tile kernel
 // ---------------------------------------------------------------------------
+typedef float f16_t __attribute__((ext_vector_type(16)));
+
+template <bool F16>
+__device__ __forceinline__ f16_t mfma32(u4_t a, u4_t b, f16_t c) {
+    if (F16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8_t, a),
+                                                      __builtin_bit_cast(h8_t, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8_t, a),
+                                                   __builtin_bit_cast(bf8_t, b), c, 0, 0, 0);
+}
+
+// Every LDS access of this wave has finished, then the other waves' too.  (As
+// __syncthreads, but the loads from memory in flight stay in flight.)
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
 
 // BM rows of x by BN weight rows (swiglu: BN / 2 output columns, their gate and
-// up rows in turn by fragments of 16), waves of WM x WN.  In LDS a row of 64
-// elements is eight 16-byte pieces, piece j of row r at j ^ (r & 7), so that the
-// 16 lanes that read one piece of 16 rows reach all banks.
+// up rows in turn by fragments of 32), four waves of WM x WN.  In LDS a row of 64
+// elements is eight 16-byte pieces, piece j of row r at j ^ (r & 7), so that
+// eight lanes that read one piece of eight rows reach all banks.
+//
+// A step is four 16-K parts.  While one part's MFMAs run, the next part's
+// fragments come from LDS; the next step's tile, loaded to registers a step ago,
+// is written to the other stage during parts 0 and 1, and the loads of the step
+// after it are issued then.  The one barrier stands before part 3, whose
+// fragments are in registers by then: behind it the other stage is complete,
+// and nobody reads this one any more.
 template <bool F16, bool ALIGNED, bool SWIGLU, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void tile_kernel(LinearParams p,
-                                                                          int tiles_m,
-                                                                          int tiles_n) {
-    constexpr int kThreads = (BM / WM) * (BN / WN) * 64;
+__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(LinearParams p, int tiles_m,
+                                                                      int tiles_n) {
+    static_assert((BM / WM) * (BN / WN) == 4, "four waves");
+    constexpr int kThreads = 256;
     constexpr int kNX = BM * 8 / kThreads, kNW = BN * 8 / kThreads;   // pieces per thread
-    constexpr int FM = WM / 16, FN = WN / 16;
+    constexpr int FM = WM / 32, FN = WN / 32;
     extern __shared__ u4_t lds[];                  // [2][BM + BN][8]
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int c = lane & 15, g = lane >> 4;
+    const int c = lane & 31, g = lane >> 5;
     // Blocks go round the eight XCDs; each XCD takes a run of tiles, eight
     // tile rows deep, so that its L2 serves their shared operands.
     const int total = tiles_m * tiles_n, per = (total + 7) / 8;
     const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if (id >= total) return;
+    if (static_cast<int>(blockIdx.x >> 3) >= per || id >= total) return;
     const int band = id / (8 * tiles_n), in_band = id - band * 8 * tiles_n;
     const int depth = min(8, tiles_m - band * 8);
     const int m0 = (band * 8 + in_band % depth) * BM;
@@ -286,112 +327,227 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void tile_kernel(Linear
     const int rows = min(SWIGLU ? BN / 2 : BN, p.N - n0);
     weight_rows<ALIGNED>(p, n0, rows, wr);          // n0 is even: no skew
     const int skew = weight_rows<ALIGNED>(p, SWIGLU ? int64_t{n0} + p.N : n0, rows, ur);
-    int x_off[kNX], w_off[kNW], x_lds[kNX], w_lds[kNW];
-    const int piece = threadIdx.x & 7;
+    int x_off[kNX], w_off[kNW];
+    const int piece = threadIdx.x & 7, row0 = threadIdx.x >> 3;
 #pragma unroll
-    for (int i = 0; i < kNX; ++i) {
-        const int r = (threadIdx.x >> 3) + i * (kThreads / 8);
-        x_off[i] = min(r, p.M - 1 - m0) * static_cast<int>(bytes) + 16 * piece;
-        x_lds[i] = r * 8 + (piece ^ (r & 7));
-    }
+    for (int i = 0; i < kNX; ++i)
+        x_off[i] = min(row0 + 32 * i, p.M - 1 - m0) * static_cast<int>(bytes) + 16 * piece;
 #pragma unroll
     for (int i = 0; i < kNW; ++i) {
-        const int r = (threadIdx.x >> 3) + i * (kThreads / 8);
-        const int row = SWIGLU ? (r >> 5) * 16 + (r & 15) : r;
+        const int row = SWIGLU ? (i >> 1) * 32 + row0 : 32 * i + row0;   // odd i: up rows
         w_off[i] = min(row, p.N - 1 - n0) * static_cast<int>(bytes) + 16 * piece +
-                   (SWIGLU && (r & 16) ? skew : 0);
-        w_lds[i] = (BM + r) * 8 + (piece ^ (r & 7));
+                   (SWIGLU && (i & 1) ? skew : 0);
     }
+    // rows 32 apart share their swizzle
+    u4_t *const put_at = lds + row0 * 8 + (piece ^ (row0 & 7));
     u4_t xs[kNX], ws[kNW];
     const int steps = (p.K + 63) / 64;
     auto fetch = [&](int step) {
-        const int off = step * 128;
-        if (step * 64 + 64 <= p.K) {
+        const int off = step * 128, valid = p.K - step * 64 - 8 * piece;
+        if (ALIGNED) {
+            // pieces behind K: zeros, from behind the buffer's end
+            const bool in = valid > 0;
 #pragma unroll
-            for (int i = 0; i < kNX; ++i) xs[i] = eight<ALIGNED, 0>(xr, x_off[i], off);
+            for (int i = 0; i < kNX; ++i) xs[i] = load16<0>(xr, in ? x_off[i] : kNowhere, off);
 #pragma unroll
-            for (int i = 0; i < kNW; ++i) {
-                if (!SWIGLU) {
-                    ws[i] = eight<ALIGNED, 0>(wr, w_off[i], off);
-                } else {
-                    // 64 lanes hold eight rows: all gate or all up
-                    const int r = uniform((threadIdx.x >> 3) + i * (kThreads / 8));
-                    ws[i] = r & 16 ? eight<ALIGNED, 0>(ur, w_off[i], off)
-                                   : eight<ALIGNED, 0>(wr, w_off[i], off);
-                }
-            }
+            for (int i = 0; i < kNW; ++i)
+                ws[i] = load16<0>(SWIGLU && (i & 1) ? ur : wr, in ? w_off[i] : kNowhere, off);
+        } else if (step * 64 + 64 <= p.K) {
+#pragma unroll
+            for (int i = 0; i < kNX; ++i) xs[i] = eight<false, 0>(xr, x_off[i], off);
+#pragma unroll
+            for (int i = 0; i < kNW; ++i)
+                ws[i] = eight<false, 0>(SWIGLU && (i & 1) ? ur : wr, w_off[i], off);
         } else {
-            const int valid = p.K - step * 64 - 8 * piece;
 #pragma unroll
-            for (int i = 0; i < kNX; ++i) xs[i] = eight_tail<ALIGNED>(xr, x_off[i], off, valid);
+            for (int i = 0; i < kNX; ++i) xs[i] = eight_tail<false>(xr, x_off[i], off, valid);
 #pragma unroll
-            for (int i = 0; i < kNW; ++i) {
-                const int r = uniform((threadIdx.x >> 3) + i * (kThreads / 8));
-                ws[i] = SWIGLU && (r & 16) ? eight_tail<ALIGNED>(ur, w_off[i], off, valid)
-                                           : eight_tail<ALIGNED>(wr, w_off[i], off, valid);
-            }
+            for (int i = 0; i < kNW; ++i)
+                ws[i] = eight_tail<false>(SWIGLU && (i & 1) ? ur : wr, w_off[i], off, valid);
         }
-    };
-    auto put = [&](int stage) {
-        u4_t *s = lds + stage * (BM + BN) * 8;
-#pragma unroll
-        for (int i = 0; i < kNX; ++i) s[x_lds[i]] = xs[i];
-#pragma unroll
-        for (int i = 0; i < kNW; ++i) s[w_lds[i]] = ws[i];
     };
     const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
-    f4_t acc[FM][FN] = {};
+    const u4_t *const x_at = lds + (wm + c) * 8, *const w_at = lds + (BM + wn + c) * 8;
+    constexpr int kStage = (BM + BN) * 8;
+    u4_t a[2][FM], b[2][FN];
+    auto get = [&](int to, int stage, int part) {
+        const int at = stage * kStage + ((2 * part + g) ^ (c & 7));
+#pragma unroll
+        for (int i = 0; i < FM; ++i) a[to][i] = x_at[at + 32 * 8 * i];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) b[to][j] = w_at[at + 32 * 8 * j];
+    };
+    f16_t acc[FM][FN] = {};
+    auto multiply = [&](int from) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                acc[i][j] = mfma32<F16>(b[from][j], a[from][i], acc[i][j]);
+    };
+    auto put_x = [&](int stage) {
+#pragma unroll
+        for (int i = 0; i < kNX; ++i) put_at[stage * kStage + 32 * 8 * i] = xs[i];
+    };
+    auto put_w = [&](int stage) {
+#pragma unroll
+        for (int i = 0; i < kNW; ++i) put_at[stage * kStage + (BM + 32 * i) * 8] = ws[i];
+    };
     fetch(0);
-    put(0);
-    __syncthreads();
-    for (int step = 0; step < steps; ++step) {
-        const bool more = step + 1 < steps;
-        if (more) fetch(step + 1);
-        const u4_t *s = lds + (step & 1) * (BM + BN) * 8;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            u4_t a[FM], b[FN];
-#pragma unroll
-            for (int f = 0; f < FM; ++f)
-                a[f] = s[(wm + 16 * f + c) * 8 + ((4 * k + g) ^ (c & 7))];
-#pragma unroll
-            for (int f = 0; f < FN; ++f)
-                b[f] = s[(BM + wn + 16 * f + c) * 8 + ((4 * k + g) ^ (c & 7))];
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j) acc[i][j] = mfma<F16>(b[j], a[i], acc[i][j]);
-        }
-        if (more) put((step + 1) & 1);
-        __syncthreads();
+    put_x(0);
+    put_w(0);
+    if (steps > 1) fetch(1);
+    lds_barrier();
+    get(0, 0, 0);
+    for (int step = 0; step + 1 < steps; ++step) {
+        const int cur = step & 1;
+        get(1, cur, 1);
+        put_x(cur ^ 1);
+        multiply(0);
+        get(0, cur, 2);
+        put_w(cur ^ 1);
+        multiply(1);
+        get(1, cur, 3);
+        if (step + 2 < steps) fetch(step + 2);
+        multiply(0);
+        lds_barrier();
+        get(0, cur ^ 1, 0);
+        multiply(1);
     }
-    // Lane (c, g) holds row 16 i + c, columns 16 j + 4 g .. + 3.  Sixteen rows at
-    // a time go through LDS (the wave's own part of the stages, which every wave
-    // is done with), so that the epilogue reads and writes whole runs of columns.
+    const int cur = (steps - 1) & 1;
+    get(1, cur, 1);
+    multiply(0);
+    get(0, cur, 2);
+    multiply(1);
+    get(1, cur, 3);
+    multiply(0);
+    multiply(1);
+    // Lane (c, g) holds row 32 i + c, columns 32 j + 8 r + 4 g .. + 3, r < 4.  32 rows
+    // at a time go through LDS (the wave's own part of the stages), so that the
+    // epilogue reads and writes whole runs of columns.
     constexpr int kPitch = WN + 4;     // spreads the rows over the banks
     constexpr int kCols = SWIGLU ? WN / 2 : WN;
-    float *slab = reinterpret_cast<float *>(lds) + wave * 16 * kPitch;
+    constexpr int kSlab = 32 * kPitch + 16 * kCols;    // floats: sums, then residual rows
+    static_assert(4 * kSlab * 4 <= 2 * kStage * 16, "the waves' rows fit the stages");
+    float *slab = reinterpret_cast<float *>(lds) + wave * kSlab;
+    u4_t *res_at = reinterpret_cast<u4_t *>(slab + 32 * kPitch);
     const int col0 = n0 + (SWIGLU ? wn / 2 : wn);
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        const int row0 = m0 + wm + 16 * i;
-        if (row0 >= p.M) break;
+    auto put_sums = [&](int i) {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-            *reinterpret_cast<f4_t *>(&slab[c * kPitch + 16 * j + 4 * g]) = acc[i][j];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *reinterpret_cast<f4_t *>(&slab[c * kPitch + 32 * j + 8 * r + 4 * g]) =
+                    f4_t{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2],
+                         acc[i][j][4 * r + 3]};
+    };
+    auto wave_sync = [] {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-        for (int o = lane; o < 16 * (kCols / 4); o += 64) {
-            const int r = o / (kCols / 4), col = o % (kCols / 4) * 4;
-            if (row0 + r >= p.M || col0 + col >= p.N) continue;
-            const float *at = slab + r * kPitch + (SWIGLU ? (col >> 4) * 32 + (col & 15) : col);
-            const f4_t v = *reinterpret_cast<const f4_t *>(at + (SWIGLU ? 16 : 0));
-            const f4_t gate = *reinterpret_cast<const f4_t *>(at);
-            finish<SWIGLU, F16>(p, row0 + r, col0 + col, v, gate);
+    };
+    lds_barrier();
+    if (p.wide) {
+        // Eight columns per lane, the same ones in every row it takes: their
+        // bias is loaded once, and the next 32 rows' residual while these are
+        // finished.  (With both loaded where they are used a 4096 x 7168 x 4096
+        // product took 130 us longer: one wave per SIMD hides no latency.)
+        constexpr int kLanes = kCols / 8, kRows = 64 / kLanes, kTurns = 32 / kRows;
+        const int er = lane / kLanes, n = col0 + lane % kLanes * 8;
+        const bool in = n < p.N;
+        float bias[8] = {}, gate_bias[8] = {};
+        if (p.bias && in)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                bias[j] = element(p.bias, n + j + (SWIGLU ? p.N : 0), p.bias_f32, F16);
+                if (SWIGLU) gate_bias[j] = element(p.bias, n + j, p.bias_f32, F16);
+            }
+        u4_t res[kTurns];
+        auto fetch_res = [&](int i) {
+            const int first = m0 + wm + 32 * i + er;
+#pragma unroll
+            for (int k = 0; k < kTurns; ++k) {
+                const int64_t m = min(first + k * kRows, p.M - 1);
+                if (in) res[k] = load<u4_t>(p.residual + m * p.N + n);
+            }
+        };
+        if (p.residual) fetch_res(0);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int first = m0 + wm + 32 * i;
+            if (first >= p.M) break;
+            put_sums(i);
+            if (p.residual) {
+#pragma unroll
+                for (int k = 0; k < kTurns; ++k) res_at[k * 64 + lane] = res[k];
+                if (i + 1 < FM) fetch_res(i + 1);
+            }
+            wave_sync();
+#pragma unroll 2
+            for (int k = 0; k < kTurns; ++k) {
+                const int r = k * kRows + er, m = first + r;
+                if (m >= p.M || !in) continue;
+                const float *at = slab + r * kPitch;
+                const int col = lane % kLanes * 8;
+                const float *up = at + (SWIGLU ? (col >> 5) * 64 + 32 + (col & 31) : col);
+                const float *gate = at + (col >> 5) * 64 + (col & 31);
+                float y[8];
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    const f4_t v = load<f4_t>(up + j);
+                    if (SWIGLU) {
+                        const f4_t gt = load<f4_t>(gate + j);
+#pragma unroll
+                        for (int l = 0; l < 4; ++l)
+                            y[j + l] = silu(gt[l] + gate_bias[j + l]) * (v[l] + bias[j + l]);
+                    } else {
+#pragma unroll
+                        for (int l = 0; l < 4; ++l) y[j + l] = v[l] + bias[j + l];
+                    }
+                }
+                if (!SWIGLU) activate8(y, p.act);
+                if (p.residual) {
+                    const u4_t h = res_at[k * 64 + lane];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint16_t b = h[j >> 1] >> (16 * (j & 1));
+                        y[j] += F16 ? static_cast<float>(__builtin_bit_cast(_Float16, b))
+                                    : bf16_f32(b);
+                    }
+                }
+                const int64_t o = static_cast<int64_t>(m) * p.N + n;
+                if (p.out_f32) {
+                    float *out = static_cast<float *>(p.out) + o;
+                    *reinterpret_cast<f4_t *>(out) = f4_t{y[0], y[1], y[2], y[3]};
+                    *reinterpret_cast<f4_t *>(out + 4) = f4_t{y[4], y[5], y[6], y[7]};
+                } else {
+                    u4_t h;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        h[j] = F16 ? pack_f16(y[2 * j], y[2 * j + 1])
+                                   : pack_bf16(y[2 * j], y[2 * j + 1]);
+                    *reinterpret_cast<u4_t *>(static_cast<uint16_t *>(p.out) + o) = h;
+                }
+            }
+            wave_sync();
         }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int first = m0 + wm + 32 * i;
+        if (first >= p.M) break;
+        put_sums(i);
+        wave_sync();
+#pragma unroll 1
+        for (int o = lane; o < 32 * (kCols / 4); o += 64) {
+            const int r = o / (kCols / 4), col = o % (kCols / 4) * 4;
+            if (first + r >= p.M || col0 + col >= p.N) continue;
+            const float *at = slab + r * kPitch + (SWIGLU ? (col >> 5) * 64 + (col & 31) : col);
+            const f4_t v = *reinterpret_cast<const f4_t *>(at + (SWIGLU ? 32 : 0));
+            const f4_t gate = *reinterpret_cast<const f4_t *>(at);
+            finish<SWIGLU, F16>(p, first + r, col0 + col, v, gate);
+        }
+        wave_sync();
     }
 }
 
@@ -417,7 +573,7 @@ hipError_t launch_tiles(const LinearParams &p, hipStream_t stream) {
     const int tm = (p.M + BM - 1) / BM, tn = (p.N + cols - 1) / cols;
     const int64_t grid = (static_cast<int64_t>(tm) * tn + 7) / 8 * 8;
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)),
-                       dim3((BM / WM) * (BN / WN) * 64), lds, stream, p, tm, tn);
+                       dim3(256), lds, stream, p, tm, tn);
     return hipGetLastError();
 }
 
@@ -429,10 +585,10 @@ hipError_t launch_linear_t(const LinearParams &p, hipStream_t stream) {
     const int64_t cols = SWIGLU ? 128 : 256;
     const int64_t big = ((p.M + 255) / 256) * ((p.N + cols - 1) / cols);
     if (ALIGNED && big >= 192)
-        return launch_tiles<F16, ALIGNED, SWIGLU, 256, 256, 128, 64>(p, stream);
+        return launch_tiles<F16, ALIGNED, SWIGLU, 256, 256, 128, 128>(p, stream);
     const int64_t mid = ((p.M + 127) / 128) * ((p.N + cols / 2 - 1) / (cols / 2));
     if (mid >= 128) return launch_tiles<F16, ALIGNED, SWIGLU, 128, 128, 64, 64>(p, stream);
-    return launch_tiles<F16, ALIGNED, SWIGLU, 64, 64, 32, 32>(p, stream);
+    return launch_tiles<F16, ALIGNED, SWIGLU, 64, SWIGLU ? 128 : 64, 32, SWIGLU ? 64 : 32>(p, stream);
 }
 
 template <bool F16, bool ALIGNED>

@@ -66,7 +66,7 @@ def test_linear_empty_is_a_no_op():
     (dict(bias=desc(F16, 32)), BAD_DTYPE),
     (dict(residual=desc(F32, 0, 32)), BAD_DTYPE),
     (dict(residual=desc(BF16, 0, 16)), BAD_SHAPE),
-    (dict(x=desc(BF16, 0, (1 << 22) + 8), w=desc(BF16, 32, (1 << 22) + 8)), UNSUPPORTED),
+    (dict(x=desc(BF16, 0, (1 << 21) + 8), w=desc(BF16, 32, (1 << 21) + 8)), UNSUPPORTED),
     (dict(x=desc(BF16, 1 << 31, 64), out=desc(BF16, 1 << 31, 32)), UNSUPPORTED),
     (dict(x=desc(BF16, 4, 64, data=FAKE + 8), out=desc(BF16, 4, 32)), BAD_ALIGN),
     (dict(x=desc(BF16, 4, 64), out=desc(BF16, 4, 32, data=FAKE + 4)), BAD_ALIGN),
