@@ -290,17 +290,36 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+// Spreads a part's LDS reads, LDS writes and memory loads over its MFMAs (as the
+// compiler would leave them, they come in runs that the MFMAs wait for).
+template <int MFMAS, int READS, int WRITES, int LOADS>
+__device__ __forceinline__ void spread() {
+#ifndef NOSPREAD
+    constexpr int kTurns = MFMAS > 1 ? MFMAS / 2 : 1;
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        // reads in the first half: their latency runs under the second
+        constexpr int kR = (READS * 2 + kTurns - 1) / kTurns;
+        constexpr int kW = (WRITES + kTurns - 1) / kTurns, kL = (LOADS + kTurns - 1) / kTurns;
+        if (READS && i * kR < READS) __builtin_amdgcn_sched_group_barrier(0x100, kR, 0);
+        if (WRITES && i * kW < WRITES) __builtin_amdgcn_sched_group_barrier(0x200, kW, 0);
+        if (LOADS && i * kL < LOADS) __builtin_amdgcn_sched_group_barrier(0x20, kL, 0);
+        __builtin_amdgcn_sched_group_barrier(0x8, MFMAS / kTurns, 0);
+    }
+#endif
+}
+
 // BM rows of x by BN weight rows (swiglu: BN / 2 output columns, their gate and
 // up rows in turn by fragments of 32), four waves of WM x WN.  In LDS a row of 64
 // elements is eight 16-byte pieces, piece j of row r at j ^ (r & 7), so that
 // eight lanes that read one piece of eight rows reach all banks.
 //
 // A step is four 16-K parts.  While one part's MFMAs run, the next part's
-// fragments come from LDS; the next step's tile, loaded to registers a step ago,
-// is written to the other stage during parts 0 and 1, and the loads of the step
-// after it are issued then.  The one barrier stands before part 3, whose
-// fragments are in registers by then: behind it the other stage is complete,
-// and nobody reads this one any more.
+// fragments come from LDS.  The next step's tile, loaded to registers three parts
+// earlier, is written to the other stage during parts 1 (x) and 2 (w), and each
+// half's loads of the step after it follow at once.  The one barrier stands
+// before part 3, whose fragments are in registers by then: behind it the other
+// stage is complete, and nobody reads this one any more.
 template <bool F16, bool ALIGNED, bool SWIGLU, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(LinearParams p, int tiles_m,
                                                                       int tiles_n) {
@@ -342,29 +361,24 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(LinearPara
     u4_t *const put_at = lds + row0 * 8 + (piece ^ (row0 & 7));
     u4_t xs[kNX], ws[kNW];
     const int steps = (p.K + 63) / 64;
-    auto fetch = [&](int step) {
+    // x's or w's pieces of a step (behind the last step: zeros)
+    auto fetch = [&](auto &to, const auto &offs, auto which, int step) {
+        constexpr int n = sizeof(to) / sizeof(to[0]);
         const int off = step * 128, valid = p.K - step * 64 - 8 * piece;
-        if (ALIGNED) {
-            // pieces behind K: zeros, from behind the buffer's end
-            const bool in = valid > 0;
 #pragma unroll
-            for (int i = 0; i < kNX; ++i) xs[i] = load16<0>(xr, in ? x_off[i] : kNowhere, off);
-#pragma unroll
-            for (int i = 0; i < kNW; ++i)
-                ws[i] = load16<0>(SWIGLU && (i & 1) ? ur : wr, in ? w_off[i] : kNowhere, off);
-        } else if (step * 64 + 64 <= p.K) {
-#pragma unroll
-            for (int i = 0; i < kNX; ++i) xs[i] = eight<false, 0>(xr, x_off[i], off);
-#pragma unroll
-            for (int i = 0; i < kNW; ++i)
-                ws[i] = eight<false, 0>(SWIGLU && (i & 1) ? ur : wr, w_off[i], off);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kNX; ++i) xs[i] = eight_tail<false>(xr, x_off[i], off, valid);
-#pragma unroll
-            for (int i = 0; i < kNW; ++i)
-                ws[i] = eight_tail<false>(SWIGLU && (i & 1) ? ur : wr, w_off[i], off, valid);
+        for (int i = 0; i < n; ++i) {
+            const rsrc_t r = which(i);
+            if (ALIGNED)
+                // pieces behind K: zeros, from behind the buffer's end
+                to[i] = load16<0>(r, valid > 0 ? offs[i] : kNowhere, off);
+            else
+                to[i] = step * 64 + 64 <= p.K ? eight<false, 0>(r, offs[i], off)
+                                              : eight_tail<false>(r, offs[i], off, valid);
         }
+    };
+    auto fetch_x = [&](int step) { fetch(xs, x_off, [&](int) { return xr; }, step); };
+    auto fetch_w = [&](int step) {
+        fetch(ws, w_off, [&](int i) { return SWIGLU && (i & 1) ? ur : wr; }, step);
     };
     const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
     const u4_t *const x_at = lds + (wm + c) * 8, *const w_at = lds + (BM + wn + c) * 8;
@@ -393,26 +407,33 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(LinearPara
 #pragma unroll
         for (int i = 0; i < kNW; ++i) put_at[stage * kStage + (BM + 32 * i) * 8] = ws[i];
     };
-    fetch(0);
+    fetch_x(0);
+    fetch_w(0);
     put_x(0);
     put_w(0);
-    if (steps > 1) fetch(1);
+    fetch_x(1);
+    fetch_w(1);
     lds_barrier();
     get(0, 0, 0);
     for (int step = 0; step + 1 < steps; ++step) {
         const int cur = step & 1;
         get(1, cur, 1);
-        put_x(cur ^ 1);
         multiply(0);
+        spread<FM * FN, FM + FN, 0, 0>();
         get(0, cur, 2);
-        put_w(cur ^ 1);
+        put_x(cur ^ 1);
         multiply(1);
+        spread<FM * FN, FM + FN, kNX, 0>();
         get(1, cur, 3);
-        if (step + 2 < steps) fetch(step + 2);
+        fetch_x(step + 2);
+        put_w(cur ^ 1);
         multiply(0);
+        spread<FM * FN, FM + FN, kNW, kNX>();
         lds_barrier();
         get(0, cur ^ 1, 0);
+        fetch_w(step + 2);
         multiply(1);
+        spread<FM * FN, FM + FN, 0, kNW>();
     }
     const int cur = (steps - 1) & 1;
     get(1, cur, 1);
