@@ -7,21 +7,22 @@ checked by the library, which raises GfrError here.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import _binding as b
-from ._binding import GfrError, GfrOptions, _need, _on_device, _ref, tensor_desc
+from ._binding import DTYPES, GfrError, _need
 
-_T, _O, _P = ctypes.POINTER(b.GfrTensor), ctypes.POINTER(GfrOptions), ctypes.c_void_p
+_P = ctypes.c_void_p
 _SIZE = ctypes.POINTER(ctypes.c_size_t)
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5}
 SCORINGS = {"softmax": 0, "sigmoid": 1}
 DECODE_MAX_TOKENS = 64   # GFR_DECODE_MAX_TOKENS
+WORKSPACE_TOO_SMALL = 6  # GFR_ERR_WORKSPACE_TOO_SMALL
 
 _ready = False
 
@@ -30,19 +31,18 @@ def _lib():
     global _ready
     lib = b.load_library()
     if not _ready:
-        lib.gfr_linear.argtypes = [_T] * 4 + [ctypes.c_int, _T, _P, _O]
-        lib.gfr_linear_workspace_size.argtypes = [_T] * 4 + [ctypes.c_int, _T, _SIZE]
-        lib.gfr_moe_decode.argtypes = [_T] * 8 + [ctypes.c_float, _T, ctypes.c_int, ctypes.c_int,
-                                                  _P, _O]
-        lib.gfr_moe_decode_workspace_size.argtypes = [ctypes.c_int64] * 6 + \
-            [ctypes.c_int] * 2 + [_SIZE]
-        lib.gfr_moe_route.argtypes = [_T, _T] + [ctypes.c_int] * 4 + [ctypes.c_float] + \
-            [_T] * 8 + [_P, _O]
+        i = ctypes.c_int
+        # descriptors and options are passed by address (_pack)
+        lib.gfr_linear.argtypes = [_P] * 4 + [i] + [_P] * 3
+        lib.gfr_linear_workspace_size.argtypes = [_P] * 4 + [i, _P, _SIZE]
+        lib.gfr_moe_decode.argtypes = [_P] * 8 + [ctypes.c_float, _P, i, i] + [_P] * 2
+        lib.gfr_moe_decode_workspace_size.argtypes = [ctypes.c_int64] * 6 + [i, i, _SIZE]
+        lib.gfr_moe_route.argtypes = [_P] * 2 + [i] * 4 + [ctypes.c_float] + [_P] * 10
         lib.gfr_moe_route_workspace_size.argtypes = [ctypes.c_int64] * 3 + [_SIZE]
         for f in (lib.gfr_linear, lib.gfr_linear_workspace_size, lib.gfr_moe_decode,
                   lib.gfr_moe_decode_workspace_size, lib.gfr_moe_route,
                   lib.gfr_moe_route_workspace_size):
-            f.restype = ctypes.c_int
+            f.restype = i
         _ready = True
     return lib
 
@@ -52,32 +52,85 @@ def _check(rc: int):
         raise GfrError(rc, b.status_string(rc))
 
 
-@contextlib.contextmanager
-def _on_stream(dev, stream: Optional[int]):
+_PAD = ((), (0, 0, 0), (0, 0), (0,), ())     # of a shape of 1 .. 4 extents
+
+
+@functools.lru_cache(maxsize=None)
+def _words(n: int):
+    return ctypes.c_int64 * n
+
+
+def _pack(dev, tensors, workspace=None, status=None):
+    """The tensors' gfr_tensor descriptors and a gfr_options behind them in one
+    array of 64-bit words, and their addresses (None for an absent tensor).  One
+    array costs a fifth of a ctypes structure per tensor, and the smallest calls
+    take little longer on the GPU than that.  The array has to outlive the call.
+    """
+    v, at = [], []
+    for t in tensors:
+        if t is None:
+            at.append(None)
+            continue
+        # what the descriptors cannot carry
+        if t.device != dev or not t.is_cuda:
+            raise ValueError("all tensors must be on one CUDA device")
+        if not t.is_contiguous():
+            raise ValueError("all tensors must be contiguous")
+        s = t.shape
+        n = len(s)
+        _need(1 <= n <= 4, f"rank {n} is outside 1..4")
+        code = DTYPES.get(t.dtype)
+        _need(code is not None, f"dtype {t.dtype} has no gfr_dtype")
+        at.append(8 * len(v))
+        v += (t.data_ptr(), code | n << 32, *s, *_PAD[n])
+    end = 8 * len(v)
+    for t in (workspace, status):
+        if t is not None and (t.device != dev or not t.is_contiguous()):
+            raise ValueError("workspace and status must be contiguous and on the tensors' device")
+    v += (0, 0, 0, 0, 0)
+    if workspace is not None:
+        v[-4], v[-3] = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if status is not None:
+        _need(status.dtype == torch.int32 and status.numel() >= 1, "status must be int32")
+        v[-2] = status.data_ptr()
+    words = _words(len(v))(*v)
+    base = ctypes.addressof(words)
+    return words, [None if a is None else base + a for a in at], base + end
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+class _OnStream:
     """The call's device and stream made current, so that what is allocated
     within belongs to the stream that uses it; gives the stream's handle."""
-    if stream is None:
-        with torch.cuda.device(dev):
-            yield torch.cuda.current_stream(dev).cuda_stream
-    else:
-        s = torch.cuda.ExternalStream(stream, device=dev) if stream else \
-            torch.cuda.default_stream(dev)
-        with torch.cuda.stream(s):
-            yield stream
+
+    def __init__(self, dev, stream: Optional[int]):
+        self.dev, self.stream, self.inner = dev, stream, None
+
+    def __enter__(self):
+        if self.stream is None:
+            index = self.dev.index
+            if index is None or index != torch.cuda.current_device():
+                self.inner = torch.cuda.device(self.dev)
+                self.inner.__enter__()
+                index = torch.cuda.current_device()
+            return _raw_stream(index)
+        s = torch.cuda.ExternalStream(self.stream, device=self.dev) if self.stream else \
+            torch.cuda.default_stream(self.dev)
+        self.inner = torch.cuda.stream(s)
+        self.inner.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.inner is not None:
+            self.inner.__exit__(*exc)
 
 
-def _workspace(given, need: int, dev):
-    """The caller's workspace, or a new one of `need` bytes (None for none)."""
-    if given is not None or need == 0:
-        return given
-    return torch.empty(need, dtype=torch.uint8, device=dev)
-
-
-def _options(workspace, status=None):
-    if workspace is None:
-        return GfrOptions(0, None, 0, None if status is None else status.data_ptr(), 0, 0)
-    return GfrOptions(0, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                      None if status is None else status.data_ptr(), 0, 0)
+def _cuda(t, name: str):
+    _need(t.is_cuda, f"{name} must be on a CUDA device")
+    return t.device
 
 
 def linear(x, w, bias=None, *, activation="none", residual=None, out_dtype=None, out=None,
@@ -91,27 +144,28 @@ def linear(x, w, bias=None, *, activation="none", residual=None, out_dtype=None,
     in x's dtype (may be out); out_dtype x's (default) or float32.
     """
     lib = _lib()
-    dev = x.device
-    _need(activation in ACTIVATIONS, f"activation must be one of {sorted(ACTIVATIONS)}")
+    act = ACTIVATIONS.get(activation)
+    _need(act is not None, f"activation must be one of {sorted(ACTIVATIONS)}")
+    dev = _cuda(x, "x")
     _need(x.dim() == 2 and w.dim() == 2, "x must be [M, K] and w [N, K]")
-    _on_device([x, w, bias, residual, out, workspace], dev)
-    if out is not None:
-        _need(out_dtype is None or out.dtype == out_dtype, "out must have out_dtype")
-    act = ACTIVATIONS[activation]
-    with _on_stream(dev, stream) as handle:
+    _need(out is None or out_dtype is None or out.dtype == out_dtype, "out must have out_dtype")
+    with _OnStream(dev, stream) as handle:
         if out is None:
             n = w.shape[0] // 2 if act == 5 else w.shape[0]
             out = torch.empty((x.shape[0], n), dtype=out_dtype or x.dtype, device=dev)
-        d = [tensor_desc(t) for t in (x, w, bias, residual)]
-        do = tensor_desc(out)
-        need = ctypes.c_size_t(0)
-        _check(lib.gfr_linear_workspace_size(*map(_ref, d), act, _ref(do), ctypes.byref(need)))
-        workspace = _workspace(workspace, need.value, dev)
-        _check(lib.gfr_linear(*map(_ref, d), act, _ref(do), handle,
-                              ctypes.byref(_options(workspace))))
+        words, (px, pw, pb, pr, po), opts = _pack(dev, (x, w, bias, residual, out), workspace)
+        rc = lib.gfr_linear(px, pw, pb, pr, act, po, handle, opts)
+        if rc == WORKSPACE_TOO_SMALL and workspace is None:
+            need = ctypes.c_size_t(0)
+            _check(lib.gfr_linear_workspace_size(px, pw, pb, pr, act, po, ctypes.byref(need)))
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+            words, (px, pw, pb, pr, po), opts = _pack(dev, (x, w, bias, residual, out), workspace)
+            rc = lib.gfr_linear(px, pw, pb, pr, act, po, handle, opts)
+        _check(rc)
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def moe_decode_workspace_size(T: int, k: int, E: int, H: int, I: int, N: int,
                               transpose_w13: bool = False, transpose_w2: bool = False) -> int:
     """Workspace bytes of a moe_decode call of these sizes."""
@@ -139,26 +193,24 @@ def moe_decode(x, w13, scale13, w2, scale2, topk_ids, topk_weights, *, transpose
     none is given; calls that overlap in time need one each.
     """
     lib = _lib()
-    dev = x.device
+    dev = _cuda(x, "x")
     _need(x.dim() == 2 and w2.dim() == 3 and topk_ids.dim() == 2,
           "x must be [T, H], w2 3-D and topk_ids [T, k]")
-    _on_device([x, w13, scale13, w2, scale2, topk_ids, topk_weights, shared_input, out,
-                workspace, status], dev)
     T, k = topk_ids.shape
     E, I, N = w2.shape
     if transpose_w2:
         I, N = N, I
-    with _on_stream(dev, stream) as handle:
+    t13, t2 = int(bool(transpose_w13)), int(bool(transpose_w2))
+    with _OnStream(dev, stream) as handle:
         if out is None:
             out = torch.empty((x.shape[0], N), dtype=out_dtype, device=dev)
         if workspace is None:
-            workspace = _workspace(None, moe_decode_workspace_size(
-                T, k, E, x.shape[1], I, N, transpose_w13, transpose_w2), dev)
-        d = [tensor_desc(t) for t in (x, w13, scale13, w2, scale2, topk_ids, topk_weights,
-                                      shared_input, out)]
-        _check(lib.gfr_moe_decode(*map(_ref, d[:8]), float(shared_input_weight), _ref(d[8]),
-                                  int(bool(transpose_w13)), int(bool(transpose_w2)), handle,
-                                  ctypes.byref(_options(workspace, status))))
+            need = moe_decode_workspace_size(T, k, E, x.shape[1], I, N, t13, t2)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        words, at, opts = _pack(dev, (x, w13, scale13, w2, scale2, topk_ids, topk_weights,
+                                      shared_input, out), workspace, status)
+        _check(lib.gfr_moe_decode(*at[:8], float(shared_input_weight), at[8], t13, t2, handle,
+                                  opts))
     return out
 
 
@@ -192,31 +244,36 @@ def moe_route(logits, top_k, *, x=None, bias=None, scoring="softmax", n_group=1,
     gmm_finalize_routing).
     """
     lib = _lib()
-    dev = logits.device
-    _need(scoring in SCORINGS, f"scoring must be one of {sorted(SCORINGS)}")
+    score = SCORINGS.get(scoring)
+    _need(score is not None, f"scoring must be one of {sorted(SCORINGS)}")
     _need(logits.dim() == 2, "logits must be [T, E]")
     _need(x is None or x.dim() == 2, "x must be [T, H]")
-    _on_device([logits, bias, x, workspace], dev)
     T, E = logits.shape
     k = int(top_k)
     _need(k >= 1, "top_k must be positive")
-    with _on_stream(dev, stream) as handle:
-        r = RouteResult(torch.empty((T, k), dtype=torch.int32, device=dev),
-                        torch.empty((T, k), dtype=torch.float32, device=dev))
+    dev = _cuda(logits, "logits")
+    empty = functools.partial(torch.empty, device=dev)
+    with _OnStream(dev, stream) as handle:
+        ids, weights = empty((T, k), dtype=torch.int32), empty((T, k), dtype=torch.float32)
+        rows = (None,) * 5
         if x is not None:
             H, n = x.shape[1], T * k
-            r = RouteResult(
-                r.topk_ids, r.topk_weights,
-                torch.empty((n, H), dtype=out_dtype, device=dev),
-                torch.empty((n, (H + 63) // 64, 2), dtype=torch.uint8, device=dev),
-                torch.empty(E, dtype=torch.int64, device=dev),
-                torch.empty(n, dtype=torch.int32, device=dev),
-                torch.empty(n, dtype=torch.float32, device=dev))
-            need = ctypes.c_size_t(0)
-            _check(lib.gfr_moe_route_workspace_size(T, E, k, ctypes.byref(need)))
-            workspace = _workspace(workspace, need.value, dev)
-        d = [tensor_desc(t) for t in (logits, bias, r.topk_ids, r.topk_weights, x, *r[2:])]
-        _check(lib.gfr_moe_route(_ref(d[0]), _ref(d[1]), SCORINGS[scoring], int(n_group),
-                                 int(topk_group), int(bool(renormalize)), float(scaling),
-                                 *map(_ref, d[2:]), handle, ctypes.byref(_options(workspace))))
-    return r
+            rows = (empty((n, H), dtype=out_dtype),
+                    empty((n, (H + 63) // 64, 2), dtype=torch.uint8),
+                    empty(E, dtype=torch.int64), empty(n, dtype=torch.int32),
+                    empty(n, dtype=torch.float32))
+            if workspace is None:
+                need = _route_workspace_size(T, E, k)
+                if need:
+                    workspace = empty(need, dtype=torch.uint8)
+        words, at, opts = _pack(dev, (logits, bias, ids, weights, x, *rows), workspace)
+        _check(lib.gfr_moe_route(at[0], at[1], score, int(n_group), int(topk_group),
+                                 int(bool(renormalize)), float(scaling), *at[2:], handle, opts))
+    return RouteResult(ids, weights, *rows)
+
+
+@functools.lru_cache(maxsize=4096)
+def _route_workspace_size(T: int, E: int, k: int) -> int:
+    need = ctypes.c_size_t(0)
+    _check(_lib().gfr_moe_route_workspace_size(T, E, k, ctypes.byref(need)))
+    return need.value

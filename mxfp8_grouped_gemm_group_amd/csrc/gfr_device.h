@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace gfr {
 namespace {
 
@@ -89,19 +91,19 @@ __device__ __forceinline__ float silu(float v) {
     return v * __builtin_amdgcn_rcpf(1.0f + exp_f32(-v));
 }
 
-// The current device's CU count, looked up once per device.
-inline int cu_count() {
-    static int cached[64] = {0};
+// Lets kernel K have up to 128 KB of dynamic LDS; the runtime is asked once per
+// device.
+template <auto K>
+hipError_t allow_lds(int bytes) {
+    if (bytes <= (32 << 10)) return hipSuccess;
+    static std::atomic<bool> done[64];
     int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-    if (!cached[dev]) {
-        int n = 0;
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
-            n <= 0)
-            n = 256;
-        cached[dev] = n;
-    }
-    return cached[dev];
+    if (hipError_t e = hipGetDevice(&dev); e != hipSuccess) return e;
+    if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_relaxed)) return hipSuccess;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(K),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, 128 << 10);
+    if (e == hipSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+    return e;
 }
 
 }  // namespace

@@ -321,10 +321,9 @@ __device__ __forceinline__ void spread() {
 // before part 3, whose fragments are in registers by then: behind it the other
 // stage is complete, and nobody reads this one any more.
 template <bool F16, bool ALIGNED, bool SWIGLU, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(LinearParams p, int tiles_m,
-                                                                      int tiles_n) {
-    static_assert((BM / WM) * (BN / WN) == 4, "four waves");
-    constexpr int kThreads = 256;
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, BM == 256 ? BM / WM * (BN / WN) / 4 : 2)
+void tile_kernel(LinearParams p, int tiles_m, int tiles_n) {
+    constexpr int kWaves = (BM / WM) * (BN / WN), kThreads = kWaves * 64, kRowsPer = kThreads / 8;
     constexpr int kNX = BM * 8 / kThreads, kNW = BN * 8 / kThreads;   // pieces per thread
     constexpr int FM = WM / 32, FN = WN / 32;
     extern __shared__ u4_t lds[];                  // [2][BM + BN][8]
@@ -350,14 +349,16 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(LinearPara
     const int piece = threadIdx.x & 7, row0 = threadIdx.x >> 3;
 #pragma unroll
     for (int i = 0; i < kNX; ++i)
-        x_off[i] = min(row0 + 32 * i, p.M - 1 - m0) * static_cast<int>(bytes) + 16 * piece;
+        x_off[i] = min(row0 + kRowsPer * i, p.M - 1 - m0) * static_cast<int>(bytes) + 16 * piece;
+    // (a wave holds eight rows of a pass: all gate or all up rows)
+    auto is_up = [&](int i) { return SWIGLU && (uniform(row0) + kRowsPer * i & 32); };
 #pragma unroll
     for (int i = 0; i < kNW; ++i) {
-        const int row = SWIGLU ? (i >> 1) * 32 + row0 : 32 * i + row0;   // odd i: up rows
+        const int r = row0 + kRowsPer * i, row = SWIGLU ? (r >> 6) * 32 + (r & 31) : r;
         w_off[i] = min(row, p.N - 1 - n0) * static_cast<int>(bytes) + 16 * piece +
-                   (SWIGLU && (i & 1) ? skew : 0);
+                   (is_up(i) ? skew : 0);
     }
-    // rows 32 apart share their swizzle
+    // rows a multiple of 8 apart share their swizzle
     u4_t *const put_at = lds + row0 * 8 + (piece ^ (row0 & 7));
     u4_t xs[kNX], ws[kNW];
     const int steps = (p.K + 63) / 64;
@@ -378,7 +379,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(LinearPara
     };
     auto fetch_x = [&](int step) { fetch(xs, x_off, [&](int) { return xr; }, step); };
     auto fetch_w = [&](int step) {
-        fetch(ws, w_off, [&](int i) { return SWIGLU && (i & 1) ? ur : wr; }, step);
+        fetch(ws, w_off, [&](int i) { return is_up(i) ? ur : wr; }, step);
     };
     const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
     const u4_t *const x_at = lds + (wm + c) * 8, *const w_at = lds + (BM + wn + c) * 8;
@@ -401,11 +402,11 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(LinearPara
     };
     auto put_x = [&](int stage) {
 #pragma unroll
-        for (int i = 0; i < kNX; ++i) put_at[stage * kStage + 32 * 8 * i] = xs[i];
+        for (int i = 0; i < kNX; ++i) put_at[stage * kStage + kRowsPer * 8 * i] = xs[i];
     };
     auto put_w = [&](int stage) {
 #pragma unroll
-        for (int i = 0; i < kNW; ++i) put_at[stage * kStage + (BM + 32 * i) * 8] = ws[i];
+        for (int i = 0; i < kNW; ++i) put_at[stage * kStage + (BM + kRowsPer * i) * 8] = ws[i];
     };
     fetch_x(0);
     fetch_w(0);
@@ -449,7 +450,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void tile_kernel(LinearPara
     constexpr int kPitch = WN + 4;     // spreads the rows over the banks
     constexpr int kCols = SWIGLU ? WN / 2 : WN;
     constexpr int kSlab = 32 * kPitch + 16 * kCols;    // floats: sums, then residual rows
-    static_assert(4 * kSlab * 4 <= 2 * kStage * 16, "the waves' rows fit the stages");
+    static_assert(kWaves * kSlab * 4 <= 2 * kStage * 16, "the waves' rows fit the stages");
     float *slab = reinterpret_cast<float *>(lds) + wave * kSlab;
     u4_t *res_at = reinterpret_cast<u4_t *>(slab + 32 * kPitch);
     const int col0 = n0 + (SWIGLU ? wn / 2 : wn);
@@ -585,16 +586,12 @@ template <bool F16, bool ALIGNED, bool SWIGLU, int BM, int BN, int WM, int WN>
 hipError_t launch_tiles(const LinearParams &p, hipStream_t stream) {
     constexpr int lds = 2 * (BM + BN) * 8 * 16;
     constexpr int cols = SWIGLU ? BN / 2 : BN;
-    auto kernel = &tile_kernel<F16, ALIGNED, SWIGLU, BM, BN, WM, WN>;
-    if (lds > (64 << 10)) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (e != hipSuccess) return e;
-    }
+    constexpr auto kernel = &tile_kernel<F16, ALIGNED, SWIGLU, BM, BN, WM, WN>;
+    if (hipError_t e = allow_lds<kernel>(lds); e != hipSuccess) return e;
     const int tm = (p.M + BM - 1) / BM, tn = (p.N + cols - 1) / cols;
     const int64_t grid = (static_cast<int64_t>(tm) * tn + 7) / 8 * 8;
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)),
-                       dim3(256), lds, stream, p, tm, tn);
+                       dim3((BM / WM) * (BN / WN) * 64), lds, stream, p, tm, tn);
     return hipGetLastError();
 }
 
@@ -606,7 +603,7 @@ hipError_t launch_linear_t(const LinearParams &p, hipStream_t stream) {
     const int64_t cols = SWIGLU ? 128 : 256;
     const int64_t big = ((p.M + 255) / 256) * ((p.N + cols - 1) / cols);
     if (ALIGNED && big >= 192)
-        return launch_tiles<F16, ALIGNED, SWIGLU, 256, 256, 128, 128>(p, stream);
+        return launch_tiles<F16, ALIGNED, SWIGLU, 256, 256, 128, 64>(p, stream);
     const int64_t mid = ((p.M + 127) / 128) * ((p.N + cols / 2 - 1) / (cols / 2));
     if (mid >= 128) return launch_tiles<F16, ALIGNED, SWIGLU, 128, 128, 64, 64>(p, stream);
     return launch_tiles<F16, ALIGNED, SWIGLU, 64, SWIGLU ? 128 : 64, 32, SWIGLU ? 64 : 32>(p, stream);

@@ -642,12 +642,8 @@ hipError_t launch_product(const DecodeParams &p, hipStream_t stream) {
     const int lds = operand > kMaskBytes ? operand : kMaskBytes;
     const int tiles = (cols + Stream::kTile - 1) / Stream::kTile;
     const int runs = (tiles + d.run * kWaves - 1) / (d.run * kWaves);
-    auto kernel = &product_kernel<Stream, RG, TERMS>;
-    if (lds > (32 << 10)) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (e != hipSuccess) return e;
-    }
+    constexpr auto kernel = &product_kernel<Stream, RG, TERMS>;
+    if (hipError_t e = allow_lds<kernel>(lds); e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel,
                        dim3(runs, d.chunks, static_cast<uint32_t>(max_groups(p.T * p.k, p.E, RG))),
                        dim3(kThreads), lds, stream, p);

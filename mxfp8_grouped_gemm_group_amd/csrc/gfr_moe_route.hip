@@ -463,14 +463,11 @@ template <int V, bool WIDE>
 hipError_t launch_route_t(const RouteParams &p, hipStream_t stream) {
     const size_t keys = WIDE && p.n_group > 1 ? sizeof(double) * p.E : 0;
     if (p.x && p.T <= kFewTokens) {
-        // 16 waves' keys: at most 128 KB of LDS at E = 1024
-        if (16 * keys > (32u << 10)) {
-            const hipError_t e = hipFuncSetAttribute(
-                reinterpret_cast<const void *>(&route_few_kernel<V, WIDE>),
-                hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(16 * keys));
-            if (e != hipSuccess) return e;
-        }
-        hipLaunchKernelGGL((route_few_kernel<V, WIDE>), dim3(p.T), dim3(1024), 16 * keys, stream,
+        // 16 waves' keys: at most 128 KB of LDS, at E = 1024
+        constexpr auto kernel = &route_few_kernel<V, WIDE>;
+        if (hipError_t e = allow_lds<kernel>(static_cast<int>(16 * keys)); e != hipSuccess)
+            return e;
+        hipLaunchKernelGGL(kernel, dim3(p.T), dim3(1024), 16 * keys, stream,
                            p);
         return hipGetLastError();
     }
