@@ -7,6 +7,7 @@ checked by the library, which raises GfrError here.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 from typing import NamedTuple, Optional
@@ -55,46 +56,41 @@ def _check(rc: int):
 _PAD = ((), (0, 0, 0), (0, 0), (0,), ())     # of a shape of 1 .. 4 extents
 
 
-@functools.lru_cache(maxsize=None)
-def _words(n: int):
-    return ctypes.c_int64 * n
-
-
-def _pack(dev, tensors, workspace=None, status=None):
+def _pack(index, tensors, workspace=None, status=None):
     """The tensors' gfr_tensor descriptors and a gfr_options behind them in one
     array of 64-bit words, and their addresses (None for an absent tensor).  One
-    array costs a fifth of a ctypes structure per tensor, and the smallest calls
-    take little longer on the GPU than that.  The array has to outlive the call.
-    """
+    array costs a fraction of a ctypes structure per tensor, and the smallest
+    calls take little longer on the GPU than that.  The array has to outlive
+    the call.  Raises for what the descriptors cannot carry."""
     v, at = [], []
     for t in tensors:
         if t is None:
             at.append(None)
             continue
-        # what the descriptors cannot carry
-        if t.device != dev or not t.is_cuda:
+        if t.get_device() != index:
             raise ValueError("all tensors must be on one CUDA device")
         if not t.is_contiguous():
             raise ValueError("all tensors must be contiguous")
-        s = t.shape
-        n = len(s)
-        _need(1 <= n <= 4, f"rank {n} is outside 1..4")
-        code = DTYPES.get(t.dtype)
-        _need(code is not None, f"dtype {t.dtype} has no gfr_dtype")
+        shape, code = t.shape, DTYPES.get(t.dtype)
+        n = len(shape)
+        if code is None:
+            raise ValueError(f"dtype {t.dtype} has no gfr_dtype")
+        if not 1 <= n <= 4:
+            raise ValueError(f"rank {n} is outside 1..4")
         at.append(8 * len(v))
-        v += (t.data_ptr(), code | n << 32, *s, *_PAD[n])
+        v += (t.data_ptr(), code | n << 32, *shape, *_PAD[n])
     end = 8 * len(v)
-    for t in (workspace, status):
-        if t is not None and (t.device != dev or not t.is_contiguous()):
-            raise ValueError("workspace and status must be contiguous and on the tensors' device")
     v += (0, 0, 0, 0, 0)
+    for t in (workspace, status):
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            raise ValueError("workspace and status must be contiguous and on the tensors' device")
     if workspace is not None:
         v[-4], v[-3] = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if status is not None:
         _need(status.dtype == torch.int32 and status.numel() >= 1, "status must be int32")
         v[-2] = status.data_ptr()
-    words = _words(len(v))(*v)
-    base = ctypes.addressof(words)
+    words = array.array("q", v)
+    base = words.buffer_info()[0]
     return words, [None if a is None else base + a for a in at], base + end
 
 
@@ -102,35 +98,19 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-class _OnStream:
-    """The call's device and stream made current, so that what is allocated
-    within belongs to the stream that uses it; gives the stream's handle."""
-
-    def __init__(self, dev, stream: Optional[int]):
-        self.dev, self.stream, self.inner = dev, stream, None
-
-    def __enter__(self):
-        if self.stream is None:
-            index = self.dev.index
-            if index is None or index != torch.cuda.current_device():
-                self.inner = torch.cuda.device(self.dev)
-                self.inner.__enter__()
-                index = torch.cuda.current_device()
-            return _raw_stream(index)
-        s = torch.cuda.ExternalStream(self.stream, device=self.dev) if self.stream else \
-            torch.cuda.default_stream(self.dev)
-        self.inner = torch.cuda.stream(s)
-        self.inner.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.inner is not None:
-            self.inner.__exit__(*exc)
+def _elsewhere(index: int, stream: Optional[int]):
+    """A context that makes the call's device and stream current, so that what is
+    allocated within belongs to the stream that uses it; None if they are."""
+    if stream is not None:
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=index) if stream
+                                 else torch.cuda.default_stream(index))
+    return None if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
-def _cuda(t, name: str):
-    _need(t.is_cuda, f"{name} must be on a CUDA device")
-    return t.device
+def _device(t, name: str) -> int:
+    index = t.get_device()
+    _need(index >= 0, f"{name} must be on a CUDA device")
+    return index
 
 
 def linear(x, w, bias=None, *, activation="none", residual=None, out_dtype=None, out=None,
@@ -146,22 +126,27 @@ def linear(x, w, bias=None, *, activation="none", residual=None, out_dtype=None,
     lib = _lib()
     act = ACTIVATIONS.get(activation)
     _need(act is not None, f"activation must be one of {sorted(ACTIVATIONS)}")
-    dev = _cuda(x, "x")
+    index = _device(x, "x")
     _need(x.dim() == 2 and w.dim() == 2, "x must be [M, K] and w [N, K]")
     _need(out is None or out_dtype is None or out.dtype == out_dtype, "out must have out_dtype")
-    with _OnStream(dev, stream) as handle:
-        if out is None:
-            n = w.shape[0] // 2 if act == 5 else w.shape[0]
-            out = torch.empty((x.shape[0], n), dtype=out_dtype or x.dtype, device=dev)
-        words, (px, pw, pb, pr, po), opts = _pack(dev, (x, w, bias, residual, out), workspace)
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return linear(x, w, bias, activation=activation, residual=residual,
+                          out_dtype=out_dtype, out=out, workspace=workspace)
+    if out is None:
+        n = w.shape[0] // 2 if act == 5 else w.shape[0]
+        out = torch.empty((x.shape[0], n), dtype=out_dtype or x.dtype, device=x.device)
+    tensors, handle = (x, w, bias, residual, out), _raw_stream(index)
+    words, (px, pw, pb, pr, po), opts = _pack(index, tensors, workspace)
+    rc = lib.gfr_linear(px, pw, pb, pr, act, po, handle, opts)
+    if rc == WORKSPACE_TOO_SMALL and workspace is None:
+        need = ctypes.c_size_t(0)
+        _check(lib.gfr_linear_workspace_size(px, pw, pb, pr, act, po, ctypes.byref(need)))
+        workspace = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+        words, (px, pw, pb, pr, po), opts = _pack(index, tensors, workspace)
         rc = lib.gfr_linear(px, pw, pb, pr, act, po, handle, opts)
-        if rc == WORKSPACE_TOO_SMALL and workspace is None:
-            need = ctypes.c_size_t(0)
-            _check(lib.gfr_linear_workspace_size(px, pw, pb, pr, act, po, ctypes.byref(need)))
-            workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
-            words, (px, pw, pb, pr, po), opts = _pack(dev, (x, w, bias, residual, out), workspace)
-            rc = lib.gfr_linear(px, pw, pb, pr, act, po, handle, opts)
-        _check(rc)
+    _check(rc)
     return out
 
 
@@ -193,24 +178,30 @@ def moe_decode(x, w13, scale13, w2, scale2, topk_ids, topk_weights, *, transpose
     none is given; calls that overlap in time need one each.
     """
     lib = _lib()
-    dev = _cuda(x, "x")
+    index = _device(x, "x")
     _need(x.dim() == 2 and w2.dim() == 3 and topk_ids.dim() == 2,
           "x must be [T, H], w2 3-D and topk_ids [T, k]")
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return moe_decode(x, w13, scale13, w2, scale2, topk_ids, topk_weights,
+                              transpose_w13=transpose_w13, transpose_w2=transpose_w2,
+                              shared_input=shared_input, shared_input_weight=shared_input_weight,
+                              out_dtype=out_dtype, out=out, workspace=workspace, status=status)
     T, k = topk_ids.shape
     E, I, N = w2.shape
     if transpose_w2:
         I, N = N, I
     t13, t2 = int(bool(transpose_w13)), int(bool(transpose_w2))
-    with _OnStream(dev, stream) as handle:
-        if out is None:
-            out = torch.empty((x.shape[0], N), dtype=out_dtype, device=dev)
-        if workspace is None:
-            need = moe_decode_workspace_size(T, k, E, x.shape[1], I, N, t13, t2)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        words, at, opts = _pack(dev, (x, w13, scale13, w2, scale2, topk_ids, topk_weights,
-                                      shared_input, out), workspace, status)
-        _check(lib.gfr_moe_decode(*at[:8], float(shared_input_weight), at[8], t13, t2, handle,
-                                  opts))
+    if out is None:
+        out = torch.empty((x.shape[0], N), dtype=out_dtype, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(moe_decode_workspace_size(T, k, E, x.shape[1], I, N, t13, t2),
+                                dtype=torch.uint8, device=x.device)
+    words, at, opts = _pack(index, (x, w13, scale13, w2, scale2, topk_ids, topk_weights,
+                                    shared_input, out), workspace, status)
+    _check(lib.gfr_moe_decode(*at[:8], float(shared_input_weight), at[8], t13, t2,
+                              _raw_stream(index), opts))
     return out
 
 
@@ -251,24 +242,32 @@ def moe_route(logits, top_k, *, x=None, bias=None, scoring="softmax", n_group=1,
     T, E = logits.shape
     k = int(top_k)
     _need(k >= 1, "top_k must be positive")
-    dev = _cuda(logits, "logits")
-    empty = functools.partial(torch.empty, device=dev)
-    with _OnStream(dev, stream) as handle:
-        ids, weights = empty((T, k), dtype=torch.int32), empty((T, k), dtype=torch.float32)
-        rows = (None,) * 5
-        if x is not None:
-            H, n = x.shape[1], T * k
-            rows = (empty((n, H), dtype=out_dtype),
-                    empty((n, (H + 63) // 64, 2), dtype=torch.uint8),
-                    empty(E, dtype=torch.int64), empty(n, dtype=torch.int32),
-                    empty(n, dtype=torch.float32))
-            if workspace is None:
-                need = _route_workspace_size(T, E, k)
-                if need:
-                    workspace = empty(need, dtype=torch.uint8)
-        words, at, opts = _pack(dev, (logits, bias, ids, weights, x, *rows), workspace)
-        _check(lib.gfr_moe_route(at[0], at[1], score, int(n_group), int(topk_group),
-                                 int(bool(renormalize)), float(scaling), *at[2:], handle, opts))
+    index = _device(logits, "logits")
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return moe_route(logits, top_k, x=x, bias=bias, scoring=scoring, n_group=n_group,
+                             topk_group=topk_group, renormalize=renormalize, scaling=scaling,
+                             out_dtype=out_dtype, workspace=workspace)
+    dev = logits.device
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    rows = (None,) * 5
+    if x is not None:
+        H, n = x.shape[1], T * k
+        rows = (torch.empty((n, H), dtype=out_dtype, device=dev),
+                torch.empty((n, (H + 63) // 64, 2), dtype=torch.uint8, device=dev),
+                torch.empty(E, dtype=torch.int64, device=dev),
+                torch.empty(n, dtype=torch.int32, device=dev),
+                torch.empty(n, dtype=torch.float32, device=dev))
+        if workspace is None:
+            need = _route_workspace_size(T, E, k)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    words, at, opts = _pack(index, (logits, bias, ids, weights, x, *rows), workspace)
+    _check(lib.gfr_moe_route(at[0], at[1], score, int(n_group), int(topk_group),
+                             int(bool(renormalize)), float(scaling), *at[2:],
+                             _raw_stream(index), opts))
     return RouteResult(ids, weights, *rows)
 
 

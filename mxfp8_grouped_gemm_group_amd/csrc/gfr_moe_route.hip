@@ -30,7 +30,7 @@ namespace gfr {
 namespace {
 
 constexpr int kChunk = 16;          // tokens per block of the long path
-constexpr int kFewTokens = 32;      // one-launch path up to here
+constexpr int kFewTokens = 64;      // one-launch path up to here
 constexpr int kMoveThreads = 256;
 
 constexpr float kNegInf = -INFINITY;

@@ -68,7 +68,8 @@ def test_choice(T, E, k, bias, kw):
 @pytest.mark.parametrize("fp8", [torch.float8_e4m3fn, torch.float8_e5m2])
 @pytest.mark.parametrize("xdt", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("T, E, k, H", [
-    (1, 8, 2, 32), (3, 16, 4, 96), (32, 24, 3, 128), (33, 24, 3, 1056), (100, 64, 6, 64),
+    (1, 8, 2, 32), (3, 16, 4, 96), (32, 24, 3, 128), (33, 24, 3, 1056), (64, 40, 5, 64),
+    (65, 40, 5, 64), (100, 64, 6, 64),
     (49, 256, 8, 1024), (300, 7, 7, 160)])
 def test_rows(T, E, k, H, xdt, fp8):
     print(f"T {T} E {E} k {k} H {H} {xdt} {fp8}", flush=True)
