@@ -33,6 +33,10 @@ constexpr int kChunk = 16;          // tokens per block of the long path
 constexpr int kFewTokens = 64;      // one-launch path up to here
 constexpr int kMoveThreads = 256;
 
+// Waves of a route_kernel block: one per token of a chunk, or as many as V's
+// registers leave.
+constexpr int route_waves(int V) { return V == 16 ? 8 : kChunk; }
+
 constexpr float kNegInf = -INFINITY;
 
 template <int CTRL, int ROWS>
@@ -87,26 +91,51 @@ __device__ __forceinline__ double wave_sum(double x) {
 }
 
 // Strikes out the experts of all but the topk_group best groups.  Lane q adds
-// up its group's two largest keys (the keys go through LDS, `s`, E doubles of
-// this wave's own), and group q stays if fewer than topk_group groups are
-// better (larger, or equal and of lower index).
+// up its group's two largest keys, and group q stays if fewer than topk_group
+// groups are better (larger, or equal and of lower index).  The keys go through
+// LDS (`s`, E doubles of this wave's own): all of them, or, where no lane holds
+// experts of two groups, each lane's two largest (256 experts in 8 groups: 8
+// reads instead of 32).
 template <int V>
 __device__ __forceinline__ void keep_groups(const RouteParams &p, double (&key)[V], double *s,
                                             int lane) {
     const int width = p.E / p.n_group;
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        if (lane * V + v < p.E) s[lane * V + v] = key[v];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
     double first = kNegInf, second = kNegInf;
-    if (lane < p.n_group)
-        for (int i = 0; i < width; ++i) {
-            const double d = s[lane * width + i];
-            second = fmax(second, fmin(first, d));
-            first = fmax(first, d);
+    __builtin_amdgcn_wave_barrier();
+    if (V > 1 && width % V == 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            second = fmax(second, fmin(first, key[v]));
+            first = fmax(first, key[v]);
         }
+        if (lane * V < p.E) s[2 * lane] = first, s[2 * lane + 1] = second;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const int lanes = width / V;
+        first = second = kNegInf;
+        if (lane < p.n_group) {
+#pragma unroll 4
+            for (int i = 0; i < lanes; ++i) {
+                const double a = s[2 * (lane * lanes + i)], b = s[2 * (lane * lanes + i) + 1];
+                second = fmax(fmax(second, b), fmin(first, a));
+                first = fmax(first, a);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (lane * V + v < p.E) s[lane * V + v] = key[v];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (lane < p.n_group) {
+#pragma unroll 4
+            for (int i = 0; i < width; ++i) {
+                const double d = s[lane * width + i];
+                second = fmax(second, fmin(first, d));
+                first = fmax(first, d);
+            }
+        }
+    }
     const double value = first + (second > kNegInf ? second : 0.0);
     int better = 0;
     for (int q = 0; q < p.n_group; ++q) {
@@ -355,19 +384,19 @@ __global__ __launch_bounds__(1024) void route_few_kernel(RouteParams p) {
 // The choice alone, and the long path.
 // ---------------------------------------------------------------------------
 
-// Four waves take `per_block` tokens; with counts, the pairs of the block per
-// expert (bucket E: pairs without one) go to counts[bucket][block].
+// A block's waves take `per_block` tokens; with counts, the pairs of the block
+// per expert (bucket E: pairs without one) go to counts[bucket][block].
 template <int V, bool WIDE>
-__global__ __launch_bounds__(256) void route_kernel(RouteParams p, int per_block) {
-    extern __shared__ double keys[];            // WIDE with groups: 4 x E
+__global__ __launch_bounds__(64 * route_waves(V)) void route_kernel(RouteParams p, int per_block) {
+    extern __shared__ double keys[];            // WIDE with groups: waves x E
     __shared__ int hist[GFR_MAX_EXPERTS + 1];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     if (p.counts) {
-        for (int e = threadIdx.x; e <= p.E; e += 256) hist[e] = 0;
+        for (int e = threadIdx.x; e <= p.E; e += blockDim.x) hist[e] = 0;
         __syncthreads();
     }
     const int t0 = blockIdx.x * per_block, t1 = min(t0 + per_block, p.T);
-    for (int t = t0 + wave; t < t1; t += 4) {
+    for (int t = t0 + wave; t < t1; t += waves) {
         int id;
         float weight;
         choose<V, WIDE>(p, t, lane, WIDE ? keys + wave * p.E : nullptr, id, weight);
@@ -380,7 +409,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteParams p, int per_block
     }
     if (p.counts) {
         __syncthreads();
-        for (int e = threadIdx.x; e <= p.E; e += 256)
+        for (int e = threadIdx.x; e <= p.E; e += blockDim.x)
             p.counts[static_cast<int64_t>(e) * gridDim.x + blockIdx.x] = hist[e];
     }
 }
@@ -446,12 +475,14 @@ __global__ __launch_bounds__(kMoveThreads) void move_kernel(RouteParams p, int c
         for (int o = 0; o < i; ++o) rank += bucket[o] == b;
         const int at = start[b] + rank;
         pos[i] = b < p.E ? at : ~at;
-        p.row_index[at] = t0 + i / p.k;
-        p.logit[at] = p.weights[q0 + i];
+        if (blockIdx.y == 0) {
+            p.row_index[at] = t0 + i / p.k;
+            p.logit[at] = p.weights[q0 + i];
+        }
     }
     __syncthreads();
     for (int t = wave; t < nt; t += kMoveThreads / 64)
-        move_row_any(p, t0 + t, pos + t * p.k, lane, 64);
+        move_row_any(p, t0 + t, pos + t * p.k, blockIdx.y * 64 + lane, gridDim.y * 64);
 }
 
 __global__ void clear_groups_kernel(int64_t *g, int n) {
@@ -471,16 +502,22 @@ hipError_t launch_route_t(const RouteParams &p, hipStream_t stream) {
                            p);
         return hipGetLastError();
     }
-    // the choice alone: blocks of four tokens while they are few, so that no
-    // wave has to take two
-    const int per_block = p.x ? kChunk : p.T <= 4096 ? 4 : kChunk;
+    // the choice alone: single waves while they are few, so that each has a CU's
+    // units to itself
+    const int per_block = p.x || p.T > 4096 ? kChunk : 1;
+    const int waves = per_block == 1 ? 1 : route_waves(V);
     const int blocks = (p.T + per_block - 1) / per_block;
-    hipLaunchKernelGGL((route_kernel<V, WIDE>), dim3(blocks), dim3(256), 4 * keys, stream, p,
-                       per_block);
+    constexpr auto kernel = &route_kernel<V, WIDE>;
+    if (hipError_t e = allow_lds<kernel>(static_cast<int>(waves * keys)); e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(64 * waves), waves * keys, stream, p, per_block);
     if (hipError_t e = hipGetLastError(); e != hipSuccess || !p.x) return e;
     hipLaunchKernelGGL(scan_kernel, dim3(p.E + 1), dim3(256), 0, stream, p, blocks);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    hipLaunchKernelGGL(move_kernel, dim3(blocks), dim3(kMoveThreads), 0, stream, p, blocks);
+    // few chunks: their rows' columns over several blocks each
+    const int pieces = (p.H / 16 + 63) / 64;
+    int split = 1;
+    while (blocks * split < 1024 && split * 2 <= pieces) split *= 2;
+    hipLaunchKernelGGL(move_kernel, dim3(blocks, split), dim3(kMoveThreads), 0, stream, p, blocks);
     return hipGetLastError();
 }
 
