@@ -4,8 +4,8 @@
 //
 // A wave takes a token.  Lane l holds experts l V .. l V + V - 1 in registers
 // (V = 1, 2, 4, 8 or 16 with E), and each of the k rounds takes the maximum
-// over the wave (six DPP steps, no LDS), finds its lowest holder with a ballot
-// and strikes it out there.  Choosing by the logits compares FP32; with a bias
+// over the wave (six DPP steps per word, no LDS), finds its lowest holder with a
+// ballot and strikes it out there.  Choosing by the logits compares FP32; with a bias
 // or expert groups the values compared are FP64, since two scores that differ
 // by less than an FP32 rounding would otherwise change places.
 //
@@ -13,8 +13,9 @@
 //   few tokens    one launch, one block per token: every block chooses for all
 //                 tokens (cheaper than a launch that hands the choice over) and
 //                 counts the pairs ahead of its own token's;
-//   more tokens   route_kernel (choice, counts per chunk of 16 tokens and
-//                 expert), scan_kernel (a block per expert over the chunks),
+//   more tokens   route_kernel (choice, counts per chunk of 8 tokens and
+//                 expert), scan_kernel (a block per expert over the chunks; few
+//                 chunks are summed by each block of the next instead),
 //                 move_kernel (a block per chunk: ranks within it, rows).
 // Moving rows bounds the long calls: each row is read once, quantised in
 // registers and written to its k places in 16-byte stores.
@@ -29,34 +30,20 @@
 namespace gfr {
 namespace {
 
-constexpr int kChunk = 16;          // tokens per block of the long path
+constexpr int kChunk = 8;           // tokens per block of the long path
 constexpr int kFewTokens = 64;      // one-launch path up to here
+constexpr int kFewChunks = 64;      // no scan launch up to here
 constexpr int kMoveThreads = 256;
 
-// Waves of a route_kernel block: one per token of a chunk, or as many as V's
-// registers leave.
-constexpr int route_waves(int V) { return V == 16 ? 8 : kChunk; }
 
 constexpr float kNegInf = -INFINITY;
 
 template <int CTRL, int ROWS>
-__device__ __forceinline__ float dpp_max(float x) {
-    const float y = __uint_as_float(
-        dpp<CTRL, ROWS, 0xf, false>(__float_as_uint(kNegInf), __float_as_uint(x)));
-    return fmaxf(x, y);
-}
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double dpp_f64(double x, double old) {
-    const uint64_t b = __double_as_longlong(x), o = __double_as_longlong(old);
-    const uint32_t lo = dpp<CTRL, ROWS, 0xf, false>(static_cast<uint32_t>(o),
-                                                    static_cast<uint32_t>(b));
-    const uint32_t hi = dpp<CTRL, ROWS, 0xf, false>(static_cast<uint32_t>(o >> 32),
-                                                    static_cast<uint32_t>(b >> 32));
+__device__ __forceinline__ double dpp_f64(double x) {
+    const uint64_t b = __double_as_longlong(x);
+    const uint32_t lo = dpp<CTRL, ROWS, 0xf, true>(0, static_cast<uint32_t>(b));
+    const uint32_t hi = dpp<CTRL, ROWS, 0xf, true>(0, static_cast<uint32_t>(b >> 32));
     return __longlong_as_double(static_cast<uint64_t>(hi) << 32 | lo);
-}
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double dpp_max(double x) {
-    return fmax(x, dpp_f64<CTRL, ROWS>(x, static_cast<double>(kNegInf)));
 }
 
 __device__ __forceinline__ float lane_value(float x, int lane) {
@@ -69,25 +56,38 @@ __device__ __forceinline__ double lane_value(double x, int lane) {
     return __longlong_as_double(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-// Maximum over the wave (row shifts, then row broadcasts; lane 63 has it).
-template <class K>
-__device__ __forceinline__ K wave_max(K x) {
-    x = dpp_max<0x111, 0xf>(x);
-    x = dpp_max<0x112, 0xf>(x);
-    x = dpp_max<0x114, 0xf>(x);
-    x = dpp_max<0x118, 0xf>(x);
-    x = dpp_max<0x142, 0xa>(x);
-    x = dpp_max<0x143, 0xc>(x);
-    return lane_value(x, 63);
+// Over the wave: row shifts, then row broadcasts; lane 63 has the result.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+    x = max(x, dpp<0x111, 0xf, 0xf, true>(0, x));
+    x = max(x, dpp<0x112, 0xf, 0xf, true>(0, x));
+    x = max(x, dpp<0x114, 0xf, 0xf, true>(0, x));
+    x = max(x, dpp<0x118, 0xf, 0xf, true>(0, x));
+    x = max(x, dpp<0x142, 0xa, 0xf, true>(0, x));
+    x = max(x, dpp<0x143, 0xc, 0xf, true>(0, x));
+    return __builtin_amdgcn_readlane(x, 63);
 }
 __device__ __forceinline__ double wave_sum(double x) {
-    x += dpp_f64<0x111, 0xf>(x, 0.0);
-    x += dpp_f64<0x112, 0xf>(x, 0.0);
-    x += dpp_f64<0x114, 0xf>(x, 0.0);
-    x += dpp_f64<0x118, 0xf>(x, 0.0);
-    x += dpp_f64<0x142, 0xa>(x, 0.0);
-    x += dpp_f64<0x143, 0xc>(x, 0.0);
+    x += dpp_f64<0x111, 0xf>(x);
+    x += dpp_f64<0x112, 0xf>(x);
+    x += dpp_f64<0x114, 0xf>(x);
+    x += dpp_f64<0x118, 0xf>(x);
+    x += dpp_f64<0x142, 0xa>(x);
+    x += dpp_f64<0x143, 0xc>(x);
     return lane_value(x, 63);
+}
+
+// Unsigned integers in the order of floats above -inf (0 stands for -inf and
+// for what is struck out).
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t b = __float_as_uint(x == 0.0f ? 0.0f : x);     // -0 equals 0
+    return x > kNegInf ? (b >> 31 ? ~b : b | 0x80000000u) : 0;
+}
+__device__ __forceinline__ float from_ordered(uint32_t k) {
+    return k == 0 ? kNegInf : __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ uint64_t ordered(double x) {
+    const uint64_t b = __double_as_longlong(x == 0.0 ? 0.0 : x);
+    return x > static_cast<double>(kNegInf) ? (b >> 63 ? ~b : b | uint64_t{1} << 63) : 0;
 }
 
 // Strikes out the experts of all but the topk_group best groups.  Lane q adds
@@ -150,32 +150,39 @@ __device__ __forceinline__ void keep_groups(const RouteParams &p, double (&key)[
     }
 }
 
-// The choice of one token: lane j < k returns its j-th expert (-1: none) and
-// weight.  WIDE: FP64 keys (bias or groups); s as keep_groups.
-template <int V, bool WIDE>
-__device__ __forceinline__ void choose(const RouteParams &p, int t, int lane, double *s, int &id,
-                                       float &weight) {
-    typedef typename std::conditional<WIDE, double, float>::type K;
+// A token's logits: lane l's V experts, -inf for what is not live.
+template <int V>
+__device__ __forceinline__ void load_logits(const RouteParams &p, int t, int lane, float (&z)[V]) {
     const int64_t row = static_cast<int64_t>(t) * p.E;
-    float z[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int e = lane * V + v;
-        float l = kNegInf;
+        z[v] = kNegInf;
         if (e < p.E)
-            l = p.logits_bf16 ? bf16_f32(static_cast<const uint16_t *>(p.logits)[row + e])
-                              : static_cast<const float *>(p.logits)[row + e];
-        z[v] = l > kNegInf ? l : kNegInf;   // NaN: not live
+            z[v] = p.logits_bf16 ? bf16_f32(static_cast<const uint16_t *>(p.logits)[row + e])
+                                 : static_cast<const float *>(p.logits)[row + e];
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v) z[v] = z[v] > kNegInf ? z[v] : kNegInf;   // NaN: not live
+}
+
+// The choice of one token: lane j < k returns its j-th expert (-1: none) and
+// weight.  WIDE: FP64 keys (bias or groups); s as keep_groups.  Keys are compared
+// as ordered integers, an FP64 key's halves one after the other: a wave maximum
+// of words is six instructions, one of doubles some thirty.
+template <int V, bool WIDE>
+__device__ __forceinline__ void choose(const RouteParams &p, const float (&z)[V], int lane,
+                                       double *s, int &id, float &weight) {
+    typedef typename std::conditional<WIDE, double, float>::type K;
     float top = 0.0f;
     if (!p.sigmoid) {
-        top = z[0];
+        uint32_t m = 0;
 #pragma unroll
-        for (int v = 1; v < V; ++v) top = fmaxf(top, z[v]);
-        top = wave_max(top);
+        for (int v = 0; v < V; ++v) m = max(m, ordered(z[v]));
+        top = from_ordered(wave_max(m));
         if (top == kNegInf) top = 0.0f;
     }
-    K key[V], score[V];
+    K score[V];
     double sum = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -198,42 +205,51 @@ __device__ __forceinline__ void choose(const RouteParams &p, int t, int lane, do
             scale = static_cast<K>(1.0 / sum);
         }
     }
+    uint32_t hi[V], lo[V];
+    if (WIDE) {
+        double key[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        if (WIDE) {
+        for (int v = 0; v < V; ++v) {
             const int e = lane * V + v;
-            const K d = score[v] + (p.bias && e < p.E ? static_cast<K>(p.bias[e]) : K(0));
-            key[v] = z[v] > kNegInf && d > kNegInf ? d : K(kNegInf);
-        } else {
-            key[v] = z[v];
+            const double d = score[v] + (p.bias && e < p.E ? p.bias[e] : 0.0f);
+            key[v] = z[v] > kNegInf && d > kNegInf ? d : kNegInf;
         }
-    }
-    if (WIDE && p.n_group > 1) {
-        double d[V];
+        if (p.n_group > 1) keep_groups(p, key, s, lane);
 #pragma unroll
-        for (int v = 0; v < V; ++v) d[v] = key[v];
-        keep_groups(p, d, s, lane);
+        for (int v = 0; v < V; ++v) {
+            const uint64_t o = ordered(key[v]);
+            hi[v] = static_cast<uint32_t>(o >> 32);
+            lo[v] = static_cast<uint32_t>(o);
+        }
+    } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = static_cast<K>(d[v]);
+        for (int v = 0; v < V; ++v) hi[v] = ordered(z[v]), lo[v] = 0;
     }
     id = -1;
     K mine = 0, total = 0;
     for (int j = 0; j < p.k; ++j) {
-        K best = key[0], worth = score[0];
+        uint32_t h = hi[0], l = lo[0];
+        K worth = score[0];
         int slot = 0;
 #pragma unroll
         for (int v = 1; v < V; ++v)
-            if (key[v] > best) best = key[v], worth = score[v], slot = v;
-        const K most = wave_max(best);
-        if (!(most > K(kNegInf))) break;
-        const int holder = __ffsll(static_cast<unsigned long long>(__ballot(best == most))) - 1;
+            if (hi[v] > h || (WIDE && hi[v] == h && lo[v] > l))
+                h = hi[v], l = lo[v], worth = score[v], slot = v;
+        const uint32_t most = wave_max(h);
+        if (most == 0) break;
+        uint64_t holders = __ballot(h == most);
+        if (WIDE && (holders & (holders - 1))) {     // several: by the low halves
+            const uint32_t low = wave_max(h == most ? l : 0);
+            holders = __ballot(h == most && l == low);
+        }
+        const int holder = __ffsll(static_cast<unsigned long long>(holders)) - 1;
         const int at = __builtin_amdgcn_readlane(slot, holder);
         const K value = lane_value(worth, holder);
         total += value;
         if (lane == j) id = holder * V + at, mine = value;
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (lane == holder && v == at) key[v] = K(kNegInf);
+            if (lane == holder && v == at) hi[v] = lo[v] = 0;
     }
     if (p.renormalize)   // a zero sum leaves zeros, a NaN goes through
         mine = total == K(0) ? K(0) : mine / total;
@@ -339,10 +355,15 @@ __global__ __launch_bounds__(1024) void route_few_kernel(RouteParams p) {
     __shared__ float own_weight[GFR_MAX_TOPK];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int me = blockIdx.x, n = p.T * p.k;
+    float z[V], next[V];
+    if (wave < p.T) load_logits(p, wave, lane, z);
     for (int t = wave; t < p.T; t += 16) {
+        if (t + 16 < p.T) load_logits(p, t + 16, lane, next);
         int id;
         float weight;
-        choose<V, WIDE>(p, t, lane, WIDE ? keys + wave * p.E : nullptr, id, weight);
+        choose<V, WIDE>(p, z, lane, WIDE ? keys + wave * p.E : nullptr, id, weight);
+#pragma unroll
+        for (int v = 0; v < V; ++v) z[v] = next[v];
         if (lane < p.k) {
             bucket[t * p.k + lane] = id < 0 ? p.E : id;
             if (t == me) {
@@ -387,7 +408,7 @@ __global__ __launch_bounds__(1024) void route_few_kernel(RouteParams p) {
 // A block's waves take `per_block` tokens; with counts, the pairs of the block
 // per expert (bucket E: pairs without one) go to counts[bucket][block].
 template <int V, bool WIDE>
-__global__ __launch_bounds__(64 * route_waves(V)) void route_kernel(RouteParams p, int per_block) {
+__global__ __launch_bounds__(64 * kChunk) void route_kernel(RouteParams p, int per_block) {
     extern __shared__ double keys[];            // WIDE with groups: waves x E
     __shared__ int hist[GFR_MAX_EXPERTS + 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
@@ -398,8 +419,9 @@ __global__ __launch_bounds__(64 * route_waves(V)) void route_kernel(RouteParams 
     const int t0 = blockIdx.x * per_block, t1 = min(t0 + per_block, p.T);
     for (int t = t0 + wave; t < t1; t += waves) {
         int id;
-        float weight;
-        choose<V, WIDE>(p, t, lane, WIDE ? keys + wave * p.E : nullptr, id, weight);
+        float weight, z[V];
+        load_logits(p, t, lane, z);
+        choose<V, WIDE>(p, z, lane, WIDE ? keys + wave * p.E : nullptr, id, weight);
         if (lane < p.k) {
             const int64_t at = static_cast<int64_t>(t) * p.k + lane;
             p.ids[at] = id;
@@ -441,6 +463,8 @@ __global__ __launch_bounds__(256) void scan_kernel(RouteParams p, int chunks) {
 // A block per chunk of tokens: where each bucket's pairs of this chunk begin
 // (pairs of smaller experts, and of this one in earlier chunks), each pair's
 // rank among the chunk's equals, then the rows.
+// SCANNED: scan_kernel ran; otherwise (few chunks) every block sums the counts.
+template <bool SCANNED>
 __global__ __launch_bounds__(kMoveThreads) void move_kernel(RouteParams p, int chunks) {
     __shared__ int start[GFR_MAX_EXPERTS + 1];
     __shared__ int bucket[kChunk * GFR_MAX_TOPK];
@@ -456,7 +480,23 @@ __global__ __launch_bounds__(kMoveThreads) void move_kernel(RouteParams p, int c
     uint32_t carry = 0;
     for (int base = 0; base <= p.E; base += kMoveThreads) {
         const int e = base + threadIdx.x;
-        const uint32_t v = e < p.E ? static_cast<uint32_t>(p.group_list[e]) : 0;
+        uint32_t v = 0, earlier = 0;
+        if (e <= p.E) {
+            const int *c = p.counts + static_cast<int64_t>(e) * chunks;
+            if (SCANNED) {
+                v = e < p.E ? static_cast<uint32_t>(p.group_list[e]) : 0;
+                earlier = c[blockIdx.x];
+            } else {
+#pragma unroll 8
+                for (int i = 0; i < chunks; ++i) {
+                    const uint32_t n_i = c[i];
+                    v += n_i;
+                    earlier += i < static_cast<int>(blockIdx.x) ? n_i : 0;
+                }
+                if (e == p.E) v = 0;
+                else if (blockIdx.x == 0 && blockIdx.y == 0) p.group_list[e] = v;
+            }
+        }
         const uint32_t incl = wave_prefix(v);
         if (lane == 63) totals[wave] = incl;
         __syncthreads();
@@ -465,8 +505,7 @@ __global__ __launch_bounds__(kMoveThreads) void move_kernel(RouteParams p, int c
             if (w < wave) before += totals[w];
             carry += totals[w];
         }
-        if (e <= p.E)
-            start[e] = before + incl - v + p.counts[static_cast<int64_t>(e) * chunks + blockIdx.x];
+        if (e <= p.E) start[e] = before + incl - v + earlier;
         __syncthreads();
     }
     for (int i = threadIdx.x; i < n; i += kMoveThreads) {
@@ -505,19 +544,25 @@ hipError_t launch_route_t(const RouteParams &p, hipStream_t stream) {
     // the choice alone: single waves while they are few, so that each has a CU's
     // units to itself
     const int per_block = p.x || p.T > 4096 ? kChunk : 1;
-    const int waves = per_block == 1 ? 1 : route_waves(V);
+    const int waves = per_block;
     const int blocks = (p.T + per_block - 1) / per_block;
     constexpr auto kernel = &route_kernel<V, WIDE>;
     if (hipError_t e = allow_lds<kernel>(static_cast<int>(waves * keys)); e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, dim3(blocks), dim3(64 * waves), waves * keys, stream, p, per_block);
     if (hipError_t e = hipGetLastError(); e != hipSuccess || !p.x) return e;
-    hipLaunchKernelGGL(scan_kernel, dim3(p.E + 1), dim3(256), 0, stream, p, blocks);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    // few chunks: their rows' columns over several blocks each
+    // few chunks: their rows' columns over several blocks each, and no scan
     const int pieces = (p.H / 16 + 63) / 64;
     int split = 1;
     while (blocks * split < 1024 && split * 2 <= pieces) split *= 2;
-    hipLaunchKernelGGL(move_kernel, dim3(blocks, split), dim3(kMoveThreads), 0, stream, p, blocks);
+    if (blocks <= kFewChunks) {
+        hipLaunchKernelGGL((move_kernel<false>), dim3(blocks, split), dim3(kMoveThreads), 0,
+                           stream, p, blocks);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL(scan_kernel, dim3(p.E + 1), dim3(256), 0, stream, p, blocks);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    hipLaunchKernelGGL((move_kernel<true>), dim3(blocks, split), dim3(kMoveThreads), 0, stream, p,
+                       blocks);
     return hipGetLastError();
 }
 
