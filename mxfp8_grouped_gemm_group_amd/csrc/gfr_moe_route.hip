@@ -13,7 +13,7 @@
 //   few tokens    one launch, one block per token: every block chooses for all
 //                 tokens (cheaper than a launch that hands the choice over) and
 //                 counts the pairs ahead of its own token's;
-//   more tokens   route_kernel (choice, counts per chunk of 8 tokens and
+//   more tokens   route_kernel (choice, counts per chunk of tokens and
 //                 expert), scan_kernel (a block per expert over the chunks; few
 //                 chunks are summed by each block of the next instead),
 //                 move_kernel (a block per chunk: ranks within it, rows).
@@ -30,8 +30,9 @@
 namespace gfr {
 namespace {
 
-constexpr int kChunk = 8;           // tokens per block of the long path
-constexpr int kFewTokens = 64;      // one-launch path up to here
+constexpr int kRouteWaves = 8;      // of a block of the long path, which takes
+constexpr int kMaxChunk = 16;       // at most so many tokens (a chunk)
+constexpr int kFewTokens = 16;      // one-launch path up to here
 constexpr int kFewChunks = 64;      // no scan launch up to here
 constexpr int kMoveThreads = 256;
 
@@ -150,20 +151,24 @@ __device__ __forceinline__ void keep_groups(const RouteParams &p, double (&key)[
     }
 }
 
-// A token's logits: lane l's V experts, -inf for what is not live.
+// A token's logits: lane l's V experts, -inf for what is not live.  (Loads
+// without a branch between them, at clamped places: under conditions the
+// compiler waits for each before the next.)
 template <int V>
 __device__ __forceinline__ void load_logits(const RouteParams &p, int t, int lane, float (&z)[V]) {
     const int64_t row = static_cast<int64_t>(t) * p.E;
+    if (p.logits_bf16) {
+        const uint16_t *at = static_cast<const uint16_t *>(p.logits) + row;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = lane * V + v;
-        z[v] = kNegInf;
-        if (e < p.E)
-            z[v] = p.logits_bf16 ? bf16_f32(static_cast<const uint16_t *>(p.logits)[row + e])
-                                 : static_cast<const float *>(p.logits)[row + e];
+        for (int v = 0; v < V; ++v) z[v] = bf16_f32(at[min(lane * V + v, p.E - 1)]);
+    } else {
+        const float *at = static_cast<const float *>(p.logits) + row;
+#pragma unroll
+        for (int v = 0; v < V; ++v) z[v] = at[min(lane * V + v, p.E - 1)];
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) z[v] = z[v] > kNegInf ? z[v] : kNegInf;   // NaN: not live
+    for (int v = 0; v < V; ++v)                        // NaN: not live
+        z[v] = lane * V + v < p.E && z[v] > kNegInf ? z[v] : kNegInf;
 }
 
 // The choice of one token: lane j < k returns its j-th expert (-1: none) and
@@ -182,17 +187,24 @@ __device__ __forceinline__ void choose(const RouteParams &p, const float (&z)[V]
         top = from_ordered(wave_max(m));
         if (top == kNegInf) top = 0.0f;
     }
+    float bias[V] = {};
+    if (WIDE && p.bias)
+#pragma unroll
+        for (int v = 0; v < V; ++v) bias[v] = p.bias[min(lane * V + v, p.E - 1)];
     K score[V];
     double sum = 0.0;
+    if (p.sigmoid) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        if (WIDE) {
-            const double d = z[v];
-            score[v] = p.sigmoid ? 1.0 / (1.0 + exp(-d)) : exp(d - top);
-        } else {
-            score[v] = p.sigmoid ? 1.0f / (1.0f + expf(-z[v])) : expf(z[v] - top);
+        for (int v = 0; v < V; ++v)
+            score[v] = WIDE ? static_cast<K>(1.0 / (1.0 + exp(-static_cast<double>(z[v]))))
+                            : static_cast<K>(1.0f / (1.0f + expf(-z[v])));
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            score[v] = WIDE ? static_cast<K>(exp(static_cast<double>(z[v]) - top))
+                            : static_cast<K>(expf(z[v] - top));
+            sum += score[v];
         }
-        sum += score[v];
     }
     // softmax's denominator; without FP64 keys and with renormalize it cancels
     K scale = 1;
@@ -210,8 +222,7 @@ __device__ __forceinline__ void choose(const RouteParams &p, const float (&z)[V]
         double key[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = lane * V + v;
-            const double d = score[v] + (p.bias && e < p.E ? p.bias[e] : 0.0f);
+            const double d = score[v] + bias[v];
             key[v] = z[v] > kNegInf && d > kNegInf ? d : kNegInf;
         }
         if (p.n_group > 1) keep_groups(p, key, s, lane);
@@ -408,7 +419,7 @@ __global__ __launch_bounds__(1024) void route_few_kernel(RouteParams p) {
 // A block's waves take `per_block` tokens; with counts, the pairs of the block
 // per expert (bucket E: pairs without one) go to counts[bucket][block].
 template <int V, bool WIDE>
-__global__ __launch_bounds__(64 * kChunk) void route_kernel(RouteParams p, int per_block) {
+__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteParams p, int per_block) {
     extern __shared__ double keys[];            // WIDE with groups: waves x E
     __shared__ int hist[GFR_MAX_EXPERTS + 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
@@ -465,13 +476,13 @@ __global__ __launch_bounds__(256) void scan_kernel(RouteParams p, int chunks) {
 // rank among the chunk's equals, then the rows.
 // SCANNED: scan_kernel ran; otherwise (few chunks) every block sums the counts.
 template <bool SCANNED>
-__global__ __launch_bounds__(kMoveThreads) void move_kernel(RouteParams p, int chunks) {
+__global__ __launch_bounds__(kMoveThreads) void move_kernel(RouteParams p, int chunk, int chunks) {
     __shared__ int start[GFR_MAX_EXPERTS + 1];
-    __shared__ int bucket[kChunk * GFR_MAX_TOPK];
-    __shared__ int pos[kChunk * GFR_MAX_TOPK];
+    __shared__ int bucket[kMaxChunk * GFR_MAX_TOPK];
+    __shared__ int pos[kMaxChunk * GFR_MAX_TOPK];
     __shared__ uint32_t totals[4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int t0 = blockIdx.x * kChunk, nt = min(kChunk, p.T - t0), n = nt * p.k;
+    const int t0 = blockIdx.x * chunk, nt = min(chunk, p.T - t0), n = nt * p.k;
     const int64_t q0 = static_cast<int64_t>(t0) * p.k;
     for (int i = threadIdx.x; i < n; i += kMoveThreads) {
         const int id = p.ids[q0 + i];
@@ -529,6 +540,10 @@ __global__ void clear_groups_kernel(int64_t *g, int n) {
     if (i < n) g[i] = 0;
 }
 
+// Tokens per chunk: one per wave while that spreads them over the CUs, two (half
+// the counts to scan) beyond.
+int64_t chunk_of(int64_t T) { return T <= 4096 ? 8 : kMaxChunk; }
+
 template <int V, bool WIDE>
 hipError_t launch_route_t(const RouteParams &p, hipStream_t stream) {
     const size_t keys = WIDE && p.n_group > 1 ? sizeof(double) * p.E : 0;
@@ -543,8 +558,8 @@ hipError_t launch_route_t(const RouteParams &p, hipStream_t stream) {
     }
     // the choice alone: single waves while they are few, so that each has a CU's
     // units to itself
-    const int per_block = p.x || p.T > 4096 ? kChunk : 1;
-    const int waves = per_block;
+    const int per_block = p.x || p.T > 4096 ? static_cast<int>(chunk_of(p.T)) : 1;
+    const int waves = per_block < kRouteWaves ? per_block : kRouteWaves;
     const int blocks = (p.T + per_block - 1) / per_block;
     constexpr auto kernel = &route_kernel<V, WIDE>;
     if (hipError_t e = allow_lds<kernel>(static_cast<int>(waves * keys)); e != hipSuccess) return e;
@@ -556,13 +571,13 @@ hipError_t launch_route_t(const RouteParams &p, hipStream_t stream) {
     while (blocks * split < 1024 && split * 2 <= pieces) split *= 2;
     if (blocks <= kFewChunks) {
         hipLaunchKernelGGL((move_kernel<false>), dim3(blocks, split), dim3(kMoveThreads), 0,
-                           stream, p, blocks);
+                           stream, p, per_block, blocks);
         return hipGetLastError();
     }
     hipLaunchKernelGGL(scan_kernel, dim3(p.E + 1), dim3(256), 0, stream, p, blocks);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     hipLaunchKernelGGL((move_kernel<true>), dim3(blocks, split), dim3(kMoveThreads), 0, stream, p,
-                       blocks);
+                       per_block, blocks);
     return hipGetLastError();
 }
 
@@ -580,7 +595,8 @@ hipError_t launch_route_v(const RouteParams &p, hipStream_t stream) {
 size_t route_workspace(int64_t T, int64_t E, int64_t k) {
     (void)k;
     if (T <= kFewTokens) return 0;
-    const size_t chunks = static_cast<size_t>(T + kChunk - 1) / kChunk;
+    const int64_t chunk = chunk_of(T);
+    const size_t chunks = static_cast<size_t>((T + chunk - 1) / chunk);
     return (chunks * (E + 1) * sizeof(int) + 255) & ~static_cast<size_t>(255);
 }
 
