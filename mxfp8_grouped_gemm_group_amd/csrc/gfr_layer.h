@@ -14,7 +14,7 @@ struct LinearParams {
     const void *bias;          // may be null
     const uint16_t *residual;  // may be null
     void *out;                 // [M, N]
-    float *partial;            // split K: [S][M][rows of w]
+    float *partial;            // split K: [split][M][columns, to a multiple of 8]
     int32_t bias_f32, out_f32, f16, act;
     int32_t wide;              // rows of out and residual are whole, aligned 16 bytes
     int32_t M, N, K, split;

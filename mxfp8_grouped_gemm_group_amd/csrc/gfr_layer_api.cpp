@@ -64,7 +64,8 @@ int resolve_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *b
 
 size_t linear_bytes(const gfr::LinearParams &p) {
     if (p.split <= 1 || p.M == 0 || p.N == 0) return 0;
-    const size_t rows = p.act == GFR_ACT_SWIGLU ? 2 * static_cast<size_t>(p.N) : p.N;
+    const size_t pitch = (static_cast<size_t>(p.N) + 7) / 8 * 8;
+    const size_t rows = p.act == GFR_ACT_SWIGLU ? 2 * pitch : pitch;
     return (sizeof(float) * p.split * p.M * rows + 255) & ~static_cast<size_t>(255);
 }
 

@@ -11,7 +11,8 @@
 //                bytes along K, straight into MFMA operands.
 //   tile kernel  more rows: BM x BN tiles, 64-K steps through LDS in two
 //                stages (the next step's loads are in flight in registers
-//                while the present one is multiplied).
+//                while the present one is multiplied).  Few tiles split K;
+//                a second launch then adds the partial sums and finishes.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -117,53 +118,71 @@ __device__ __forceinline__ float element(const void *p, int64_t i, bool f32, boo
     return f16 ? static_cast<float>(__builtin_bit_cast(_Float16, h)) : bf16_f32(h);
 }
 
-// Four columns n .. n + 3 of row m: activation (gate rows of swiglu in `gate`),
-// residual, rounding, store.  v already holds the sums; columns past N are
-// dropped.
+// y = act(v + bias) (swiglu: silu(gate + its bias) * (v + bias)) of column n.
 template <bool SWIGLU, bool F16>
-__device__ __forceinline__ void finish(const LinearParams &p, int m, int n, f4_t v, f4_t gate) {
-    const int64_t at = static_cast<int64_t>(m) * p.N + n;
-    const int cols = min(p.N - n, 4);
-    float y[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (p.bias && j < cols) {
-            v[j] += element(p.bias, n + j + (SWIGLU ? p.N : 0), p.bias_f32, F16);
-            if (SWIGLU) gate[j] += element(p.bias, n + j, p.bias_f32, F16);
-        }
-        y[j] = SWIGLU ? silu(gate[j]) * v[j] : activate(v[j], p.act);
+__device__ __forceinline__ float finish1(const LinearParams &p, int n, float v, float gate) {
+    if (p.bias) {
+        v += element(p.bias, n + (SWIGLU ? p.N : 0), p.bias_f32, F16);
+        if (SWIGLU) gate += element(p.bias, n, p.bias_f32, F16);
     }
-    if (cols == 4 && (p.N & 3) == 0) {     // rows of whole, aligned fours
-        if (p.residual) {
-            const u2_t h = load<u2_t>(p.residual + at);
+    return SWIGLU ? silu(gate) * v : activate(v, p.act);
+}
+
+template <bool F16>
+__device__ __forceinline__ void store1(const LinearParams &p, int64_t at, float y) {
+    if (p.out_f32)
+        static_cast<float *>(p.out)[at] = y;
+    else
+        static_cast<uint16_t *>(p.out)[at] = static_cast<uint16_t>(
+            F16 ? pack_f16(y, 0.0f) : pack_bf16(y, 0.0f));
+}
+
+// Eight finished columns (16-byte aligned rows: p.wide).
+template <bool F16>
+__device__ __forceinline__ void store8(const LinearParams &p, int64_t at, const float (&y)[8]) {
+    if (p.out_f32) {
+        float *out = static_cast<float *>(p.out) + at;
+        *reinterpret_cast<f4_t *>(out) = f4_t{y[0], y[1], y[2], y[3]};
+        *reinterpret_cast<f4_t *>(out + 4) = f4_t{y[4], y[5], y[6], y[7]};
+    } else {
+        u4_t h;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint16_t b = h[j >> 1] >> (16 * (j & 1));
-                y[j] += F16 ? static_cast<float>(__builtin_bit_cast(_Float16, b)) : bf16_f32(b);
-            }
-        }
-        if (p.out_f32) {
-            *reinterpret_cast<u2_t *>(static_cast<float *>(p.out) + at) =
-                u2_t{__float_as_uint(y[0]), __float_as_uint(y[1])};
-            *reinterpret_cast<u2_t *>(static_cast<float *>(p.out) + at + 2) =
-                u2_t{__float_as_uint(y[2]), __float_as_uint(y[3])};
-        } else {
-            *reinterpret_cast<u2_t *>(static_cast<uint16_t *>(p.out) + at) =
-                F16 ? u2_t{pack_f16(y[0], y[1]), pack_f16(y[2], y[3])}
-                    : u2_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
-        }
+        for (int j = 0; j < 4; ++j)
+            h[j] = F16 ? pack_f16(y[2 * j], y[2 * j + 1]) : pack_bf16(y[2 * j], y[2 * j + 1]);
+        *reinterpret_cast<u4_t *>(static_cast<uint16_t *>(p.out) + at) = h;
+    }
+}
+
+template <bool F16>
+__device__ __forceinline__ void add8(float (&y)[8], u4_t h) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint16_t b = h[j >> 1] >> (16 * (j & 1));
+        y[j] += F16 ? static_cast<float>(__builtin_bit_cast(_Float16, b)) : bf16_f32(b);
+    }
+}
+
+// Columns n .. n + 7 of row m, as far as they exist: the whole epilogue.
+template <bool SWIGLU, bool F16>
+__device__ __forceinline__ void finish8(const LinearParams &p, int m, int n, const float (&v)[8],
+                                        const float (&gate)[8]) {
+    const int64_t at = static_cast<int64_t>(m) * p.N + n;
+    if (p.wide) {
+        u4_t h = {0, 0, 0, 0};
+        if (p.residual) h = load<u4_t>(p.residual + at);
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = finish1<SWIGLU, F16>(p, n + j, v[j], gate[j]);
+        if (p.residual) add8<F16>(y, h);
+        store8<F16>(p, at, y);
         return;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (j >= cols) break;
-        if (p.residual) y[j] += element(p.residual, at + j, false, F16);
-        if (p.out_f32)
-            static_cast<float *>(p.out)[at + j] = y[j];
-        else
-            static_cast<uint16_t *>(p.out)[at + j] =
-                F16 ? static_cast<uint16_t>(pack_f16(y[j], 0.0f))
-                    : static_cast<uint16_t>(pack_bf16(y[j], 0.0f));
+    for (int j = 0; j < 8; ++j) {
+        if (n + j >= p.N) return;
+        float y = finish1<SWIGLU, F16>(p, n + j, v[j], gate[j]);
+        if (p.residual) y += element(p.residual, at + j, false, F16);
+        store1<F16>(p, at + j, y);
     }
 }
 
@@ -255,18 +274,22 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(LinearParams p) {
             for (int i = 0; i < 4; ++i)
                 tiles[wave][16 * q + 4 * g + i][16 * f + c] = acc[q][f][i];
     __syncthreads();
-    constexpr int kFours = SWIGLU ? 4 : kTile / 4;
+    constexpr int kCols = SWIGLU ? 16 : kTile;
     const int rows = min(p.M, 16 * RG);
-    for (int i = threadIdx.x; i < rows * kFours; i += kRowThreads) {
-        const int m = i / kFours, col = i % kFours * 4;
-        if (n0 + col >= p.N) continue;
-        f4_t v = {0, 0, 0, 0}, gate = {0, 0, 0, 0};
+    for (int i = threadIdx.x; i < rows * kCols; i += kRowThreads) {
+        const int m = i / kCols, col = i % kCols, n = n0 + col;
+        if (n >= p.N) continue;
+        const int64_t at = static_cast<int64_t>(m) * p.N + n;
+        const float r = p.residual ? element(p.residual, at, false, F16) : 0.0f;
+        float v = 0.0f, gate = 0.0f;
 #pragma unroll
         for (int w = 0; w < kRowWaves; ++w) {
-            v += *reinterpret_cast<const f4_t *>(&tiles[w][m][SWIGLU ? 16 + col : col]);
-            if (SWIGLU) gate += *reinterpret_cast<const f4_t *>(&tiles[w][m][col]);
+            v += tiles[w][m][SWIGLU ? 16 + col : col];
+            if (SWIGLU) gate += tiles[w][m][col];
         }
-        finish<SWIGLU, F16>(p, m, n0 + col, v, gate);
+        float y = finish1<SWIGLU, F16>(p, n, v, gate);
+        if (p.residual) y += r;
+        store1<F16>(p, at, y);
     }
 }
 
@@ -282,6 +305,13 @@ __device__ __forceinline__ f16_t mfma32(u4_t a, u4_t b, f16_t c) {
                                                       __builtin_bit_cast(h8_t, b), c, 0, 0, 0);
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8_t, a),
                                                    __builtin_bit_cast(bf8_t, b), c, 0, 0, 0);
+}
+
+// LDS bytes of a tile: two stages, or the waves' rows of the epilogue.
+constexpr int tile_lds(int bm, int bn, int wm, int wn, bool swiglu) {
+    const int stages = 2 * (bm + bn) * 8 * 16;
+    const int rows = bm / wm * (bn / wn) * (32 * (wn + 4) + 16 * (swiglu ? wn / 2 : wn)) * 4;
+    return stages > rows ? stages : rows;
 }
 
 // Every LDS access of this wave has finished, then the other waves' too.  (As
@@ -361,10 +391,13 @@ void tile_kernel(LinearParams p, int tiles_m, int tiles_n) {
     // rows a multiple of 8 apart share their swizzle
     u4_t *const put_at = lds + row0 * 8 + (piece ^ (row0 & 7));
     u4_t xs[kNX], ws[kNW];
-    const int steps = (p.K + 63) / 64;
+    // this block's steps: all, or a K split's
+    const int all = (p.K + 63) / 64, sp = blockIdx.y;
+    const int s0 = all * sp / p.split, steps = all * (sp + 1) / p.split - s0;
     // x's or w's pieces of a step (behind the last step: zeros)
     auto fetch = [&](auto &to, const auto &offs, auto which, int step) {
         constexpr int n = sizeof(to) / sizeof(to[0]);
+        step += s0;
         const int off = step * 128, valid = p.K - step * 64 - 8 * piece;
 #pragma unroll
         for (int i = 0; i < n; ++i) {
@@ -450,7 +483,7 @@ void tile_kernel(LinearParams p, int tiles_m, int tiles_n) {
     constexpr int kPitch = WN + 4;     // spreads the rows over the banks
     constexpr int kCols = SWIGLU ? WN / 2 : WN;
     constexpr int kSlab = 32 * kPitch + 16 * kCols;    // floats: sums, then residual rows
-    static_assert(kWaves * kSlab * 4 <= 2 * kStage * 16, "the waves' rows fit the stages");
+    static_assert(kWaves * kSlab * 4 <= tile_lds(BM, BN, WM, WN, SWIGLU), "the waves' rows fit");
     float *slab = reinterpret_cast<float *>(lds) + wave * kSlab;
     u4_t *res_at = reinterpret_cast<u4_t *>(slab + 32 * kPitch);
     const int col0 = n0 + (SWIGLU ? wn / 2 : wn);
@@ -468,6 +501,32 @@ void tile_kernel(LinearParams p, int tiles_m, int tiles_n) {
         __builtin_amdgcn_wave_barrier();
     };
     lds_barrier();
+    if (p.split > 1) {
+        // partial sums [split][M][gate,] up, eight-column rows
+        const int pitch = (p.N + 7) / 8 * 8, width = SWIGLU ? 2 * pitch : pitch;
+        constexpr int kLanes = kCols / 8, kRows = 64 / kLanes;
+        const int er = lane / kLanes, col = lane % kLanes * 8, n = col0 + col;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int first = m0 + wm + 32 * i;
+            if (first >= p.M) break;
+            put_sums(i);
+            wave_sync();
+#pragma unroll 2
+            for (int r = er; r < 32; r += kRows) {
+                if (first + r >= p.M || n >= p.N) continue;
+                float *to = p.partial + (static_cast<int64_t>(sp) * p.M + first + r) * width + n;
+                const float *at = slab + r * kPitch + (SWIGLU ? (col >> 5) * 64 + (col & 31) : col);
+#pragma unroll
+                for (int h = 0; h < (SWIGLU ? 2 : 1); ++h)
+#pragma unroll
+                    for (int j = 0; j < 8; j += 4)
+                        *reinterpret_cast<f4_t *>(to + h * pitch + j) = load<f4_t>(at + 32 * h + j);
+            }
+            wave_sync();
+        }
+        return;
+    }
     if (p.wide) {
         // Eight columns per lane, the same ones in every row it takes: their
         // bias is loaded once, and the next 32 rows' residual while these are
@@ -527,33 +586,20 @@ void tile_kernel(LinearParams p, int tiles_m, int tiles_n) {
                     }
                 }
                 if (!SWIGLU) activate8(y, p.act);
-                if (p.residual) {
-                    const u4_t h = res_at[k * 64 + lane];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint16_t b = h[j >> 1] >> (16 * (j & 1));
-                        y[j] += F16 ? static_cast<float>(__builtin_bit_cast(_Float16, b))
-                                    : bf16_f32(b);
-                    }
-                }
-                const int64_t o = static_cast<int64_t>(m) * p.N + n;
-                if (p.out_f32) {
-                    float *out = static_cast<float *>(p.out) + o;
-                    *reinterpret_cast<f4_t *>(out) = f4_t{y[0], y[1], y[2], y[3]};
-                    *reinterpret_cast<f4_t *>(out + 4) = f4_t{y[4], y[5], y[6], y[7]};
-                } else {
-                    u4_t h;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        h[j] = F16 ? pack_f16(y[2 * j], y[2 * j + 1])
-                                   : pack_bf16(y[2 * j], y[2 * j + 1]);
-                    *reinterpret_cast<u4_t *>(static_cast<uint16_t *>(p.out) + o) = h;
-                }
+                if (p.residual) add8<F16>(y, res_at[k * 64 + lane]);
+                store8<F16>(p, static_cast<int64_t>(m) * p.N + n, y);
             }
             wave_sync();
         }
         return;
     }
+    // Rows that begin anywhere: a column per lane, eight rows' residual ahead.
+    static_assert(kCols <= 64, "a lane keeps its column");
+    constexpr int kRows = 64 / kCols, kTurns = 32 / kRows;
+    const int er = lane / kCols, col = lane % kCols, n = col0 + col;
+    const bool in = n < p.N;
+    const float bias = p.bias && in ? element(p.bias, n + (SWIGLU ? p.N : 0), p.bias_f32, F16) : 0;
+    const float gate_bias = SWIGLU && p.bias && in ? element(p.bias, n, p.bias_f32, F16) : 0;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int first = m0 + wm + 32 * i;
@@ -561,16 +607,61 @@ void tile_kernel(LinearParams p, int tiles_m, int tiles_n) {
         put_sums(i);
         wave_sync();
 #pragma unroll 1
-        for (int o = lane; o < 32 * (kCols / 4); o += 64) {
-            const int r = o / (kCols / 4), col = o % (kCols / 4) * 4;
-            if (first + r >= p.M || col0 + col >= p.N) continue;
-            const float *at = slab + r * kPitch + (SWIGLU ? (col >> 5) * 64 + (col & 31) : col);
-            const f4_t v = *reinterpret_cast<const f4_t *>(at + (SWIGLU ? 32 : 0));
-            const f4_t gate = *reinterpret_cast<const f4_t *>(at);
-            finish<SWIGLU, F16>(p, first + r, col0 + col, v, gate);
+        for (int k = 0; k < kTurns; k += 8) {
+            float y[8];
+            uint16_t res[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int64_t m = min(first + (k + j) * kRows + er, p.M - 1);
+                res[j] = 0;
+                if (p.residual && in) res[j] = p.residual[m * p.N + n];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float *at = slab + ((k + j) * kRows + er) * kPitch;
+                if (SWIGLU) {
+                    const int c0 = (col >> 5) * 64 + (col & 31);
+                    y[j] = silu(at[c0] + gate_bias) * (at[c0 + 32] + bias);
+                } else {
+                    y[j] = at[col] + bias;
+                }
+            }
+            if (!SWIGLU) activate8(y, p.act);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int m = first + (k + j) * kRows + er;
+                if (m >= p.M || !in) continue;
+                if (p.residual)
+                    y[j] += F16 ? static_cast<float>(__builtin_bit_cast(_Float16, res[j]))
+                                : bf16_f32(res[j]);
+                store1<F16>(p, static_cast<int64_t>(m) * p.N + n, y[j]);
+            }
         }
         wave_sync();
     }
+}
+
+// Adds up a split's partial sums, in order, and finishes eight columns.
+template <bool SWIGLU, bool F16>
+__global__ __launch_bounds__(256) void join_kernel(LinearParams p) {
+    const int pitch = (p.N + 7) / 8 * 8, width = SWIGLU ? 2 * pitch : pitch;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= static_cast<int64_t>(p.M) * (pitch / 8)) return;
+    const int m = static_cast<int>(i / (pitch / 8)), n = static_cast<int>(i % (pitch / 8)) * 8;
+    const float *at = p.partial + static_cast<int64_t>(m) * width + n;
+    const int64_t plane = static_cast<int64_t>(p.M) * width;
+    f4_t v[2] = {}, gate[2] = {};
+#pragma unroll 2
+    for (int s = 0; s < p.split; ++s, at += plane)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            v[h] += load<f4_t>(at + (SWIGLU ? pitch : 0) + 4 * h);
+            if (SWIGLU) gate[h] += load<f4_t>(at + 4 * h);
+        }
+    const float a[8] = {v[0][0], v[0][1], v[0][2], v[0][3], v[1][0], v[1][1], v[1][2], v[1][3]};
+    const float g[8] = {gate[0][0], gate[0][1], gate[0][2], gate[0][3],
+                        gate[1][0], gate[1][1], gate[1][2], gate[1][3]};
+    finish8<SWIGLU, F16>(p, m, n, a, g);
 }
 
 template <bool F16, bool ALIGNED, bool SWIGLU, int RG>
@@ -584,29 +675,79 @@ hipError_t launch_rows(const LinearParams &p, hipStream_t stream) {
 
 template <bool F16, bool ALIGNED, bool SWIGLU, int BM, int BN, int WM, int WN>
 hipError_t launch_tiles(const LinearParams &p, hipStream_t stream) {
-    constexpr int lds = 2 * (BM + BN) * 8 * 16;
+    constexpr int lds = tile_lds(BM, BN, WM, WN, SWIGLU);
     constexpr int cols = SWIGLU ? BN / 2 : BN;
     constexpr auto kernel = &tile_kernel<F16, ALIGNED, SWIGLU, BM, BN, WM, WN>;
     if (hipError_t e = allow_lds<kernel>(lds); e != hipSuccess) return e;
     const int tm = (p.M + BM - 1) / BM, tn = (p.N + cols - 1) / cols;
     const int64_t grid = (static_cast<int64_t>(tm) * tn + 7) / 8 * 8;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)),
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid), p.split),
                        dim3((BM / WM) * (BN / WN) * 64), lds, stream, p, tm, tn);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess || p.split == 1) return e;
+    const int64_t eights = static_cast<int64_t>(p.M) * ((p.N + 7) / 8);
+    hipLaunchKernelGGL((join_kernel<SWIGLU, F16>), dim3(static_cast<uint32_t>((eights + 255) / 256)),
+                       dim3(256), 0, stream, p);
     return hipGetLastError();
+}
+
+// The kernel for a size and its K split, by estimated time: rounds of 256 blocks
+// times a block's time per 64-K step (measured at K = 4096: a larger tile feeds
+// more MFMAs per byte brought to the CU), and for a split the partial sums'
+// traffic at 4 TB/s and the joining launch.
+struct Choice {
+    enum Kind { kRows, k256, k256x128, k128, k64 } kind;
+    int split;
+};
+Choice choose_kernel(int64_t M, int64_t N, int64_t K, bool swiglu) {
+    if (M <= 64) return {Choice::kRows, 1};
+    const int64_t rows = swiglu ? 2 * N : N, steps = (K + 63) / 64;
+    const bool aligned = K % 8 == 0;
+    struct Tile {
+        Choice::Kind kind;
+        int64_t bm, bn;
+        double us;     // per step
+    };
+    const Tile tiles[] = {{Choice::k256, 256, 256, 1.65},
+                          {Choice::k256x128, 256, 128, 0.95},
+                          {Choice::k128, 128, 128, 0.62},
+                          {Choice::k64, 64, swiglu ? 128 : 64, swiglu ? 0.42 : 0.28}};
+    Choice best{Choice::k64, 1};
+    double least = 1e30;
+    for (const Tile &t : tiles) {
+        if (!aligned && (t.kind == Choice::k256 || t.kind == Choice::k256x128)) continue;
+        const int64_t n = ((M + t.bm - 1) / t.bm) * ((rows + t.bn - 1) / t.bn);
+        for (int split = 1; split <= (t.kind == Choice::k128 ? 8 : 1); ++split) {
+            if (split > 1 && (steps / split < 6 || n * split > 256)) break;
+            const double rounds = static_cast<double>((n * split + 255) / 256);
+            double us = rounds * (4.0 + t.us * static_cast<double>((steps + split - 1) / split));
+            if (split > 1) us += 4.0 + 8.0 * static_cast<double>(M * rows * split) / 4e6;
+            if (us < least) least = us, best = {t.kind, split};
+        }
+    }
+    return best;
 }
 
 template <bool F16, bool ALIGNED, bool SWIGLU>
 hipError_t launch_linear_t(const LinearParams &p, hipStream_t stream) {
-    if (p.M <= 16) return launch_rows<F16, ALIGNED, SWIGLU, 1>(p, stream);
-    if (p.M <= 32) return launch_rows<F16, ALIGNED, SWIGLU, 2>(p, stream);
-    if (p.M <= 64) return launch_rows<F16, ALIGNED, SWIGLU, 4>(p, stream);
-    const int64_t cols = SWIGLU ? 128 : 256;
-    const int64_t big = ((p.M + 255) / 256) * ((p.N + cols - 1) / cols);
-    if (ALIGNED && big >= 192)
-        return launch_tiles<F16, ALIGNED, SWIGLU, 256, 256, 128, 64>(p, stream);
-    const int64_t mid = ((p.M + 127) / 128) * ((p.N + cols / 2 - 1) / (cols / 2));
-    if (mid >= 128) return launch_tiles<F16, ALIGNED, SWIGLU, 128, 128, 64, 64>(p, stream);
-    return launch_tiles<F16, ALIGNED, SWIGLU, 64, SWIGLU ? 128 : 64, 32, SWIGLU ? 64 : 32>(p, stream);
+    switch (choose_kernel(p.M, p.N, p.K, SWIGLU).kind) {
+    case Choice::kRows:
+        if (p.M <= 16) return launch_rows<F16, ALIGNED, SWIGLU, 1>(p, stream);
+        if (p.M <= 32) return launch_rows<F16, ALIGNED, SWIGLU, 2>(p, stream);
+        return launch_rows<F16, ALIGNED, SWIGLU, 4>(p, stream);
+    case Choice::k256:
+        if constexpr (ALIGNED)
+            return launch_tiles<F16, ALIGNED, SWIGLU, 256, 256, 128, 64>(p, stream);
+        return hipErrorInvalidValue;
+    case Choice::k256x128:
+        if constexpr (ALIGNED)
+            return launch_tiles<F16, ALIGNED, SWIGLU, 256, 128, 64, 64>(p, stream);
+        return hipErrorInvalidValue;
+    case Choice::k128:
+        return launch_tiles<F16, ALIGNED, SWIGLU, 128, 128, 64, 64>(p, stream);
+    default:
+        return launch_tiles<F16, ALIGNED, SWIGLU, 64, SWIGLU ? 128 : 64, 32, SWIGLU ? 64 : 32>(
+            p, stream);
+    }
 }
 
 template <bool F16, bool ALIGNED>
@@ -618,8 +759,7 @@ hipError_t launch_linear_a(const LinearParams &p, hipStream_t stream) {
 }  // namespace
 
 int linear_split(int64_t M, int64_t N, int64_t K, int act) {
-    (void)M, (void)N, (void)K, (void)act;
-    return 1;
+    return choose_kernel(M, N, K, act == GFR_ACT_SWIGLU).split;
 }
 
 hipError_t launch_linear(const LinearParams &p, hipStream_t stream) {
