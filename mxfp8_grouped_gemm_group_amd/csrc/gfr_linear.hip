@@ -17,6 +17,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gfr.h"
 #include "gfr_device.h"
 #include "gfr_layer.h"
@@ -346,7 +348,7 @@ __device__ __forceinline__ void spread() {
 //
 // A step is four 16-K parts.  While one part's MFMAs run, the next part's
 // fragments come from LDS.  The next step's tile, loaded to registers three parts
-// earlier, is written to the other stage during parts 1 (x) and 2 (w), and each
+// (or a step and three parts) earlier, is written to the other stage during parts 1 (x) and 2 (w), and each
 // half's loads of the step after it follow at once.  The one barrier stands
 // before part 3, whose fragments are in registers by then: behind it the other
 // stage is complete, and nobody reads this one any more.
@@ -390,7 +392,10 @@ void tile_kernel(LinearParams p, int tiles_m, int tiles_n) {
     }
     // rows a multiple of 8 apart share their swizzle
     u4_t *const put_at = lds + row0 * 8 + (piece ^ (row0 & 7));
-    u4_t xs[kNX], ws[kNW];
+    // Steps' tiles on their way: two where the registers leave room (a step of
+    // the smaller tiles is shorter than a load takes).
+    constexpr int D = BM * BN < 256 * 256 ? 2 : 1;
+    u4_t xs[D][kNX], ws[D][kNW];
     // this block's steps: all, or a K split's
     const int all = (p.K + 63) / 64, sp = blockIdx.y;
     const int s0 = all * sp / p.split, steps = all * (sp + 1) / p.split - s0;
@@ -410,9 +415,11 @@ void tile_kernel(LinearParams p, int tiles_m, int tiles_n) {
                                               : eight_tail<false>(r, offs[i], off, valid);
         }
     };
-    auto fetch_x = [&](int step) { fetch(xs, x_off, [&](int) { return xr; }, step); };
-    auto fetch_w = [&](int step) {
-        fetch(ws, w_off, [&](int i) { return is_up(i) ? ur : wr; }, step);
+    auto fetch_x = [&](auto set, int step) {
+        fetch(xs[set], x_off, [&](int) { return xr; }, step);
+    };
+    auto fetch_w = [&](auto set, int step) {
+        fetch(ws[set], w_off, [&](int i) { return is_up(i) ? ur : wr; }, step);
     };
     const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
     const u4_t *const x_at = lds + (wm + c) * 8, *const w_at = lds + (BM + wn + c) * 8;
@@ -433,41 +440,56 @@ void tile_kernel(LinearParams p, int tiles_m, int tiles_n) {
             for (int j = 0; j < FN; ++j)
                 acc[i][j] = mfma32<F16>(b[from][j], a[from][i], acc[i][j]);
     };
-    auto put_x = [&](int stage) {
+    auto put_x = [&](auto set, int stage) {
 #pragma unroll
-        for (int i = 0; i < kNX; ++i) put_at[stage * kStage + kRowsPer * 8 * i] = xs[i];
+        for (int i = 0; i < kNX; ++i) put_at[stage * kStage + kRowsPer * 8 * i] = xs[set][i];
     };
-    auto put_w = [&](int stage) {
+    auto put_w = [&](auto set, int stage) {
 #pragma unroll
-        for (int i = 0; i < kNW; ++i) put_at[stage * kStage + (BM + kRowsPer * i) * 8] = ws[i];
+        for (int i = 0; i < kNW; ++i) put_at[stage * kStage + (BM + kRowsPer * i) * 8] = ws[set][i];
     };
-    fetch_x(0);
-    fetch_w(0);
-    put_x(0);
-    put_w(0);
-    fetch_x(1);
-    fetch_w(1);
+    const std::integral_constant<int, 0> s0_{};
+    const std::integral_constant<int, D - 1> s1_{};
+    fetch_x(s0_, 0);
+    fetch_w(s0_, 0);
+    if (D == 2) fetch_x(s1_, 1), fetch_w(s1_, 1);
+    put_x(s0_, 0);
+    put_w(s0_, 0);
+    fetch_x(s0_, D);
+    fetch_w(s0_, D);
     lds_barrier();
     get(0, 0, 0);
-    for (int step = 0; step + 1 < steps; ++step) {
+    // One step; the next one's tile is in set `next`, which then takes the one D
+    // steps behind that.
+    auto run_step = [&](int step, auto next) {
         const int cur = step & 1;
         get(1, cur, 1);
         multiply(0);
         spread<FM * FN, FM + FN, 0, 0>();
         get(0, cur, 2);
-        put_x(cur ^ 1);
+        put_x(next, cur ^ 1);
         multiply(1);
         spread<FM * FN, FM + FN, kNX, 0>();
         get(1, cur, 3);
-        fetch_x(step + 2);
-        put_w(cur ^ 1);
+        fetch_x(next, step + 1 + D);
+        put_w(next, cur ^ 1);
         multiply(0);
         spread<FM * FN, FM + FN, kNW, kNX>();
         lds_barrier();
         get(0, cur ^ 1, 0);
-        fetch_w(step + 2);
+        fetch_w(next, step + 1 + D);
         multiply(1);
         spread<FM * FN, FM + FN, 0, kNW>();
+    };
+    if (D == 1) {
+        for (int step = 0; step + 1 < steps; ++step) run_step(step, s0_);
+    } else {
+        int step = 0;
+        for (; step + 2 < steps; step += 2) {
+            run_step(step, s1_);
+            run_step(step + 1, s0_);
+        }
+        if (step + 1 < steps) run_step(step, s1_);
     }
     const int cur = (steps - 1) & 1;
     get(1, cur, 1);
