@@ -40,6 +40,7 @@ struct DecodeParams {
     int32_t *status;           // may be null
     float *gu;                 // [gate_up.chunks][T k][2I]: partial sums of x w13
     float *y;                  // [down.chunks][T k][N]: partial sums of h w2
+    uint16_t *h;               // [2][T k][I]: silu(gate) * up as two bf16 terms, or null
     int64_t s13_e, s2_e;       // bytes between experts' scales (0: shared)
     float shared_w;
     int32_t out_f32;
@@ -50,7 +51,8 @@ struct DecodeParams {
 // Workspace layout of moe_decode (256-byte aligned regions) and the products'
 // shapes.
 struct DecodeLayout {
-    size_t gu, y, total;
+    size_t gu, y, h, total;
+    bool activate;             // h is made by a launch of its own
     DecodePart gate_up, down;
 };
 DecodeLayout decode_layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int64_t N,

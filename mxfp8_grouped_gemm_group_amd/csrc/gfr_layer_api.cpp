@@ -183,6 +183,7 @@ int gfr_moe_decode(const gfr_tensor *x, const gfr_tensor *w13, const gfr_tensor 
     p.status = opts->status_dev;
     p.gu = reinterpret_cast<float *>(ws + d.gu);
     p.y = reinterpret_cast<float *>(ws + d.y);
+    p.h = d.activate ? reinterpret_cast<uint16_t *>(ws + d.h) : nullptr;
     p.gate_up = d.gate_up;
     p.down = d.down;
     p.T = static_cast<int32_t>(T);

@@ -164,28 +164,18 @@ __device__ __forceinline__ void add8(float (&y)[8], u4_t h) {
     }
 }
 
-// Columns n .. n + 7 of row m, as far as they exist: the whole epilogue.
+// Columns n .. n + 7 of row m (p.wide): the whole epilogue.
 template <bool SWIGLU, bool F16>
 __device__ __forceinline__ void finish8(const LinearParams &p, int m, int n, const float (&v)[8],
                                         const float (&gate)[8]) {
     const int64_t at = static_cast<int64_t>(m) * p.N + n;
-    if (p.wide) {
-        u4_t h = {0, 0, 0, 0};
-        if (p.residual) h = load<u4_t>(p.residual + at);
-        float y[8];
+    u4_t h = {0, 0, 0, 0};
+    if (p.residual) h = load<u4_t>(p.residual + at);
+    float y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = finish1<SWIGLU, F16>(p, n + j, v[j], gate[j]);
-        if (p.residual) add8<F16>(y, h);
-        store8<F16>(p, at, y);
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (n + j >= p.N) return;
-        float y = finish1<SWIGLU, F16>(p, n + j, v[j], gate[j]);
-        if (p.residual) y += element(p.residual, at + j, false, F16);
-        store1<F16>(p, at + j, y);
-    }
+    for (int j = 0; j < 8; ++j) y[j] = finish1<SWIGLU, F16>(p, n + j, v[j], gate[j]);
+    if (p.residual) add8<F16>(y, h);
+    store8<F16>(p, at, y);
 }
 
 // ---------------------------------------------------------------------------
@@ -663,11 +653,29 @@ void tile_kernel(LinearParams p, int tiles_m, int tiles_n) {
     }
 }
 
-// Adds up a split's partial sums, in order, and finishes eight columns.
+// Adds up a split's partial sums, in order, and finishes eight columns per thread
+// (one where rows begin anywhere).
 template <bool SWIGLU, bool F16>
 __global__ __launch_bounds__(256) void join_kernel(LinearParams p) {
     const int pitch = (p.N + 7) / 8 * 8, width = SWIGLU ? 2 * pitch : pitch;
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (!p.wide) {
+        if (i >= static_cast<int64_t>(p.M) * p.N) return;
+        const int m = static_cast<int>(i / p.N), n = static_cast<int>(i % p.N);
+        const float *at = p.partial + static_cast<int64_t>(m) * width + n;
+        const int64_t plane = static_cast<int64_t>(p.M) * width;
+        const float r = p.residual ? element(p.residual, i, false, F16) : 0.0f;
+        float v = 0.0f, gate = 0.0f;
+#pragma unroll 2
+        for (int s = 0; s < p.split; ++s, at += plane) {
+            v += at[SWIGLU ? pitch : 0];
+            if (SWIGLU) gate += at[0];
+        }
+        float y = finish1<SWIGLU, F16>(p, n, v, gate);
+        if (p.residual) y += r;
+        store1<F16>(p, i, y);
+        return;
+    }
     if (i >= static_cast<int64_t>(p.M) * (pitch / 8)) return;
     const int m = static_cast<int>(i / (pitch / 8)), n = static_cast<int>(i % (pitch / 8)) * 8;
     const float *at = p.partial + static_cast<int64_t>(m) * width + n;
@@ -706,9 +714,9 @@ hipError_t launch_tiles(const LinearParams &p, hipStream_t stream) {
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid), p.split),
                        dim3((BM / WM) * (BN / WN) * 64), lds, stream, p, tm, tn);
     if (hipError_t e = hipGetLastError(); e != hipSuccess || p.split == 1) return e;
-    const int64_t eights = static_cast<int64_t>(p.M) * ((p.N + 7) / 8);
-    hipLaunchKernelGGL((join_kernel<SWIGLU, F16>), dim3(static_cast<uint32_t>((eights + 255) / 256)),
-                       dim3(256), 0, stream, p);
+    const int64_t threads = static_cast<int64_t>(p.M) * (p.wide ? (p.N + 7) / 8 : p.N);
+    hipLaunchKernelGGL((join_kernel<SWIGLU, F16>),
+                       dim3(static_cast<uint32_t>((threads + 255) / 256)), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 

@@ -481,6 +481,17 @@ __global__ __launch_bounds__(kThreads, 2) void product_kernel(DecodeParams p) {
             *reinterpret_cast<u4_t *>(lds + r * pitch + 2 * k) =
                 k < real ? load<u4_t>(p.x + t * p.H + k0 + k) : u4_t{0, 0, 0, 0};
         }
+    } else if (p.h) {
+        const int64_t plane = static_cast<int64_t>(n) * p.I;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < count * (width / 8); i += kThreads) {
+            const int r = i / (width / 8), k = i % (width / 8) * 8;
+            const uint16_t *at = p.h + static_cast<int64_t>(plan.pairs[first + r]) * p.I + k0 + k;
+            u4_t hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
+            if (k < real) hi = load<u4_t>(at), lo = load<u4_t>(at + plane);
+            *reinterpret_cast<u4_t *>(lds + r * pitch + 2 * k) = hi;
+            *reinterpret_cast<u4_t *>(lds + (R + r) * pitch + 2 * k) = lo;
+        }
     } else {
         const int64_t plane = static_cast<int64_t>(n) * 2 * p.I;
         const int last = p.gate_up.chunks - 1;
@@ -534,6 +545,27 @@ __global__ __launch_bounds__(kThreads, 2) void product_kernel(DecodeParams p) {
                 tile += kWaves;
             }
         }
+}
+
+// h = silu(gate) * up as two bf16 terms, once for all blocks of the down product.
+__global__ __launch_bounds__(kThreads) void activate_kernel(DecodeParams p) {
+    const int64_t n = static_cast<int64_t>(p.T) * p.k, fours = p.I / 4;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (i >= n * fours) return;
+    const int64_t q = i / fours, k = i % fours * 4;
+    const int id = p.ids[q];
+    if (id < 0 || id >= p.E) return;             // nothing wrote, or reads, its row
+    const float *at = p.gu + q * 2 * p.I + k;
+    f4_t gate = {0, 0, 0, 0}, up = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = 0; s < p.gate_up.chunks; ++s, at += n * 2 * p.I) {
+        gate += load<f4_t>(at);
+        up += load<f4_t>(at + p.I);
+    }
+    u2_t hi, lo;
+    two_terms(gate, up, hi, lo);
+    *reinterpret_cast<u2_t *>(p.h + q * p.I + k) = hi;
+    *reinterpret_cast<u2_t *>(p.h + (n + q) * p.I + k) = lo;
 }
 
 // out[t, n .. n + 3] = sum over t's pairs j and y's chunks s of weight[t, j]
@@ -656,6 +688,12 @@ hipError_t launch_decode_t(const DecodeParams &p, int t13, int t2, hipStream_t s
     hipError_t e = t13 ? launch_product<StreamNK<FMT, KL>, RG, 1>(p, stream)
                        : launch_product<StreamKN<FMT>, RG, 1>(p, stream);
     if (e != hipSuccess) return e;
+    if (p.h) {
+        const int64_t fours = static_cast<int64_t>(p.T) * p.k * (p.I / 4);
+        hipLaunchKernelGGL(activate_kernel, dim3(static_cast<uint32_t>((fours + kThreads - 1) / kThreads)),
+                           dim3(kThreads), 0, stream, p);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
     e = t2 ? launch_product<StreamNK<FMT, KL>, RG, 2>(p, stream)
            : launch_product<StreamKN<FMT>, RG, 2>(p, stream);
     if (e != hipSuccess) return e;
@@ -680,7 +718,12 @@ DecodeLayout decode_layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I
     d.down = part_shape(groups, I, N, transpose_w2, rg, 2);
     d.gu = 0;
     d.y = up(sizeof(float) * d.gate_up.chunks * pairs * 2 * I);
-    d.total = d.y + up(sizeof(float) * d.down.chunks * pairs * N);
+#ifndef ACT
+#define ACT 32
+#endif
+    d.h = d.y + up(sizeof(float) * d.down.chunks * pairs * N);
+    d.activate = pairs >= ACT;
+    d.total = d.h + (d.activate ? up(sizeof(uint16_t) * 2 * pairs * I) : 0);
     return d;
 }
 
