@@ -25,9 +25,9 @@ int linear_split(int64_t M, int64_t N, int64_t K, int act);
 hipError_t launch_linear(const LinearParams &p, hipStream_t stream);
 
 // One of moe_decode's two products: the K chunks whose partial sums are kept
-// apart, and the column tiles each wave of a block takes.
+// apart, the column tiles each wave of a block takes, and its waves.
 struct DecodePart {
-    int32_t chunks, run;
+    int32_t chunks, run, waves;
 };
 
 struct DecodeParams {

@@ -1,4 +1,5 @@
-// The experts of a MoE block for a few tokens, in three launches.
+// The experts of a MoE block for a few tokens, in three launches (four from
+// kActivatePairs pairs on).
 // include/gfr.h states the operator.
 //
 // At these token counts the bytes of the chosen experts' weights bound the
@@ -38,10 +39,14 @@
 namespace gfr {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
+constexpr int kMaxWaves = 8;               // of a block of product_kernel
+constexpr int kSumThreads = 256;           // of the small kernels
 constexpr int kMaxPairs = 1024;
-constexpr int kOperandBytes = 64 << 10;    // of LDS for a chunk's operand rows
+// From this many pairs on h is made once, by a launch of its own, for the down
+// product's blocks, which otherwise each form their rows of it: 96 pairs of 8
+// experts 145 -> 135 us, 256 pairs 137 -> 113, but 8 pairs 21 -> 23.
+constexpr int kActivatePairs = 32;
+constexpr int kOperandBytes = 16 << 10;    // of LDS per wave, for a chunk's operand rows
 
 // ---------------------------------------------------------------------------
 // Plan: the pairs grouped by expert.  Every block makes its own from the ids
@@ -54,7 +59,7 @@ constexpr int kOperandBytes = 64 << 10;    // of LDS for a chunk's operand rows
 struct Plan {
     int start[GFR_MAX_EXPERTS];        // counts, then first index into pairs
     uint16_t pairs[kMaxPairs];         // grouped by expert
-    uint32_t totals[kWaves];
+    uint32_t totals[kMaxWaves];
     int expert, first, count;          // this block's group
 };
 constexpr int kMaskWords = kMaxPairs / 32;
@@ -92,9 +97,10 @@ __device__ __forceinline__ bool make_small_plan(const DecodeParams &p, Plan &s, 
 
 // Fills `s` for group `mine`; false if there are fewer groups.  `mask`: kMaskBytes
 // of LDS that nothing else uses meanwhile.
-template <int R>
+template <int R, int kWaves>
 __device__ __forceinline__ bool make_plan(const DecodeParams &p, Plan &s, uint32_t *mask,
                                           int mine) {
+    constexpr int kThreads = 64 * kWaves;
     constexpr int kPer = kMaxPairs / kThreads, kExperts = GFR_MAX_EXPERTS / kThreads;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n = p.T * p.k;
@@ -418,8 +424,9 @@ __device__ __forceinline__ void two_terms(f4_t gate, f4_t up, u2_t &hi, u2_t &lo
 // Partial sums of a K chunk.  TERMS = 1: operand x, out gu [chunks][pairs][2I];
 // TERMS = 2: operand h from gu, out y [chunks][pairs][N].  Grid: (column runs,
 // chunks, groups).
-template <class Stream, int RG, int TERMS>
-__global__ __launch_bounds__(kThreads, 2) void product_kernel(DecodeParams p) {
+template <class Stream, int RG, int TERMS, int kWaves>
+__global__ __launch_bounds__(64 * kWaves, 2) void product_kernel(DecodeParams p) {
+    constexpr int kThreads = 64 * kWaves;
     // (aligned: 16-byte accesses to LDS at odd words take about twice as long)
     extern __shared__ __align__(16) uint8_t lds[];
     __shared__ __align__(16) Plan plan;
@@ -428,7 +435,7 @@ __global__ __launch_bounds__(kThreads, 2) void product_kernel(DecodeParams p) {
     if (p.T * p.k <= 64) {
         if (!make_small_plan<R>(p, plan, blockIdx.z, e, first, count)) return;
     } else {
-        if (!make_plan<R>(p, plan, reinterpret_cast<uint32_t *>(lds), blockIdx.z)) return;
+        if (!make_plan<R, kWaves>(p, plan, reinterpret_cast<uint32_t *>(lds), blockIdx.z)) return;
         e = uniform(plan.expert), first = uniform(plan.first), count = uniform(plan.count);
     }
     const DecodePart &d = TERMS == 1 ? p.gate_up : p.down;
@@ -548,9 +555,9 @@ __global__ __launch_bounds__(kThreads, 2) void product_kernel(DecodeParams p) {
 }
 
 // h = silu(gate) * up as two bf16 terms, once for all blocks of the down product.
-__global__ __launch_bounds__(kThreads) void activate_kernel(DecodeParams p) {
+__global__ __launch_bounds__(kSumThreads) void activate_kernel(DecodeParams p) {
     const int64_t n = static_cast<int64_t>(p.T) * p.k, fours = p.I / 4;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kSumThreads + threadIdx.x;
     if (i >= n * fours) return;
     const int64_t q = i / fours, k = i % fours * 4;
     const int id = p.ids[q];
@@ -572,8 +579,8 @@ __global__ __launch_bounds__(kThreads) void activate_kernel(DecodeParams p) {
 // y[s][t k + j], plus the shared term.  A block takes 128 columns of a token:
 // eight slices of the (j, s) terms at a time, so that the loads of one token's
 // few columns run side by side; then the slices in order.
-constexpr int kSlices = 8, kFours = kThreads / kSlices;
-__global__ __launch_bounds__(kThreads) void combine_kernel(DecodeParams p) {
+constexpr int kSlices = 8, kFours = kSumThreads / kSlices;
+__global__ __launch_bounds__(kSumThreads) void combine_kernel(DecodeParams p) {
     __shared__ float weight[GFR_MAX_TOPK];
     __shared__ int live[GFR_MAX_TOPK];
     __shared__ f4_t part[kSlices][kFours];
@@ -622,10 +629,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(DecodeParams p) {
 // enough for the second reading of its weights to matter; one otherwise.
 int row_fragments(int64_t T, int64_t k, int64_t E) {
     const int64_t mean = T * k / E;
-#ifndef MEAN
-#define MEAN 8
-#endif
-    return T <= 16 || mean <= MEAN ? 1 : 2;
+    return T <= 16 || mean <= 8 ? 1 : 2;
 }
 
 // Groups of the plan, at most.
@@ -637,34 +641,42 @@ int64_t max_groups(int64_t pairs, int64_t E, int rg) {
 // Lines of K per [N, K] step (StreamNK's KL).
 constexpr int lines(int rg) { return rg == 1 ? 2 : 1; }
 
-// Chunks and runs of one product.  As few chunks as the LDS allows; runs as
-// long as leaves kBlocks blocks; if even runs of one tile per wave are fewer,
-// more chunks, down to two steps.
-DecodePart part_shape(double groups, int64_t K, int64_t cols, int transpose, int rg, int terms) {
-#ifndef KBL
-#define KBL 448
-#endif
-    const double kBlocks = rg == 1 ? 768 : KBL;
+// Chunks, runs and waves of one product.  As few chunks as the LDS allows; runs as
+// long as leaves enough blocks; if even runs of one tile per wave are fewer, more
+// chunks.  Blocks of eight waves, one to a CU, hold chunks twice as wide as two
+// of four waves, which halves the partial sums and the operand's reading: worth
+// it where a group has rows enough for that to count and blocks are many (64
+// tokens of 32 experts, 4096 x 8192: 577 -> 518 us; 8 tokens of 16, 157 -> 172).
+DecodePart part_shape(double groups, double rows, int64_t K, int64_t cols, int transpose, int rg,
+                      int terms) {
     const int64_t step = transpose ? 128 * lines(rg) : 64;
     const int64_t tile = transpose ? 64 / lines(rg) : 128;
     const int64_t steps = (K + step - 1) / step, tiles = (cols + tile - 1) / tile;
-    const int64_t wide = kOperandBytes / (2 * terms * 16 * rg) / step;   // steps per chunk, most
-    int64_t chunks = (steps + wide - 1) / wide;
-    int64_t run = static_cast<int64_t>(groups * chunks * tiles / (kWaves * kBlocks));
-    if (run < 1) {
-        run = 1;
-        const double blocks = groups * ((tiles + kWaves - 1) / kWaves);
-        while (blocks * chunks < kBlocks && steps / (chunks + 1) >= (transpose ? 1 : 2) && chunks < 8) ++chunks;
+    DecodePart d{};
+    for (int waves : {4, 8}) {
+        const double blocks = (rg == 1 ? 3072.0 : 1792.0) / waves;   // wanted
+        // steps per chunk, at most
+        const int64_t wide = kOperandBytes * waves / (2 * terms * 16 * rg) / step;
+        int64_t chunks = (steps + wide - 1) / wide;
+        const double runs = groups * chunks * tiles / (waves * blocks);
+        if (waves == 8 && (rows < 4.0 || d.run * d.chunks == 0)) break;
+        int64_t run = static_cast<int64_t>(runs);
+        const bool enough = run >= 1;
+        if (!enough) {
+            run = 1;
+            const double got = groups * ((tiles + waves - 1) / waves);
+            while (got * chunks < blocks && steps / (chunks + 1) >= (transpose ? 1 : 2) &&
+                   chunks < 8)
+                ++chunks;
+        }
+        const int64_t most = (tiles + waves - 1) / waves;
+        d = {static_cast<int32_t>(chunks), static_cast<int32_t>(run < most ? run : most), waves};
+        if (!enough) break;
     }
-    const int64_t most = (tiles + kWaves - 1) / kWaves;
-    if (run > most) run = most;
-    DecodePart d;
-    d.chunks = static_cast<int32_t>(chunks);
-    d.run = static_cast<int32_t>(run);
     return d;
 }
 
-template <class Stream, int RG, int TERMS>
+template <class Stream, int RG, int TERMS, int kWaves>
 hipError_t launch_product(const DecodeParams &p, hipStream_t stream) {
     const DecodePart &d = TERMS == 1 ? p.gate_up : p.down;
     const int K = TERMS == 1 ? p.H : p.I, cols = TERMS == 1 ? 2 * p.I : p.N;
@@ -674,31 +686,39 @@ hipError_t launch_product(const DecodeParams &p, hipStream_t stream) {
     const int lds = operand > kMaskBytes ? operand : kMaskBytes;
     const int tiles = (cols + Stream::kTile - 1) / Stream::kTile;
     const int runs = (tiles + d.run * kWaves - 1) / (d.run * kWaves);
-    constexpr auto kernel = &product_kernel<Stream, RG, TERMS>;
+    constexpr auto kernel = &product_kernel<Stream, RG, TERMS, kWaves>;
     if (hipError_t e = allow_lds<kernel>(lds); e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel,
                        dim3(runs, d.chunks, static_cast<uint32_t>(max_groups(p.T * p.k, p.E, RG))),
-                       dim3(kThreads), lds, stream, p);
+                       dim3(64 * kWaves), lds, stream, p);
     return hipGetLastError();
+}
+
+template <int FMT, int RG, int TERMS>
+hipError_t launch_product_any(const DecodeParams &p, int transpose, hipStream_t stream) {
+    typedef StreamNK<FMT, lines(RG)> NK;
+    typedef StreamKN<FMT> KN;
+    if ((TERMS == 1 ? p.gate_up : p.down).waves == 8)
+        return transpose ? launch_product<NK, RG, TERMS, 8>(p, stream)
+                         : launch_product<KN, RG, TERMS, 8>(p, stream);
+    return transpose ? launch_product<NK, RG, TERMS, 4>(p, stream)
+                     : launch_product<KN, RG, TERMS, 4>(p, stream);
 }
 
 template <int FMT, int RG>
 hipError_t launch_decode_t(const DecodeParams &p, int t13, int t2, hipStream_t stream) {
-    constexpr int KL = lines(RG);
-    hipError_t e = t13 ? launch_product<StreamNK<FMT, KL>, RG, 1>(p, stream)
-                       : launch_product<StreamKN<FMT>, RG, 1>(p, stream);
+    hipError_t e = launch_product_any<FMT, RG, 1>(p, t13, stream);
     if (e != hipSuccess) return e;
     if (p.h) {
         const int64_t fours = static_cast<int64_t>(p.T) * p.k * (p.I / 4);
-        hipLaunchKernelGGL(activate_kernel, dim3(static_cast<uint32_t>((fours + kThreads - 1) / kThreads)),
-                           dim3(kThreads), 0, stream, p);
+        hipLaunchKernelGGL(activate_kernel, dim3(static_cast<uint32_t>((fours + kSumThreads - 1) / kSumThreads)),
+                           dim3(kSumThreads), 0, stream, p);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    e = t2 ? launch_product<StreamNK<FMT, KL>, RG, 2>(p, stream)
-           : launch_product<StreamKN<FMT>, RG, 2>(p, stream);
+    e = launch_product_any<FMT, RG, 2>(p, t2, stream);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(combine_kernel, dim3((p.N + 4 * kFours - 1) / (4 * kFours), p.T),
-                       dim3(kThreads), 0, stream, p);
+                       dim3(kSumThreads), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -712,17 +732,14 @@ DecodeLayout decode_layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I
     const int rg = row_fragments(T, k, E);
     // experts that get a pair if the choice is even, each with its rows' groups
     double groups = E * (1.0 - pow(1.0 - 1.0 / E, static_cast<double>(pairs)));
-    const double rows = pairs / (groups * 16 * rg);
-    if (rows > 1.0) groups *= rows;
-    d.gate_up = part_shape(groups, H, 2 * I, transpose_w13, rg, 1);
-    d.down = part_shape(groups, I, N, transpose_w2, rg, 2);
+    const double full = pairs / (groups * 16 * rg);
+    if (full > 1.0) groups *= full;
+    d.gate_up = part_shape(groups, pairs / groups, H, 2 * I, transpose_w13, rg, 1);
+    d.down = part_shape(groups, pairs / groups, I, N, transpose_w2, rg, 2);
     d.gu = 0;
     d.y = up(sizeof(float) * d.gate_up.chunks * pairs * 2 * I);
-#ifndef ACT
-#define ACT 32
-#endif
     d.h = d.y + up(sizeof(float) * d.down.chunks * pairs * N);
-    d.activate = pairs >= ACT;
+    d.activate = pairs >= kActivatePairs;
     d.total = d.h + (d.activate ? up(sizeof(uint16_t) * 2 * pairs * I) : 0);
     return d;
 }
