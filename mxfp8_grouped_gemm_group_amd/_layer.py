@@ -136,14 +136,14 @@ def linear(x, w, bias=None, *, activation="none", residual=None, out_dtype=None,
                           out_dtype=out_dtype, out=out, workspace=workspace)
     if out is None:
         n = w.shape[0] // 2 if act == 5 else w.shape[0]
-        out = torch.empty((x.shape[0], n), dtype=out_dtype or x.dtype, device=x.device)
+        out = x.new_empty((x.shape[0], n), dtype=out_dtype or x.dtype)
     tensors, handle = (x, w, bias, residual, out), _raw_stream(index)
     words, (px, pw, pb, pr, po), opts = _pack(index, tensors, workspace)
     rc = lib.gfr_linear(px, pw, pb, pr, act, po, handle, opts)
     if rc == WORKSPACE_TOO_SMALL and workspace is None:
         need = ctypes.c_size_t(0)
         _check(lib.gfr_linear_workspace_size(px, pw, pb, pr, act, po, ctypes.byref(need)))
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+        workspace = x.new_empty(need.value, dtype=torch.uint8)
         words, (px, pw, pb, pr, po), opts = _pack(index, tensors, workspace)
         rc = lib.gfr_linear(px, pw, pb, pr, act, po, handle, opts)
     _check(rc)
@@ -194,10 +194,10 @@ def moe_decode(x, w13, scale13, w2, scale2, topk_ids, topk_weights, *, transpose
         I, N = N, I
     t13, t2 = int(bool(transpose_w13)), int(bool(transpose_w2))
     if out is None:
-        out = torch.empty((x.shape[0], N), dtype=out_dtype, device=x.device)
+        out = x.new_empty((x.shape[0], N), dtype=out_dtype)
     if workspace is None:
-        workspace = torch.empty(moe_decode_workspace_size(T, k, E, x.shape[1], I, N, t13, t2),
-                                dtype=torch.uint8, device=x.device)
+        workspace = x.new_empty(moe_decode_workspace_size(T, k, E, x.shape[1], I, N, t13, t2),
+                                dtype=torch.uint8)
     words, at, opts = _pack(index, (x, w13, scale13, w2, scale2, topk_ids, topk_weights,
                                     shared_input, out), workspace, status)
     _check(lib.gfr_moe_decode(*at[:8], float(shared_input_weight), at[8], t13, t2,
@@ -249,21 +249,20 @@ def moe_route(logits, top_k, *, x=None, bias=None, scoring="softmax", n_group=1,
             return moe_route(logits, top_k, x=x, bias=bias, scoring=scoring, n_group=n_group,
                              topk_group=topk_group, renormalize=renormalize, scaling=scaling,
                              out_dtype=out_dtype, workspace=workspace)
-    dev = logits.device
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    empty = logits.new_empty
+    ids, weights = empty((T, k), dtype=torch.int32), empty((T, k), dtype=torch.float32)
     rows = (None,) * 5
     if x is not None:
         H, n = x.shape[1], T * k
-        rows = (torch.empty((n, H), dtype=out_dtype, device=dev),
-                torch.empty((n, (H + 63) // 64, 2), dtype=torch.uint8, device=dev),
-                torch.empty(E, dtype=torch.int64, device=dev),
-                torch.empty(n, dtype=torch.int32, device=dev),
-                torch.empty(n, dtype=torch.float32, device=dev))
+        rows = (empty((n, H), dtype=out_dtype),
+                empty((n, (H + 63) // 64, 2), dtype=torch.uint8),
+                empty(E, dtype=torch.int64),
+                empty(n, dtype=torch.int32),
+                empty(n, dtype=torch.float32))
         if workspace is None:
             need = _route_workspace_size(T, E, k)
             if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                workspace = empty(need, dtype=torch.uint8)
     words, at, opts = _pack(index, (logits, bias, ids, weights, x, *rows), workspace)
     _check(lib.gfr_moe_route(at[0], at[1], score, int(n_group), int(topk_group),
                              int(bool(renormalize)), float(scaling), *at[2:],

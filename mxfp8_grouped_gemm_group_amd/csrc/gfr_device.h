@@ -64,6 +64,20 @@ __device__ __forceinline__ uint32_t dpp(uint32_t old, uint32_t x) {
         static_cast<int>(old), static_cast<int>(x), CTRL, ROWS, BANKS, BOUND));
 }
 
+// a of lanes l % 16 >= 8 and b of the others trade places, across eight lanes: of
+// 16 rows' 128-byte lines, loaded as a = rows 0-7 (lane (c, g): row c % 8, 16-byte
+// piece g + 4 (c / 8)) and b = rows 8-15 likewise, lane (c, g) then holds pieces g
+// (a) and 4 + g (b) of row c, the operands of two 16-row MFMAs.  Loading those as
+// such would touch 16 half lines at a time.
+__device__ __forceinline__ void swap_halves(u4_t &a, u4_t &b) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t x = a[j], y = b[j];
+        a[j] = dpp<0x128, 0xf, 0xc, false>(x, y);
+        b[j] = dpp<0x128, 0xf, 0x3, false>(y, x);
+    }
+}
+
 // Inclusive prefix sum over the 64 lanes: DPP row shifts, then the row totals
 // broadcast into the rows behind them.
 __device__ __forceinline__ uint32_t wave_prefix(uint32_t v) {

@@ -194,7 +194,7 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(LinearParams p) {
     const int n0 = blockIdx.x * (SWIGLU ? 16 : kTile);
     const int64_t bytes = 2 * static_cast<int64_t>(p.K);   // of a row
     rsrc_t wr[NF];
-    int w_off[NF], x_off[RG];
+    int w_off[NF][2], x_off[RG];
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
         // the fragment's rows; rows past the end read the last one
@@ -202,7 +202,12 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(LinearParams p) {
         const int at = min(first, last);
         const int skew = weight_rows<ALIGNED>(p, SWIGLU && f ? p.N + at : at, last - at + 1,
                                               wr[f]);
-        w_off[f] = min(c, last - at) * static_cast<int>(bytes) + 16 * g + skew;
+        // whole lines, swapped into operands (swap_halves), or each lane's own piece
+        for (int b = 0; b < 2; ++b)
+            w_off[f][b] = ALIGNED ? min((c & 7) + 8 * b, last - at) * static_cast<int>(bytes) +
+                                        16 * (g + 4 * (c >> 3))
+                                  : min(c, last - at) * static_cast<int>(bytes) + 16 * g +
+                                        64 * b + skew;
     }
     const rsrc_t xr = buffer(p.x, p.M * bytes);
 #pragma unroll
@@ -220,13 +225,16 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(LinearParams p) {
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int f = 0; f < NF; ++f)
-                s.w[f][h] = eight<ALIGNED, kNt>(wr[f], w_off[f], step * 128 + 64 * h);
+                s.w[f][h] = eight<ALIGNED, kNt>(wr[f], w_off[f][h], step * 128);
 #pragma unroll
             for (int q = 0; q < RG; ++q)
                 s.x[q][h] = eight<ALIGNED, 0>(xr, x_off[q], step * 128 + 64 * h);
         }
     };
-    auto use = [&](const Stage &s) {
+    auto use = [&](Stage &s, bool swapped) {
+        if (ALIGNED && swapped)
+#pragma unroll
+            for (int f = 0; f < NF; ++f) swap_halves(s.w[f][0], s.w[f][1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -242,21 +250,27 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(LinearParams p) {
 #pragma unroll
         for (int d = 0; d < kDepth; ++d)
             if (s + d < s1) {
-                use(st[d]);
+                use(st[d], true);
                 if (s + d + kDepth < s1) fetch(st[d], s + d + kDepth);
             }
     if (wave == kRowWaves - 1 && p.K % 64 != 0) {
+        int own_off[NF];       // this lane's own pieces
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+            own_off[f] = min(c, p.N - 1 - min(SWIGLU ? n0 : n0 + 16 * f, p.N - 1)) *
+                             static_cast<int>(bytes) + 16 * g;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int valid = p.K - (64 * steps + 32 * h + 8 * g);
 #pragma unroll
             for (int f = 0; f < NF; ++f)
-                st[0].w[f][h] = eight_tail<ALIGNED>(wr[f], w_off[f], steps * 128 + 64 * h, valid);
+                st[0].w[f][h] = eight_tail<ALIGNED>(
+                    wr[f], ALIGNED ? own_off[f] : w_off[f][0], steps * 128 + 64 * h, valid);
 #pragma unroll
             for (int q = 0; q < RG; ++q)
                 st[0].x[q][h] = eight_tail<ALIGNED>(xr, x_off[q], steps * 128 + 64 * h, valid);
         }
-        use(st[0]);
+        use(st[0], false);
     }
 #pragma unroll
     for (int q = 0; q < RG; ++q)

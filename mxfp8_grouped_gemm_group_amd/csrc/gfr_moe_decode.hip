@@ -295,15 +295,13 @@ struct StreamKN {
 };
 
 // Weights [N, K]: a step is KL 128-byte lines of columns 16 f + r, f < NF = 4 /
-// KL; accumulator f holds columns 16 f + r for fragment rows r.  The MFMA wants
-// 16-byte pieces g and 4 + g of column c's line in lane (c, g).  Loading them so
-// would touch 16 half lines at a time; instead one load takes columns 0-7's whole
-// lines and one columns 8-15's, and the lanes with c < 8 swap what is not theirs
-// with those eight further (one DPP move per word).  The step's scales of column
-// c, eight 16-bit pairs, are read two to a lane and handed round, for the same
-// reason.
-// KL = 2 with one row fragment (16 experts of 4096 x 6144, 8 tokens: 156 us;
-// KL = 1 185, KL = 4 170), 1 with two, whose operand reads a wider tile shares.
+// KL, loaded whole and swapped into operands (swap_halves); accumulator f holds
+// columns 16 f + r for fragment rows r.  The step's scales of column c, eight
+// 16-bit pairs, are read two to a lane and handed round: a load per fragment and
+// half would touch as many lines as the weights do.  (16 experts of 4096 x 6144, 8
+// tokens: half-line loads and scale loads apart 237 us, scales handed round 175,
+// whole lines 157.)  KL = 2 with one row fragment (there: KL = 1 185 us, KL = 4
+// 170), 1 with two, whose operand reads a wider tile shares.
 template <int FMT, int KL>
 struct StreamNK {
     static constexpr bool kKN = false;
@@ -331,15 +329,6 @@ struct StreamNK {
 #pragma unroll
         for (int v = 0; v < 2; ++v)
             f.s[v] = load2(a.sc, a.sc_off, n0 * (a.ld >> 5) + (k0 >> 5) + 2 * v);
-    }
-    // Swaps lanes c < 8's second words with lanes c + 8's first.
-    static __device__ __forceinline__ void swap_halves(u4_t &a, u4_t &b) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t x = a[j], y = b[j];
-            a[j] = dpp<0x128, 0xf, 0xc, false>(x, y);
-            b[j] = dpp<0x128, 0xf, 0x3, false>(y, x);
-        }
     }
     template <int RG, int TERMS>
     static __device__ __forceinline__ void use(Stage &f, const Operand &x, int k, int left,
