@@ -393,8 +393,8 @@ enum gfr_activation {
  * N = 0 is a no-op.  The sizes fix the summation order: two calls give the
  * same bits.  Errors:
  * GFR_ERR_NULL_ARG, GFR_ERR_BAD_DTYPE, GFR_ERR_BAD_RANK, GFR_ERR_BAD_SHAPE,
- * GFR_ERR_BAD_ARG (activation), GFR_ERR_UNSUPPORTED (M, N or K >= 2^31, or K >
- * 2^21), GFR_ERR_BAD_ALIGNMENT (x or w not 16-byte, bias, residual or out not
+ * GFR_ERR_BAD_ARG (activation), GFR_ERR_UNSUPPORTED (M or w's rows > 2^30, K >
+ * 2^21, or more than 2^23 - 8 tiles), GFR_ERR_BAD_ALIGNMENT (x or w not 16-byte, bias, residual or out not
  * 8-byte aligned, workspace not 256), GFR_ERR_WORKSPACE_TOO_SMALL, GFR_ERR_HIP.
  */
 int gfr_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *bias,
@@ -413,7 +413,7 @@ int gfr_linear_workspace_size(const gfr_tensor *x, const gfr_tensor *w, const gf
 
 /*
  * gfr_moe_decode — the expert part of a MoE block for at most
- * GFR_DECODE_MAX_TOKENS tokens, in three launches:
+ * GFR_DECODE_MAX_TOKENS tokens, in three launches (four from 32 pairs on):
  *
  *   gate, up  = x[t] @ w13[e]                      e = topk_ids[t, j]
  *   out[t]    = sum_j topk_weights[t, j] * ((silu(gate) * up) @ w2[e])
@@ -434,7 +434,7 @@ int gfr_linear_workspace_size(const gfr_tensor *x, const gfr_tensor *w, const gf
  *  topk_ids      I32 [T, k], 1 <= k <= GFR_MAX_TOPK, each in [0, E), or -1 for
  *                no expert.  Other values are skipped and set
  *                GFR_DEV_BAD_EXPERT.  An expert named twice counts twice.
- *  topk_weights  F32 [T, k]; those of skipped pairs are not read.
+ *  topk_weights  F32 [T, k]; those of skipped pairs are not used.
  *  shared_input  BF16 [T, N], or NULL; shared_input_weight its factor.
  *  out           BF16 or F32 [T, N]; overwritten (a token without an expert
  *                gets the shared term, or zero).
@@ -504,10 +504,11 @@ enum gfr_scoring { GFR_SCORE_SOFTMAX = 0, GFR_SCORE_SIGMOID = 1 };
  *                the other fields are ignored.
  *
  * Needs 1 <= k <= GFR_MAX_TOPK, k <= E <= GFR_MAX_EXPERTS, E divisible by
- * n_group, 1 <= topk_group <= n_group <= 64, T k < 2^31 (GFR_ERR_BAD_ARG or
- * GFR_ERR_UNSUPPORTED); x, xin 16-byte aligned, logits, topk_ids, topk_weights,
- * row_index, logit 4-byte, group_list 8-byte (GFR_ERR_BAD_ALIGNMENT).  T = 0 clears group_list and does nothing
- * else.  Other errors as gfr_linear.
+ * n_group, 1 <= topk_group <= n_group <= 64, T <= 2^26, T k < 2^31 (GFR_ERR_BAD_ARG
+ * or GFR_ERR_UNSUPPORTED); x, xin 16-byte aligned, logits, topk_ids,
+ * topk_weights, row_index, logit 4-byte, group_list 8-byte
+ * (GFR_ERR_BAD_ALIGNMENT).  T = 0 clears group_list and does nothing else.
+ * Other errors as gfr_linear.
  */
 int gfr_moe_route(const gfr_tensor *logits, const gfr_tensor *bias, int scoring, int n_group,
                   int topk_group, int renormalize, float scaling, const gfr_tensor *topk_ids,

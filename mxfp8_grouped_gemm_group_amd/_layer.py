@@ -163,8 +163,8 @@ def moe_decode_workspace_size(T: int, k: int, E: int, H: int, I: int, N: int,
 def moe_decode(x, w13, scale13, w2, scale2, topk_ids, topk_weights, *, transpose_w13=False,
                transpose_w2=False, shared_input=None, shared_input_weight=1.0,
                out_dtype=torch.bfloat16, out=None, workspace=None, status=None, stream=None):
-    """The experts of a MoE block for at most DECODE_MAX_TOKENS tokens, in three
-    launches (include/gfr.h, gfr_moe_decode); returns out.
+    """The experts of a MoE block for at most DECODE_MAX_TOKENS tokens
+    (include/gfr.h, gfr_moe_decode); returns out.
 
     out[t] = sum_j topk_weights[t, j] * swiglu(x[t] @ w13[e]) @ w2[e]
              + shared_input_weight * shared_input[t],   e = topk_ids[t, j]

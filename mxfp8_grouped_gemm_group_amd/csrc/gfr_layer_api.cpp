@@ -11,6 +11,9 @@
 
 namespace {
 
+// Of moe_route: 16 a block of 512 threads, and a grid has at most 2^32 threads.
+constexpr int64_t kMaxTokens = int64_t{1} << 26;
+
 // Workspace of `need` bytes in opts.
 int check_workspace(const gfr_options *opts, size_t need) {
     if (need == 0) return GFR_OK;
@@ -39,7 +42,8 @@ int resolve_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *b
         GFR_TRY(check_desc(residual, {2}, {x->dtype}));
         if (!shape_is(residual, {M, N})) return GFR_ERR_BAD_SHAPE;
     }
-    if (M > kMaxRows || rows > kMaxRows || K > int64_t{1} << 21) return GFR_ERR_UNSUPPORTED;
+    if (M > int64_t{1} << 30 || rows > int64_t{1} << 30 || K > int64_t{1} << 21)
+        return GFR_ERR_UNSUPPORTED;
     if (!aligned(x->data, 16) || !aligned(w->data, 16) || !aligned(out->data, 8) ||
         (present(bias) && !aligned(bias->data, 8)) ||
         (present(residual) && !aligned(residual->data, 8)))
@@ -59,7 +63,7 @@ int resolve_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *b
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);
     p.split = gfr::linear_split(M, N, K, activation);
-    return GFR_OK;
+    return p.split > 0 ? GFR_OK : GFR_ERR_UNSUPPORTED;
 }
 
 size_t linear_bytes(const gfr::LinearParams &p) {
@@ -201,7 +205,7 @@ int gfr_moe_decode(const gfr_tensor *x, const gfr_tensor *w13, const gfr_tensor 
 int gfr_moe_route_workspace_size(int64_t T, int64_t E, int64_t k, size_t *bytes) {
     if (!bytes) return GFR_ERR_NULL_ARG;
     if (T < 0 || E < 1 || k < 1 || k > E) return GFR_ERR_BAD_SHAPE;
-    if (E > GFR_MAX_EXPERTS || k > GFR_MAX_TOPK || T > kMaxRows || T * k > kMaxRows)
+    if (E > GFR_MAX_EXPERTS || k > GFR_MAX_TOPK || T > kMaxTokens || T * k > kMaxRows)
         return GFR_ERR_UNSUPPORTED;
     *bytes = gfr::route_workspace(T, E, k);
     return GFR_OK;
@@ -227,7 +231,7 @@ int gfr_moe_route(const gfr_tensor *logits, const gfr_tensor *bias, int scoring,
         if (!shape_is(bias, {E})) return GFR_ERR_BAD_SHAPE;
         if (!aligned(bias->data, 4)) return GFR_ERR_BAD_ALIGNMENT;
     }
-    if (E > GFR_MAX_EXPERTS || k > GFR_MAX_TOPK || T > kMaxRows || T * k > kMaxRows)
+    if (E > GFR_MAX_EXPERTS || k > GFR_MAX_TOPK || T > kMaxTokens || T * k > kMaxRows)
         return GFR_ERR_UNSUPPORTED;
     if (n_group < 1 || n_group > 64 || E % n_group != 0 || topk_group < 1 || topk_group > n_group)
         return GFR_ERR_BAD_ARG;

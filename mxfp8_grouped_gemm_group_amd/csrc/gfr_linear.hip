@@ -1,18 +1,22 @@
 // Dense product with bias, activation and residual in its epilogue.
 // include/gfr.h states the operator.
 //
-// Both kernels run v_mfma_f32_16x16x32 on bf16 or f16 with FP32 sums, and apply
-// the epilogue to the sums in registers or LDS, so nothing but the result goes
-// to memory.
+// Both kernels multiply bf16 or f16 on the matrix cores with FP32 sums and apply
+// the epilogue to the sums in LDS, so nothing but the result goes to memory.
 //
-//   row kernel   up to 64 rows.  The weights' bytes bound it: a block takes
-//                16 or 32 columns (a gate and an up fragment for swiglu), its
-//                waves split K, and the sums meet in LDS; a lane reads 16
-//                bytes along K, straight into MFMA operands.
-//   tile kernel  more rows: BM x BN tiles, 64-K steps through LDS in two
-//                stages (the next step's loads are in flight in registers
-//                while the present one is multiplied).  Few tiles split K;
-//                a second launch then adds the partial sums and finishes.
+//   row kernel   up to 64 rows of a short K, v_mfma_f32_16x16x32.  The weights' bytes bound
+//                it: a block takes 16 columns (for swiglu their gate and up
+//                rows), its waves split K, and the sums meet in LDS; a lane
+//                reads 16 bytes along K, straight into MFMA operands.  (Gate/up
+//                of 4096 x 6144 with 5 rows, 101 MB: 22.1 us, 4.6 TB/s.)
+//   tile kernel  more rows, v_mfma_f32_32x32x16: BM x BN tiles, 64-K steps
+//                through LDS in two stages (the next step's loads are in flight
+//                in registers while the present one is multiplied).  What a CU
+//                takes in from L2 and LDS bounds it, so tiles are as large as
+//                the size fills 256 CUs with.  (4096 x 7168 x 4096 with
+//                residual: 235 us, 1.02 PFLOP/s.)  Few tiles split K; a second
+//                launch then adds the partial sums and finishes.  (128 x 4096 x
+//                4096: 18 us split eight ways, 29 us not split.)
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -184,29 +188,30 @@ __device__ __forceinline__ void finish8(const LinearParams &p, int m, int n, con
 constexpr int kRowThreads = 512;
 constexpr int kRowWaves = kRowThreads / 64;
 
-// RG fragments of 16 rows, NF of 16 weight rows (swiglu: NF = 2, gate and up).
+// RG fragments of 16 rows, NF of 16 weight rows (1, or 2 for swiglu: gate and up).
+// Weight lines come whole and are swapped into operands: half lines took 25.3 us
+// where whole ones take 22.1 (gate/up of 4096 x 6144, 5 rows).
 template <bool F16, bool ALIGNED, bool SWIGLU, int RG, int NF>
 __global__ __launch_bounds__(kRowThreads) void row_kernel(LinearParams p) {
+    static_assert(NF == (SWIGLU ? 2 : 1), "16 columns a block");
     constexpr int kTile = 16 * NF, kDepth = RG == 1 ? 4 : RG == 2 ? 3 : 2;
     __shared__ float tiles[kRowWaves][16 * RG][kTile];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-    const int n0 = blockIdx.x * (SWIGLU ? 16 : kTile);
+    const int n0 = blockIdx.x * 16;
     const int64_t bytes = 2 * static_cast<int64_t>(p.K);   // of a row
     rsrc_t wr[NF];
     int w_off[NF][2], x_off[RG];
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
-        // the fragment's rows; rows past the end read the last one
-        const int first = SWIGLU ? n0 : n0 + 16 * f, last = p.N - 1;
-        const int at = min(first, last);
-        const int skew = weight_rows<ALIGNED>(p, SWIGLU && f ? p.N + at : at, last - at + 1,
-                                              wr[f]);
+        // (columns past the end read the last one's row)
+        const int last = p.N - 1 - n0;
+        const int skew = weight_rows<ALIGNED>(p, f ? int64_t{n0} + p.N : n0, last + 1, wr[f]);
         // whole lines, swapped into operands (swap_halves), or each lane's own piece
         for (int b = 0; b < 2; ++b)
-            w_off[f][b] = ALIGNED ? min((c & 7) + 8 * b, last - at) * static_cast<int>(bytes) +
+            w_off[f][b] = ALIGNED ? min((c & 7) + 8 * b, last) * static_cast<int>(bytes) +
                                         16 * (g + 4 * (c >> 3))
-                                  : min(c, last - at) * static_cast<int>(bytes) + 16 * g +
+                                  : min(c, last) * static_cast<int>(bytes) + 16 * g +
                                         64 * b + skew;
     }
     const rsrc_t xr = buffer(p.x, p.M * bytes);
@@ -254,18 +259,14 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(LinearParams p) {
                 if (s + d + kDepth < s1) fetch(st[d], s + d + kDepth);
             }
     if (wave == kRowWaves - 1 && p.K % 64 != 0) {
-        int own_off[NF];       // this lane's own pieces
-#pragma unroll
-        for (int f = 0; f < NF; ++f)
-            own_off[f] = min(c, p.N - 1 - min(SWIGLU ? n0 : n0 + 16 * f, p.N - 1)) *
-                             static_cast<int>(bytes) + 16 * g;
+        const int own_off = min(c, p.N - 1 - n0) * static_cast<int>(bytes) + 16 * g;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int valid = p.K - (64 * steps + 32 * h + 8 * g);
 #pragma unroll
             for (int f = 0; f < NF; ++f)
                 st[0].w[f][h] = eight_tail<ALIGNED>(
-                    wr[f], ALIGNED ? own_off[f] : w_off[f][0], steps * 128 + 64 * h, valid);
+                    wr[f], ALIGNED ? own_off : w_off[f][0], steps * 128 + 64 * h, valid);
 #pragma unroll
             for (int q = 0; q < RG; ++q)
                 st[0].x[q][h] = eight_tail<ALIGNED>(xr, x_off[q], steps * 128 + 64 * h, valid);
@@ -280,10 +281,9 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(LinearParams p) {
             for (int i = 0; i < 4; ++i)
                 tiles[wave][16 * q + 4 * g + i][16 * f + c] = acc[q][f][i];
     __syncthreads();
-    constexpr int kCols = SWIGLU ? 16 : kTile;
     const int rows = min(p.M, 16 * RG);
-    for (int i = threadIdx.x; i < rows * kCols; i += kRowThreads) {
-        const int m = i / kCols, col = i % kCols, n = n0 + col;
+    for (int i = threadIdx.x; i < rows * 16; i += kRowThreads) {
+        const int m = i / 16, col = i % 16, n = n0 + col;
         if (n >= p.N) continue;
         const int64_t at = static_cast<int64_t>(m) * p.N + n;
         const float r = p.residual ? element(p.residual, at, false, F16) : 0.0f;
@@ -330,7 +330,6 @@ __device__ __forceinline__ void lds_barrier() {
 // compiler would leave them, they come in runs that the MFMAs wait for).
 template <int MFMAS, int READS, int WRITES, int LOADS>
 __device__ __forceinline__ void spread() {
-#ifndef NOSPREAD
     constexpr int kTurns = MFMAS > 1 ? MFMAS / 2 : 1;
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
@@ -342,7 +341,6 @@ __device__ __forceinline__ void spread() {
         if (LOADS && i * kL < LOADS) __builtin_amdgcn_sched_group_barrier(0x20, kL, 0);
         __builtin_amdgcn_sched_group_barrier(0x8, MFMAS / kTurns, 0);
     }
-#endif
 }
 
 // BM rows of x by BN weight rows (swiglu: BN / 2 output columns, their gate and
@@ -352,10 +350,11 @@ __device__ __forceinline__ void spread() {
 //
 // A step is four 16-K parts.  While one part's MFMAs run, the next part's
 // fragments come from LDS.  The next step's tile, loaded to registers three parts
-// (or a step and three parts) earlier, is written to the other stage during parts 1 (x) and 2 (w), and each
-// half's loads of the step after it follow at once.  The one barrier stands
-// before part 3, whose fragments are in registers by then: behind it the other
-// stage is complete, and nobody reads this one any more.
+// (with two steps on their way: seven) earlier, is written to the other stage
+// during parts 1 (x) and 2 (w), and each half's loads of a later step follow at
+// once.  The one barrier stands before part 3, whose fragments are in registers
+// by then: behind it the other stage is complete, and nobody reads this one any
+// more.
 template <bool F16, bool ALIGNED, bool SWIGLU, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, BM == 256 ? BM / WM * (BN / WN) / 4 : 2)
 void tile_kernel(LinearParams p, int tiles_m, int tiles_n) {
@@ -397,7 +396,8 @@ void tile_kernel(LinearParams p, int tiles_m, int tiles_n) {
     // rows a multiple of 8 apart share their swizzle
     u4_t *const put_at = lds + row0 * 8 + (piece ^ (row0 & 7));
     // Steps' tiles on their way: two where the registers leave room (a step of
-    // the smaller tiles is shorter than a load takes).
+    // the smaller tiles is shorter than a load takes: 256 x 4096 x 4096 30 us
+    // with one, 20 with two).
     constexpr int D = BM * BN < 256 * 256 ? 2 : 1;
     u4_t xs[D][kNX], ws[D][kNW];
     // this block's steps: all, or a K split's
@@ -710,10 +710,8 @@ __global__ __launch_bounds__(256) void join_kernel(LinearParams p) {
 
 template <bool F16, bool ALIGNED, bool SWIGLU, int RG>
 hipError_t launch_rows(const LinearParams &p, hipStream_t stream) {
-    constexpr int NF = SWIGLU ? 2 : 1;
-    const int cols = 16;
-    hipLaunchKernelGGL((row_kernel<F16, ALIGNED, SWIGLU, RG, NF>),
-                       dim3((p.N + cols - 1) / cols), dim3(kRowThreads), 0, stream, p);
+    hipLaunchKernelGGL((row_kernel<F16, ALIGNED, SWIGLU, RG, SWIGLU ? 2 : 1>),
+                       dim3((p.N + 15) / 16), dim3(kRowThreads), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -734,16 +732,20 @@ hipError_t launch_tiles(const LinearParams &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// The kernel for a size and its K split, by estimated time: rounds of 256 blocks
-// times a block's time per 64-K step (measured at K = 4096: a larger tile feeds
-// more MFMAs per byte brought to the CU), and for a split the partial sums'
-// traffic at 4 TB/s and the joining launch.
+// The kernel for a size and its K split, by estimated time.  Tiles: rounds of 256
+// blocks times a block's time per 64-K step (measured at K = 4096: a larger tile
+// feeds more MFMAs per byte brought to the CU), and for a split the partial sums'
+// traffic at 4 TB/s and the joining launch.  Rows: a wave's eighth of the steps,
+// each about as long as its loads take, times the blocks per CU.  Neither is faster
+// than the weights come at 4.5 TB/s.  (Rows against
+// tiles, N x K: 1 x 4096 x 4096 9.3 us against 11; 16 x 256 x 7168 15.1 against
+// 9.5; 32 x 1024 x 1024 5.3 against 7.0; 64 x 4096 x 4096 21.3 against 13.0.)
 struct Choice {
     enum Kind { kRows, k256, k256x128, k128, k64 } kind;
-    int split;
+    int split;     // 0: too large for a grid
 };
+constexpr int64_t kMaxBlocks = (int64_t{1} << 23) - 8;    // 2^32 threads, up to 512 a block
 Choice choose_kernel(int64_t M, int64_t N, int64_t K, bool swiglu) {
-    if (M <= 64) return {Choice::kRows, 1};
     const int64_t rows = swiglu ? 2 * N : N, steps = (K + 63) / 64;
     const bool aligned = K % 8 == 0;
     struct Tile {
@@ -755,16 +757,29 @@ Choice choose_kernel(int64_t M, int64_t N, int64_t K, bool swiglu) {
                           {Choice::k256x128, 256, 128, 0.95},
                           {Choice::k128, 128, 128, 0.62},
                           {Choice::k64, 64, swiglu ? 128 : 64, swiglu ? 0.42 : 0.28}};
-    Choice best{Choice::k64, 1};
+    Choice best{Choice::k64, 0};
     double least = 1e30;
+    const double memory = 2.0 * static_cast<double>(rows) * static_cast<double>(K) / 4.5e6;
+    // (the longer of the two hides most of the other)
+    auto both = [](double a, double b) { return a > b ? a + 0.2 * b : b + 0.2 * a; };
+    if (const int64_t n = (N + 15) / 16; M <= 64 && n <= kMaxBlocks) {
+        const double step = (M <= 16 ? 1.0 : M <= 32 ? 1.5 : 2.3) * (swiglu ? 1.6 : 1.0);
+        least = both(2.0 + step * static_cast<double>((steps + 7) / 8) *
+                               (n > 256 ? static_cast<double>(n) / 256.0 : 1.0),
+                     memory);
+        best = {Choice::kRows, 1};
+    }
     for (const Tile &t : tiles) {
         if (!aligned && (t.kind == Choice::k256 || t.kind == Choice::k256x128)) continue;
         const int64_t n = ((M + t.bm - 1) / t.bm) * ((rows + t.bn - 1) / t.bn);
-        for (int split = 1; split <= (t.kind == Choice::k128 ? 8 : 1); ++split) {
+        if (n > kMaxBlocks) continue;
+        for (int split = 1; split <= (t.kind == Choice::k128 || t.kind == Choice::k64 ? 8 : 1);
+             ++split) {
             if (split > 1 && (steps / split < 6 || n * split > 256)) break;
             const double rounds = static_cast<double>((n * split + 255) / 256);
             double us = rounds * (4.0 + t.us * static_cast<double>((steps + split - 1) / split));
-            if (split > 1) us += 4.0 + 8.0 * static_cast<double>(M * rows * split) / 4e6;
+            us = both(us, 2.0 + memory);
+            if (split > 1) us += 2.0 + 8.0 * static_cast<double>(M * rows * split) / 4e6;
             if (us < least) least = us, best = {t.kind, split};
         }
     }

@@ -32,10 +32,11 @@ namespace {
 
 constexpr int kRouteWaves = 8;      // of a block of the long path, which takes
 constexpr int kMaxChunk = 16;       // at most so many tokens (a chunk)
-constexpr int kFewTokens = 16;      // one-launch path up to here
+// One-launch path up to here: its blocks, one a token, each choose for all tokens,
+// a wave a token.
+constexpr int kFewTokens = 16;
 constexpr int kFewChunks = 64;      // no scan launch up to here
 constexpr int kMoveThreads = 256;
-
 
 constexpr float kNegInf = -INFINITY;
 

@@ -68,6 +68,10 @@ def test_linear_empty_is_a_no_op():
     (dict(residual=desc(BF16, 0, 16)), BAD_SHAPE),
     (dict(x=desc(BF16, 0, (1 << 21) + 8), w=desc(BF16, 32, (1 << 21) + 8)), UNSUPPORTED),
     (dict(x=desc(BF16, 1 << 31, 64), out=desc(BF16, 1 << 31, 32)), UNSUPPORTED),
+    # more tiles than a grid has room for, of both kernels
+    (dict(x=desc(BF16, 1 << 30, 64), w=desc(BF16, 2048, 64), out=desc(BF16, 1 << 30, 2048)),
+     UNSUPPORTED),
+    (dict(x=desc(BF16, 4, 8), w=desc(BF16, 1 << 30, 8), out=desc(BF16, 4, 1 << 30)), UNSUPPORTED),
     (dict(x=desc(BF16, 4, 64, data=FAKE + 8), out=desc(BF16, 4, 32)), BAD_ALIGN),
     (dict(x=desc(BF16, 4, 64), out=desc(BF16, 4, 32, data=FAKE + 4)), BAD_ALIGN),
 ])
@@ -183,6 +187,8 @@ def test_route_empty_is_a_no_op():
     (dict(H=48), UNSUPPORTED),
     (dict(E=1025), UNSUPPORTED),
     (dict(E=64, k=33), UNSUPPORTED),
+    (dict(T=(1 << 26) + 1, k=1, with_x=False), UNSUPPORTED),
+    (dict(T=1 << 26, E=64, k=32), UNSUPPORTED),             # 2^31 pairs
     (dict(scoring=2), BAD_ARG), (dict(renorm=2), BAD_ARG),
     (dict(n_group=3), BAD_ARG), (dict(n_group=0), BAD_ARG),
     (dict(n_group=4, topk_group=5), BAD_ARG), (dict(n_group=4, topk_group=0), BAD_ARG),

@@ -91,6 +91,41 @@ def test_large_tiles(M, N, K, act):
     run(M, N, K, torch.bfloat16, act, bias=torch.bfloat16, residual=True)
 
 
+# few tiles of a long K: the K split and its joining launch, rows that begin
+# anywhere and aligned ones, two split halves under swiglu
+@pytest.mark.parametrize("M, N, K, act", [(100, 72, 4104, "silu"), (100, 75, 4107, "none"),
+                                          (700, 600, 4104, "none"), (200, 264, 2056, "swiglu"),
+                                          (200, 259, 2051, "swiglu"), (50, 72, 4104, "relu"),
+                                          (331, 4099, 1544, "gelu"), (450, 2056, 2059, "none"),
+                                          (450, 1032, 1544, "swiglu"),
+                                          (450, 1029, 1549, "swiglu")])
+def test_split_k(M, N, K, act):
+    run(M, N, K, torch.bfloat16, act, bias=torch.bfloat16, residual=True)
+    run(M, N, K, torch.float16, act, out_dtype=torch.float32)
+
+
+# tiles of 256 x 128, aligned columns and not
+@pytest.mark.parametrize("M, N, K, act", [(2100, 2050, 72, "none"), (2100, 1032, 136, "swiglu"),
+                                          (2600, 1041, 200, "swiglu")])
+def test_oblong_tiles(M, N, K, act):
+    run(M, N, K, torch.float16, act, bias=torch.float32, residual=True)
+
+
+def test_split_k_in_place_and_workspace_of_the_caller():
+    from mxfp8_grouped_gemm_group_amd import _layer
+    M, N, K = 100, 72, 4104
+    a = make(M, N, K, torch.bfloat16, residual=True)
+    want = gfr.linear(a["x"], a["w"], residual=a["residual"])
+    ws = torch.full((1 << 22,), 255, dtype=torch.uint8, device=DEV)      # NaN sums
+    out = a["residual"].clone()
+    gfr.linear(a["x"], a["w"], residual=out, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    with pytest.raises(gfr.GfrError) as e:
+        gfr.linear(a["x"], a["w"], workspace=ws[:256])
+    assert e.value.code == _layer.WORKSPACE_TOO_SMALL
+
+
 def test_long_k():
     run(4, 64, 28672, torch.bfloat16, out_dtype=torch.float32)
     run(100, 64, 28680, torch.float16)

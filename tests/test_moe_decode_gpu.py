@@ -93,6 +93,23 @@ def test_bf16_out_and_wide_layers(t):
     check(a, out, "wide")
 
 
+# many blocks of many rows: blocks of eight waves and runs of several tiles, of
+# the gate/up product (wide I) and the down product (wide N)
+@pytest.mark.parametrize("T, k, E, H, I, N, t", [
+    (60, 6, 64, 128, 3200, 64, False), (60, 6, 64, 64, 128, 6400, False),
+    (60, 6, 64, 128, 3200, 64, True), (60, 6, 64, 64, 128, 3328, True),
+    (64, 10, 64, 64, 3648, 64, False), (64, 10, 64, 64, 128, 3648, False),
+    (64, 10, 64, 128, 1600, 64, True), (64, 10, 64, 64, 192, 1856, True)])
+def test_many_blocks(T, k, E, H, I, N, t):
+    what = f"T {T} k {k} E {E} H {H} I {I} N {N} {t}"
+    print(what, flush=True)
+    a = make(T, k, E, H, I, N, "e4m3", t, t, shared=True)
+    a["topk_ids"][3] = -1
+    out = call(a, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    check(a, out, what)
+
+
 def test_most_experts_and_pairs():
     a = make(64, 16, 1024, 64, 64, 64, "e5m2")
     out = call(a, out_dtype=torch.float32)
