@@ -53,15 +53,24 @@ def _check(rc: int):
         raise GfrError(rc, b.status_string(rc))
 
 
-_PAD = ((), (0, 0, 0), (0, 0), (0,), ())     # of a shape of 1 .. 4 extents
+@functools.lru_cache(maxsize=16384)
+def _words(dtype, shape):
+    """A gfr_tensor's 64-bit words behind its address."""
+    code, n = DTYPES.get(dtype), len(shape)
+    if code is None:
+        raise ValueError(f"dtype {dtype} has no gfr_dtype")
+    if not 1 <= n <= 4:
+        raise ValueError(f"rank {n} is outside 1..4")
+    return (code | n << 32, *shape, *(0,) * (4 - n))
 
 
-def _pack(index, tensors, workspace=None, status=None):
+def _pack(index, tensors, made=(), workspace=None, status=None):
     """The tensors' gfr_tensor descriptors and a gfr_options behind them in one
     array of 64-bit words, and their addresses (None for an absent tensor).  One
     array costs a fraction of a ctypes structure per tensor, and the smallest
-    calls take little longer on the GPU than that.  The array has to outlive
-    the call.  Raises for what the descriptors cannot carry."""
+    calls take little longer on the GPU than that.  ``made``, behind ``tensors``,
+    were allocated by the caller of this and need no check.  The array has to
+    outlive the call.  Raises for what the descriptors cannot carry."""
     v, at = [], []
     for t in tensors:
         if t is None:
@@ -71,14 +80,16 @@ def _pack(index, tensors, workspace=None, status=None):
             raise ValueError("all tensors must be on one CUDA device")
         if not t.is_contiguous():
             raise ValueError("all tensors must be contiguous")
-        shape, code = t.shape, DTYPES.get(t.dtype)
-        n = len(shape)
-        if code is None:
-            raise ValueError(f"dtype {t.dtype} has no gfr_dtype")
-        if not 1 <= n <= 4:
-            raise ValueError(f"rank {n} is outside 1..4")
         at.append(8 * len(v))
-        v += (t.data_ptr(), code | n << 32, *shape, *_PAD[n])
+        v.append(t.data_ptr())
+        v += _words(t.dtype, t.shape)
+    for t in made:
+        if t is None:
+            at.append(None)
+            continue
+        at.append(8 * len(v))
+        v.append(t.data_ptr())
+        v += _words(t.dtype, t.shape)
     end = 8 * len(v)
     v += (0, 0, 0, 0, 0)
     for t in (workspace, status):
@@ -134,17 +145,21 @@ def linear(x, w, bias=None, *, activation="none", residual=None, out_dtype=None,
         with away:
             return linear(x, w, bias, activation=activation, residual=residual,
                           out_dtype=out_dtype, out=out, workspace=workspace)
+    tensors, made = (x, w, bias, residual), ()
     if out is None:
         n = w.shape[0] // 2 if act == 5 else w.shape[0]
         out = x.new_empty((x.shape[0], n), dtype=out_dtype or x.dtype)
-    tensors, handle = (x, w, bias, residual, out), _raw_stream(index)
-    words, (px, pw, pb, pr, po), opts = _pack(index, tensors, workspace)
+        made = (out,)
+    else:
+        tensors += (out,)
+    handle = _raw_stream(index)
+    words, (px, pw, pb, pr, po), opts = _pack(index, tensors, made, workspace)
     rc = lib.gfr_linear(px, pw, pb, pr, act, po, handle, opts)
     if rc == WORKSPACE_TOO_SMALL and workspace is None:
         need = ctypes.c_size_t(0)
         _check(lib.gfr_linear_workspace_size(px, pw, pb, pr, act, po, ctypes.byref(need)))
         workspace = x.new_empty(need.value, dtype=torch.uint8)
-        words, (px, pw, pb, pr, po), opts = _pack(index, tensors, workspace)
+        words, (px, pw, pb, pr, po), opts = _pack(index, tensors, made, workspace)
         rc = lib.gfr_linear(px, pw, pb, pr, act, po, handle, opts)
     _check(rc)
     return out
@@ -199,7 +214,7 @@ def moe_decode(x, w13, scale13, w2, scale2, topk_ids, topk_weights, *, transpose
         workspace = x.new_empty(moe_decode_workspace_size(T, k, E, x.shape[1], I, N, t13, t2),
                                 dtype=torch.uint8)
     words, at, opts = _pack(index, (x, w13, scale13, w2, scale2, topk_ids, topk_weights,
-                                    shared_input, out), workspace, status)
+                                    shared_input, out), (), workspace, status)
     _check(lib.gfr_moe_decode(*at[:8], float(shared_input_weight), at[8], t13, t2,
                               _raw_stream(index), opts))
     return out
@@ -263,10 +278,10 @@ def moe_route(logits, top_k, *, x=None, bias=None, scoring="softmax", n_group=1,
             need = _route_workspace_size(T, E, k)
             if need:
                 workspace = empty(need, dtype=torch.uint8)
-    words, at, opts = _pack(index, (logits, bias, ids, weights, x, *rows), workspace)
+    words, at, opts = _pack(index, (logits, bias, x), (ids, weights, *rows), workspace)
     _check(lib.gfr_moe_route(at[0], at[1], score, int(n_group), int(topk_group),
-                             int(bool(renormalize)), float(scaling), *at[2:],
-                             _raw_stream(index), opts))
+                             int(bool(renormalize)), float(scaling), at[3], at[4], at[2],
+                             *at[5:], _raw_stream(index), opts))
     return RouteResult(ids, weights, *rows)
 
 

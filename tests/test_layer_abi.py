@@ -68,10 +68,11 @@ def test_linear_empty_is_a_no_op():
     (dict(residual=desc(BF16, 0, 16)), BAD_SHAPE),
     (dict(x=desc(BF16, 0, (1 << 21) + 8), w=desc(BF16, 32, (1 << 21) + 8)), UNSUPPORTED),
     (dict(x=desc(BF16, 1 << 31, 64), out=desc(BF16, 1 << 31, 32)), UNSUPPORTED),
-    # more tiles than a grid has room for, of both kernels
+    # more tiles than a grid has room for; more rows than a tile's columns count
     (dict(x=desc(BF16, 1 << 30, 64), w=desc(BF16, 2048, 64), out=desc(BF16, 1 << 30, 2048)),
      UNSUPPORTED),
-    (dict(x=desc(BF16, 4, 8), w=desc(BF16, 1 << 30, 8), out=desc(BF16, 4, 1 << 30)), UNSUPPORTED),
+    (dict(x=desc(BF16, 4, 8), w=desc(BF16, (1 << 30) + 1, 8),
+          out=desc(BF16, 4, (1 << 30) + 1)), UNSUPPORTED),
     (dict(x=desc(BF16, 4, 64, data=FAKE + 8), out=desc(BF16, 4, 32)), BAD_ALIGN),
     (dict(x=desc(BF16, 4, 64), out=desc(BF16, 4, 32, data=FAKE + 4)), BAD_ALIGN),
 ])
