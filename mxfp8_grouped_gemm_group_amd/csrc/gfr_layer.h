@@ -25,9 +25,10 @@ int linear_split(int64_t M, int64_t N, int64_t K, int act);
 hipError_t launch_linear(const LinearParams &p, hipStream_t stream);
 
 // One of moe_decode's two products: the K chunks whose partial sums are kept
-// apart, the column tiles each wave of a block takes, and its waves.
+// apart, the column tiles each wave of a block takes, its waves, and whether
+// these share one tile instead.
 struct DecodePart {
-    int32_t chunks, run, waves;
+    int32_t chunks, run, waves, shared;
 };
 
 struct DecodeParams {

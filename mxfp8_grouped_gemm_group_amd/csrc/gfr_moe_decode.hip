@@ -416,7 +416,9 @@ __device__ __forceinline__ void two_terms(f4_t gate, f4_t up, u2_t &hi, u2_t &lo
 // Partial sums of a K chunk.  TERMS = 1: operand x, out gu [chunks][pairs][2I];
 // TERMS = 2: operand h from gu, out y [chunks][pairs][N].  Grid: (column runs,
 // chunks, groups).
-template <class Stream, int RG, int TERMS, int kWaves>
+// SHARED: the block's waves share one column tile, each takes every kWaves-th step,
+// and their sums meet in LDS.
+template <class Stream, int RG, int TERMS, int kWaves, bool SHARED>
 __global__ __launch_bounds__(64 * kWaves, 2) void product_kernel(DecodeParams p) {
     constexpr int kThreads = 64 * kWaves;
     // (aligned: 16-byte accesses to LDS at odd words take about twice as long)
@@ -453,18 +455,22 @@ __global__ __launch_bounds__(64 * kWaves, 2) void product_kernel(DecodeParams p)
 
     // This wave's tiles: every kWaves-th of the block's run.
     const int tiles = (cols + kTile - 1) / kTile;
-    int tile = blockIdx.x * d.run * kWaves + wave;
+    int tile = SHARED ? blockIdx.x : blockIdx.x * d.run * kWaves + wave;
     const int mine = max(min(d.run, (tiles - tile + kWaves - 1) / kWaves), 0);
     // Blocks side by side begin at different steps and go round: rows and
     // columns a power of two apart share memory channels.
-    const int turn = (blockIdx.x + blockIdx.z) % steps;
-    const int total = mine * steps;
+    const int turn = SHARED ? wave : (blockIdx.x + blockIdx.z) % steps;
+    const int total = SHARED ? max(steps - wave + kWaves - 1, 0) / kWaves : mine * steps;
     int fetch_step = turn, fetch_n0 = tile * kTile, fetched = 0;
     typename Stream::Stage f[Stream::kDepth];
     auto fetch = [&](typename Stream::Stage &s) {
         Stream::fetch(s, a, fetch_n0, k0 + fetch_step * kStep);
-        if (++fetch_step == steps) fetch_step = 0;
-        if (fetch_step == turn) fetch_n0 += kWaves * kTile;
+        if (SHARED) {
+            fetch_step += kWaves;
+        } else {
+            if (++fetch_step == steps) fetch_step = 0;
+            if (fetch_step == turn) fetch_n0 += kWaves * kTile;
+        }
         ++fetched;
     };
 #pragma unroll
@@ -530,6 +536,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void product_kernel(DecodeParams p)
             if (i + j >= total) break;
             Stream::template use<RG, TERMS>(f[j], x, step * kStep, K - k0 - step * kStep, live, acc);
             if (fetched < total) fetch(f[j]);
+            if (SHARED) {
+                step += kWaves;
+                continue;
+            }
             if (++step == steps) step = 0;
             if (step == turn) {
 #pragma unroll
@@ -544,6 +554,33 @@ __global__ __launch_bounds__(64 * kWaves, 2) void product_kernel(DecodeParams p)
                 tile += kWaves;
             }
         }
+    if constexpr (SHARED) {
+        // A lane's 32 sums are four runs of eight columns (Stream::store); wave i adds
+        // up and stores run i of all waves, in order.
+        static_assert(Stream::kKN && RG == 1 && kWaves == 4, "four runs of eight columns");
+        f4_t *const sums = reinterpret_cast<f4_t *>(lds);
+        __syncthreads();
+        if (c < count)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    sums[((i * 2 + h) * kWaves + wave) * 64 + lane] =
+                        f4_t{acc[0][4 * h][i], acc[0][4 * h + 1][i], acc[0][4 * h + 2][i],
+                             acc[0][4 * h + 3][i]};
+        __syncthreads();
+        const int col = tile * kTile + 32 * g + 8 * wave;
+        if (c >= count || col >= cols) return;
+        float *to = out + static_cast<int64_t>(plan.pairs[first + c]) * cols + col;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f4_t *at = sums + (wave * 2 + h) * kWaves * 64 + lane;
+            f4_t v = at[0];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) v += at[64 * w];
+            *reinterpret_cast<f4_t *>(to + 4 * h) = v;
+        }
+    }
 }
 
 // h = silu(gate) * up as two bf16 terms, once for all blocks of the down product.
@@ -662,23 +699,33 @@ DecodePart part_shape(double groups, double rows, int64_t K, int64_t cols, int t
                 ++chunks;
         }
         const int64_t most = (tiles + waves - 1) / waves;
-        d = {static_cast<int32_t>(chunks), static_cast<int32_t>(run < most ? run : most), waves};
-        if (!enough) break;
+        d = {static_cast<int32_t>(chunks), static_cast<int32_t>(run < most ? run : most), waves, 0};
+        if (!enough) {
+            if (waves == 4 && rg == 1 && !transpose &&
+                groups * ((tiles + waves - 1) / waves) * chunks < blocks) {
+                for (chunks = (steps + wide - 1) / wide;
+                     groups * tiles * chunks < blocks && steps / (chunks + 1) >= 4 && chunks < 8;)
+                    ++chunks;
+                d = {static_cast<int32_t>(chunks), 1, waves, 1};
+            }
+            break;
+        }
     }
     return d;
 }
 
-template <class Stream, int RG, int TERMS, int kWaves>
+template <class Stream, int RG, int TERMS, int kWaves, bool SHARED = false>
 hipError_t launch_product(const DecodeParams &p, hipStream_t stream) {
     const DecodePart &d = TERMS == 1 ? p.gate_up : p.down;
     const int K = TERMS == 1 ? p.H : p.I, cols = TERMS == 1 ? 2 * p.I : p.N;
     const int steps = (K + Stream::kStep - 1) / Stream::kStep;
     const int width = (steps + d.chunks - 1) / d.chunks * Stream::kStep;
     const int operand = TERMS * 16 * RG * (2 * width + 16);
-    const int lds = operand > kMaskBytes ? operand : kMaskBytes;
+    constexpr int kLeast = SHARED ? 8 * kWaves * 64 * 16 : kMaskBytes;    // SHARED: the sums
+    const int lds = operand > kLeast ? operand : kLeast;
     const int tiles = (cols + Stream::kTile - 1) / Stream::kTile;
-    const int runs = (tiles + d.run * kWaves - 1) / (d.run * kWaves);
-    constexpr auto kernel = &product_kernel<Stream, RG, TERMS, kWaves>;
+    const int per_run = SHARED ? 1 : d.run * kWaves, runs = (tiles + per_run - 1) / per_run;
+    constexpr auto kernel = &product_kernel<Stream, RG, TERMS, kWaves, SHARED>;
     if (hipError_t e = allow_lds<kernel>(lds); e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel,
                        dim3(runs, d.chunks, static_cast<uint32_t>(max_groups(p.T * p.k, p.E, RG))),
@@ -690,6 +737,9 @@ template <int FMT, int RG, int TERMS>
 hipError_t launch_product_any(const DecodeParams &p, int transpose, hipStream_t stream) {
     typedef StreamNK<FMT, lines(RG)> NK;
     typedef StreamKN<FMT> KN;
+    if constexpr (RG == 1)
+        if ((TERMS == 1 ? p.gate_up : p.down).shared)
+            return launch_product<KN, RG, TERMS, 4, true>(p, stream);
     if ((TERMS == 1 ? p.gate_up : p.down).waves == 8)
         return transpose ? launch_product<NK, RG, TERMS, 8>(p, stream)
                          : launch_product<KN, RG, TERMS, 8>(p, stream);
