@@ -22,8 +22,8 @@
 // loads in flight across tile ends and no barrier.  Chunks and runs are chosen
 // (part_shape) so that even one token's few experts keep every CU's loads
 // in flight, and so that a long batch writes few partial sums.  (64 tokens of 32
-// experts of 4096 x 8192, 3.2 GB: 519 us, 6.2 TB/s.  One token, 8 of 256 experts of
-// 2048 x 512, 25 MB: 21 us, of which the two products' and the sum's latencies
+// experts of 4096 x 8192, 3.2 GB: 516 us, 6.2 TB/s.  One token, 8 of 256 experts of
+// 2048 x 512, 25 MB: 15.8 us, of which the two products' and the sum's latencies
 // one after the other are most.)
 //
 // Weights [K, N]: a lane reads 8 columns of 8 rows (128-byte row pieces per
@@ -676,6 +676,11 @@ constexpr int lines(int rg) { return rg == 1 ? 2 : 1; }
 // of four waves, which halves the partial sums and the operand's reading: worth
 // it where a group has rows enough for that to count and blocks are many (64
 // tokens of 32 experts, 4096 x 8192: 577 -> 518 us; 8 tokens of 16, 157 -> 172).
+// Where blocks of a [K, N] tile per wave are fewer than three per CU, a block's
+// waves share a tile and split its steps: four times the blocks, and no more
+// partial sums (one token, 8 of 256 experts of 2048 x 512: 21.3 -> 15.8 us; 2 of 8
+// of 4096 x 7168: 53.7 -> 46.8).  [N, K] tiles are a quarter as wide and fill the CUs
+// without.
 DecodePart part_shape(double groups, double rows, int64_t K, int64_t cols, int transpose, int rg,
                       int terms) {
     const int64_t step = transpose ? 128 * lines(rg) : 64;

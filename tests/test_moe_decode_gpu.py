@@ -110,6 +110,18 @@ def test_many_blocks(T, k, E, H, I, N, t):
     check(a, out, what)
 
 
+# few blocks: the waves of a block share a column tile, with steps left over
+@pytest.mark.parametrize("T, k, E, H, I, N", [(1, 2, 8, 1088, 704, 192), (2, 3, 5, 4160, 448, 1344),
+                                              (16, 1, 2, 576, 832, 320)])
+@pytest.mark.parametrize("fp8", ["e4m3", "e5m2"])
+def test_few_blocks(T, k, E, H, I, N, fp8):
+    print(f"T {T} k {k} E {E} H {H} I {I} N {N} {fp8}", flush=True)
+    a = make(T, k, E, H, I, N, fp8, per_expert=True, shared=True)
+    out = call(a, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    check(a, out, "few blocks")
+
+
 def test_most_experts_and_pairs():
     a = make(64, 16, 1024, 64, 64, 64, "e5m2")
     out = call(a, out_dtype=torch.float32)
