@@ -676,6 +676,9 @@ constexpr int lines(int rg) { return rg == 1 ? 2 : 1; }
 // of four waves, which halves the partial sums and the operand's reading: worth
 // it where a group has rows enough for that to count and blocks are many (64
 // tokens of 32 experts, 4096 x 8192: 577 -> 518 us; 8 tokens of 16, 157 -> 172).
+// [N, K] with two row fragments, whose tiles are wider, needs nearly two rounds of
+// them (64 tokens, 4 of 16 experts of 4096 x 4096, 2.3 rounds: 227 -> 204 us; 4 of 8
+// of 4096 x 2048, 1.1 rounds: 113 -> 123).
 // Where blocks of a [K, N] tile per wave are fewer than three per CU, a block's
 // waves share a tile and split its steps: four times the blocks, and no more
 // partial sums (one token, 8 of 256 experts of 2048 x 512: 21.3 -> 15.8 us; 2 of 8
@@ -694,6 +697,7 @@ DecodePart part_shape(double groups, double rows, int64_t K, int64_t cols, int t
         const int64_t wide = kOperandBytes * waves / (2 * terms * 16 * rg) / step;
         int64_t chunks = (steps + wide - 1) / wide;
         const double runs = groups * chunks * tiles / (waves * blocks);
+        if (waves == 8 && transpose && rg == 2 && runs < 1.75) break;
         int64_t run = static_cast<int64_t>(runs);
         const bool enough = run >= 1;
         if (!enough) {

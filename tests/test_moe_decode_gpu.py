@@ -99,7 +99,8 @@ def test_bf16_out_and_wide_layers(t):
     (60, 6, 64, 128, 3200, 64, False), (60, 6, 64, 64, 128, 6400, False),
     (60, 6, 64, 128, 3200, 64, True), (60, 6, 64, 64, 128, 3328, True),
     (64, 10, 64, 64, 3648, 64, False), (64, 10, 64, 64, 128, 3648, False),
-    (64, 10, 64, 128, 1600, 64, True), (64, 10, 64, 64, 192, 1856, True)])
+    (64, 10, 64, 128, 1600, 64, True), (64, 10, 64, 64, 192, 1856, True),
+    (64, 10, 64, 64, 192, 3264, True)])
 def test_many_blocks(T, k, E, H, I, N, t):
     what = f"T {T} k {k} E {E} H {H} I {I} N {N} {t}"
     print(what, flush=True)
