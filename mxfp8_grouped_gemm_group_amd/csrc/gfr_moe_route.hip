@@ -181,7 +181,7 @@ __device__ __forceinline__ void choose(const RouteParams &p, const float (&z)[V]
                                        double *s, int &id, float &weight) {
     typedef typename std::conditional<WIDE, double, float>::type K;
     float top = 0.0f;
-    if (!p.sigmoid) {
+    if (!p.sigmoid || (!WIDE && p.renormalize)) {
         uint32_t m = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) m = max(m, ordered(z[v]));
@@ -194,11 +194,19 @@ __device__ __forceinline__ void choose(const RouteParams &p, const float (&z)[V]
         for (int v = 0; v < V; ++v) bias[v] = p.bias[min(lane * V + v, p.E - 1)];
     K score[V];
     double sum = 0.0;
-    if (p.sigmoid) {
+    if (p.sigmoid && WIDE) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            score[v] = WIDE ? static_cast<K>(1.0 / (1.0 + exp(-static_cast<double>(z[v]))))
-                            : static_cast<K>(1.0f / (1.0f + expf(-z[v])));
+            score[v] = static_cast<K>(1.0 / (1.0 + exp(-static_cast<double>(z[v]))));
+    } else if (p.sigmoid && top < 0.0f) {
+        // times exp(-top), which cancels: all scores together may be too small for
+        // FP32
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            score[v] = static_cast<K>(expf(z[v] - top) / (1.0f + expf(z[v])));
+    } else if (p.sigmoid) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) score[v] = static_cast<K>(1.0f / (1.0f + expf(-z[v])));
     } else {
 #pragma unroll
         for (int v = 0; v < V; ++v) {

@@ -98,6 +98,19 @@ def test_masked_experts_and_padded_tokens(T, kw):
     check_rows(r, x, ids, 16, torch.float8_e4m3fn)
 
 
+@pytest.mark.parametrize("E", [16, 256])
+@pytest.mark.parametrize("shift", [-60.0, -95.0, -300.0, 95.0])
+def test_far_logits_keep_their_weights(E, shift):
+    """A row's scores may all be too small for FP32 (sigmoid of -95); their ratios
+    are not."""
+    logits, _ = make(6, E)
+    logits = logits + shift
+    for scoring in ("sigmoid", "softmax"):
+        r = gfr.moe_route(logits, 4, scoring=scoring)
+        torch.cuda.synchronize()
+        check_choice(r, logits, 4, None, scoring=scoring)
+
+
 def test_ties_go_to_the_lower_index():
     for E in (16, 64, 200, 256, 1000):
         for T in (2, 80):
