@@ -175,6 +175,16 @@ def moe_decode_workspace_size(T: int, k: int, E: int, H: int, I: int, N: int,
     return need.value
 
 
+@functools.lru_cache(maxsize=4096)
+def _decode_sizes(x, w2, topk_ids, transpose_w13, transpose_w2):
+    """out's shape and the workspace bytes of a call with tensors of these shapes."""
+    _need(len(x) == 2 and len(w2) == 3 and len(topk_ids) == 2,
+          "x must be [T, H], w2 3-D and topk_ids [T, k]")
+    E, I, N = (w2[0], w2[2], w2[1]) if transpose_w2 else w2
+    return (x[0], N), moe_decode_workspace_size(*topk_ids, E, x[1], I, N, transpose_w13,
+                                                transpose_w2)
+
+
 def moe_decode(x, w13, scale13, w2, scale2, topk_ids, topk_weights, *, transpose_w13=False,
                transpose_w2=False, shared_input=None, shared_input_weight=1.0,
                out_dtype=torch.bfloat16, out=None, workspace=None, status=None, stream=None):
@@ -194,8 +204,8 @@ def moe_decode(x, w13, scale13, w2, scale2, topk_ids, topk_weights, *, transpose
     """
     lib = _lib()
     index = _device(x, "x")
-    _need(x.dim() == 2 and w2.dim() == 3 and topk_ids.dim() == 2,
-          "x must be [T, H], w2 3-D and topk_ids [T, k]")
+    t13, t2 = int(bool(transpose_w13)), int(bool(transpose_w2))
+    shape, need = _decode_sizes(x.shape, w2.shape, topk_ids.shape, t13, t2)
     away = _elsewhere(index, stream)
     if away is not None:
         with away:
@@ -203,18 +213,15 @@ def moe_decode(x, w13, scale13, w2, scale2, topk_ids, topk_weights, *, transpose
                               transpose_w13=transpose_w13, transpose_w2=transpose_w2,
                               shared_input=shared_input, shared_input_weight=shared_input_weight,
                               out_dtype=out_dtype, out=out, workspace=workspace, status=status)
-    T, k = topk_ids.shape
-    E, I, N = w2.shape
-    if transpose_w2:
-        I, N = N, I
-    t13, t2 = int(bool(transpose_w13)), int(bool(transpose_w2))
+    tensors, made = (x, w13, scale13, w2, scale2, topk_ids, topk_weights, shared_input), ()
     if out is None:
-        out = x.new_empty((x.shape[0], N), dtype=out_dtype)
+        out = x.new_empty(shape, dtype=out_dtype)
+        made = (out,)
+    else:
+        tensors += (out,)
     if workspace is None:
-        workspace = x.new_empty(moe_decode_workspace_size(T, k, E, x.shape[1], I, N, t13, t2),
-                                dtype=torch.uint8)
-    words, at, opts = _pack(index, (x, w13, scale13, w2, scale2, topk_ids, topk_weights,
-                                    shared_input, out), (), workspace, status)
+        workspace = x.new_empty(need, dtype=torch.uint8)
+    words, at, opts = _pack(index, tensors, made, workspace, status)
     _check(lib.gfr_moe_decode(*at[:8], float(shared_input_weight), at[8], t13, t2,
                               _raw_stream(index), opts))
     return out
