@@ -394,8 +394,9 @@ enum gfr_activation {
  * same bits.  Errors:
  * GFR_ERR_NULL_ARG, GFR_ERR_BAD_DTYPE, GFR_ERR_BAD_RANK, GFR_ERR_BAD_SHAPE,
  * GFR_ERR_BAD_ARG (activation), GFR_ERR_UNSUPPORTED (M or w's rows > 2^30, K >
- * 2^21, or more than 2^23 - 8 tiles), GFR_ERR_BAD_ALIGNMENT (x or w not 16-byte, bias, residual or out not
- * 8-byte aligned, workspace not 256), GFR_ERR_WORKSPACE_TOO_SMALL, GFR_ERR_HIP.
+ * 2^21, or more than 2^23 - 8 tiles), GFR_ERR_BAD_ALIGNMENT (x or w not 16-byte,
+ * bias, residual or out not 8-byte aligned, workspace not 256),
+ * GFR_ERR_WORKSPACE_TOO_SMALL, GFR_ERR_HIP.
  */
 int gfr_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *bias,
                const gfr_tensor *residual, int activation, const gfr_tensor *out,

@@ -193,7 +193,8 @@ __device__ __forceinline__ float e8m0(uint32_t code) { return __uint_as_float(co
 template <int FMT, bool HI>
 __device__ __forceinline__ uint32_t to_bf16(uint32_t w, float scale) {
     if (FMT == 0)
-        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, HI));
+        return __builtin_bit_cast(uint32_t,
+                                  __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, HI));
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, scale, HI));
 }
 
@@ -534,7 +535,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void product_kernel(DecodeParams p)
 #pragma unroll
         for (int j = 0; j < Stream::kDepth; ++j) {
             if (i + j >= total) break;
-            Stream::template use<RG, TERMS>(f[j], x, step * kStep, K - k0 - step * kStep, live, acc);
+            Stream::template use<RG, TERMS>(f[j], x, step * kStep, K - k0 - step * kStep, live,
+                                            acc);
             if (fetched < total) fetch(f[j]);
             if (SHARED) {
                 step += kWaves;
@@ -629,7 +631,8 @@ __global__ __launch_bounds__(kSumThreads) void combine_kernel(DecodeParams p) {
 #pragma unroll 4
         for (int i = slice; i < terms; i += kSlices) {
             const int j = i / chunks, s = i - j * chunks;
-            if (live[j]) v += weight[j] * load<f4_t>(at + s * plane + static_cast<int64_t>(j) * p.N);
+            const int64_t off = s * plane + static_cast<int64_t>(j) * p.N;
+            if (live[j]) v += weight[j] * load<f4_t>(at + off);
         }
     }
     part[slice][four] = v;
@@ -692,7 +695,8 @@ DecodePart part_shape(double groups, double rows, int64_t K, int64_t cols, int t
     DecodePart d{};
     for (int waves : {4, 8}) {
         if (waves == 8 && rows < 4.0) break;
-        const double blocks = (rg == 1 ? 3072.0 : 1792.0) / waves;   // wanted
+        // wanted: 12 waves a CU, or 7 where two row fragments take their registers
+        const double blocks = 256.0 * (rg == 1 ? 12 : 7) / waves;
         // steps per chunk, at most
         const int64_t wide = kOperandBytes * waves / (2 * terms * 16 * rg) / step;
         int64_t chunks = (steps + wide - 1) / wide;
