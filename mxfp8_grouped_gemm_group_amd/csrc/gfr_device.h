@@ -105,7 +105,7 @@ __device__ __forceinline__ float silu(float v) {
     return v * __builtin_amdgcn_rcpf(1.0f + exp_f32(-v));
 }
 
-// Lets kernel K have up to 144 KB of dynamic LDS; the runtime is asked once per
+// Lets kernel K have up to 146 KB of dynamic LDS; the runtime is asked once per
 // device.
 template <auto K>
 hipError_t allow_lds(int bytes) {
@@ -115,7 +115,7 @@ hipError_t allow_lds(int bytes) {
     if (hipError_t e = hipGetDevice(&dev); e != hipSuccess) return e;
     if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_relaxed)) return hipSuccess;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(K),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, 144 << 10);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, 146 << 10);
     if (e == hipSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_relaxed);
     return e;
 }

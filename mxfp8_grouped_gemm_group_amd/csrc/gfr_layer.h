@@ -41,7 +41,7 @@ struct DecodeParams {
     int32_t *status;           // may be null
     float *gu;                 // [gate_up.chunks][T k][2I]: partial sums of x w13
     float *y;                  // [down.chunks][T k][N]: partial sums of h w2
-    uint16_t *h;               // [2][T k][I]: silu(gate) * up as two bf16 terms, or null
+    uint16_t *h;               // [3][T k][I]: silu(gate) * up as three bf16 terms, or null
     int64_t s13_e, s2_e;       // bytes between experts' scales (0: shared)
     float shared_w;
     int32_t out_f32;

@@ -10,8 +10,8 @@
 //   product_kernel  (twice)  partial sums of a K chunk: gu = x w13, then
 //                   y = h w2 with h = silu(gate) * up, formed from gu's chunks
 //                   as the operand is brought to LDS and kept there as the sum
-//                   of two bf16 terms (16 mantissa bits), so that feeding it to
-//                   the MFMAs does not round it to one;
+//                   of three bf16 terms, so that feeding it to the MFMAs does
+//                   not round it;
 //   activate_kernel  (kActivatePairs pairs and more) h once for all of them;
 //   combine_kernel  out[t] = sum over t's pairs and y's chunks, in that order,
 //                   plus the shared term, rounded once.
@@ -48,7 +48,10 @@ constexpr int kMaxPairs = 1024;
 // product's blocks, which otherwise each form their rows of it: 96 pairs of 8
 // experts 145 -> 135 us, 256 pairs 137 -> 113, but 8 pairs 21 -> 23.
 constexpr int kActivatePairs = 32;
-constexpr int kOperandBytes = 16 << 10;    // of LDS per wave, for a chunk's operand rows
+// LDS per wave for a chunk's operand rows.  Of three terms as much as two blocks of
+// four waves can have beside their plans (8 tokens of 16 experts of 4096 x 6144 with
+// 16 KB 169 us, with this 161).
+constexpr int operand_bytes(int terms) { return terms == 1 ? 16512 : 18624; }
 
 // ---------------------------------------------------------------------------
 // Plan: the pairs grouped by expert.  Every block makes its own from the ids
@@ -399,23 +402,30 @@ struct StreamNK {
     }
 };
 
-// h = silu(gate) * up of four neighbouring columns as two bf16 terms.
-__device__ __forceinline__ void two_terms(f4_t gate, f4_t up, u2_t &hi, u2_t &lo) {
+// h = silu(gate) * up of four neighbouring columns as three bf16 terms whose sum is
+// the FP32 value: 8 mantissa bits each, cut off (what is left is exact), so that the
+// matrix unit's FP32 sums see all 24.  (With two terms a bf16 result is off from
+// that of an FP32 h in 0.3 % of the elements, an FP32 result by 2.4e-6 instead of
+// 3e-7.  Bits below 2^-133, bf16's smallest, are lost.)
+__device__ __forceinline__ void three_terms(f4_t gate, f4_t up, u2_t (&term)[3]) {
     float v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = silu(gate[j]) * up[j];
-    hi = u2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        // an infinite or NaN first term stands for the whole value
-        const float head = __uint_as_float(j & 1 ? hi[j >> 1] & 0xffff0000u : hi[j >> 1] << 16);
-        v[j] = fabsf(head) < INFINITY ? v[j] - head : 0.0f;
+    for (int t = 0; t < 3; ++t) {
+        uint32_t bits[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            bits[j] = __float_as_uint(v[j]) & 0xffff0000u;
+            // an infinite or NaN first term stands for the whole value
+            v[j] = fabsf(v[j]) < INFINITY ? v[j] - __uint_as_float(bits[j]) : 0.0f;
+        }
+        term[t] = u2_t{bits[1] | bits[0] >> 16, bits[3] | bits[2] >> 16};
     }
-    lo = u2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 
 // Partial sums of a K chunk.  TERMS = 1: operand x, out gu [chunks][pairs][2I];
-// TERMS = 2: operand h from gu, out y [chunks][pairs][N].  Grid: (column runs,
+// TERMS = 3: operand h from gu, out y [chunks][pairs][N].  Grid: (column runs,
 // chunks, groups).
 // SHARED: the block's waves share one column tile, each takes every kWaves-th step,
 // and their sums meet in LDS.
@@ -493,10 +503,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void product_kernel(DecodeParams p)
         for (int i = threadIdx.x; i < count * (width / 8); i += kThreads) {
             const int r = i / (width / 8), k = i % (width / 8) * 8;
             const uint16_t *at = p.h + static_cast<int64_t>(plan.pairs[first + r]) * p.I + k0 + k;
-            u4_t hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
-            if (k < real) hi = load<u4_t>(at), lo = load<u4_t>(at + plane);
-            *reinterpret_cast<u4_t *>(lds + r * pitch + 2 * k) = hi;
-            *reinterpret_cast<u4_t *>(lds + (R + r) * pitch + 2 * k) = lo;
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t)
+                *reinterpret_cast<u4_t *>(lds + (t * R + r) * pitch + 2 * k) =
+                    k < real ? load<u4_t>(at + t * plane) : u4_t{0, 0, 0, 0};
         }
     } else {
         const int64_t plane = static_cast<int64_t>(n) * 2 * p.I;
@@ -504,7 +514,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void product_kernel(DecodeParams p)
 #pragma unroll 2
         for (int i = threadIdx.x; i < count * (width / 4); i += kThreads) {
             const int r = i / (width / 4), k = i % (width / 4) * 4;
-            u2_t hi = {0, 0}, lo = {0, 0};
+            u2_t term[3] = {};
             if (k < real) {
                 const float *at =
                     p.gu + static_cast<int64_t>(plan.pairs[first + r]) * 2 * p.I + k0 + k;
@@ -521,10 +531,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void product_kernel(DecodeParams p)
                     for (int j = 0; j < 4; ++j)
                         if (s + j <= last) gate += v[j], up += u[j];
                 }
-                two_terms(gate, up, hi, lo);
+                three_terms(gate, up, term);
             }
-            *reinterpret_cast<u2_t *>(lds + r * pitch + 2 * k) = hi;
-            *reinterpret_cast<u2_t *>(lds + (R + r) * pitch + 2 * k) = lo;
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t)
+                *reinterpret_cast<u2_t *>(lds + (t * R + r) * pitch + 2 * k) = term[t];
         }
     }
     __syncthreads();
@@ -585,7 +596,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void product_kernel(DecodeParams p)
     }
 }
 
-// h = silu(gate) * up as two bf16 terms, once for all blocks of the down product.
+// h = silu(gate) * up as three bf16 terms, once for all blocks of the down product.
 __global__ __launch_bounds__(kSumThreads) void activate_kernel(DecodeParams p) {
     const int64_t n = static_cast<int64_t>(p.T) * p.k, fours = p.I / 4;
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kSumThreads + threadIdx.x;
@@ -600,10 +611,10 @@ __global__ __launch_bounds__(kSumThreads) void activate_kernel(DecodeParams p) {
         gate += load<f4_t>(at);
         up += load<f4_t>(at + p.I);
     }
-    u2_t hi, lo;
-    two_terms(gate, up, hi, lo);
-    *reinterpret_cast<u2_t *>(p.h + q * p.I + k) = hi;
-    *reinterpret_cast<u2_t *>(p.h + (n + q) * p.I + k) = lo;
+    u2_t term[3];
+    three_terms(gate, up, term);
+#pragma unroll
+    for (int t = 0; t < 3; ++t) *reinterpret_cast<u2_t *>(p.h + (t * n + q) * p.I + k) = term[t];
 }
 
 // out[t, n .. n + 3] = sum over t's pairs j and y's chunks s of weight[t, j]
@@ -698,7 +709,8 @@ DecodePart part_shape(double groups, double rows, int64_t K, int64_t cols, int t
         // wanted: 12 waves a CU, or 7 where two row fragments take their registers
         const double blocks = 256.0 * (rg == 1 ? 12 : 7) / waves;
         // steps per chunk, at most
-        const int64_t wide = kOperandBytes * waves / (2 * terms * 16 * rg) / step;
+        const int64_t wide =
+            (operand_bytes(terms) * waves / (terms * 16 * rg) - 16) / 2 / step;
         int64_t chunks = (steps + wide - 1) / wide;
         const double runs = groups * chunks * tiles / (waves * blocks);
         if (waves == 8 && transpose && rg == 2 && runs < 1.75) break;
@@ -770,7 +782,7 @@ hipError_t launch_decode_t(const DecodeParams &p, int t13, int t2, hipStream_t s
         hipLaunchKernelGGL(activate_kernel, dim3(blocks), dim3(kSumThreads), 0, stream, p);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    e = launch_product_any<FMT, RG, 2>(p, t2, stream);
+    e = launch_product_any<FMT, RG, 3>(p, t2, stream);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(combine_kernel, dim3((p.N + 4 * kFours - 1) / (4 * kFours), p.T),
                        dim3(kSumThreads), 0, stream, p);
@@ -790,12 +802,12 @@ DecodeLayout decode_layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I
     const double full = pairs / (groups * 16 * rg);
     if (full > 1.0) groups *= full;
     d.gate_up = part_shape(groups, pairs / groups, H, 2 * I, transpose_w13, rg, 1);
-    d.down = part_shape(groups, pairs / groups, I, N, transpose_w2, rg, 2);
+    d.down = part_shape(groups, pairs / groups, I, N, transpose_w2, rg, 3);
     d.gu = 0;
     d.y = up(sizeof(float) * d.gate_up.chunks * pairs * 2 * I);
     d.h = d.y + up(sizeof(float) * d.down.chunks * pairs * N);
     d.activate = pairs >= kActivatePairs;
-    d.total = d.h + (d.activate ? up(sizeof(uint16_t) * 2 * pairs * I) : 0);
+    d.total = d.h + (d.activate ? up(sizeof(uint16_t) * 3 * pairs * I) : 0);
     return d;
 }
 

@@ -94,8 +94,8 @@ def mx_weights(codes, scale, transpose: bool, kind: int):
 
 def moe_decode(x, w13, w2, ids, weights, shared=None, shared_weight=1.0):
     """(result, bound before out's rounding).  w13 [E, H, 2I], w2 [E, I, N]
-    float64.  Ids outside [0, E) are no expert.  silu(gate) * up is kept as two
-    bf16 terms: off by at most 2^-16 of itself (half a bf16 step, twice)."""
+    float64.  Ids outside [0, E) are no expert.  silu(gate) * up is an FP32 value,
+    summed as three bf16 terms that add up to it."""
     x = np.asarray(x, np.float64)
     T, H = x.shape
     E, I, N = w2.shape
@@ -111,13 +111,13 @@ def moe_decode(x, w13, w2, ids, weights, shared=None, shared_weight=1.0):
             g, u, dg, du = gu[:I], gu[I:], d[:I], d[I:]
             h = silu(g) * u
             dh = SILU_SLOPE * (np.abs(u) + du) * dg + np.abs(silu(g)) * du
-            dh = dh + (2.0 ** -20 + 2.0 ** -16) * np.abs(h)
+            dh = dh + 2.0 ** -20 * np.abs(h)
             a = np.abs(w2[e])
             wt = float(weights[t, j])
             out[t] += wt * (h @ w2[e])
             m = np.abs(wt) * (np.abs(h) @ a)
-            # two terms: twice the additions
-            bound[t] += np.abs(wt) * (dh @ a) + 2 * I * ULP * m
+            # three terms: three times the additions
+            bound[t] += np.abs(wt) * (dh @ a) + 3 * I * ULP * m
             mags[t] += m
     if shared is not None:
         s = float(shared_weight) * np.asarray(shared, np.float64)
