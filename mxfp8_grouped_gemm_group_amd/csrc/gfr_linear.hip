@@ -93,7 +93,9 @@ __device__ __forceinline__ float activate(float v, int act) {
     switch (act) {
     case GFR_ACT_RELU: return v < 0.0f ? 0.0f : v;
     case GFR_ACT_SILU: return silu(v);
-    case GFR_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case GFR_ACT_GELU:
+        // (1 + erf x) / 2 = erfc(-x) / 2: no cancellation for negative v
+        return 0.5f * v * erfcf(v * -0.70710678118654752f);
     case GFR_ACT_GELU_TANH: {
         // (1 + tanh u) / 2 = 1 / (1 + exp(-2u)): no cancellation for negative u
         const float u = 0.79788456080286536f * (v + 0.044715f * v * v * v);

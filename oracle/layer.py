@@ -13,17 +13,13 @@ may truncate).
 from __future__ import annotations
 
 import numpy as np
+from scipy.special import erfc, expit
 
 from .gemm1 import fp8_decode, mx_quantize, silu
 
 ULP = 2.0 ** -23
 SILU_SLOPE = 1.1       # |d silu / dv| <= 1.0998
 GELU_SLOPE = 1.13      # of both gelu forms
-
-
-def _erf(v):
-    from scipy.special import erf
-    return erf(v)
 
 
 def activate(v, act: str):
@@ -34,10 +30,31 @@ def activate(v, act: str):
     if act == "silu":
         return silu(v)
     if act == "gelu":
-        return 0.5 * v * (1 + _erf(v / np.sqrt(2.0)))
+        # erfc and expit: 1 + erf and 1 + tanh cancel below zero
+        return 0.5 * v * erfc(v / -np.sqrt(2.0))
     if act == "gelu_tanh":
-        return 0.5 * v * (1 + np.tanh(np.sqrt(2 / np.pi) * (v + 0.044715 * v ** 3)))
+        return v * expit(2 * _tanh_arg(v))
     raise ValueError(act)
+
+
+def _tanh_arg(v):
+    return np.sqrt(2 / np.pi) * (v + 0.044715 * v ** 3)
+
+
+def activation_error(v, act: str):
+    """What an FP32 evaluation of the activation at an exact v may be off by, relative
+    to its result: a few units in the last place (16 for erfc, the bound OpenCL sets),
+    and what the rounding of the function's argument makes of the result.  erfc(x)
+    changes by at most 2 x^2 + 1 = v^2 + 1 times a relative change of x, here one
+    product and its constant (1.5 2^-24); exp(-2u) by 2u times that of u, here six
+    roundings (6 2^-24)."""
+    if act in ("none", "relu"):
+        return np.zeros_like(v)
+    if act == "gelu":
+        return 2.0 ** -19 + (v * v + 1) * 2.0 ** -23
+    if act == "gelu_tanh":
+        return 2.0 ** -20 + np.abs(2 * _tanh_arg(v)) * 6 * 2.0 ** -24
+    return np.full_like(v, 2.0 ** -20)
 
 
 def linear(x, w, bias, act: str, residual):
@@ -58,13 +75,12 @@ def linear(x, w, bias, act: str, residual):
     else:
         out = activate(y, act)
         d = d * (1.0 if act in ("none", "relu") else GELU_SLOPE)
-    # the activation's own FP32 evaluation, a few units in the last place of
-    # its result (or of its argument where the result is the smaller)
-    if act != "none":
+    # the activation's own FP32 evaluation (2^-40: results below that are not told
+    # from zero)
+    if act == "swiglu":
         d = d + 2.0 ** -20 * np.abs(out) + 2.0 ** -40
-    if act in ("gelu", "gelu_tanh"):
-        # 1 + erf and 1 + tanh lose to cancellation below zero: 2^-22 of v
-        d = d + 2.0 ** -22 * np.abs(y)
+    elif act != "none":
+        d = d + activation_error(y, act) * np.abs(out) + 2.0 ** -40
     if residual is not None:
         out = out + residual
         d = d + ULP * np.abs(out)
