@@ -45,7 +45,7 @@ class GfrTensor(ctypes.Structure):
 # torch dtype -> gfr_dtype (include/gfr.h)
 DTYPES = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1, torch.float4_e2m1fn_x2: 2,
           torch.float8_e8m0fnu: 3, torch.uint8: 4, torch.bfloat16: 5, torch.float32: 6,
-          torch.int64: 7, torch.int32: 8, torch.int8: 9, torch.float16: 11}
+          torch.int64: 7, torch.int32: 8, torch.int8: 9}
 
 
 def tensor_desc(t: Optional[torch.Tensor]):

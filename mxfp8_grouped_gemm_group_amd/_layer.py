@@ -15,10 +15,13 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _binding as b
-from ._binding import DTYPES, GfrError, _need
+from ._binding import GfrError, _need
 
 _P = ctypes.c_void_p
 _SIZE = ctypes.POINTER(ctypes.c_size_t)
+
+# The grouped calls take no float16: their binding refuses it by itself.
+DTYPES = {**b.DTYPES, torch.float16: 11}
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5}
 SCORINGS = {"softmax": 0, "sigmoid": 1}
