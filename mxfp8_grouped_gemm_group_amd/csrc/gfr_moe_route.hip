@@ -371,26 +371,21 @@ __global__ __launch_bounds__(1024) void route_few_kernel(RouteParams p) {
     __shared__ int bucket[kFewTokens * GFR_MAX_TOPK];
     __shared__ int hist[GFR_MAX_EXPERTS];
     __shared__ int pos[GFR_MAX_TOPK];
-    __shared__ int own_id[GFR_MAX_TOPK];
     __shared__ float own_weight[GFR_MAX_TOPK];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int me = blockIdx.x, n = p.T * p.k;
-    float z[V], next[V];
-    if (wave < p.T) load_logits(p, wave, lane, z);
-    for (int t = wave; t < p.T; t += 16) {
-        if (t + 16 < p.T) load_logits(p, t + 16, lane, next);
+    static_assert(kFewTokens <= 16, "a wave per token");
+    if (wave < p.T) {
         int id;
-        float weight;
+        float weight, z[V];
+        load_logits(p, wave, lane, z);
         choose<V, WIDE>(p, z, lane, WIDE ? keys + wave * p.E : nullptr, id, weight);
-#pragma unroll
-        for (int v = 0; v < V; ++v) z[v] = next[v];
         if (lane < p.k) {
-            bucket[t * p.k + lane] = id < 0 ? p.E : id;
-            if (t == me) {
-                own_id[lane] = id;
+            bucket[wave * p.k + lane] = id < 0 ? p.E : id;
+            if (wave == me) {
                 own_weight[lane] = weight;
-                p.ids[t * p.k + lane] = id;
-                p.weights[t * p.k + lane] = weight;
+                p.ids[wave * p.k + lane] = id;
+                p.weights[wave * p.k + lane] = weight;
             }
         }
     }
