@@ -8,6 +8,7 @@
 // ballot and strikes it out there.  Choosing by the logits compares FP32; with a bias
 // or expert groups the values compared are FP64, since two scores that differ
 // by less than an FP32 rounding would otherwise change places.
+// Weights are computed in FP64 and rounded once.
 //
 // With x, the pairs are sorted by expert, stably, by counting:
 //   few tokens    one launch, one block per token: every block chooses for all
@@ -48,9 +49,6 @@ __device__ __forceinline__ double dpp_f64(double x) {
     return __longlong_as_double(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-__device__ __forceinline__ float lane_value(float x, int lane) {
-    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), lane));
-}
 __device__ __forceinline__ double lane_value(double x, int lane) {
     const uint64_t b = __double_as_longlong(x);
     const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(b), lane);
@@ -90,6 +88,11 @@ __device__ __forceinline__ float from_ordered(uint32_t k) {
 __device__ __forceinline__ uint64_t ordered(double x) {
     const uint64_t b = __double_as_longlong(x == 0.0 ? 0.0 : x);
     return x > static_cast<double>(kNegInf) ? (b >> 63 ? ~b : b | uint64_t{1} << 63) : 0;
+}
+
+// What is subtracted from logits ahead of exp: their largest, or 0 where none is live.
+__device__ __forceinline__ double exponent_base(float top) {
+    return top == kNegInf ? 0.0 : static_cast<double>(top);
 }
 
 // Strikes out the experts of all but the topk_group best groups.  Lane q adds
@@ -175,59 +178,34 @@ __device__ __forceinline__ void load_logits(const RouteParams &p, int t, int lan
 // The choice of one token: lane j < k returns its j-th expert (-1: none) and
 // weight.  WIDE: FP64 keys (bias or groups); s as keep_groups.  Keys are compared
 // as ordered integers, an FP64 key's halves one after the other: a wave maximum
-// of words is six instructions, one of doubles some thirty.
+// of words is six instructions, one of doubles some thirty.  Scores, their sums and
+// the weights are FP64 in both forms; without FP64 keys only the chosen ones are
+// computed, a lane each.
 template <int V, bool WIDE>
 __device__ __forceinline__ void choose(const RouteParams &p, const float (&z)[V], int lane,
                                        double *s, int &id, float &weight) {
-    typedef typename std::conditional<WIDE, double, float>::type K;
-    float top = 0.0f;
-    if (!p.sigmoid || (!WIDE && p.renormalize)) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) m = max(m, ordered(z[v]));
-        top = from_ordered(wave_max(m));
-        if (top == kNegInf) top = 0.0f;
-    }
-    float bias[V] = {};
-    if (WIDE && p.bias)
-#pragma unroll
-        for (int v = 0; v < V; ++v) bias[v] = p.bias[min(lane * V + v, p.E - 1)];
-    K score[V];
-    double sum = 0.0;
-    if (p.sigmoid && WIDE) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            score[v] = static_cast<K>(1.0 / (1.0 + exp(-static_cast<double>(z[v]))));
-    } else if (p.sigmoid && top < 0.0f) {
-        // times exp(-top), which cancels: all scores together may be too small for
-        // FP32
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            score[v] = static_cast<K>(expf(z[v] - top) / (1.0f + expf(z[v])));
-    } else if (p.sigmoid) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) score[v] = static_cast<K>(1.0f / (1.0f + expf(-z[v])));
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            score[v] = WIDE ? static_cast<K>(exp(static_cast<double>(z[v]) - top))
-                            : static_cast<K>(expf(z[v] - top));
-            sum += score[v];
-        }
-    }
-    // softmax's denominator; without FP64 keys and with renormalize it cancels
-    K scale = 1;
-    if (!p.sigmoid && (WIDE || !p.renormalize)) {
-        sum = wave_sum(sum);
-        if (WIDE) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) score[v] = static_cast<K>(score[v] / sum);
-        } else {
-            scale = static_cast<K>(1.0 / sum);
-        }
-    }
     uint32_t hi[V], lo[V];
+    double score[V] = {};
     if (WIDE) {
+        if (p.sigmoid) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) score[v] = 1.0 / (1.0 + exp(-static_cast<double>(z[v])));
+        } else {
+            uint32_t m = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) m = max(m, ordered(z[v]));
+            const double top = exponent_base(from_ordered(wave_max(m)));
+            double sum = 0.0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) sum += score[v] = exp(z[v] - top);
+            sum = wave_sum(sum);
+#pragma unroll
+            for (int v = 0; v < V; ++v) score[v] /= sum;
+        }
+        float bias[V] = {};
+        if (p.bias)
+#pragma unroll
+            for (int v = 0; v < V; ++v) bias[v] = p.bias[min(lane * V + v, p.E - 1)];
         double key[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -246,10 +224,11 @@ __device__ __forceinline__ void choose(const RouteParams &p, const float (&z)[V]
         for (int v = 0; v < V; ++v) hi[v] = ordered(z[v]), lo[v] = 0;
     }
     id = -1;
-    K mine = 0, total = 0;
+    float logit = kNegInf, first = kNegInf;    // without WIDE: lane j's choice's, the largest
+    double mine = 0, total = 0;
     for (int j = 0; j < p.k; ++j) {
         uint32_t h = hi[0], l = lo[0];
-        K worth = score[0];
+        double worth = score[0];
         int slot = 0;
 #pragma unroll
         for (int v = 1; v < V; ++v)
@@ -264,18 +243,42 @@ __device__ __forceinline__ void choose(const RouteParams &p, const float (&z)[V]
         }
         const int holder = __ffsll(static_cast<unsigned long long>(holders)) - 1;
         const int at = __builtin_amdgcn_readlane(slot, holder);
-        const K value = lane_value(worth, holder);
-        total += value;
-        if (lane == j) id = holder * V + at, mine = value;
+        if (lane == j) id = holder * V + at;
+        if (WIDE) {
+            const double value = lane_value(worth, holder);
+            total += value;
+            if (lane == j) mine = value;
+        } else {
+            if (j == 0) first = from_ordered(most);
+            if (lane == j) logit = from_ordered(most);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (lane == holder && v == at) hi[v] = lo[v] = 0;
     }
+    if (!WIDE) {
+        // softmax's denominator cancels under renormalize; so does exp(-first) of
+        // sigmoids, which keeps far logits' scores from falling to zero together
+        const double top = exponent_base(first), d = logit;
+        if (!p.sigmoid)
+            mine = exp(d - top);
+        else if (p.renormalize && top < 0.0)
+            mine = exp(d - top) / (1.0 + exp(d));
+        else
+            mine = 1.0 / (1.0 + exp(-d));
+        if (id < 0) mine = 0.0;
+        if (p.renormalize) {
+            total = wave_sum(mine);
+        } else if (!p.sigmoid) {
+            double sum = 0.0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) sum += exp(z[v] - top);
+            mine /= wave_sum(sum);
+        }
+    }
     if (p.renormalize)   // a zero sum leaves zeros, a NaN goes through
-        mine = total == K(0) ? K(0) : mine / total;
-    else
-        mine *= scale;
-    weight = id < 0 ? 0.0f : static_cast<float>(mine * static_cast<K>(p.scaling));
+        mine = total == 0.0 ? 0.0 : mine / total;
+    weight = id < 0 ? 0.0f : static_cast<float>(mine * static_cast<double>(p.scaling));
 }
 
 // ---------------------------------------------------------------------------
