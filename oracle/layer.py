@@ -139,8 +139,10 @@ def moe_decode(x, w13, w2, ids, weights, shared=None, shared_weight=1.0):
         s = float(shared_weight) * np.asarray(shared, np.float64)
         out += s
         mags += np.abs(s)
-    # weighting, K splits (at most 8) and pairs: one rounding each
-    return out, bound + (8 * ids.shape[1] + 3) * ULP * mags
+    # joining the pairs' sums, which come in pieces of 64 rows of I or more; weighting;
+    # the shared term's product and addition
+    joins = ids.shape[1] * -(-I // 64)
+    return out, bound + (joins + 3) * ULP * mags
 
 
 def moe_route(logits, k, bias=None, scoring="softmax", n_group=1, topk_group=1, renormalize=True,
