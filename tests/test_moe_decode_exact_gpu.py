@@ -1,5 +1,7 @@
 """GPU results of gfr.moe_decode on inputs whose sums FP32 holds exactly
-(exact_inputs): equal to the definition, not near it."""
+(exact_inputs): equal to the definition, not near it, in every variant of the two
+products (test_dispatch asserts on the CPU that the sizes take the variants named
+here)."""
 import pytest
 import torch
 
@@ -31,3 +33,53 @@ def check(*sizes, **kw):
     (40, 2, 3, 128, 128, 64, 2), (64, 4, 16, 256, 576, 640, 1)])
 def test_silu_times_up_is_not_rounded(T, k, E, H, I, N, spread, fp8, t13, t2):
     check(T, k, E, H, I, N, fp8, t13, t2, per_expert=T % 2 == 0, spread=spread)
+
+
+# T, k, E, H, I, N, and of each product: waves of a block, whether these share a tile
+# and whether a wave takes several tiles.  Weights [K, N] and [N, K].
+KN = [
+    (1, 8, 128, 768, 256, 512, (4, 1, 0), (4, 1, 0)),
+    (2, 3, 5, 4160, 448, 1344, (4, 1, 0), (4, 1, 0)),
+    (3, 8, 8, 64, 1024, 6400, (4, 1, 0), (4, 0, 0)),
+    (8, 6, 8, 1088, 3200, 192, (4, 0, 0), (4, 1, 0)),
+    (16, 16, 128, 1088, 64, 192, (4, 0, 0), (4, 1, 0)),
+    (16, 8, 128, 512, 512, 512, (4, 1, 0), (4, 1, 0)),
+    (24, 8, 64, 64, 64, 6400, (4, 1, 0), (4, 0, 0)),
+    (48, 16, 256, 64, 64, 3264, (4, 1, 0), (4, 0, 1)),
+    (24, 16, 256, 64, 2048, 192, (4, 0, 1), (4, 0, 0)),
+    (16, 16, 64, 64, 3200, 192, (8, 0, 0), (4, 1, 0)),
+    (33, 16, 128, 64, 3200, 192, (8, 0, 1), (4, 0, 0)),
+    (16, 16, 64, 64, 64, 6400, (4, 1, 0), (8, 0, 0)),
+    (33, 16, 128, 64, 64, 6400, (4, 1, 0), (8, 0, 1)),
+    (17, 1, 1, 320, 192, 192, (4, 0, 0), (4, 0, 0)),
+    (48, 16, 64, 64, 2048, 192, (8, 0, 0), (4, 0, 0)),
+    (48, 16, 64, 64, 64, 6400, (4, 0, 0), (8, 0, 0)),
+    (64, 8, 8, 64, 3200, 6400, (4, 0, 0), (8, 0, 1)),
+]
+NK = [
+    (1, 8, 256, 512, 192, 320, (4, 0, 0), (4, 0, 0)),
+    (3, 6, 8, 64, 3200, 6400, (4, 0, 0), (4, 0, 1)),
+    (16, 8, 128, 512, 256, 512, (4, 0, 0), (4, 0, 0)),
+    (17, 6, 32, 64, 3200, 192, (4, 0, 1), (4, 0, 0)),
+    (8, 16, 16, 64, 3200, 192, (8, 0, 0), (4, 0, 0)),
+    (8, 16, 32, 64, 3200, 192, (8, 0, 1), (4, 0, 0)),
+    (8, 16, 16, 64, 64, 6400, (4, 0, 0), (8, 0, 0)),
+    (8, 16, 32, 64, 64, 6400, (4, 0, 0), (8, 0, 1)),
+    (17, 1, 1, 320, 192, 192, (4, 0, 0), (4, 0, 0)),
+    (64, 16, 16, 1088, 2048, 192, (4, 0, 1), (4, 0, 0)),
+    (64, 16, 16, 64, 3200, 192, (8, 0, 0), (4, 0, 0)),
+    (48, 16, 64, 64, 2048, 192, (8, 0, 1), (4, 0, 0)),
+    (48, 16, 16, 64, 320, 6400, (4, 0, 0), (4, 0, 1)),
+    (64, 16, 16, 64, 64, 6400, (4, 0, 0), (8, 0, 0)),
+    (48, 16, 64, 64, 64, 6400, (4, 0, 0), (8, 0, 1)),
+]
+
+
+@pytest.mark.parametrize("T, k, E, H, I, N, gate_up, down", KN)
+def test_weights_kn(T, k, E, H, I, N, gate_up, down):
+    check(T, k, E, H, I, N, "e4m3" if T % 3 else "e5m2", False, False, per_expert=T % 2 == 0)
+
+
+@pytest.mark.parametrize("T, k, E, H, I, N, gate_up, down", NK)
+def test_weights_nk(T, k, E, H, I, N, gate_up, down):
+    check(T, k, E, H, I, N, "e4m3" if T % 3 else "e5m2", True, True, per_expert=T % 2 == 0)
