@@ -8,6 +8,13 @@
 
 namespace gfr {
 
+// The kernel for a size (the tiled ones by their tile) and its K split.
+struct LinearChoice {
+    enum Kernel : int32_t { kRows, k256, k256x128, k128, k64 } kernel;
+    int32_t split;             // 0: too large for a grid
+};
+LinearChoice linear_choice(int64_t M, int64_t N, int64_t K, int act);
+
 struct LinearParams {
     const uint16_t *x;         // [M, K]
     const uint16_t *w;         // [N, K], or [2N, K] (swiglu)
@@ -17,11 +24,11 @@ struct LinearParams {
     float *partial;            // split K: [split][M][columns, to a multiple of 8]
     int32_t bias_f32, out_f32, f16, act;
     int32_t wide;              // rows of out and residual are whole, aligned 16 bytes
-    int32_t M, N, K, split;
+    int32_t M, N, K;
+    LinearChoice::Kernel kernel;
+    int32_t split;             // 1: no partial sums
 };
 
-// K splits of the tiled kernel for these sizes (1: no workspace).
-int linear_split(int64_t M, int64_t N, int64_t K, int act);
 hipError_t launch_linear(const LinearParams &p, hipStream_t stream);
 
 // One of moe_decode's two products: the K chunks whose partial sums are kept
@@ -46,6 +53,7 @@ struct DecodeParams {
     float shared_w;
     int32_t out_f32;
     int32_t T, k, E, H, I, N;
+    int32_t row_fragments;     // of 16 pairs, per group
     DecodePart gate_up, down;
 };
 
@@ -53,7 +61,8 @@ struct DecodeParams {
 // shapes.
 struct DecodeLayout {
     size_t gu, y, h, total;
-    bool activate;             // h is made by a launch of its own
+    int32_t activate;          // h is made by a launch of its own
+    int32_t row_fragments;
     DecodePart gate_up, down;
 };
 DecodeLayout decode_layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int64_t N,

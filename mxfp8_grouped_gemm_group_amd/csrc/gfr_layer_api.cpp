@@ -62,7 +62,9 @@ int resolve_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *b
     p.M = static_cast<int32_t>(M);
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);
-    p.split = gfr::linear_split(M, N, K, activation);
+    const gfr::LinearChoice choice = gfr::linear_choice(M, N, K, activation);
+    p.kernel = choice.kernel;
+    p.split = choice.split;
     return p.split > 0 ? GFR_OK : GFR_ERR_UNSUPPORTED;
 }
 
@@ -188,6 +190,7 @@ int gfr_moe_decode(const gfr_tensor *x, const gfr_tensor *w13, const gfr_tensor 
     p.gu = reinterpret_cast<float *>(ws + d.gu);
     p.y = reinterpret_cast<float *>(ws + d.y);
     p.h = d.activate ? reinterpret_cast<uint16_t *>(ws + d.h) : nullptr;
+    p.row_fragments = d.row_fragments;
     p.gate_up = d.gate_up;
     p.down = d.down;
     p.T = static_cast<int32_t>(T);

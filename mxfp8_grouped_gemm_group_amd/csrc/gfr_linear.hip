@@ -742,16 +742,13 @@ hipError_t launch_tiles(const LinearParams &p, hipStream_t stream) {
 // than the weights come at 4.5 TB/s.  (Rows against
 // tiles, N x K: 1 x 4096 x 4096 9.3 us against 11; 16 x 256 x 7168 15.1 against
 // 9.5; 32 x 1024 x 1024 5.3 against 7.0; 64 x 4096 x 4096 21.3 against 13.0.)
-struct Choice {
-    enum Kind { kRows, k256, k256x128, k128, k64 } kind;
-    int split;     // 0: too large for a grid
-};
 constexpr int64_t kMaxBlocks = (int64_t{1} << 23) - 8;    // 2^32 threads, up to 512 a block
-Choice choose_kernel(int64_t M, int64_t N, int64_t K, bool swiglu) {
+LinearChoice choose_kernel(int64_t M, int64_t N, int64_t K, bool swiglu) {
+    typedef LinearChoice Choice;
     const int64_t rows = swiglu ? 2 * N : N, steps = (K + 63) / 64;
     const bool aligned = K % 8 == 0;
     struct Tile {
-        Choice::Kind kind;
+        Choice::Kernel kernel;
         int64_t bm, bn;
         double us;     // per step
     };
@@ -772,17 +769,17 @@ Choice choose_kernel(int64_t M, int64_t N, int64_t K, bool swiglu) {
         best = {Choice::kRows, 1};
     }
     for (const Tile &t : tiles) {
-        if (!aligned && (t.kind == Choice::k256 || t.kind == Choice::k256x128)) continue;
+        if (!aligned && (t.kernel == Choice::k256 || t.kernel == Choice::k256x128)) continue;
         const int64_t n = ((M + t.bm - 1) / t.bm) * ((rows + t.bn - 1) / t.bn);
         if (n > kMaxBlocks) continue;
-        for (int split = 1; split <= (t.kind == Choice::k128 || t.kind == Choice::k64 ? 8 : 1);
+        for (int split = 1; split <= (t.kernel == Choice::k128 || t.kernel == Choice::k64 ? 8 : 1);
              ++split) {
             if (split > 1 && (steps / split < 6 || n * split > 256)) break;
             const double rounds = static_cast<double>((n * split + 255) / 256);
             double us = rounds * (4.0 + t.us * static_cast<double>((steps + split - 1) / split));
             us = both(us, 2.0 + memory);
             if (split > 1) us += 2.0 + 8.0 * static_cast<double>(M * rows * split) / 4e6;
-            if (us < least) least = us, best = {t.kind, split};
+            if (us < least) least = us, best = {t.kernel, split};
         }
     }
     return best;
@@ -790,20 +787,20 @@ Choice choose_kernel(int64_t M, int64_t N, int64_t K, bool swiglu) {
 
 template <bool F16, bool ALIGNED, bool SWIGLU>
 hipError_t launch_linear_t(const LinearParams &p, hipStream_t stream) {
-    switch (choose_kernel(p.M, p.N, p.K, SWIGLU).kind) {
-    case Choice::kRows:
+    switch (p.kernel) {
+    case LinearChoice::kRows:
         if (p.M <= 16) return launch_rows<F16, ALIGNED, SWIGLU, 1>(p, stream);
         if (p.M <= 32) return launch_rows<F16, ALIGNED, SWIGLU, 2>(p, stream);
         return launch_rows<F16, ALIGNED, SWIGLU, 4>(p, stream);
-    case Choice::k256:
+    case LinearChoice::k256:
         if constexpr (ALIGNED)
             return launch_tiles<F16, ALIGNED, SWIGLU, 256, 256, 128, 64>(p, stream);
         return hipErrorInvalidValue;
-    case Choice::k256x128:
+    case LinearChoice::k256x128:
         if constexpr (ALIGNED)
             return launch_tiles<F16, ALIGNED, SWIGLU, 256, 128, 64, 64>(p, stream);
         return hipErrorInvalidValue;
-    case Choice::k128:
+    case LinearChoice::k128:
         return launch_tiles<F16, ALIGNED, SWIGLU, 128, 128, 64, 64>(p, stream);
     default:
         return launch_tiles<F16, ALIGNED, SWIGLU, 64, SWIGLU ? 128 : 64, 32, SWIGLU ? 64 : 32>(
@@ -819,8 +816,8 @@ hipError_t launch_linear_a(const LinearParams &p, hipStream_t stream) {
 
 }  // namespace
 
-int linear_split(int64_t M, int64_t N, int64_t K, int act) {
-    return choose_kernel(M, N, K, act == GFR_ACT_SWIGLU).split;
+LinearChoice linear_choice(int64_t M, int64_t N, int64_t K, int act) {
+    return choose_kernel(M, N, K, act == GFR_ACT_SWIGLU);
 }
 
 hipError_t launch_linear(const LinearParams &p, hipStream_t stream) {

@@ -803,6 +803,7 @@ DecodeLayout decode_layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I
     if (full > 1.0) groups *= full;
     d.gate_up = part_shape(groups, pairs / groups, H, 2 * I, transpose_w13, rg, 1);
     d.down = part_shape(groups, pairs / groups, I, N, transpose_w2, rg, 3);
+    d.row_fragments = rg;
     d.gu = 0;
     d.y = up(sizeof(float) * d.gate_up.chunks * pairs * 2 * I);
     d.h = d.y + up(sizeof(float) * d.down.chunks * pairs * N);
@@ -813,12 +814,11 @@ DecodeLayout decode_layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I
 
 hipError_t launch_decode(const DecodeParams &p, int transpose_w13, int transpose_w2, int e5m2,
                          hipStream_t stream) {
-    const int rg = row_fragments(p.T, p.k, p.E);
     if (e5m2) {
-        if (rg == 1) return launch_decode_t<1, 1>(p, transpose_w13, transpose_w2, stream);
+        if (p.row_fragments == 1) return launch_decode_t<1, 1>(p, transpose_w13, transpose_w2, stream);
         return launch_decode_t<1, 2>(p, transpose_w13, transpose_w2, stream);
     }
-    if (rg == 1) return launch_decode_t<0, 1>(p, transpose_w13, transpose_w2, stream);
+    if (p.row_fragments == 1) return launch_decode_t<0, 1>(p, transpose_w13, transpose_w2, stream);
     return launch_decode_t<0, 2>(p, transpose_w13, transpose_w2, stream);
 }
 
