@@ -423,7 +423,8 @@ int gfr_linear_workspace_size(const gfr_tensor *x, const gfr_tensor *w, const gf
  * gfr_gemm1_swiglu_quant's and gmm_finalize_routing's products on the same
  * weights, but with bf16 activations (nothing is quantised: silu(gate) * up
  * stays in FP32, the only rounding to fewer bits is out's), and reading only the
- * chosen experts' weights.  Longer batches take the grouped calls.
+ * chosen experts' weights.  (A weight, code times scale, below 2^-133 is rounded to
+ * a multiple of that, and infinite from 2^128 on.)  Longer batches take the grouped calls.
  *
  *  x             BF16 [T, H], T <= GFR_DECODE_MAX_TOKENS.
  *  w13           FP8_E4M3FN or FP8_E5M2 [E, H, 2I] (gate columns, then up),

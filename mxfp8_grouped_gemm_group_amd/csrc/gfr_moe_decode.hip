@@ -3,8 +3,9 @@
 // At these token counts the bytes of the chosen experts' weights bound the
 // time: each is read once, in FP8, and turned into bf16 MFMA operands in
 // registers (v_cvt_scalef32_pk_bf16_*, which multiplies by the block's E8M0
-// scale on the way; exact, since bf16 has more mantissa bits than FP8 and E8M0's
-// exponent range).  The pairs (token, expert) of one expert are the columns of
+// scale on the way).  That is exact from 2^-133, bf16's smallest value, to below
+// 2^128, where FP32 ends too: bf16 has more mantissa bits than FP8, and any code is a
+// multiple of 2^-133 at scales from 2^-124 (E4M3) or 2^-117 (E5M2) on.  The pairs (token, expert) of one expert are the columns of
 // v_mfma_f32_16x16x32_bf16's second operand, 16 to a fragment.
 //
 //   product_kernel  (twice)  partial sums of a K chunk: gu = x w13, then
@@ -190,6 +191,8 @@ __device__ __forceinline__ bool make_plan(const DecodeParams &p, Plan &s, uint32
 // Weight streams
 // ---------------------------------------------------------------------------
 
+// The scale operand of the conversion, which takes the exponent field alone: 2^(code -
+// 127) also for code 0, NaN for 255.
 __device__ __forceinline__ float e8m0(uint32_t code) { return __uint_as_float(code << 23); }
 
 // Two FP8 values (the low or high half of w) times scale, in bf16.

@@ -83,3 +83,40 @@ def test_weights_kn(T, k, E, H, I, N, gate_up, down):
 @pytest.mark.parametrize("T, k, E, H, I, N, gate_up, down", NK)
 def test_weights_nk(T, k, E, H, I, N, gate_up, down):
     check(T, k, E, H, I, N, "e4m3" if T % 3 else "e5m2", True, True, per_expert=T % 2 == 0)
+
+
+# E8M0's ends: code 0 is 2^-127, and a weight is exact while it is a multiple of 2^-133,
+# bf16's smallest value (any code times 2^-124 for E4M3, 2^-117 for E5M2)
+@pytest.mark.parametrize("t", [False, True])
+@pytest.mark.parametrize("fp8, exact_from, values", [
+    ("e4m3", 3, [1.0, 1.875, 448.0, 2.0 ** -6, 1.75 * 2.0 ** -6, 1.5 * 2.0 ** -8, 2.0 ** -9]),
+    ("e5m2", 10, [1.0, 1.75, 57344.0, 2.0 ** -14, 1.5 * 2.0 ** -15, 2.0 ** -16])])
+def test_smallest_and_largest_scales(fp8, exact_from, values, t):
+    x = torch.zeros(1, 64)
+    x[0, 0], x[0, 1] = 2.0 ** 60, 2.0 ** 50       # gate and up: h = 2^110
+    w13 = torch.zeros(1, 64, 128)
+    w13[0, 0, :64] = w13[0, 1, 64:] = 1
+    s13 = torch.full((1, 128, 2), 127, dtype=torch.uint8)
+    flip = lambda v, *dims: (v.permute(*dims) if t else v).contiguous().to(DEV)
+    for value in values:
+        w2 = torch.zeros(1, 64, 64)
+        w2[0, 0] = value
+        # h * weight stays below 2^128 (codes in order, then up to 2^4)
+        codes = torch.tensor([*range(40), *range(100, 124)], dtype=torch.uint8)
+        for s in (codes, codes + 8 if value <= 1 else codes):
+            s2 = torch.full((1, 64, 2), 127, dtype=torch.uint8)
+            s2[0, :, 0] = s
+            out = gfr.moe_decode(
+                x.bfloat16().to(DEV), flip(w13.to(exact_inputs.FP8[fp8]), 0, 2, 1),
+                flip(s13, 1, 0, 2), flip(w2.to(exact_inputs.FP8[fp8]), 0, 2, 1),
+                flip(s2, 1, 0, 2), torch.zeros(1, 1, dtype=torch.int32, device=DEV),
+                torch.ones(1, 1, device=DEV), transpose_w13=t, transpose_w2=t,
+                out_dtype=torch.float32).double().cpu()[0]
+            want = value * 2.0 ** (110.0 + s.double() - 127)
+            assert want.max() < 2.0 ** 128
+            smallest = value * 2.0 ** (s.double() - 127)
+            whole = (smallest / 2.0 ** -133) % 1 == 0
+            assert torch.equal(out[whole], want[whole]), (fp8, value)
+            assert whole[s >= exact_from].all()
+            # below, off by at most one such step
+            assert ((out - want).abs() <= 2.0 ** (110 - 133)).all()
