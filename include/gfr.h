@@ -443,7 +443,8 @@ int gfr_linear_workspace_size(const gfr_tensor *x, const gfr_tensor *w, const gf
  *  opts          workspace and workspace_bytes (gfr_moe_decode_workspace_size,
  *                256-byte aligned), status_dev; the other fields are ignored.
  *
- * The summation order is fixed: two calls give the same bits.  Calls that
+ * The sizes and a token's own experts fix the summation order: two calls give the
+ * same bits, and so does a token whose neighbours choose otherwise.  Calls that
  * overlap in time need workspaces of their own.  Needs H, I and N multiples of
  * 64, E <= GFR_MAX_EXPERTS and T * k <= 1024 (GFR_ERR_UNSUPPORTED); data
  * 16-byte aligned (GFR_ERR_BAD_ALIGNMENT).  Other errors as gfr_linear.

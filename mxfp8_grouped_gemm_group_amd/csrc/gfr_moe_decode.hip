@@ -472,8 +472,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void product_kernel(DecodeParams p)
     int tile = SHARED ? blockIdx.x : blockIdx.x * d.run * kWaves + wave;
     const int mine = max(min(d.run, (tiles - tile + kWaves - 1) / kWaves), 0);
     // Blocks side by side begin at different steps and go round: rows and
-    // columns a power of two apart share memory channels.
-    const int turn = SHARED ? wave : (blockIdx.x + blockIdx.z) % steps;
+    // columns a power of two apart share memory channels.  (By the expert and not by
+    // the group: where other tokens' groups lie must not change a token's sums.)
+    const int turn = SHARED ? wave : (blockIdx.x + e) % steps;
     const int total = SHARED ? max(steps - wave + kWaves - 1, 0) / kWaves : mine * steps;
     int fetch_step = turn, fetch_n0 = tile * kTile, fetched = 0;
     typename Stream::Stage f[Stream::kDepth];
