@@ -249,7 +249,8 @@ def moe_route(logits, top_k, *, x=None, bias=None, scoring="softmax", n_group=1,
 
     logits float32 or bfloat16 [T, E]; scoring "softmax" or "sigmoid"; bias
     float32 [E] is added to the scores for the choice only; n_group > 1 keeps
-    the topk_group best of n_group equal runs of experts; the weights are the
+    the topk_group best of n_group equal runs of experts, by the sum of each
+    run's two largest scores (with bias; not by the largest one); the weights are the
     chosen scores, summing to 1 under renormalize, times scaling.
 
     Returns topk_ids int32 [T, k] (-1 where a row has too few live experts),

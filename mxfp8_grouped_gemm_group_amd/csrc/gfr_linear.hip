@@ -14,9 +14,11 @@
 //                in registers while the present one is multiplied).  What a CU
 //                takes in from L2 and LDS bounds it, so tiles are as large as
 //                the size fills 256 CUs with.  (4096 x 7168 x 4096 with
-//                residual: 235 us, 1.02 PFLOP/s.)  Few tiles split K; a second
+//                residual: 237 us, 1.01 PFLOP/s.)  Few tiles split K; a second
 //                launch then adds the partial sums and finishes.  (128 x 4096 x
-//                4096: 18 us split eight ways, 29 us not split.)
+//                4096: 64 x 64 tiles split two ways, 17.7 us.)  K not a multiple
+//                of 8 is loaded in words and shifted: 1.6 to 2.8 times as long
+//                (24 x 4096 x 4099 30 us, x 4096 18).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

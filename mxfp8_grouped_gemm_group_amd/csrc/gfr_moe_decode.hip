@@ -5,7 +5,8 @@
 // registers (v_cvt_scalef32_pk_bf16_*, which multiplies by the block's E8M0
 // scale on the way).  That is exact from 2^-133, bf16's smallest value, to below
 // 2^128, where FP32 ends too: bf16 has more mantissa bits than FP8, and any code is a
-// multiple of 2^-133 at scales from 2^-124 (E4M3) or 2^-117 (E5M2) on.  The pairs (token, expert) of one expert are the columns of
+// multiple of 2^-133 at scales from 2^-124 (E4M3) or 2^-117 (E5M2) on.  The pairs
+// (token, expert) of one expert are the columns of
 // v_mfma_f32_16x16x32_bf16's second operand, 16 to a fragment.
 //
 //   product_kernel  (twice)  partial sums of a K chunk: gu = x w13, then
@@ -23,7 +24,7 @@
 // loads in flight across tile ends and no barrier.  Chunks and runs are chosen
 // (part_shape) so that even one token's few experts keep every CU's loads
 // in flight, and so that a long batch writes few partial sums.  (64 tokens of 32
-// experts of 4096 x 8192, 3.2 GB: 516 us, 6.2 TB/s.  One token, 8 of 256 experts of
+// experts of 4096 x 8192, 3.2 GB: 530 us, 6.1 TB/s.  One token, 8 of 256 experts of
 // 2048 x 512, 25 MB: 15.8 us, of which the two products' and the sum's latencies
 // one after the other are most.)
 //
@@ -49,9 +50,9 @@ constexpr int kMaxPairs = 1024;
 // product's blocks, which otherwise each form their rows of it: 96 pairs of 8
 // experts 145 -> 135 us, 256 pairs 137 -> 113, but 8 pairs 21 -> 23.
 constexpr int kActivatePairs = 32;
-// LDS per wave for a chunk's operand rows.  Of three terms as much as two blocks of
-// four waves can have beside their plans (8 tokens of 16 experts of 4096 x 6144 with
-// 16 KB 169 us, with this 161).
+// LDS per wave for a chunk's operand rows and their padding.  Of three terms as much
+// as two blocks of four waves can have beside their plans (8 tokens of 16 experts of
+// 4096 x 6144 with 16 KB 169 us, with this 161).
 constexpr int operand_bytes(int terms) { return terms == 1 ? 16512 : 18624; }
 
 // ---------------------------------------------------------------------------
@@ -701,7 +702,8 @@ constexpr int lines(int rg) { return rg == 1 ? 2 : 1; }
 // waves share a tile and split its steps: four times the blocks, and no more
 // partial sums (one token, 8 of 256 experts of 2048 x 512: 21.3 -> 15.8 us; 2 of 8
 // of 4096 x 7168: 53.7 -> 46.8).  [N, K] tiles are a quarter as wide and fill the CUs
-// without.
+// without.  (These pairs of times were measured with the down product's operand in two
+// terms; three cost it up to 8 %.)
 DecodePart part_shape(double groups, double rows, int64_t K, int64_t cols, int transpose, int rg,
                       int terms) {
     const int64_t step = transpose ? 128 * lines(rg) : 64;
@@ -819,7 +821,8 @@ DecodeLayout decode_layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I
 hipError_t launch_decode(const DecodeParams &p, int transpose_w13, int transpose_w2, int e5m2,
                          hipStream_t stream) {
     if (e5m2) {
-        if (p.row_fragments == 1) return launch_decode_t<1, 1>(p, transpose_w13, transpose_w2, stream);
+        if (p.row_fragments == 1)
+            return launch_decode_t<1, 1>(p, transpose_w13, transpose_w2, stream);
         return launch_decode_t<1, 2>(p, transpose_w13, transpose_w2, stream);
     }
     if (p.row_fragments == 1) return launch_decode_t<0, 1>(p, transpose_w13, transpose_w2, stream);

@@ -24,7 +24,8 @@ DECODE = [(1, 2, 4, 128, 512, 512, 1), (5, 2, 3, 4160, 448, 1344, 1), (40, 2, 3,
 def test_decode_notices_silu_times_up_in_fewer_bits(T, k, E, H, I, N, spread):
     _, want, p = exact_inputs.decode_case(T, k, E, H, I, N, spread=spread)
     for h_of in (bf16, two_terms):
-        got, _, _ = exact_inputs.decode_expected(p["x"], p["w13"], p["w2"], p["ids"], p["weights"], h_of)
+        got, _, _ = exact_inputs.decode_expected(p["x"], p["w13"], p["w2"], p["ids"],
+                                                 p["weights"], h_of)
         assert (got != want).mean() > 0.25
     h = np.abs(p["h"][p["h"] != 0])
     assert np.log2(h).max() >= 17
