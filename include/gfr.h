@@ -95,7 +95,8 @@ enum gfr_dtype {
     GFR_DT_I32 = 8,
     GFR_DT_I8 = 9,
     GFR_DT_INT4X2 = 10,      /* signed 4-bit (two's complement) elements, packed */
-    GFR_DT_F16 = 11          /* IEEE half (gfr_linear, gfr_moe_route's x) */
+    GFR_DT_F16 = 11          /* IEEE half (gfr_linear, gfr_moe_route's x, the 16-bit
+                                grouped products, gfr_lora_linear) */
 };
 
 /* A tensor argument: device pointer to contiguous row-major storage of
@@ -523,6 +524,68 @@ int gfr_moe_route(const gfr_tensor *logits, const gfr_tensor *bias, int scoring,
 /* Workspace bytes of gfr_moe_route with x for T tokens and E experts (0
  * without x, and for few tokens).  Pure host arithmetic. */
 int gfr_moe_route_workspace_size(int64_t T, int64_t E, int64_t k, size_t *bytes);
+
+/* ======================================================================== *
+ * Products whose weight is chosen by the row, in 16 bits: a row's expert    *
+ * (with gradients) or the adapter of a row's request.  Descriptor calls     *
+ * with the conventions above.                                               *
+ * ======================================================================== */
+
+/*
+ * gfr_grouped_linear — rows sorted by expert times their expert's weights:
+ *
+ *   out[t, n] = sum_k x[t, k] * w[e, k, n]        t in expert e's range
+ *
+ * accumulated in FP32, rounded once to out's type.  The unquantised experts of a
+ * MoE block (rows in moe_route's order: its row_index and group_list), and with
+ * the other layout of the same weights the gradient by x.
+ *
+ *  x           BF16 or F16 [M, K], rows sorted by expert.
+ *  w           x's dtype [E, K, N], or [E, N, K] when transpose_w.
+ *  group_list  I64 [E], format per group_list_type.
+ *  transpose_w 0 or 1.
+ *  fill        0: rows of no expert's range are left as they are in out; 1: they
+ *              are cleared.
+ *  out         x's dtype or F32 [M, N]; must not overlap the inputs.
+ *  opts        NULL, or status_dev (GFR_DEV_BAD_GROUP_LIST: a count below zero or
+ *              above M is taken as 0 or M, and what reaches beyond M is cut off); the
+ *              other fields are ignored.
+ *
+ * Any M, N >= 0 and K >= 1 (K, and N with [E, K, N] weights, multiples of 8 are the
+ * fast path).  M = 0 or N = 0 is a no-op.  The sizes fix the summation order of a
+ * row, whatever group sizes surround it: two calls give the same bits.  Errors:
+ * GFR_ERR_NULL_ARG, GFR_ERR_BAD_DTYPE, GFR_ERR_BAD_RANK, GFR_ERR_BAD_SHAPE,
+ * GFR_ERR_BAD_ARG, GFR_ERR_UNSUPPORTED (E outside [1, GFR_MAX_EXPERTS], M > 2^30, K or
+ * N > 2^21), GFR_ERR_BAD_ALIGNMENT (x, w or out not 16-byte, group_list not 8-byte
+ * aligned), GFR_ERR_HIP.
+ */
+int gfr_grouped_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *group_list,
+                       int group_list_type, int transpose_w, int fill, const gfr_tensor *out,
+                       void *stream, const gfr_options *opts);
+
+/*
+ * gfr_grouped_linear_wgrad — the gradient of gfr_grouped_linear by its weights:
+ *
+ *   out[e, k, n] (+)= sum over t in expert e's range of x[t, k] * dy[t, n]
+ *
+ * accumulated in FP32, rounded once to out's type.
+ *
+ *  x           BF16 or F16 [M, K], rows sorted by expert.
+ *  dy          x's dtype [M, N].
+ *  group_list, group_list_type, opts: as gfr_grouped_linear.
+ *  transpose_w 0: out is [E, K, N]; 1: [E, N, K].
+ *  accumulate  0: out is overwritten (zeros for an empty range); 1: the sums are
+ *              added to it.
+ *  out         x's dtype or F32; must not overlap the inputs.
+ *
+ * Any M, K, N >= 0 (K and N multiples of 8 are the fast path); rows of no range do
+ * not take part.  The sizes of a range fix its summation order.  Errors as
+ * gfr_grouped_linear.
+ */
+int gfr_grouped_linear_wgrad(const gfr_tensor *x, const gfr_tensor *dy,
+                             const gfr_tensor *group_list, int group_list_type, int transpose_w,
+                             int accumulate, const gfr_tensor *out, void *stream,
+                             const gfr_options *opts);
 
 /* ======================================================================== *
  * Raw calls: device pointers plus sizes, semantics as the descriptor calls *

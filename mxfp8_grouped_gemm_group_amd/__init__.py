@@ -11,11 +11,11 @@ from ._binding import (DEV_BAD_EXPERT, DEV_BAD_GROUP_LIST, DEV_BAD_ROW_INDEX, Gf
                        gemm1_swiglu_quant, gmm_finalize_routing,
                        gmm_finalize_routing_det_noalloc, load_library, status_string,
                        w4a8_finalize_routing, workspace_size)
-from ._layer import (DECODE_MAX_TOKENS, RouteResult, linear, moe_decode,
-                     moe_decode_workspace_size, moe_route)
+from ._layer import (DECODE_MAX_TOKENS, RouteResult, grouped_linear, grouped_linear_wgrad, linear,
+                     moe_decode, moe_decode_workspace_size, moe_route)
 
 __all__ = ["gmm_finalize_routing", "gmm_finalize_routing_det_noalloc", "gemm1_swiglu_quant",
            "w4a8_finalize_routing", "workspace_size", "status_string", "load_library",
            "GfrError", "DEV_BAD_GROUP_LIST", "DEV_BAD_ROW_INDEX", "DEV_BAD_EXPERT", "linear",
            "moe_decode", "moe_decode_workspace_size", "moe_route", "RouteResult",
-           "DECODE_MAX_TOKENS"]
+           "DECODE_MAX_TOKENS", "grouped_linear", "grouped_linear_wgrad"]

@@ -1,6 +1,7 @@
 """ctypes binding of the rest of the MoE block (include/gfr.h): the dense
 product with its epilogue, the router's choice with the tokens in expert order,
-and the experts for a few tokens.
+the experts for a few tokens, and the experts' products in 16 bits with their
+gradients.
 
 Argument marshalling only, like ``_binding``: dtypes, ranks and shapes are
 checked by the library, which raises GfrError here.
@@ -8,6 +9,7 @@ checked by the library, which raises GfrError here.
 from __future__ import annotations
 
 import array
+import contextlib
 import ctypes
 import functools
 from typing import NamedTuple, Optional
@@ -43,9 +45,12 @@ def _lib():
         lib.gfr_moe_decode_workspace_size.argtypes = [ctypes.c_int64] * 6 + [i, i, _SIZE]
         lib.gfr_moe_route.argtypes = [_P] * 2 + [i] * 4 + [ctypes.c_float] + [_P] * 10
         lib.gfr_moe_route_workspace_size.argtypes = [ctypes.c_int64] * 3 + [_SIZE]
+        lib.gfr_grouped_linear.argtypes = [_P] * 3 + [i] * 3 + [_P] * 3
+        lib.gfr_grouped_linear_wgrad.argtypes = [_P] * 3 + [i] * 3 + [_P] * 3
         for f in (lib.gfr_linear, lib.gfr_linear_workspace_size, lib.gfr_moe_decode,
                   lib.gfr_moe_decode_workspace_size, lib.gfr_moe_route,
-                  lib.gfr_moe_route_workspace_size):
+                  lib.gfr_moe_route_workspace_size, lib.gfr_grouped_linear,
+                  lib.gfr_grouped_linear_wgrad):
             f.restype = i
         _ready = True
     return lib
@@ -301,3 +306,116 @@ def _route_workspace_size(T: int, E: int, k: int) -> int:
     need = ctypes.c_size_t(0)
     _check(_lib().gfr_moe_route_workspace_size(T, E, k, ctypes.byref(need)))
     return need.value
+
+
+def _grouped(x, w, group_list, group_list_type, transpose_w, out_dtype, out, status):
+    index = _device(x, "x")
+    _need(x.dim() == 2 and w.dim() == 3, "x must be [M, K] and w 3-D")
+    tensors, made, fill = (x, w, group_list), (), 0
+    if out is None:
+        n = w.shape[1] if transpose_w else w.shape[2]
+        out = x.new_empty((x.shape[0], n), dtype=out_dtype or x.dtype)
+        made, fill = (out,), 1
+    else:
+        tensors += (out,)
+    words, (px, pw, pg, po), opts = _pack(index, tensors, made, None, status)
+    _check(_lib().gfr_grouped_linear(px, pw, pg, group_list_type, int(bool(transpose_w)), fill, po,
+                                     _raw_stream(index), opts))
+    return out
+
+
+def _wgrad(x, dy, group_list, group_list_type, transpose_w, out_dtype, out, accumulate, status):
+    index = _device(x, "x")
+    _need(x.dim() == 2 and dy.dim() == 2, "x must be [M, K] and dy [M, N]")
+    tensors, made = (x, dy, group_list), ()
+    if out is None:
+        shape = (dy.shape[1], x.shape[1]) if transpose_w else (x.shape[1], dy.shape[1])
+        out = x.new_empty((group_list.numel(), *shape), dtype=out_dtype or x.dtype)
+        made = (out,)
+    else:
+        tensors += (out,)
+    words, (px, pd, pg, po), opts = _pack(index, tensors, made, None, status)
+    _check(_lib().gfr_grouped_linear_wgrad(px, pd, pg, group_list_type, int(bool(transpose_w)),
+                                           int(bool(accumulate)), po, _raw_stream(index), opts))
+    return out
+
+
+class _GroupedLinear(torch.autograd.Function):
+    """grouped_linear with its two gradients, each one launch."""
+
+    @staticmethod
+    def forward(ctx, x, w, group_list, group_list_type, transpose_w, out_dtype, status):
+        ctx.save_for_backward(x, w, group_list)
+        ctx.args = group_list_type, transpose_w
+        return _grouped(x, w, group_list, group_list_type, transpose_w, out_dtype, None, status)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, w, group_list = ctx.saved_tensors
+        group_list_type, transpose_w = ctx.args
+        # (an FP32 result's gradient comes in FP32: the products take x's type)
+        dy = dy.to(x.dtype).contiguous()
+        away = _elsewhere(x.get_device(), None)
+        with away if away is not None else contextlib.nullcontext():
+            dx = dw = None
+            if ctx.needs_input_grad[0]:
+                dx = _grouped(dy, w, group_list, group_list_type, not transpose_w, x.dtype, None,
+                              None)
+            if ctx.needs_input_grad[1]:
+                dw = _wgrad(x, dy, group_list, group_list_type, transpose_w, w.dtype, None, False,
+                            None)
+        return dx, dw, None, None, None, None, None
+
+
+def grouped_linear(x, w, group_list, group_list_type, *, transpose_w=False, out_dtype=None,
+                   out=None, status=None, stream=None):
+    """Rows sorted by expert times their expert's 16-bit weights, accumulated in
+    FP32 (include/gfr.h, gfr_grouped_linear); returns out.
+
+    x bfloat16 or float16 [M, K]; w x's dtype [E, K, N], or [E, N, K] with
+    transpose_w; group_list int64 [E] (0: prefix sums, 1: counts); out_dtype x's
+    (default) or float32.  Rows of no expert's range are left as they were in
+    ``out``, and zeros in one that the call allocates.  ``status`` (int32, 1
+    element) receives DEV_BAD_GROUP_LIST.
+
+    Differentiable by x and w (then ``out`` has to be None): their gradients have
+    their dtypes; dy is rounded to x's dtype first where out_dtype is float32.
+    Gradients kept in float32 take grouped_linear_wgrad.  A step that is captured
+    into a graph needs leaves of which no eager graph is alive, as every autograd
+    function does.
+    """
+    index = _device(x, "x")
+    _need(out is None or out_dtype is None or out.dtype == out_dtype, "out must have out_dtype")
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return grouped_linear(x, w, group_list, group_list_type, transpose_w=transpose_w,
+                                  out_dtype=out_dtype, out=out, status=status)
+    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
+        _need(out is None, "out must be None where a gradient is wanted")
+        return _GroupedLinear.apply(x, w, group_list, int(group_list_type), bool(transpose_w),
+                                    out_dtype, status)
+    return _grouped(x, w, group_list, int(group_list_type), transpose_w, out_dtype, out, status)
+
+
+def grouped_linear_wgrad(x, dy, group_list, group_list_type, *, transpose_w=False, out_dtype=None,
+                         out=None, accumulate=False, status=None, stream=None):
+    """The gradient of grouped_linear by its weights (include/gfr.h,
+    gfr_grouped_linear_wgrad): out[e] = x[rows of e].T @ dy[rows of e], or its
+    transpose with transpose_w; returns out.
+
+    x bfloat16 or float16 [M, K], dy x's dtype [M, N]; out_dtype x's (default) or
+    float32; ``accumulate`` adds to ``out`` (which must be given).
+    """
+    index = _device(x, "x")
+    _need(out is None or out_dtype is None or out.dtype == out_dtype, "out must have out_dtype")
+    _need(out is not None or not accumulate, "accumulate needs an out to add to")
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return grouped_linear_wgrad(x, dy, group_list, group_list_type,
+                                        transpose_w=transpose_w, out_dtype=out_dtype, out=out,
+                                        accumulate=accumulate, status=status)
+    return _wgrad(x, dy, group_list, int(group_list_type), transpose_w, out_dtype, out, accumulate,
+                  status)

@@ -1,6 +1,6 @@
 // Internal interface between the host API (gfr_layer_api.cpp) and the kernels
-// of the dense product, the few-token experts and the router (gfr_linear.hip,
-// gfr_moe_decode.hip, gfr_moe_route.hip).
+// of the dense product, the few-token experts, the router and the 16-bit grouped
+// products (gfr_linear.hip, gfr_moe_decode.hip, gfr_moe_route.hip, gfr_grouped.hip).
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -91,5 +91,21 @@ struct RouteParams {
 // Workspace bytes of moe_route with x.
 size_t route_workspace(int64_t T, int64_t E, int64_t k);
 hipError_t launch_route(const RouteParams &p, hipStream_t stream);
+
+struct GroupedParams {
+    const uint16_t *x;         // [M, K]
+    const uint16_t *w;         // forward: [E, K, N] ([E, N, K] transposed); wgrad: [M, N]
+    void *out;                 // forward: [M, N]; wgrad: [E, K, N]
+    const int64_t *group_list; // [E]
+    int32_t *status;           // may be null
+    int32_t wgrad, transpose, cumsum;
+    int32_t fill;              // forward: rows of no group are cleared
+    int32_t accumulate;        // wgrad: out is added to
+    int32_t f16, out_f32;
+    int32_t wide;              // N is a multiple of 4 and out 16-byte (f32) or 8-byte aligned
+    int32_t M, E, K, N;
+};
+
+hipError_t launch_grouped(const GroupedParams &p, hipStream_t stream);
 
 }  // namespace gfr

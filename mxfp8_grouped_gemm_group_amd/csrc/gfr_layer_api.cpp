@@ -1,5 +1,6 @@
 // Host side of the descriptor calls for the rest of the MoE block: gfr_linear,
-// gfr_moe_decode, gfr_moe_route (include/gfr.h).  As in gfr_api.cpp every error
+// gfr_moe_decode, gfr_moe_route, gfr_grouped_linear and its weights' gradient
+// (include/gfr.h).  As in gfr_api.cpp every error
 // is returned before anything is enqueued, no device memory is read and
 // nothing is synchronised.
 #include <hip/hip_runtime_api.h>
@@ -99,6 +100,33 @@ int resolve_weights(const gfr_tensor *w, const gfr_tensor *scale, int transpose,
     if (per_expert ? !shape_is(scale, {E, s0, s1, 2}) : !shape_is(scale, {s0, s1, 2}))
         return GFR_ERR_BAD_SHAPE;
     scale_e = per_expert ? kb * N * 2 : 0;
+    return GFR_OK;
+}
+
+// The arguments that the grouped product and its weights' gradient share: x [M, K],
+// group_list [E] and where E, M and the other width N fit.
+int resolve_groups(const gfr_tensor *x, const gfr_tensor *group_list, int group_list_type,
+                   int transpose_w, int flag, int64_t E, int64_t N, const gfr_tensor *out,
+                   const gfr_options *opts, gfr::GroupedParams &p) {
+    if ((group_list_type != GFR_GROUP_LIST_CUMSUM && group_list_type != GFR_GROUP_LIST_COUNT) ||
+        (transpose_w != 0 && transpose_w != 1) || (flag != 0 && flag != 1))
+        return GFR_ERR_BAD_ARG;
+    GFR_TRY(check_desc(group_list, {1}, {GFR_DT_I64}));
+    if (!shape_is(group_list, {E})) return GFR_ERR_BAD_SHAPE;
+    const int64_t M = x->shape[0], K = x->shape[1];
+    if (E < 1 || E > GFR_MAX_EXPERTS || M > int64_t{1} << 30 || K > int64_t{1} << 21 ||
+        N > int64_t{1} << 21)
+        return GFR_ERR_UNSUPPORTED;
+    if (!aligned(x->data, 16) || !aligned(out->data, 16) || !aligned(group_list->data, 8))
+        return GFR_ERR_BAD_ALIGNMENT;
+    p.group_list = static_cast<const int64_t *>(group_list->data);
+    p.cumsum = group_list_type == GFR_GROUP_LIST_CUMSUM;
+    p.status = opts ? opts->status_dev : nullptr;
+    p.out = out->data;
+    p.f16 = x->dtype == GFR_DT_F16;
+    p.out_f32 = out->dtype == GFR_DT_F32;
+    p.M = static_cast<int32_t>(M);
+    p.E = static_cast<int32_t>(E);
     return GFR_OK;
 }
 
@@ -289,6 +317,61 @@ int gfr_moe_route(const gfr_tensor *logits, const gfr_tensor *bias, int scoring,
     p.k = static_cast<int32_t>(k);
     return gfr::launch_route(p, static_cast<hipStream_t>(stream)) == hipSuccess ? GFR_OK
                                                                                 : GFR_ERR_HIP;
+}
+
+int gfr_grouped_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *group_list,
+                       int group_list_type, int transpose_w, int fill, const gfr_tensor *out,
+                       void *stream, const gfr_options *opts) {
+    if (!x || !w || !group_list || !out) return GFR_ERR_NULL_ARG;
+    GFR_TRY(check_desc(x, {2}, {GFR_DT_BF16, GFR_DT_F16}));
+    GFR_TRY(check_desc(w, {3}, {x->dtype}));
+    GFR_TRY(check_desc(out, {2}, {x->dtype, GFR_DT_F32}));
+    const int64_t M = x->shape[0], K = x->shape[1], E = w->shape[0];
+    const int64_t N = w->shape[transpose_w ? 1 : 2];
+    gfr::GroupedParams p{};
+    if (K < 1 || w->shape[transpose_w ? 2 : 1] != K || !shape_is(out, {M, N}))
+        return GFR_ERR_BAD_SHAPE;
+    GFR_TRY(resolve_groups(x, group_list, group_list_type, transpose_w, fill, E, N, out, opts, p));
+    if (!aligned(w->data, 16)) return GFR_ERR_BAD_ALIGNMENT;
+    if (M == 0 || N == 0) return GFR_OK;
+    p.x = static_cast<const uint16_t *>(x->data);
+    p.w = static_cast<const uint16_t *>(w->data);
+    p.K = static_cast<int32_t>(K);
+    p.N = static_cast<int32_t>(N);
+    p.transpose = transpose_w;
+    p.fill = fill;
+    p.wide = N % 4 == 0;
+    return gfr::launch_grouped(p, static_cast<hipStream_t>(stream)) == hipSuccess ? GFR_OK
+                                                                                  : GFR_ERR_HIP;
+}
+
+int gfr_grouped_linear_wgrad(const gfr_tensor *x, const gfr_tensor *dy,
+                             const gfr_tensor *group_list, int group_list_type, int transpose_w,
+                             int accumulate, const gfr_tensor *out, void *stream,
+                             const gfr_options *opts) {
+    if (!x || !dy || !group_list || !out) return GFR_ERR_NULL_ARG;
+    GFR_TRY(check_desc(x, {2}, {GFR_DT_BF16, GFR_DT_F16}));
+    GFR_TRY(check_desc(dy, {2}, {x->dtype}));
+    GFR_TRY(check_desc(out, {3}, {x->dtype, GFR_DT_F32}));
+    const int64_t M = x->shape[0], K = x->shape[1], N = dy->shape[1], E = out->shape[0];
+    if (dy->shape[0] != M || !(transpose_w ? shape_is(out, {E, N, K}) : shape_is(out, {E, K, N})))
+        return GFR_ERR_BAD_SHAPE;
+    gfr::GroupedParams p{};
+    GFR_TRY(resolve_groups(x, group_list, group_list_type, transpose_w, accumulate, E, N, out, opts,
+                           p));
+    if (!aligned(dy->data, 16)) return GFR_ERR_BAD_ALIGNMENT;
+    if (K == 0 || N == 0 || (M == 0 && accumulate)) return GFR_OK;
+    // the gradient of transposed weights is that of the other product, dy^T x
+    const gfr_tensor *rows = transpose_w ? dy : x, *columns = transpose_w ? x : dy;
+    p.x = static_cast<const uint16_t *>(rows->data);
+    p.w = static_cast<const uint16_t *>(columns->data);
+    p.K = static_cast<int32_t>(rows->shape[1]);
+    p.N = static_cast<int32_t>(columns->shape[1]);
+    p.wgrad = 1;
+    p.accumulate = accumulate;
+    p.wide = p.N % 4 == 0;
+    return gfr::launch_grouped(p, static_cast<hipStream_t>(stream)) == hipSuccess ? GFR_OK
+                                                                                  : GFR_ERR_HIP;
 }
 
 }  // extern "C"
