@@ -126,6 +126,7 @@ enum gfr_group_list_type { GFR_GROUP_LIST_CUMSUM = 0, GFR_GROUP_LIST_COUNT = 1 }
 #define GFR_DEV_BAD_ROW_INDEX 0x2  /* row_index outside [0, batch): token skipped */
 
 #define GFR_DEV_BAD_EXPERT 0x4    /* a top-k id below -1 or not below E: pair skipped */
+#define GFR_DEV_BAD_ADAPTER 0x8   /* an adapter id below -1 or not below L: no adapter */
 
 /* Limits of this implementation. */
 #define GFR_MAX_EXPERTS 1024       /* [P3] Atlas 350 notes: e <= 1024 */
@@ -586,6 +587,53 @@ int gfr_grouped_linear_wgrad(const gfr_tensor *x, const gfr_tensor *dy,
                              const gfr_tensor *group_list, int group_list_type, int transpose_w,
                              int accumulate, const gfr_tensor *out, void *stream,
                              const gfr_options *opts);
+
+/* Limit of gfr_lora_linear. */
+#define GFR_MAX_RANK 256
+
+/*
+ * gfr_lora_linear — a dense product with the low-rank adapter of each row's own
+ * request:
+ *
+ *   out[m, n] = sum_k x[m, k] * w[n, k] + bias[n]
+ *               + sum_j inner[m, j] * lora_b[i, n, j] + residual[m, n]
+ *   inner[m, j] = scaling[i] * sum_k x[m, k] * lora_a[i, j, k]     i = adapter_ids[m]
+ *
+ * accumulated in FP32, rounded once to out's type; inner keeps at least 16 bits of
+ * mantissa.  Rows of any order and mix of adapters; what a row gets depends on
+ * its own adapter alone, whatever the others' hold.
+ *
+ *  x            BF16 or F16 [M, K].
+ *  w            x's dtype [N, K].
+ *  bias         x's dtype or F32 [N], or NULL.
+ *  residual     x's dtype [M, N], or NULL; may be out itself, but not overlap it
+ *               otherwise.
+ *  lora_a       x's dtype [L, r, K], lora_b x's dtype [L, N, r], 1 <= r <=
+ *               GFR_MAX_RANK (adapters of a lower rank: zero rows of lora_a).
+ *  adapter_ids  I32 [M], each in [0, L), or -1 for no adapter.  Other values count
+ *               as -1 and set GFR_DEV_BAD_ADAPTER.
+ *  scaling      F32 [L], or NULL for 1.
+ *  out          x's dtype or F32 [M, N]; overwritten, must not overlap x, w, lora_a
+ *               or lora_b.
+ *  opts         workspace (gfr_lora_linear_workspace_size, 256-byte aligned) and
+ *               status_dev; the other fields are ignored.
+ *
+ * Any M, N >= 0 and K >= 1 (K and r multiples of 8 are the fast path).  M = 0 or N = 0
+ * is a no-op.  The sizes fix the summation order: two calls give the same bits.  Calls
+ * that overlap in time need workspaces of their own.  With F16, inner and its products
+ * are to stay within F16's range, as an F16 layer's own intermediate row.  Errors as
+ * gfr_linear, and GFR_ERR_UNSUPPORTED for r outside [1, GFR_MAX_RANK], L outside
+ * [1, 2^20] or M > 2^26; lora_a, lora_b 16-byte, adapter_ids and scaling 4-byte aligned.
+ */
+int gfr_lora_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *bias,
+                    const gfr_tensor *residual, const gfr_tensor *lora_a,
+                    const gfr_tensor *lora_b, const gfr_tensor *adapter_ids,
+                    const gfr_tensor *scaling, const gfr_tensor *out, void *stream,
+                    const gfr_options *opts);
+
+/* Workspace bytes of gfr_lora_linear for M rows, w [N, K] and adapters of rank r.  Pure
+ * host arithmetic. */
+int gfr_lora_linear_workspace_size(int64_t M, int64_t N, int64_t K, int64_t r, size_t *bytes);
 
 /* ======================================================================== *
  * Raw calls: device pointers plus sizes, semantics as the descriptor calls *

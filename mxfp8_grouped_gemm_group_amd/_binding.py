@@ -18,6 +18,7 @@ GFR_OK = 0
 DEV_BAD_GROUP_LIST = 0x1
 DEV_BAD_ROW_INDEX = 0x2
 DEV_BAD_EXPERT = 0x4
+DEV_BAD_ADAPTER = 0x8
 
 _FP8_KIND = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1, torch.float4_e2m1fn_x2: 2}
 _PACKED = torch.float4_e2m1fn_x2   # two E2M1 elements per byte along the last axis

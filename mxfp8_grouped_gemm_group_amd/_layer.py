@@ -1,7 +1,7 @@
 """ctypes binding of the rest of the MoE block (include/gfr.h): the dense
 product with its epilogue, the router's choice with the tokens in expert order,
-the experts for a few tokens, and the experts' products in 16 bits with their
-gradients.
+the experts for a few tokens, the experts' products in 16 bits with their
+gradients, and the dense product with an adapter per request.
 
 Argument marshalling only, like ``_binding``: dtypes, ranks and shapes are
 checked by the library, which raises GfrError here.
@@ -47,10 +47,13 @@ def _lib():
         lib.gfr_moe_route_workspace_size.argtypes = [ctypes.c_int64] * 3 + [_SIZE]
         lib.gfr_grouped_linear.argtypes = [_P] * 3 + [i] * 3 + [_P] * 3
         lib.gfr_grouped_linear_wgrad.argtypes = [_P] * 3 + [i] * 3 + [_P] * 3
+        lib.gfr_lora_linear.argtypes = [_P] * 11
+        lib.gfr_lora_linear_workspace_size.argtypes = [ctypes.c_int64] * 4 + [_SIZE]
         for f in (lib.gfr_linear, lib.gfr_linear_workspace_size, lib.gfr_moe_decode,
                   lib.gfr_moe_decode_workspace_size, lib.gfr_moe_route,
                   lib.gfr_moe_route_workspace_size, lib.gfr_grouped_linear,
-                  lib.gfr_grouped_linear_wgrad):
+                  lib.gfr_grouped_linear_wgrad, lib.gfr_lora_linear,
+                  lib.gfr_lora_linear_workspace_size):
             f.restype = i
         _ready = True
     return lib
@@ -419,3 +422,53 @@ def grouped_linear_wgrad(x, dy, group_list, group_list_type, *, transpose_w=Fals
                                         accumulate=accumulate, status=status)
     return _wgrad(x, dy, group_list, int(group_list_type), transpose_w, out_dtype, out, accumulate,
                   status)
+
+
+@functools.lru_cache(maxsize=4096)
+def lora_linear_workspace_size(M: int, N: int, K: int, r: int) -> int:
+    """Workspace bytes of a lora_linear call of these sizes."""
+    need = ctypes.c_size_t(0)
+    _check(_lib().gfr_lora_linear_workspace_size(M, N, K, r, ctypes.byref(need)))
+    return need.value
+
+
+def lora_linear(x, w, lora_a, lora_b, adapter_ids, *, scaling=None, bias=None, residual=None,
+                out_dtype=None, out=None, workspace=None, status=None, stream=None):
+    """x @ w.T + bias + residual and beside it the low-rank adapter of each row's own
+    request (include/gfr.h, gfr_lora_linear); returns out.
+
+    out[t] = x[t] @ w.T + bias + scaling[i] * (x[t] @ lora_a[i].T) @ lora_b[i].T
+             + residual[t],   i = adapter_ids[t]
+
+    x bfloat16 or float16 [M, K]; w [N, K], lora_a [L, r, K], lora_b [L, N, r] and
+    residual [M, N] of x's dtype (residual may be out); adapter_ids int32 [M] (-1:
+    no adapter), in any order; scaling float32 [L] or None (1); bias [N] in x's
+    dtype or float32; out_dtype x's (default) or float32.  ``status`` (int32, 1
+    element) receives DEV_BAD_ADAPTER if an id is out of range.  ``workspace``
+    (uint8, lora_linear_workspace_size bytes) is allocated here if none is given;
+    calls that overlap in time need one each.
+    """
+    lib = _lib()
+    index = _device(x, "x")
+    _need(x.dim() == 2 and w.dim() == 2 and lora_a.dim() == 3,
+          "x must be [M, K], w [N, K] and lora_a [L, r, K]")
+    _need(out is None or out_dtype is None or out.dtype == out_dtype, "out must have out_dtype")
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return lora_linear(x, w, lora_a, lora_b, adapter_ids, scaling=scaling, bias=bias,
+                               residual=residual, out_dtype=out_dtype, out=out,
+                               workspace=workspace, status=status)
+    M, N = x.shape[0], w.shape[0]
+    tensors, made = (x, w, bias, residual, lora_a, lora_b, adapter_ids, scaling), ()
+    if out is None:
+        out = x.new_empty((M, N), dtype=out_dtype or x.dtype)
+        made = (out,)
+    else:
+        tensors += (out,)
+    if workspace is None:
+        workspace = x.new_empty(lora_linear_workspace_size(M, N, x.shape[1], lora_a.shape[1]),
+                                dtype=torch.uint8)
+    words, at, opts = _pack(index, tensors, made, workspace, status)
+    _check(lib.gfr_lora_linear(*at, _raw_stream(index), opts))
+    return out

@@ -13,7 +13,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgfr.so")
 SOURCES = [os.path.join(CSRC, f) for f in (
     "gfr_kernels.hip", "gfr_api.cpp", "gfr_linear.hip", "gfr_moe_decode.hip",
-    "gfr_moe_route.hip", "gfr_grouped.hip", "gfr_layer_api.cpp")]
+    "gfr_moe_route.hip", "gfr_grouped.hip", "gfr_lora.hip", "gfr_layer_api.cpp")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

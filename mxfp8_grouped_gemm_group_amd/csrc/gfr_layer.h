@@ -1,6 +1,7 @@
 // Internal interface between the host API (gfr_layer_api.cpp) and the kernels
 // of the dense product, the few-token experts, the router and the 16-bit grouped
-// products (gfr_linear.hip, gfr_moe_decode.hip, gfr_moe_route.hip, gfr_grouped.hip).
+// products and the adapters (gfr_linear.hip, gfr_moe_decode.hip, gfr_moe_route.hip,
+// gfr_grouped.hip, gfr_lora.hip).
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -107,5 +108,32 @@ struct GroupedParams {
 };
 
 hipError_t launch_grouped(const GroupedParams &p, hipStream_t stream);
+
+struct LoraParams {
+    const uint16_t *x;         // [M, K]
+    const uint16_t *w;         // [N, K]
+    const uint16_t *a;         // [L, r, K]
+    const uint16_t *b;         // [L, N, r]
+    const int32_t *ids;        // [M]
+    const float *scaling;      // [L] or null
+    const void *bias;          // [N] or null
+    const uint16_t *residual;  // [M, N] or null
+    void *out;                 // [M, N]
+    int32_t *status;           // may be null
+    float *inner;              // workspace: [M][r], scaled
+    float *dense;              // workspace: [M][N]
+    float *partial;            // workspace of the dense product's K split
+    LinearChoice choice;
+    int32_t bias_f32, out_f32, f16;
+    int32_t M, N, K, L, r;
+};
+
+// Workspace layout of lora_linear (256-byte aligned regions; inner at 0).
+struct LoraLayout {
+    size_t dense, partial, total;
+    LinearChoice choice;       // of the dense product
+};
+LoraLayout lora_layout(int64_t M, int64_t N, int64_t K, int64_t r);
+hipError_t launch_lora(const LoraParams &p, hipStream_t stream);
 
 }  // namespace gfr

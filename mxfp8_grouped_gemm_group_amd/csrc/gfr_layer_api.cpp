@@ -1,6 +1,6 @@
 // Host side of the descriptor calls for the rest of the MoE block: gfr_linear,
-// gfr_moe_decode, gfr_moe_route, gfr_grouped_linear and its weights' gradient
-// (include/gfr.h).  As in gfr_api.cpp every error
+// gfr_moe_decode, gfr_moe_route, gfr_grouped_linear and its weights' gradient,
+// gfr_lora_linear (include/gfr.h).  As in gfr_api.cpp every error
 // is returned before anything is enqueued, no device memory is read and
 // nothing is synchronised.
 #include <hip/hip_runtime_api.h>
@@ -128,6 +128,14 @@ int resolve_groups(const gfr_tensor *x, const gfr_tensor *group_list, int group_
     p.M = static_cast<int32_t>(M);
     p.E = static_cast<int32_t>(E);
     return GFR_OK;
+}
+
+int check_lora_sizes(int64_t M, int64_t N, int64_t K, int64_t r) {
+    if (M < 0 || N < 0 || K < 1) return GFR_ERR_BAD_SHAPE;
+    if (r < 1 || r > GFR_MAX_RANK || M > int64_t{1} << 26 || N > int64_t{1} << 30 ||
+        K > int64_t{1} << 21)
+        return GFR_ERR_UNSUPPORTED;
+    return gfr::linear_choice(M, N, K, GFR_ACT_NONE).split > 0 ? GFR_OK : GFR_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -372,6 +380,67 @@ int gfr_grouped_linear_wgrad(const gfr_tensor *x, const gfr_tensor *dy,
     p.wide = p.N % 4 == 0;
     return gfr::launch_grouped(p, static_cast<hipStream_t>(stream)) == hipSuccess ? GFR_OK
                                                                                   : GFR_ERR_HIP;
+}
+
+int gfr_lora_linear_workspace_size(int64_t M, int64_t N, int64_t K, int64_t r, size_t *bytes) {
+    if (!bytes) return GFR_ERR_NULL_ARG;
+    GFR_TRY(check_lora_sizes(M, N, K, r));
+    *bytes = M > 0 && N > 0 ? gfr::lora_layout(M, N, K, r).total : 0;
+    return GFR_OK;
+}
+
+int gfr_lora_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *bias,
+                    const gfr_tensor *residual, const gfr_tensor *lora_a,
+                    const gfr_tensor *lora_b, const gfr_tensor *adapter_ids,
+                    const gfr_tensor *scaling, const gfr_tensor *out, void *stream,
+                    const gfr_options *opts) {
+    if (!lora_a || !lora_b || !adapter_ids) return GFR_ERR_NULL_ARG;
+    gfr::LinearParams d{};
+    GFR_TRY(resolve_linear(x, w, bias, residual, GFR_ACT_NONE, out, d));
+    GFR_TRY(check_desc(lora_a, {3}, {x->dtype}));
+    GFR_TRY(check_desc(lora_b, {3}, {x->dtype}));
+    GFR_TRY(check_desc(adapter_ids, {1}, {GFR_DT_I32}));
+    const int64_t M = d.M, N = d.N, K = d.K, L = lora_a->shape[0], r = lora_a->shape[1];
+    if (lora_a->shape[2] != K || !shape_is(lora_b, {L, N, r}) || !shape_is(adapter_ids, {M}))
+        return GFR_ERR_BAD_SHAPE;
+    if (present(scaling)) {
+        GFR_TRY(check_desc(scaling, {1}, {GFR_DT_F32}));
+        if (!shape_is(scaling, {L})) return GFR_ERR_BAD_SHAPE;
+        if (!aligned(scaling->data, 4)) return GFR_ERR_BAD_ALIGNMENT;
+    }
+    GFR_TRY(check_lora_sizes(M, N, K, r));
+    if (L < 1 || L > int64_t{1} << 20) return GFR_ERR_UNSUPPORTED;
+    if (!aligned(lora_a->data, 16) || !aligned(lora_b->data, 16) || !aligned(adapter_ids->data, 4))
+        return GFR_ERR_BAD_ALIGNMENT;
+    if (M == 0 || N == 0) return GFR_OK;
+    const gfr::LoraLayout l = gfr::lora_layout(M, N, K, r);
+    GFR_TRY(check_workspace(opts, l.total));
+    char *ws = static_cast<char *>(opts->workspace);
+    gfr::LoraParams p{};
+    p.x = d.x;
+    p.w = d.w;
+    p.a = static_cast<const uint16_t *>(lora_a->data);
+    p.b = static_cast<const uint16_t *>(lora_b->data);
+    p.ids = static_cast<const int32_t *>(adapter_ids->data);
+    p.scaling = present(scaling) ? static_cast<const float *>(scaling->data) : nullptr;
+    p.bias = d.bias;
+    p.residual = d.residual;
+    p.out = d.out;
+    p.status = opts->status_dev;
+    p.inner = reinterpret_cast<float *>(ws);
+    p.dense = reinterpret_cast<float *>(ws + l.dense);
+    p.partial = reinterpret_cast<float *>(ws + l.partial);
+    p.choice = l.choice;
+    p.bias_f32 = d.bias_f32;
+    p.out_f32 = d.out_f32;
+    p.f16 = d.f16;
+    p.M = d.M;
+    p.N = d.N;
+    p.K = d.K;
+    p.L = static_cast<int32_t>(L);
+    p.r = static_cast<int32_t>(r);
+    return gfr::launch_lora(p, static_cast<hipStream_t>(stream)) == hipSuccess ? GFR_OK
+                                                                               : GFR_ERR_HIP;
 }
 
 }  // extern "C"
