@@ -105,8 +105,9 @@ __device__ __forceinline__ float silu(float v) {
     return v * __builtin_amdgcn_rcpf(1.0f + exp_f32(-v));
 }
 
-// Lets kernel K have up to 146 KB of dynamic LDS; the runtime is asked once per
-// device.
+// Lets kernel K have up to 159 KB of dynamic LDS (a CU has 160); the runtime is asked
+// once per device.
+constexpr int kMaxLds = 159 << 10;
 template <auto K>
 hipError_t allow_lds(int bytes) {
     if (bytes <= (32 << 10)) return hipSuccess;
@@ -115,7 +116,7 @@ hipError_t allow_lds(int bytes) {
     if (hipError_t e = hipGetDevice(&dev); e != hipSuccess) return e;
     if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_relaxed)) return hipSuccess;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(K),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, 146 << 10);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
     if (e == hipSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_relaxed);
     return e;
 }

@@ -11,6 +11,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gfr.h"
 #include "gfr_device.h"
 #include "gfr_layer.h"
@@ -103,10 +105,10 @@ __device__ __forceinline__ int expert_of(const Groups &s, int E, int u) {
     int lo = 0, hi = E;                  // units[lo] <= u < units[hi + 1]
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if (s.units[mid] <= u) lo = mid;
+        if (uniform(s.units[mid]) <= u) lo = mid;
         else hi = mid - 1;
     }
-    return uniform(lo);
+    return lo;
 }
 
 // Four neighbouring results of a row, columns n .. n + 3 of N.
@@ -227,7 +229,7 @@ __global__ __launch_bounds__(256, 2) void general_kernel(GroupedParams p) {
             b = {p.w + static_cast<int64_t>(first) * p.N + n0, p.N,
                  static_cast<int64_t>(count) * p.N - n0, count, 128, {}};
         } else {
-            const int u = static_cast<int>(id / tiles_n);
+            const int u = uniform(static_cast<int>(id / tiles_n));
             e = expert_of(s, p.E, u);
             m0 = s.start[e] + (u - s.units[e]) * 128;
             rows = min(128, s.start[e + 1] - m0);
@@ -281,6 +283,212 @@ __global__ __launch_bounds__(256, 2) void general_kernel(GroupedParams p) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// Direct kernel: rows of whole pieces
+// ---------------------------------------------------------------------------
+
+// BM x BN tiles in waves of WM x WN; a step is 64 of the summed index in two LDS
+// stages, filled straight from memory, and four parts of 16.  While one part's MFMAs
+// run, the next part's fragments come from LDS.  The one barrier of a step stands
+// ahead of part 3, whose fragments are in registers by then: behind it the next
+// step's stage is complete, and the loads of the step behind that go to this one.
+constexpr int kPitch = 36;       // floats of a row of 32 results in LDS: spreads rows over banks
+
+template <int BM, int BN, int WM, int WN>
+constexpr int direct_lds() {
+    return 2 * (BM + BN) * 128 + (BM / WM) * (BN / WN) * 32 * kPitch * 4 +
+           static_cast<int>(sizeof(Groups));
+}
+
+// 32 x 32 results of a wave (lane l: row l % 32, columns 8 r + 4 (l / 32) .. + 3) to
+// `rows` rows from `row` on, columns from n0 on.
+template <bool F16>
+__device__ __forceinline__ void put_block(const GroupedParams &p, float *slab, const f16_t &v,
+                                          int64_t row, int rows, int n0, int lane) {
+    auto wave_sync = [] {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<f4_t *>(&slab[(lane & 31) * kPitch + 8 * r + 4 * (lane >> 5)]) =
+            f4_t{v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
+    wave_sync();
+    if (p.wide) {
+        const int n = n0 + 8 * (lane & 3);
+#pragma unroll 1
+        for (int q = lane >> 2; q < 32; q += 16) {
+            if (q >= rows || n >= p.N) break;
+            const float *from = &slab[q * kPitch + 8 * (lane & 3)];
+            f4_t y[2] = {load<f4_t>(from), load<f4_t>(from + 4)};
+            const int64_t at = (row + q) * p.N + n;
+            if (p.out_f32) {
+                f4_t *to = reinterpret_cast<f4_t *>(static_cast<float *>(p.out) + at);
+                if (p.accumulate) y[0] += to[0], y[1] += to[1];
+                to[0] = y[0];
+                to[1] = y[1];
+            } else {
+                u4_t *to = reinterpret_cast<u4_t *>(static_cast<uint16_t *>(p.out) + at);
+                if (p.accumulate) {
+                    const u4_t old = *to;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        y[j >> 2][j & 3] += unpack1<F16>(old[j >> 1] >> (16 * (j & 1)));
+                }
+                u4_t h;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    h[j] = pack2<F16>(y[j >> 1][2 * (j & 1)], y[j >> 1][2 * (j & 1) + 1]);
+                *to = h;
+            }
+        }
+    } else {
+        // rows that begin anywhere: a column per lane
+        const int n = n0 + (lane & 31);
+#pragma unroll 1
+        for (int q = lane >> 5; q < 32; q += 2) {
+            if (q >= rows || n >= p.N) break;
+            float y = slab[q * kPitch + (lane & 31)];
+            const int64_t at = (row + q) * p.N + n;
+            if (p.out_f32) {
+                float *to = static_cast<float *>(p.out) + at;
+                *to = p.accumulate ? *to + y : y;
+            } else {
+                uint16_t *to = static_cast<uint16_t *>(p.out) + at;
+                if (p.accumulate) y += unpack1<F16>(*to);
+                *to = static_cast<uint16_t>(pack2<F16>(y, 0.0f));
+            }
+        }
+    }
+    wave_sync();
+}
+
+template <bool F16, bool WGRAD, bool WLINE, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, (BM / WM) * (BN / WN) / 4)
+void direct_kernel(GroupedParams p) {
+    constexpr int kWaves = (BM / WM) * (BN / WN);
+    constexpr int FM = WM / 32, FN = WN / 32;
+    constexpr int kStage = (BM + BN) * 8;                  // pieces
+    extern __shared__ u4_t lds[];            // [2][BM + BN][8], the waves' results, the groups
+    Groups &s = *reinterpret_cast<Groups *>(lds + 2 * kStage + kWaves * 32 * kPitch / 4);
+    find_groups<BM>(p, s);
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
+    float *const slab = reinterpret_cast<float *>(lds + 2 * kStage) + wave * 32 * kPitch;
+    const int tiles_n = (p.N + BN - 1) / BN, tiles_k = (p.K + BM - 1) / BM;
+    const int total = tiles_n * (WGRAD ? p.E * tiles_k : uniform(s.units[p.fill ? p.E + 1 : p.E]));
+    // Blocks go round the eight XCDs; each XCD takes a run of tiles.
+    const int per = (total + 7) / 8, xcd = blockIdx.x & 7;
+    const int end = min(total, (xcd + 1) * per);
+    const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+        (__attribute__((address_space(3))) void *)lds));
+    for (int id = xcd * per + (blockIdx.x >> 3); id < end; id += gridDim.x >> 3) {
+        int e, m0, n0, rows, steps;
+        Direct<WGRAD, BM, kWaves> da;
+        Direct<WLINE, BN, kWaves> db;
+        if (WGRAD) {
+            const int rest = uniform(id / tiles_n);
+            n0 = uniform(id % tiles_n) * BN;
+            e = uniform(rest / tiles_k);
+            m0 = uniform(rest % tiles_k) * BM;
+            rows = min(BM, p.K - m0);
+            const int first = uniform(s.start[e]), count = uniform(s.start[e + 1]) - first;
+            steps = (count + 63) / 64;
+            if (p.accumulate && count == 0) continue;
+            da.init(p.x + static_cast<int64_t>(first) * p.K + m0, p.K, 0, count, m0, wave, lane);
+            db.init(p.w + static_cast<int64_t>(first) * p.N + n0, p.N, 0, count, n0, wave, lane);
+        } else {
+            e = uniform(expert_of(s, p.E, uniform(id / tiles_n)));
+            // within an expert, bands of eight units by all columns
+            const int u0 = uniform(s.units[e]), units = uniform(s.units[e + 1]) - u0;
+            const int at = id - u0 * tiles_n;
+            const int band = at / (8 * tiles_n), in_band = at - band * 8 * tiles_n;
+            const int depth = min(8, units - band * 8);
+            n0 = uniform(in_band / depth) * BN;
+            m0 = uniform(s.start[e]) + uniform(band * 8 + in_band % depth) * BM;
+            rows = min(BM, uniform(s.start[e + 1]) - m0);
+            steps = e < p.E ? (p.K + 63) / 64 : 0;
+            const uint16_t *w = p.w + static_cast<int64_t>(e) * p.K * p.N;
+            da.init(p.x + static_cast<int64_t>(m0) * p.K, p.K, rows, p.K, 0, wave, lane);
+            if (WLINE)
+                db.init(w + n0, p.N, 0, p.K, n0, wave, lane);
+            else
+                db.init(w + static_cast<int64_t>(n0) * p.K, p.K, min(BN, p.N - n0), p.K, 0, wave,
+                        lane);
+        }
+        f16_t acc[FM][FN] = {};
+        u4_t a[2][FM], b[2][FN];
+        constexpr int kA = decltype(da)::kLoads, kLoads = kA + decltype(db)::kLoads;
+        auto load = [&](int i, int stage) {
+            const uint32_t to = lds0 + stage * kStage * 16;
+            if (i < kA) da.load(i, to, wave);
+            else db.load(i - kA, to + BM * 128, wave);
+        };
+        auto fetch = [&](int step) {
+            da.at(step);
+            db.at(step);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) load(i, step & 1);
+        };
+        auto get = [&](int to, int stage, int part, int i) {
+            const u4_t *tile = lds + stage * kStage;
+            if (i < FM) a[to][i] = fragment<WGRAD, BM>(tile, wm + 32 * i, part, lane);
+            else b[to][i - FM] = fragment<WLINE, BN>(tile + BM * 8, wn + 32 * (i - FM), part, lane);
+        };
+        // One part: its MFMAs, and between them the next part's fragments and loads.
+        auto run_part = [&](int from, int stage, int part, auto loads, int to_stage) {
+            constexpr int kGets = FM + FN, kMfmas = FM * FN;
+            constexpr int kGet = (2 * kGets + kMfmas - 1) / kMfmas;
+            constexpr int kLoad = (kLoads + kMfmas - 1) / kMfmas;
+#pragma unroll
+            for (int m = 0; m < kMfmas; ++m) {
+#pragma unroll
+                for (int i = m * kGet; i < (m + 1) * kGet && i < kGets; ++i)
+                    get(from ^ 1, stage, part, i);
+                if (loads)
+#pragma unroll
+                    for (int i = m * kLoad; i < (m + 1) * kLoad && i < kLoads; ++i)
+                        load(i, to_stage);
+                acc[m / FN][m % FN] = mfma32<F16>(b[from][m % FN], a[from][m / FN],
+                                                  acc[m / FN][m % FN]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        const std::integral_constant<bool, true> yes{};
+        const std::integral_constant<bool, false> no{};
+        if (steps > 0) {
+            fetch(0);
+            fetch(1);
+            direct_wait<kLoads>();
+#pragma unroll
+            for (int i = 0; i < FM + FN; ++i) get(0, 0, 0, i);
+            // (behind the last step loads bring zeros and fragments go unused: cheaper
+            // than a second copy of the loop)
+            for (int step = 0; step < steps; ++step) {
+                const int cur = step & 1;
+                run_part(0, cur, 1, no, 0);
+                run_part(1, cur, 2, no, 0);
+                run_part(0, cur, 3, no, 0);
+                direct_wait<0>();
+                da.at(step + 2);
+                db.at(step + 2);
+                run_part(1, cur ^ 1, 0, yes, cur);
+            }
+        }
+        // A lane holds four columns of a row at a time: 32 x 32 results go through the
+        // wave's own LDS, so that rows are written in runs.
+        const int64_t row0 = WGRAD ? static_cast<int64_t>(e) * p.K + m0 : m0;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                put_block<F16>(p, slab, acc[i][j], row0 + wm + 32 * i, rows - wm - 32 * i,
+                               n0 + wn + 32 * j, lane);
+        // the next tile's loads go where this one's last fragments came from
+        direct_wait<0>();
+    }
+}
+
 template <bool F16, bool WGRAD, bool WLINE>
 hipError_t launch_general(const GroupedParams &p, hipStream_t stream) {
     const int64_t tn = (p.N + 127) / 128, tk = (p.K + 127) / 128;
@@ -290,8 +498,24 @@ hipError_t launch_general(const GroupedParams &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <bool F16, bool WGRAD, bool WLINE, int BM, int BN, int WM, int WN>
+hipError_t launch_direct(const GroupedParams &p, hipStream_t stream) {
+    constexpr int lds = direct_lds<BM, BN, WM, WN>();
+    static_assert(lds <= kMaxLds, "as allow_lds allows");
+    constexpr auto kernel = &direct_kernel<F16, WGRAD, WLINE, BM, BN, WM, WN>;
+    if (hipError_t e = allow_lds<kernel>(lds); e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(256), dim3((BM / WM) * (BN / WN) * 64), lds, stream, p);
+    return hipGetLastError();
+}
+
 template <bool F16>
 hipError_t launch_grouped_t(const GroupedParams &p, hipStream_t stream) {
+    // rows of whole pieces, of every operand that is loaded
+    if (p.K % 8 == 0 && (p.N % 8 == 0 || (!p.wgrad && p.transpose))) {
+        if (p.wgrad) return launch_direct<F16, true, true, 256, 256, 128, 128>(p, stream);
+        return p.transpose ? launch_direct<F16, false, false, 256, 256, 128, 128>(p, stream)
+                           : launch_direct<F16, false, true, 256, 256, 128, 128>(p, stream);
+    }
     if (p.wgrad) return launch_general<F16, true, true>(p, stream);
     return p.transpose ? launch_general<F16, false, false>(p, stream)
                        : launch_general<F16, false, true>(p, stream);

@@ -103,7 +103,7 @@ struct GroupedParams {
     int32_t fill;              // forward: rows of no group are cleared
     int32_t accumulate;        // wgrad: out is added to
     int32_t f16, out_f32;
-    int32_t wide;              // N is a multiple of 4 and out 16-byte (f32) or 8-byte aligned
+    int32_t wide;              // rows of out are whole, aligned 16 bytes
     int32_t M, E, K, N;
 };
 

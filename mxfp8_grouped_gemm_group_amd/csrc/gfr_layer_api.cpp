@@ -348,7 +348,9 @@ int gfr_grouped_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tenso
     p.N = static_cast<int32_t>(N);
     p.transpose = transpose_w;
     p.fill = fill;
-    p.wide = N % 4 == 0;
+    p.wide = N % 8 == 0;
+    // (tiles are counted in 32 bits)
+    if ((M / 64 + E + 2) * ((N + 63) / 64) > kMaxRows) return GFR_ERR_UNSUPPORTED;
     return gfr::launch_grouped(p, static_cast<hipStream_t>(stream)) == hipSuccess ? GFR_OK
                                                                                   : GFR_ERR_HIP;
 }
@@ -377,7 +379,8 @@ int gfr_grouped_linear_wgrad(const gfr_tensor *x, const gfr_tensor *dy,
     p.N = static_cast<int32_t>(columns->shape[1]);
     p.wgrad = 1;
     p.accumulate = accumulate;
-    p.wide = p.N % 4 == 0;
+    p.wide = p.N % 8 == 0;
+    if (E * ((K + 63) / 64) * ((N + 63) / 64) > kMaxRows) return GFR_ERR_UNSUPPORTED;
     return gfr::launch_grouped(p, static_cast<hipStream_t>(stream)) == hipSuccess ? GFR_OK
                                                                                   : GFR_ERR_HIP;
 }

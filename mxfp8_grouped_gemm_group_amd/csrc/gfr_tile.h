@@ -89,6 +89,76 @@ __device__ __forceinline__ u4_t eight_first(rsrc_t r, int off, int valid) {
     return s;
 }
 
+// 16 bytes a lane from memory straight to LDS, 1024 consecutive bytes from `lds` on.
+// (Assembly, because behind the builtin the compiler waits for all of them ahead of
+// every later LDS read.  It writes no register; direct_wait is its wait.)
+__device__ __forceinline__ void load_lds(rsrc_t r, int lane_off, int off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(lds), "v"(lane_off), "s"(r), "s"(off) : "memory");
+}
+// All but this wave's N latest loads have landed, and its LDS reads are through; then
+// the same of the block's other waves.
+template <int N>
+__device__ __forceinline__ void direct_wait() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(N) : "memory");
+}
+
+// One operand's loads of a step, straight to LDS, for rows of whole pieces (row
+// lengths multiples of 8).  A load takes 1024 bytes of the tile; its lanes choose
+// their piece by the layout's swizzle.  Pieces behind the summed index's end are
+// zeros (their offsets lie behind the buffer's end), and so is all of a step behind
+// it; what lies behind the last line belongs to lines that are not stored.
+template <bool LINE, int BX, int WAVES>
+struct Direct {
+    static constexpr int kLoads = BX / 8 / WAVES;      // a wave's, per step
+    static constexpr int kRows = LINE ? 512 / BX : 8;  // of the tile in a load
+    const char *base;
+    int64_t bytes;                 // line-major: from base to the end of the summed rows
+    rsrc_t r;
+    int row_bytes, first;          // first: the wave's first row times row_bytes
+    int offs[2], piece_k;          // line-major: of loads whose first k is even, odd (in kRows)
+    int K, off;
+
+    // k-major: `base` is the first of `lines` lines, K long.  line-major: `base` is
+    // the first column at k = 0, `ld` a row's length.
+    __device__ __forceinline__ void init(const uint16_t *from, int64_t ld, int lines, int K_,
+                                         int skipped, int wave, int lane) {
+        base = reinterpret_cast<const char *>(from);
+        row_bytes = static_cast<int>(2 * ld);
+        K = K_;
+        first = wave * kLoads * kRows * row_bytes;
+        if (LINE) {
+            bytes = 2 * (K * ld - skipped);
+            constexpr int kLanes = 64 / kRows;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = lane / kLanes, k = (h * kRows + row) & 3;
+                offs[h] = row * row_bytes + 16 * ((lane % kLanes) ^ (4 * k));
+            }
+        } else {
+            bytes = static_cast<int64_t>(lines) * row_bytes;
+            r = buffer(base, bytes);
+            piece_k = 8 * ((lane & 7) ^ (lane >> 3));
+            offs[0] = (lane >> 3) * row_bytes + 2 * piece_k;
+        }
+    }
+    // Ahead of a step's loads.
+    __device__ __forceinline__ void at(int step) {
+        if (LINE) {
+            const int64_t gone = static_cast<int64_t>(step) * 64 * row_bytes;
+            r = buffer(base + gone, bytes > gone ? bytes - gone : 0);
+            off = first;
+        } else {
+            off = first + 128 * step;
+            offs[1] = 64 * step + piece_k < K ? offs[0] : kPast;
+        }
+    }
+    __device__ __forceinline__ void load(int i, uint32_t tile, int wave) const {
+        load_lds(r, LINE ? offs[kRows == 2 ? i & 1 : 0] : offs[1], off + i * kRows * row_bytes,
+                 tile + (wave * kLoads + i) * 1024);
+    }
+};
+
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return F16 ? pack_f16(a, b) : pack_bf16(a, b);
