@@ -286,207 +286,301 @@ __global__ __launch_bounds__(256, 2) void general_kernel(GroupedParams p) {
 // ---------------------------------------------------------------------------
 // Direct kernel: rows of whole pieces
 // ---------------------------------------------------------------------------
+constexpr int kTile = 256, kWaves = 4;
+constexpr int kStage = 2 * kTile * 8;       // pieces: an operand's 256 lines, the other's
+constexpr int kPitch = 36;      // floats of a row of 32 results in LDS: spreads rows over banks
+constexpr int kDirectLds = 2 * kStage * 16 + kWaves * 32 * kPitch * 4 +
+                           static_cast<int>(sizeof(Groups));
+static_assert(kDirectLds <= kMaxLds, "as allow_lds allows");
 
-// BM x BN tiles in waves of WM x WN; a step is 64 of the summed index in two LDS
-// stages, filled straight from memory, and four parts of 16.  While one part's MFMAs
-// run, the next part's fragments come from LDS.  The one barrier of a step stands
-// ahead of part 3, whose fragments are in registers by then: behind it the next
-// step's stage is complete, and the loads of the step behind that go to this one.
-constexpr int kPitch = 36;       // floats of a row of 32 results in LDS: spreads rows over banks
+#define GFR_INLINE __attribute__((always_inline))
+template <int N>
+using Int = std::integral_constant<int, N>;
 
-template <int BM, int BN, int WM, int WN>
-constexpr int direct_lds() {
-    return 2 * (BM + BN) * 128 + (BM / WM) * (BN / WN) * 32 * kPitch * 4 +
-           static_cast<int>(sizeof(Groups));
+// A tile: `rows` rows of out from row0 on (forward: of x too), columns from n0 on.
+struct TileAt {
+    int e, m0, n0, rows, steps;
+};
+
+// The expert whose units hold unit u (E: the rows behind the last group): the last one
+// that begins at u or before, found by a wave side by side.
+__device__ __forceinline__ int expert_at(const Groups &s, int E, int u, int lane) {
+    int n = 0;
+    for (int e = 0; e <= E; e += 64)
+        n += __builtin_popcountll(__builtin_amdgcn_ballot_w64(
+            (e + lane <= E) & (s.units[min(e + lane, E)] <= u)));
+    return uniform(n - 1);
 }
+
+// How results are written: FP32 or 16 bits, added to what is there or not; or, for rows
+// that begin anywhere, element by element.
+enum Store { kF32, kF32Add, k16, k16Add, kElements };
 
 // 32 x 32 results of a wave (lane l: row l % 32, columns 8 r + 4 (l / 32) .. + 3) to
-// `rows` rows from `row` on, columns from n0 on.
-template <bool F16>
+// `rows` rows from `row` on, columns from n0 on.  No branch of a lane's own: the block's
+// tiles and loads stay in scalar registers.
+template <bool F16, int STORE>
 __device__ __forceinline__ void put_block(const GroupedParams &p, float *slab, const f16_t &v,
                                           int64_t row, int rows, int n0, int lane) {
-    auto wave_sync = [] {
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-    };
+    const int shift = STORE == kF32 || STORE == kF32Add ? 2 : STORE == kElements ? p.out_f32 + 1 : 1;
+    const int row_bytes = p.N << shift, g = lane >> 5;
+    char *const out = static_cast<char *>(p.out) + row * row_bytes;
+    // (a buffer over the rows: what is behind the last one is not written)
+    const int64_t bytes = static_cast<int64_t>(max(0, min(32, rows))) * row_bytes;
+    if (STORE == kElements) {
+        auto wave_sync = [] {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        };
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-        *reinterpret_cast<f4_t *>(&slab[(lane & 31) * kPitch + 8 * r + 4 * (lane >> 5)]) =
-            f4_t{v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
-    wave_sync();
-    if (p.wide) {
-        const int n = n0 + 8 * (lane & 3);
+        for (int r = 0; r < 4; ++r)
+            *reinterpret_cast<f4_t *>(&slab[(lane & 31) * kPitch + 8 * r + 4 * g]) =
+                f4_t{v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
+        wave_sync();
+        // through the wave's own LDS: a column per lane
+        const int n = n0 + (lane & 31), skew = reinterpret_cast<uintptr_t>(out) & 2;
+        const rsrc_t to = uniform_buffer(out - skew, bytes + skew);
 #pragma unroll 1
-        for (int q = lane >> 2; q < 32; q += 16) {
-            if (q >= rows || n >= p.N) break;
-            const float *from = &slab[q * kPitch + 8 * (lane & 3)];
-            f4_t y[2] = {load<f4_t>(from), load<f4_t>(from + 4)};
-            const int64_t at = (row + q) * p.N + n;
-            if (p.out_f32) {
-                f4_t *to = reinterpret_cast<f4_t *>(static_cast<float *>(p.out) + at);
-                if (p.accumulate) y[0] += to[0], y[1] += to[1];
-                to[0] = y[0];
-                to[1] = y[1];
-            } else {
-                u4_t *to = reinterpret_cast<u4_t *>(static_cast<uint16_t *>(p.out) + at);
-                if (p.accumulate) {
-                    const u4_t old = *to;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        y[j >> 2][j & 3] += unpack1<F16>(old[j >> 1] >> (16 * (j & 1)));
-                }
-                u4_t h;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    h[j] = pack2<F16>(y[j >> 1][2 * (j & 1)], y[j >> 1][2 * (j & 1) + 1]);
-                *to = h;
-            }
+        for (int q = 0; q < 16; ++q) {
+            const int m = 2 * q + g;
+            const float y = slab[m * kPitch + (lane & 31)];
+            const int off = n < p.N ? m * row_bytes + (n << shift) + skew : kPast;
+            if (p.out_f32)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y), to, off, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(pack2<F16>(y, 0.0f)),
+                                                      to, off, 0, 0);
         }
-    } else {
-        // rows that begin anywhere: a column per lane
-        const int n = n0 + (lane & 31);
-#pragma unroll 1
-        for (int q = lane >> 5; q < 32; q += 2) {
-            if (q >= rows || n >= p.N) break;
-            float y = slab[q * kPitch + (lane & 31)];
-            const int64_t at = (row + q) * p.N + n;
-            if (p.out_f32) {
-                float *to = static_cast<float *>(p.out) + at;
-                *to = p.accumulate ? *to + y : y;
-            } else {
-                uint16_t *to = static_cast<uint16_t *>(p.out) + at;
-                if (p.accumulate) y += unpack1<F16>(*to);
-                *to = static_cast<uint16_t>(pack2<F16>(y, 0.0f));
-            }
-        }
+        wave_sync();
+        return;
     }
-    wave_sync();
+    const rsrc_t to = uniform_buffer(out, bytes);
+    const int at = (lane & 31) * row_bytes;
+    if (STORE == kF32 || STORE == kF32Add) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int n = n0 + 8 * r + 4 * g, off = n < p.N ? at + 4 * n : kPast;
+            f4_t y = {v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
+            if (STORE == kF32Add) y += __builtin_bit_cast(f4_t, load16<0>(to, off, 0));
+            store16(to, __builtin_bit_cast(u4_t, y), off);
+        }
+        return;
+    }
+    // the two lanes of a row trade halves, so that each has eight columns
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int n = n0 + 16 * q + 8 * g, off = n < p.N ? at + 2 * n : kPast;
+        u4_t h;
+        if (STORE == k16Add) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[8 * q + j]),
+                                                                __float_as_uint(v[8 * q + 4 + j]),
+                                                                false, false);
+                y[j] = __uint_as_float(w[0]);
+                y[4 + j] = __uint_as_float(w[1]);
+            }
+            const u4_t old = load16<0>(to, off, 0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] += unpack1<F16>(old[j >> 1] >> (16 * (j & 1)));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = pack2<F16>(y[2 * j], y[2 * j + 1]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const auto w = __builtin_amdgcn_permlane32_swap(
+                    pack2<F16>(v[8 * q + 2 * j], v[8 * q + 2 * j + 1]),
+                    pack2<F16>(v[8 * q + 4 + 2 * j], v[8 * q + 5 + 2 * j]), false, false);
+                h[j] = w[0];
+                h[2 + j] = w[1];
+            }
+        }
+        store16(to, h, off);
+    }
 }
 
-template <bool F16, bool WGRAD, bool WLINE, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, (BM / WM) * (BN / WN) / 4)
-void direct_kernel(GroupedParams p) {
-    constexpr int kWaves = (BM / WM) * (BN / WN);
-    constexpr int FM = WM / 32, FN = WN / 32;
-    constexpr int kStage = (BM + BN) * 8;                  // pieces
-    extern __shared__ u4_t lds[];            // [2][BM + BN][8], the waves' results, the groups
+// 256 x 256 tiles of four waves, one block to a CU, which goes through its tiles'
+// steps (64 of the summed index) as one run: two LDS stages, filled straight from
+// memory two steps ahead, also over the end of a tile.  A step is four parts of 16;
+// each part's fragments have registers of their own, so that a stage is read within
+// three parts and filled in the other five of its two steps:
+//
+//   part 0   reads the step's last fragments; then a barrier: the stage is free
+//   part 1   begins the loads of the step after next; then a barrier: the next stage
+//            has landed
+//   part 2   reads the next step's fragments 0 and 1, goes on loading
+//   part 3   reads fragment 2, goes on loading
+//
+// (One barrier a step, and all loads behind it, took 400 clocks of 2048 more: a CU's
+// loads take 16 clocks each, 64 a step.)  Tiles of at most 128 rows split their
+// columns over the waves and take half the time.
+template <bool F16, bool WGRAD, bool WLINE>
+__global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p) {
+    extern __shared__ u4_t lds[];     // [2][A's 256 lines, B's][8], the waves' results, the groups
     Groups &s = *reinterpret_cast<Groups *>(lds + 2 * kStage + kWaves * 32 * kPitch / 4);
-    find_groups<BM>(p, s);
+    find_groups<kTile>(p, s);
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
     float *const slab = reinterpret_cast<float *>(lds + 2 * kStage) + wave * 32 * kPitch;
-    const int tiles_n = (p.N + BN - 1) / BN, tiles_k = (p.K + BM - 1) / BM;
+    const int tiles_n = (p.N + kTile - 1) / kTile, tiles_k = (p.K + kTile - 1) / kTile;
     const int total = tiles_n * (WGRAD ? p.E * tiles_k : uniform(s.units[p.fill ? p.E + 1 : p.E]));
     // Blocks go round the eight XCDs; each XCD takes a run of tiles.
-    const int per = (total + 7) / 8, xcd = blockIdx.x & 7;
-    const int end = min(total, (xcd + 1) * per);
-    const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
-        (__attribute__((address_space(3))) void *)lds));
-    for (int id = xcd * per + (blockIdx.x >> 3); id < end; id += gridDim.x >> 3) {
-        int e, m0, n0, rows, steps;
-        Direct<WGRAD, BM, kWaves> da;
-        Direct<WLINE, BN, kWaves> db;
+    const int per = (total + 7) / 8, xcd = blockIdx.x & 7, stride = gridDim.x >> 3;
+    const int end = uniform(min(total, (xcd + 1) * per));
+    auto tile_at = [&](int id) GFR_INLINE {
+        TileAt t;
         if (WGRAD) {
             const int rest = uniform(id / tiles_n);
-            n0 = uniform(id % tiles_n) * BN;
-            e = uniform(rest / tiles_k);
-            m0 = uniform(rest % tiles_k) * BM;
-            rows = min(BM, p.K - m0);
-            const int first = uniform(s.start[e]), count = uniform(s.start[e + 1]) - first;
-            steps = (count + 63) / 64;
-            if (p.accumulate && count == 0) continue;
-            da.init(p.x + static_cast<int64_t>(first) * p.K + m0, p.K, 0, count, m0, wave, lane);
-            db.init(p.w + static_cast<int64_t>(first) * p.N + n0, p.N, 0, count, n0, wave, lane);
+            t.n0 = uniform(id % tiles_n) * kTile;
+            t.e = uniform(rest / tiles_k);
+            t.m0 = uniform(rest % tiles_k) * kTile;
+            t.rows = min(kTile, p.K - t.m0);
+            t.steps = (uniform(s.start[t.e + 1]) - uniform(s.start[t.e]) + 63) / 64;
         } else {
-            e = uniform(expert_of(s, p.E, uniform(id / tiles_n)));
+            t.e = expert_at(s, p.E, uniform(id / tiles_n), lane);
             // within an expert, bands of eight units by all columns
-            const int u0 = uniform(s.units[e]), units = uniform(s.units[e + 1]) - u0;
+            const int u0 = uniform(s.units[t.e]), units = uniform(s.units[t.e + 1]) - u0;
             const int at = id - u0 * tiles_n;
-            const int band = at / (8 * tiles_n), in_band = at - band * 8 * tiles_n;
+            const int band = uniform(at / (8 * tiles_n)), in_band = at - band * 8 * tiles_n;
             const int depth = min(8, units - band * 8);
-            n0 = uniform(in_band / depth) * BN;
-            m0 = uniform(s.start[e]) + uniform(band * 8 + in_band % depth) * BM;
-            rows = min(BM, uniform(s.start[e + 1]) - m0);
-            steps = e < p.E ? (p.K + 63) / 64 : 0;
-            const uint16_t *w = p.w + static_cast<int64_t>(e) * p.K * p.N;
-            da.init(p.x + static_cast<int64_t>(m0) * p.K, p.K, rows, p.K, 0, wave, lane);
-            if (WLINE)
-                db.init(w + n0, p.N, 0, p.K, n0, wave, lane);
-            else
-                db.init(w + static_cast<int64_t>(n0) * p.K, p.K, min(BN, p.N - n0), p.K, 0, wave,
-                        lane);
+            t.n0 = uniform(in_band / depth) * kTile;
+            t.m0 = uniform(s.start[t.e]) + uniform(band * 8 + in_band % depth) * kTile;
+            t.rows = uniform(min(kTile, uniform(s.start[t.e + 1]) - t.m0));
+            t.steps = uniform(t.e < p.E ? (p.K + 63) / 64 : 0);
         }
-        f16_t acc[FM][FN] = {};
-        u4_t a[2][FM], b[2][FN];
-        constexpr int kA = decltype(da)::kLoads, kLoads = kA + decltype(db)::kLoads;
-        auto load = [&](int i, int stage) {
-            const uint32_t to = lds0 + stage * kStage * 16;
-            if (i < kA) da.load(i, to, wave);
-            else db.load(i - kA, to + BM * 128, wave);
-        };
-        auto fetch = [&](int step) {
-            da.at(step);
-            db.at(step);
+        return t;
+    };
+
+    // The loads' place: the operands of a tile, its next step.
+    Direct<WGRAD, kTile, kWaves> da;
+    Direct<WLINE, kTile, kWaves> db;
+    da.init(p.K, wave, lane);
+    db.init(WLINE ? p.N : p.K, wave, lane);
+    int load_id = uniform(xcd * per + (blockIdx.x >> 3) - stride), load_step = 0, load_steps = 0;
+    auto next_loads = [&]() GFR_INLINE {
+        load_step = uniform(load_step + 1);
+        if (load_step < uniform(load_steps)) return;
+        load_step = 0;
+        load_steps = 0x7fffffff;             // no tile left: zeros
+        TileAt t;
+        do {
+            load_id = uniform(load_id + stride);
+            if (load_id >= end) {
+                da.tile(p.x, 0, 0);
+                db.tile(p.w, 0, 0);
+                return;
+            }
+            t = tile_at(load_id);
+        } while (t.steps == 0);
+        load_steps = t.steps;
+        if (WGRAD) {
+            const int first = uniform(s.start[t.e]), count = uniform(s.start[t.e + 1]) - first;
+            const int64_t k = p.K, n = p.N;
+            da.tile(p.x + first * k + t.m0, 2 * (count * k - t.m0), count);
+            db.tile(p.w + first * n + t.n0, 2 * (count * n - t.n0), count);
+        } else {
+            const int64_t k = p.K, n = p.N;
+            const uint16_t *w = p.w + t.e * k * n;
+            da.tile(p.x + t.m0 * k, 2 * t.rows * k, p.K);
+            if (WLINE) db.tile(w + t.n0, 2 * (k * n - t.n0), p.K);
+            else db.tile(w + t.n0 * k, 2 * min(kTile, p.N - t.n0) * k, p.K);
+        }
+    };
+    const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+        (__attribute__((address_space(3))) void *)lds));
+    constexpr int kA = decltype(da)::kLoads, kLoads = kA + decltype(db)::kLoads;
+    auto load = [&](int i, int stage) GFR_INLINE {
+        const uint32_t to = lds0 + stage * kStage * 16;
+        if (i < kA) da.load(i, to, wave);
+        else db.load(i - kA, to + kTile * 128, wave);
+    };
+    int now = 0;                              // the stage of the step that is multiplied
+    int id = load_id + stride;
+    if (id >= end) return;
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) load(i, step & 1);
-        };
-        auto get = [&](int to, int stage, int part, int i) {
+    for (int i = 0; i < 2; ++i) {
+        next_loads();
+        da.at(load_step);
+        db.at(load_step);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) load(j, i);
+    }
+    direct_wait<kLoads>();
+
+    // A tile in waves of 32 FM x 32 FN, kWaves / COLS by COLS of them.
+    auto run_tile = [&](const TileAt &t, auto fm, auto fn, auto cols) GFR_INLINE {
+        constexpr int FM = fm, FN = fn, COLS = cols;
+        constexpr int kGets = FM + FN, kMfmas = FM * FN;
+        const int wm = wave / COLS * (32 * FM), wn = wave % COLS * (32 * FN);
+        u4_t a[4][FM], b[4][FN];
+        auto get = [&](int part, int stage, int i) GFR_INLINE {
             const u4_t *tile = lds + stage * kStage;
-            if (i < FM) a[to][i] = fragment<WGRAD, BM>(tile, wm + 32 * i, part, lane);
-            else b[to][i - FM] = fragment<WLINE, BN>(tile + BM * 8, wn + 32 * (i - FM), part, lane);
+            if (i < FM)
+                a[part][i] = fragment<WGRAD, kTile>(tile, wm + 32 * i, part, lane);
+            else
+                b[part][i - FM] =
+                    fragment<WLINE, kTile>(tile + kTile * 8, wn + 32 * (i - FM), part, lane);
         };
-        // One part: its MFMAs, and between them the next part's fragments and loads.
-        auto run_part = [&](int from, int stage, int part, auto loads, int to_stage) {
-            constexpr int kGets = FM + FN, kMfmas = FM * FN;
-            constexpr int kGet = (2 * kGets + kMfmas - 1) / kMfmas;
-            constexpr int kLoad = (kLoads + kMfmas - 1) / kMfmas;
+        f16_t acc[FM][FN] = {};
+        // A part: its MFMAs, and between them `gets` fragments from part `first` on
+        // of a stage, and loads [from, to).
+        auto run_part = [&](auto part, auto gets, auto first, int stage, auto from, auto to,
+                            int into) GFR_INLINE {
+            constexpr int kG = (gets + kMfmas - 1) / kMfmas;
+            constexpr int kL = (to - from + kMfmas - 1) / kMfmas;
 #pragma unroll
             for (int m = 0; m < kMfmas; ++m) {
 #pragma unroll
-                for (int i = m * kGet; i < (m + 1) * kGet && i < kGets; ++i)
-                    get(from ^ 1, stage, part, i);
-                if (loads)
+                for (int h = 0; h < kG; ++h)
+                    if (const int i = m * kG + h; i < gets)
+                        get(first + i / kGets, stage, i % kGets);
 #pragma unroll
-                    for (int i = m * kLoad; i < (m + 1) * kLoad && i < kLoads; ++i)
-                        load(i, to_stage);
-                acc[m / FN][m % FN] = mfma32<F16>(b[from][m % FN], a[from][m / FN],
+                for (int h = 0; h < kL; ++h)
+                    if (const int i = from + m * kL + h; i < to) load(i, into);
+                acc[m / FN][m % FN] = mfma32<F16>(b[part][m % FN], a[part][m / FN],
                                                   acc[m / FN][m % FN]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
-        const std::integral_constant<bool, true> yes{};
-        const std::integral_constant<bool, false> no{};
-        if (steps > 0) {
-            fetch(0);
-            fetch(1);
-            direct_wait<kLoads>();
 #pragma unroll
-            for (int i = 0; i < FM + FN; ++i) get(0, 0, 0, i);
-            // (behind the last step loads bring zeros and fragments go unused: cheaper
-            // than a second copy of the loop)
-            for (int step = 0; step < steps; ++step) {
-                const int cur = step & 1;
-                run_part(0, cur, 1, no, 0);
-                run_part(1, cur, 2, no, 0);
-                run_part(0, cur, 3, no, 0);
-                direct_wait<0>();
-                da.at(step + 2);
-                db.at(step + 2);
-                run_part(1, cur ^ 1, 0, yes, cur);
-            }
+        for (int i = 0; i < 3 * kGets; ++i) get(i / kGets, now, i % kGets);
+        constexpr int kFirst = (kLoads + 2) / 3, kSecond = kFirst + (kLoads - kFirst + 1) / 2;
+        for (int step = 0; step < t.steps; ++step) {
+            run_part(Int<0>{}, Int<kGets>{}, Int<3>{}, now, Int<0>{}, Int<0>{}, 0);
+            lds_wait();
+            next_loads();
+            da.at(load_step);
+            db.at(load_step);
+            run_part(Int<1>{}, Int<0>{}, Int<0>{}, 0, Int<0>{}, Int<kFirst>{}, now);
+            direct_wait<kFirst>();
+            run_part(Int<2>{}, Int<2 * kGets>{}, Int<0>{}, now ^ 1, Int<kFirst>{}, Int<kSecond>{},
+                     now);
+            run_part(Int<3>{}, Int<kGets>{}, Int<2>{}, now ^ 1, Int<kSecond>{}, Int<kLoads>{}, now);
+            now ^= 1;
         }
-        // A lane holds four columns of a row at a time: 32 x 32 results go through the
-        // wave's own LDS, so that rows are written in runs.
-        const int64_t row0 = WGRAD ? static_cast<int64_t>(e) * p.K + m0 : m0;
+        const int64_t row0 = WGRAD ? static_cast<int64_t>(t.e) * p.K + t.m0 : t.m0;
+        auto put = [&](auto store) GFR_INLINE {
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
+            for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
-                put_block<F16>(p, slab, acc[i][j], row0 + wm + 32 * i, rows - wm - 32 * i,
-                               n0 + wn + 32 * j, lane);
-        // the next tile's loads go where this one's last fragments came from
-        direct_wait<0>();
+                for (int j = 0; j < FN; ++j) {
+                    put_block<F16, store>(p, slab, acc[i][j], row0 + wm + 32 * i,
+                                          t.rows - wm - 32 * i, t.n0 + wn + 32 * j, lane);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+        };
+        if (!WGRAD && !WLINE && !p.wide) put(Int<kElements>{});
+        else if (WGRAD && p.accumulate) p.out_f32 ? put(Int<kF32Add>{}) : put(Int<k16Add>{});
+        else p.out_f32 ? put(Int<kF32>{}) : put(Int<k16>{});
+    };
+    for (; id < end; id += stride) {
+        const TileAt t = tile_at(id);
+        if (p.accumulate && t.steps == 0) continue;
+        if (t.rows > 128) run_tile(t, Int<4>{}, Int<4>{}, Int<2>{});
+        else run_tile(t, Int<4>{}, Int<2>{}, Int<4>{});
     }
+    // (no load may be on its way to LDS when the block ends)
+    direct_wait<0>();
 }
 
 template <bool F16, bool WGRAD, bool WLINE>
@@ -498,13 +592,11 @@ hipError_t launch_general(const GroupedParams &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <bool F16, bool WGRAD, bool WLINE, int BM, int BN, int WM, int WN>
+template <bool F16, bool WGRAD, bool WLINE>
 hipError_t launch_direct(const GroupedParams &p, hipStream_t stream) {
-    constexpr int lds = direct_lds<BM, BN, WM, WN>();
-    static_assert(lds <= kMaxLds, "as allow_lds allows");
-    constexpr auto kernel = &direct_kernel<F16, WGRAD, WLINE, BM, BN, WM, WN>;
-    if (hipError_t e = allow_lds<kernel>(lds); e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3(256), dim3((BM / WM) * (BN / WN) * 64), lds, stream, p);
+    constexpr auto kernel = &direct_kernel<F16, WGRAD, WLINE>;
+    if (hipError_t e = allow_lds<kernel>(kDirectLds); e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(256), dim3(kWaves * 64), kDirectLds, stream, p);
     return hipGetLastError();
 }
 
@@ -512,9 +604,9 @@ template <bool F16>
 hipError_t launch_grouped_t(const GroupedParams &p, hipStream_t stream) {
     // rows of whole pieces, of every operand that is loaded
     if (p.K % 8 == 0 && (p.N % 8 == 0 || (!p.wgrad && p.transpose))) {
-        if (p.wgrad) return launch_direct<F16, true, true, 256, 256, 128, 128>(p, stream);
-        return p.transpose ? launch_direct<F16, false, false, 256, 256, 128, 128>(p, stream)
-                           : launch_direct<F16, false, true, 256, 256, 128, 128>(p, stream);
+        if (p.wgrad) return launch_direct<F16, true, true>(p, stream);
+        return p.transpose ? launch_direct<F16, false, false>(p, stream)
+                           : launch_direct<F16, false, true>(p, stream);
     }
     if (p.wgrad) return launch_general<F16, true, true>(p, stream);
     return p.transpose ? launch_general<F16, false, false>(p, stream)

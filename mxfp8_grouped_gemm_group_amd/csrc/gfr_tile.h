@@ -6,8 +6,9 @@
 // contiguous in memory:
 //
 //   k-major     a line's 64 k are eight 16-byte pieces, piece j of line r at
-//               j ^ (r & 7): eight lanes that read one piece of eight lines reach
-//               all banks.
+//               j ^ (r / 2 & 7): sixteen lanes that read one piece of sixteen lines
+//               reach all 64 banks.  (j ^ (r & 7) reaches half of them: 137 of 280
+//               thousand LDS clocks of 16384 x 4096 x 4096 were conflicts.)
 //   line-major  of each k, BX lines in BX / 8 pieces, piece j at j ^ 4 (k & 3).
 //               Fragments come through the transposing LDS read, which gives a
 //               lane four k of one line; the 16 lanes that share it read 32 bytes
@@ -24,6 +25,7 @@ namespace {
 
 typedef float f16_t __attribute__((ext_vector_type(16)));
 typedef short s4_t __attribute__((ext_vector_type(4)));
+typedef unsigned int v4i_t __attribute__((ext_vector_type(4)));
 
 template <bool F16>
 __device__ __forceinline__ f16_t mfma32(u4_t a, u4_t b, f16_t c) {
@@ -35,7 +37,7 @@ __device__ __forceinline__ f16_t mfma32(u4_t a, u4_t b, f16_t c) {
 }
 
 // Where piece j of line r (k-major) or of k (line-major, BX lines) lies, in pieces.
-__device__ __forceinline__ int piece_k(int r, int j) { return r * 8 + (j ^ (r & 7)); }
+__device__ __forceinline__ int piece_k(int r, int j) { return r * 8 + (j ^ (r >> 1 & 7)); }
 template <int BX>
 __device__ __forceinline__ int piece_line(int k, int j) {
     return k * (BX / 8) + (j ^ (4 * (k & 3)));
@@ -59,8 +61,20 @@ __device__ __forceinline__ u4_t fragment(const u4_t *tile, int line, int part, i
     return u4_t{l2[0], l2[1], h2[0], h2[1]};
 }
 
-// Lane offset past every buffer's end: loads there give zeros.
+// Lane offset past every buffer's end: loads there give zeros, stores do nothing.
 constexpr int kPast = 0x7f000000;
+
+__device__ __forceinline__ void store16(rsrc_t r, u4_t v, int off) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i_t, v), r, off, 0, 0);
+}
+// A buffer that the compiler sees to be the same in all lanes.
+__device__ __forceinline__ rsrc_t uniform_buffer(const char *base, int64_t bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(base);
+    const uint32_t lo = uniform(static_cast<int>(at)), hi = uniform(static_cast<int>(at >> 32));
+    const int n = bytes > 0x7ffffffc ? 0x7ffffffc : static_cast<int>(bytes);
+    return __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<void *>(static_cast<uint64_t>(hi) << 32 | lo), 0, uniform(n), 0x00020000);
+}
 
 // Eight elements from byte `off` (even) on, of a buffer whose base is a whole
 // word's address: 16 bytes at once where `whole` says that all pieces begin at
@@ -96,11 +110,15 @@ __device__ __forceinline__ void load_lds(rsrc_t r, int lane_off, int off, uint32
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :: "s"(lds), "v"(lane_off), "s"(r), "s"(off) : "memory");
 }
-// All but this wave's N latest loads have landed, and its LDS reads are through; then
-// the same of the block's other waves.
+// All but this wave's N latest loads and stores are through; then the same of the
+// block's other waves.
 template <int N>
 __device__ __forceinline__ void direct_wait() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(N) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "n"(N) : "memory");
+}
+// This wave's LDS accesses are through, then the other waves' too.
+__device__ __forceinline__ void lds_wait() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 // One operand's loads of a step, straight to LDS, for rows of whole pieces (row
@@ -111,24 +129,21 @@ __device__ __forceinline__ void direct_wait() {
 template <bool LINE, int BX, int WAVES>
 struct Direct {
     static constexpr int kLoads = BX / 8 / WAVES;      // a wave's, per step
+    static_assert(kLoads % 2 == 0, "a wave's loads begin with an even one");
     static constexpr int kRows = LINE ? 512 / BX : 8;  // of the tile in a load
     const char *base;
-    int64_t bytes;                 // line-major: from base to the end of the summed rows
+    int64_t bytes;                 // from base to the end of what may be read
     rsrc_t r;
     int row_bytes, first;          // first: the wave's first row times row_bytes
-    int offs[2], piece_k;          // line-major: of loads whose first k is even, odd (in kRows)
+    int offs[2], now[2];           // of even and odd loads; those of the step
+    int piece_k;                   // k-major: first k of the lane's piece in even loads
     int K, off;
 
-    // k-major: `base` is the first of `lines` lines, K long.  line-major: `base` is
-    // the first column at k = 0, `ld` a row's length.
-    __device__ __forceinline__ void init(const uint16_t *from, int64_t ld, int lines, int K_,
-                                         int skipped, int wave, int lane) {
-        base = reinterpret_cast<const char *>(from);
+    // Rows of `ld` elements.
+    __device__ __forceinline__ void init(int64_t ld, int wave, int lane) {
         row_bytes = static_cast<int>(2 * ld);
-        K = K_;
         first = wave * kLoads * kRows * row_bytes;
         if (LINE) {
-            bytes = 2 * (K * ld - skipped);
             constexpr int kLanes = 64 / kRows;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -136,26 +151,37 @@ struct Direct {
                 offs[h] = row * row_bytes + 16 * ((lane % kLanes) ^ (4 * k));
             }
         } else {
-            bytes = static_cast<int64_t>(lines) * row_bytes;
-            r = buffer(base, bytes);
-            piece_k = 8 * ((lane & 7) ^ (lane >> 3));
-            offs[0] = (lane >> 3) * row_bytes + 2 * piece_k;
+            const int piece = (lane & 7) ^ (lane >> 4);        // (odd loads: ^ 4)
+            piece_k = 8 * piece;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                offs[h] = (lane >> 3) * row_bytes + 16 * (piece ^ (4 * h));
         }
+    }
+    // The tile whose first line begins at `from` (line-major: at k = 0), with `bytes_`
+    // from there to the end of what may be read (0: no tile) and K_ to sum over.
+    __device__ __forceinline__ void tile(const uint16_t *from, int64_t bytes_, int K_) {
+        base = reinterpret_cast<const char *>(from);
+        bytes = bytes_;
+        K = K_;
+        if (!LINE) r = uniform_buffer(base, bytes);
     }
     // Ahead of a step's loads.
     __device__ __forceinline__ void at(int step) {
         if (LINE) {
             const int64_t gone = static_cast<int64_t>(step) * 64 * row_bytes;
-            r = buffer(base + gone, bytes > gone ? bytes - gone : 0);
+            r = uniform_buffer(base + gone, bytes > gone ? bytes - gone : 0);
             off = first;
+            now[0] = offs[0];
+            now[1] = offs[kRows == 2];
         } else {
             off = first + 128 * step;
-            offs[1] = 64 * step + piece_k < K ? offs[0] : kPast;
+            now[0] = 64 * step + piece_k < K ? offs[0] : kPast;
+            now[1] = 64 * step + (piece_k ^ 32) < K ? offs[1] : kPast;
         }
     }
     __device__ __forceinline__ void load(int i, uint32_t tile, int wave) const {
-        load_lds(r, LINE ? offs[kRows == 2 ? i & 1 : 0] : offs[1], off + i * kRows * row_bytes,
-                 tile + (wave * kLoads + i) * 1024);
+        load_lds(r, now[i & 1], off + i * kRows * row_bytes, tile + (wave * kLoads + i) * 1024);
     }
 };
 
