@@ -23,10 +23,13 @@ namespace {
 
 // The groups: rows [start[e], start[e + 1]) are expert e's, start[E] all of them;
 // units[e] counts the row blocks (of a kernel's height) of the experts before e,
-// units[E] of all, and units[E + 1] also those of the rows behind the last group.
+// units[E] of all, and units[E + 1] also those of the rows behind the last group;
+// cost[e] the time of a column of tiles of the experts before e, in a measure of the
+// kernel's.
 struct Groups {
     int start[GFR_MAX_EXPERTS + 2];
     int units[GFR_MAX_EXPERTS + 2];
+    int cost[GFR_MAX_EXPERTS + 1];
     uint32_t waves[2][4];
 };
 
@@ -49,8 +52,8 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *waves, ui
 
 // Counts below zero or beyond M are clamped into [0, M], and the ranges, one behind
 // another, into [0, M); either is a bad list.  256 threads; ends with a barrier.
-template <int UNIT>
-__device__ __forceinline__ void find_groups(const GroupedParams &p, Groups &s) {
+template <int UNIT, class Cost>
+__device__ __forceinline__ void find_groups(const GroupedParams &p, Groups &s, Cost cost_of) {
     constexpr int kPer = GFR_MAX_EXPERTS / 256;
     const int e0 = threadIdx.x * kPer;
     int64_t g[kPer + 1];
@@ -73,7 +76,7 @@ __device__ __forceinline__ void find_groups(const GroupedParams &p, Groups &s) {
     const uint32_t high = block_prefix(static_cast<uint32_t>(sum >> 16), s.waves[1], high_total);
     int64_t run = static_cast<int64_t>(low) + (static_cast<int64_t>(high) << 16);
     bad |= static_cast<int64_t>(low_total) + (static_cast<int64_t>(high_total) << 16) > p.M;
-    uint32_t n = 0;
+    uint32_t n = 0, cost = 0, cost_total;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int64_t first = run < p.M ? run : p.M;
@@ -83,17 +86,24 @@ __device__ __forceinline__ void find_groups(const GroupedParams &p, Groups &s) {
         if (e0 + i < p.E) s.start[e0 + i] = static_cast<int>(first);
         if (e0 + i == p.E - 1) s.start[p.E] = static_cast<int>(end);
         n += static_cast<uint32_t>((count[i] + UNIT - 1) / UNIT);
+        if (e0 + i < p.E) cost += cost_of(static_cast<int>(count[i]));
     }
     uint32_t at = block_prefix(n, s.waves[0], total);
+    cost = block_prefix(cost, s.waves[1], cost_total);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        if (e0 + i < p.E) s.units[e0 + i] = static_cast<int>(at);
+        if (e0 + i < p.E) {
+            s.units[e0 + i] = static_cast<int>(at);
+            s.cost[e0 + i] = static_cast<int>(cost);
+        }
         at += static_cast<uint32_t>((count[i] + UNIT - 1) / UNIT);
+        cost += cost_of(static_cast<int>(count[i]));
     }
     __syncthreads();
     if (threadIdx.x == 0) {
         s.start[p.E + 1] = p.M;
         s.units[p.E] = static_cast<int>(total);
+        s.cost[p.E] = static_cast<int>(cost_total);
         s.units[p.E + 1] = static_cast<int>(total) + (p.M - s.start[p.E] + UNIT - 1) / UNIT;
     }
     if (bad && p.status && blockIdx.x == 0) atomicOr(p.status, GFR_DEV_BAD_GROUP_LIST);
@@ -205,7 +215,7 @@ template <bool F16, bool WGRAD, bool WLINE>
 __global__ __launch_bounds__(256, 2) void general_kernel(GroupedParams p) {
     __shared__ Groups s;
     __shared__ u4_t tile[2][128 * 8];
-    find_groups<128>(p, s);
+    find_groups<128>(p, s, [](int) { return 0u; });
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int wm = wave / 2 * 64, wn = wave % 2 * 64;
     const int tiles_n = (p.N + 127) / 128, tiles_k = (p.K + 127) / 128;
@@ -289,7 +299,9 @@ __global__ __launch_bounds__(256, 2) void general_kernel(GroupedParams p) {
 constexpr int kTile = 256, kWaves = 4;
 constexpr int kStage = 2 * kTile * 8;       // pieces: an operand's 256 lines, the other's
 constexpr int kPitch = 36;      // floats of a row of 32 results in LDS: spreads rows over banks
-constexpr int kDirectLds = 2 * kStage * 16 + kWaves * 32 * kPitch * 4 +
+constexpr int kSlab = 17 * kPitch;
+static_assert(kWaves * kSlab % 4 == 0, "the groups begin at a whole piece");
+constexpr int kDirectLds = 2 * kStage * 16 + kWaves * kSlab * 4 +
                            static_cast<int>(sizeof(Groups));
 static_assert(kDirectLds <= kMaxLds, "as allow_lds allows");
 
@@ -302,15 +314,29 @@ struct TileAt {
     int e, m0, n0, rows, steps;
 };
 
-// The expert whose units hold unit u (E: the rows behind the last group): the last one
-// that begins at u or before, found by a wave side by side.
-__device__ __forceinline__ int expert_at(const Groups &s, int E, int u, int lane) {
+// The last of E + 1 experts whose entry is at most u, found by a wave side by side.
+__device__ __forceinline__ int expert_at(const int *from, int E, int u, int lane) {
     int n = 0;
     for (int e = 0; e <= E; e += 64)
-        n += __builtin_popcountll(__builtin_amdgcn_ballot_w64(
-            (e + lane <= E) & (s.units[min(e + lane, E)] <= u)));
+        n += __builtin_popcountll(
+            __builtin_amdgcn_ballot_w64((e + lane <= E) & (from[min(e + lane, E)] <= u)));
     return uniform(n - 1);
 }
+
+// n / d for 0 <= n < 2^31 by d's reciprocal in FP32 (which is off by less than one for
+// quotients below 2^22, and corrected here).
+struct Divisor {
+    int d;
+    float inverse;
+    __device__ __forceinline__ explicit Divisor(int d_) : d(d_), inverse(1.0f / d_) {}
+    __device__ __forceinline__ int of(int n) const {
+        int q = static_cast<int>(static_cast<float>(n) * inverse);
+        int rest = n - q * d;
+        if (rest < 0) --q, rest += d;
+        if (rest >= d) ++q;
+        return uniform(q);
+    }
+};
 
 // How results are written: FP32 or 16 bits, added to what is there or not; or, for rows
 // that begin anywhere, element by element.
@@ -332,46 +358,69 @@ __device__ __forceinline__ void put_block(const GroupedParams &p, float *slab, c
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
         };
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            *reinterpret_cast<f4_t *>(&slab[(lane & 31) * kPitch + 8 * r + 4 * g]) =
-                f4_t{v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
-        wave_sync();
-        // through the wave's own LDS: a column per lane
+        // through the wave's own LDS, 16 rows at a time: a column per lane
         const int n = n0 + (lane & 31), skew = reinterpret_cast<uintptr_t>(out) & 2;
         const rsrc_t to = uniform_buffer(out - skew, bytes + skew);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // (the other half's go to a row that nobody reads)
+            const int line = (lane >> 4 & 1) == h ? lane & 15 : 16;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *reinterpret_cast<f4_t *>(&slab[line * kPitch + 8 * r + 4 * g]) =
+                    f4_t{v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
+            wave_sync();
 #pragma unroll 1
-        for (int q = 0; q < 16; ++q) {
-            const int m = 2 * q + g;
-            const float y = slab[m * kPitch + (lane & 31)];
-            const int off = n < p.N ? m * row_bytes + (n << shift) + skew : kPast;
-            if (p.out_f32)
-                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y), to, off, 0, 0);
-            else
-                __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(pack2<F16>(y, 0.0f)),
-                                                      to, off, 0, 0);
+            for (int q = 0; q < 8; ++q) {
+                const int m = 2 * q + g;
+                const float y = slab[m * kPitch + (lane & 31)];
+                const int off =
+                    n < p.N ? (16 * h + m) * row_bytes + (n << shift) + skew : kPast;
+                if (p.out_f32)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y), to, off, 0, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b16(
+                        static_cast<uint16_t>(pack2<F16>(y, 0.0f)), to, off, 0, 0);
+            }
+            wave_sync();
         }
-        wave_sync();
         return;
     }
+    // Lanes trade what they hold (halves of 32, then rows of 16 lanes), until a store's 64
+    // lanes have 16 rows of 64 bytes.
     const rsrc_t to = uniform_buffer(out, bytes);
-    const int at = (lane & 31) * row_bytes;
+    const int at = (lane & 15) * row_bytes;
     if (STORE == kF32 || STORE == kF32Add) {
+        const int col = 8 * (lane >> 4 & 1) + 4 * g;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int n = n0 + 8 * r + 4 * g, off = n < p.N ? at + 4 * n : kPast;
-            f4_t y = {v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
-            if (STORE == kF32Add) y += __builtin_bit_cast(f4_t, load16<0>(to, off, 0));
-            store16(to, __builtin_bit_cast(u4_t, y), off);
+        for (int q = 0; q < 2; ++q) {
+            u4_t y[2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[8 * q + j]),
+                                                                __float_as_uint(v[8 * q + 4 + j]),
+                                                                false, false);
+                y[0][j] = w[0];
+                y[1][j] = w[1];
+            }
+            const int n = n0 + 16 * q + col;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int off = n < p.N ? at + 16 * h * row_bytes + 4 * n : kPast;
+                f4_t sum = __builtin_bit_cast(f4_t, y[h]);
+                if (STORE == kF32Add) sum += __builtin_bit_cast(f4_t, load16<0>(to, off, 0));
+                store16(to, __builtin_bit_cast(u4_t, sum), off);
+            }
         }
         return;
     }
-    // the two lanes of a row trade halves, so that each has eight columns
+    const int n = n0 + 16 * (lane >> 4 & 1) + 8 * g;
+    if (STORE == k16Add) {
+        // eight columns a lane in FP32: the lane's row is lane % 32 still
+        const int full = (lane & 31) * row_bytes;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int n = n0 + 16 * q + 8 * g, off = n < p.N ? at + 2 * n : kPast;
-        u4_t h;
-        if (STORE == k16Add) {
+        for (int q = 0; q < 2; ++q) {
+            const int c = n0 + 16 * q + 8 * g, off = c < p.N ? full + 2 * c : kPast;
             float y[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -382,22 +431,40 @@ __device__ __forceinline__ void put_block(const GroupedParams &p, float *slab, c
                 y[4 + j] = __uint_as_float(w[1]);
             }
             const u4_t old = load16<0>(to, off, 0);
+            u4_t h;
 #pragma unroll
             for (int j = 0; j < 8; ++j) y[j] += unpack1<F16>(old[j >> 1] >> (16 * (j & 1)));
 #pragma unroll
             for (int j = 0; j < 4; ++j) h[j] = pack2<F16>(y[2 * j], y[2 * j + 1]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const auto w = __builtin_amdgcn_permlane32_swap(
-                    pack2<F16>(v[8 * q + 2 * j], v[8 * q + 2 * j + 1]),
-                    pack2<F16>(v[8 * q + 4 + 2 * j], v[8 * q + 5 + 2 * j]), false, false);
-                h[j] = w[0];
-                h[2 + j] = w[1];
-            }
+            store16(to, h, off);
         }
-        store16(to, h, off);
+        return;
     }
+    u4_t h[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const auto w = __builtin_amdgcn_permlane32_swap(
+                pack2<F16>(v[8 * q + 2 * j], v[8 * q + 2 * j + 1]),
+                pack2<F16>(v[8 * q + 4 + 2 * j], v[8 * q + 5 + 2 * j]), false, false);
+            h[q][j] = w[0];
+            h[q][2 + j] = w[1];
+        }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const auto w = __builtin_amdgcn_permlane16_swap(h[0][j], h[1][j], false, false);
+        h[0][j] = w[0];
+        h[1][j] = w[1];
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        store16(to, h[q], n < p.N ? at + 16 * q * row_bytes + 2 * n : kPast);
+}
+
+// Stores of a wave's 32 x 32 results, at least.
+constexpr int block_stores(int store) {
+    return store == k16 || store == k16Add ? 2 : 4;
 }
 
 // 256 x 256 tiles of four waves, one block to a CU, which goes through its tiles'
@@ -418,36 +485,59 @@ __device__ __forceinline__ void put_block(const GroupedParams &p, float *slab, c
 template <bool F16, bool WGRAD, bool WLINE>
 __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p) {
     extern __shared__ u4_t lds[];     // [2][A's 256 lines, B's][8], the waves' results, the groups
-    Groups &s = *reinterpret_cast<Groups *>(lds + 2 * kStage + kWaves * 32 * kPitch / 4);
-    find_groups<kTile>(p, s);
+    Groups &s = *reinterpret_cast<Groups *>(lds + 2 * kStage + kWaves * kSlab / 4);
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    float *const slab = reinterpret_cast<float *>(lds + 2 * kStage) + wave * 32 * kPitch;
+    float *const slab = reinterpret_cast<float *>(lds + 2 * kStage) + wave * kSlab;
+    // A tile's time: wgrad, its steps and about two more; forward, two for a tile, one for
+    // a rest of at most 128 rows.
+    find_groups<kTile>(p, s, [](int count) -> uint32_t {
+        if (WGRAD) return (count + 63) / 64 + 2;
+        const int rest = count % kTile;
+        return 2 * (count / kTile) + (rest > 128 ? 2 : rest > 0 ? 1 : 0);
+    });
     const int tiles_n = (p.N + kTile - 1) / kTile, tiles_k = (p.K + kTile - 1) / kTile;
+    const Divisor by_n(tiles_n), by_k(tiles_k), by_band(8 * tiles_n);
     const int total = tiles_n * (WGRAD ? p.E * tiles_k : uniform(s.units[p.fill ? p.E + 1 : p.E]));
-    // Blocks go round the eight XCDs; each XCD takes a run of tiles.
-    const int per = (total + 7) / 8, xcd = blockIdx.x & 7, stride = gridDim.x >> 3;
-    const int end = uniform(min(total, (xcd + 1) * per));
+    // Blocks go round the eight XCDs; each XCD takes a run of tiles, an eighth of the time.
+    const int xcd = blockIdx.x & 7, stride = gridDim.x >> 3;
+    auto run_begin = [&](int x) {
+        if (x == 0) return 0;
+        if (x == 8) return total;
+        const int64_t place = static_cast<int64_t>(uniform(s.cost[p.E])) * x;   // in eighths
+        const int e = expert_at(s.cost, p.E, static_cast<int>(place >> 3), lane);
+        if (e >= p.E) return tiles_n * (WGRAD ? p.E * tiles_k : uniform(s.units[p.E]));
+        const int64_t cost = uniform(s.cost[e + 1]) - uniform(s.cost[e]);
+        const int first = WGRAD ? e * tiles_k : uniform(s.units[e]);
+        const int units = WGRAD ? tiles_k : uniform(s.units[e + 1]) - first;
+        // (cost of the experts before e is at most the place, and that of e + 1 more)
+        const int64_t in = place - 8 * static_cast<int64_t>(uniform(s.cost[e]));
+        return uniform(first * tiles_n +
+                       static_cast<int>(in * units * tiles_n / (8 * cost)));
+    };
+    const int begin = uniform(run_begin(xcd)), end = uniform(run_begin(xcd + 1));
     auto tile_at = [&](int id) GFR_INLINE {
         TileAt t;
         if (WGRAD) {
-            const int rest = uniform(id / tiles_n);
-            t.n0 = uniform(id % tiles_n) * kTile;
-            t.e = uniform(rest / tiles_k);
-            t.m0 = uniform(rest % tiles_k) * kTile;
+            const int rest = by_n.of(id);
+            t.n0 = (id - rest * tiles_n) * kTile;
+            t.e = by_k.of(rest);
+            t.m0 = (rest - t.e * tiles_k) * kTile;
             t.rows = min(kTile, p.K - t.m0);
-            t.steps = (uniform(s.start[t.e + 1]) - uniform(s.start[t.e]) + 63) / 64;
+            t.steps = uniform((s.start[t.e + 1] - s.start[t.e] + 63) / 64);
         } else {
-            t.e = expert_at(s, p.E, uniform(id / tiles_n), lane);
+            t.e = expert_at(s.units, p.E, by_n.of(id), lane);
             // within an expert, bands of eight units by all columns
             const int u0 = uniform(s.units[t.e]), units = uniform(s.units[t.e + 1]) - u0;
             const int at = id - u0 * tiles_n;
-            const int band = uniform(at / (8 * tiles_n)), in_band = at - band * 8 * tiles_n;
-            const int depth = min(8, units - band * 8);
-            t.n0 = uniform(in_band / depth) * kTile;
-            t.m0 = uniform(s.start[t.e]) + uniform(band * 8 + in_band % depth) * kTile;
+            const int band = by_band.of(at), in_band = at - band * 8 * tiles_n;
+            const int depth = min(8, units - band * 8), column = Divisor(depth).of(in_band);
+            t.n0 = column * kTile;
+            t.m0 = uniform(s.start[t.e]) + (band * 8 + in_band - column * depth) * kTile;
             t.rows = uniform(min(kTile, uniform(s.start[t.e + 1]) - t.m0));
             t.steps = uniform(t.e < p.E ? (p.K + 63) / 64 : 0);
         }
+        t.m0 = uniform(t.m0);
+        t.n0 = uniform(t.n0);
         return t;
     };
 
@@ -456,7 +546,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
     Direct<WLINE, kTile, kWaves> db;
     da.init(p.K, wave, lane);
     db.init(WLINE ? p.N : p.K, wave, lane);
-    int load_id = uniform(xcd * per + (blockIdx.x >> 3) - stride), load_step = 0, load_steps = 0;
+    int load_id = uniform(begin + (blockIdx.x >> 3) - stride), load_step = 0, load_steps = 0;
     auto next_loads = [&]() GFR_INLINE {
         load_step = uniform(load_step + 1);
         if (load_step < uniform(load_steps)) return;
@@ -506,6 +596,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
         for (int j = 0; j < kLoads; ++j) load(j, i);
     }
     direct_wait<kLoads>();
+    int stores = 0;                           // of this wave, behind its latest loads
 
     // A tile in waves of 32 FM x 32 FN, kWaves / COLS by COLS of them.
     auto run_tile = [&](const TileAt &t, auto fm, auto fn, auto cols) GFR_INLINE {
@@ -552,7 +643,11 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
             da.at(load_step);
             db.at(load_step);
             run_part(Int<1>{}, Int<0>{}, Int<0>{}, 0, Int<0>{}, Int<kFirst>{}, now);
-            direct_wait<kFirst>();
+            // (the last tile's results may still be on their way)
+            if (stores == 0) direct_wait<kFirst>();
+            else if (stores < 32) direct_wait<kFirst + 16>();
+            else direct_wait<kFirst + 32>();
+            stores = 0;
             run_part(Int<2>{}, Int<2 * kGets>{}, Int<0>{}, now ^ 1, Int<kFirst>{}, Int<kSecond>{},
                      now);
             run_part(Int<3>{}, Int<kGets>{}, Int<2>{}, now ^ 1, Int<kSecond>{}, Int<kLoads>{}, now);
@@ -568,14 +663,37 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
                                           t.rows - wm - 32 * i, t.n0 + wn + 32 * j, lane);
                     __builtin_amdgcn_sched_barrier(0);
                 }
+            stores = FM * FN * block_stores(store);
         };
         if (!WGRAD && !WLINE && !p.wide) put(Int<kElements>{});
         else if (WGRAD && p.accumulate) p.out_f32 ? put(Int<kF32Add>{}) : put(Int<k16Add>{});
         else p.out_f32 ? put(Int<kF32>{}) : put(Int<k16>{});
     };
+    // A tile without a sum: zeros (in wgrad of an empty group, if they are not added).
+    auto clear_tile = [&](const TileAt &t) GFR_INLINE {
+        if (WGRAD && p.accumulate) return;
+        const int64_t row0 = WGRAD ? static_cast<int64_t>(t.e) * p.K + t.m0 : t.m0;
+        const int shift = p.out_f32 ? 2 : 1, row_bytes = p.N << shift;
+        const int columns = min(kTile, p.N - t.n0) << shift;
+        for (int m = wave; m < t.rows; m += kWaves) {
+            char *const to =
+                static_cast<char *>(p.out) + (row0 + m) * row_bytes + (t.n0 << shift);
+            const int skew = reinterpret_cast<uintptr_t>(to) & 2;
+            const rsrc_t r = uniform_buffer(to - skew, columns + skew);
+            if (p.wide) {
+                store16(r, u4_t{0, 0, 0, 0}, 16 * lane);
+            } else {
+                for (int i = 0; i < columns; i += 128)
+                    __builtin_amdgcn_raw_buffer_store_b16(0, r, skew + i + 2 * lane, 0, 0);
+            }
+        }
+    };
     for (; id < end; id += stride) {
         const TileAt t = tile_at(id);
-        if (p.accumulate && t.steps == 0) continue;
+        if (t.steps == 0) {
+            clear_tile(t);
+            continue;
+        }
         if (t.rows > 128) run_tile(t, Int<4>{}, Int<4>{}, Int<2>{});
         else run_tile(t, Int<4>{}, Int<2>{}, Int<4>{});
     }
