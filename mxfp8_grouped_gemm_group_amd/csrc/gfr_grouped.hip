@@ -480,20 +480,19 @@ constexpr int block_stores(int store) {
 //   part 3   reads fragment 2, goes on loading
 //
 // (One barrier a step, and all loads behind it, took 400 clocks of 2048 more: a CU's
-// loads take 16 clocks each, 64 a step.)  Tiles of at most 128 rows split their
-// columns over the waves and take half the time.
+// loads take 16 clocks each, 64 a step.)  A group's last rows take a tile of fewer:
+// up to 128 split their columns over the waves, up to 192 as the whole tile.
 template <bool F16, bool WGRAD, bool WLINE>
 __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p) {
     extern __shared__ u4_t lds[];     // [2][A's 256 lines, B's][8], the waves' results, the groups
     Groups &s = *reinterpret_cast<Groups *>(lds + 2 * kStage + kWaves * kSlab / 4);
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     float *const slab = reinterpret_cast<float *>(lds + 2 * kStage) + wave * kSlab;
-    // A tile's time: wgrad, its steps and about two more; forward, two for a tile, one for
-    // a rest of at most 128 rows.
+    // A tile's time: wgrad, its steps and about two more; forward, its rows by the tile
+    // shapes below.
     find_groups<kTile>(p, s, [](int count) -> uint32_t {
         if (WGRAD) return (count + 63) / 64 + 2;
-        const int rest = count % kTile;
-        return 2 * (count / kTile) + (rest > 128 ? 2 : rest > 0 ? 1 : 0);
+        return 4 * (count / kTile) + (count % kTile + 63) / 64;
     });
     const int tiles_n = (p.N + kTile - 1) / kTile, tiles_k = (p.K + kTile - 1) / kTile;
     const Divisor by_n(tiles_n), by_k(tiles_k), by_band(8 * tiles_n);
@@ -556,8 +555,8 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
         do {
             load_id = uniform(load_id + stride);
             if (load_id >= end) {
-                da.tile(p.x, 0, 0);
-                db.tile(p.w, 0, 0);
+                da.tile(p.x, 0, 0, 0);
+                db.tile(p.w, 0, 0, 0);
                 return;
             }
             t = tile_at(load_id);
@@ -566,23 +565,24 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
         if (WGRAD) {
             const int first = uniform(s.start[t.e]), count = uniform(s.start[t.e + 1]) - first;
             const int64_t k = p.K, n = p.N;
-            da.tile(p.x + first * k + t.m0, 2 * (count * k - t.m0), count);
-            db.tile(p.w + first * n + t.n0, 2 * (count * n - t.n0), count);
+            da.tile(p.x + first * k + t.m0, 2 * (count * k - t.m0), count, 0);
+            db.tile(p.w + first * n + t.n0, 2 * (count * n - t.n0), count, 0);
         } else {
             const int64_t k = p.K, n = p.N;
             const uint16_t *w = p.w + t.e * k * n;
-            da.tile(p.x + t.m0 * k, 2 * t.rows * k, p.K);
-            if (WLINE) db.tile(w + t.n0, 2 * (k * n - t.n0), p.K);
-            else db.tile(w + t.n0 * k, 2 * min(kTile, p.N - t.n0) * k, p.K);
+            da.tile(p.x + t.m0 * k, 2 * t.rows * k, p.K, t.rows);
+            if (WLINE) db.tile(w + t.n0, 2 * (k * n - t.n0), p.K, 0);
+            else db.tile(w + t.n0 * k, 2 * min(kTile, p.N - t.n0) * k, p.K, 0);
         }
     };
     const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) void *)lds));
-    constexpr int kA = decltype(da)::kLoads, kLoads = kA + decltype(db)::kLoads;
+    constexpr int kB = decltype(db)::kLoads, kLoads = kB + decltype(da)::kLoads;
+    // (B's first: their number does not depend on the tile's rows)
     auto load = [&](int i, int stage) GFR_INLINE {
         const uint32_t to = lds0 + stage * kStage * 16;
-        if (i < kA) da.load(i, to, wave);
-        else db.load(i - kA, to + kTile * 128, wave);
+        if (i < kB) db.load(i, to + kTile * 128, wave);
+        else if (WGRAD || i - kB < da.loads) da.load(i - kB, to, wave);
     };
     int now = 0;                              // the stage of the step that is multiplied
     int id = load_id + stride;
@@ -595,7 +595,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) load(j, i);
     }
-    direct_wait<kLoads>();
+    direct_wait<kB>();
     int stores = 0;                           // of this wave, behind its latest loads
 
     // A tile in waves of 32 FM x 32 FN, kWaves / COLS by COLS of them.
@@ -603,14 +603,18 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
         constexpr int FM = fm, FN = fn, COLS = cols;
         constexpr int kGets = FM + FN, kMfmas = FM * FN;
         const int wm = wave / COLS * (32 * FM), wn = wave % COLS * (32 * FN);
+        // (opaque: the shapes' fragment addresses are not kept over all tiles, which took
+        // the registers that loops then missed)
+        int line = lane;
+        asm volatile("" : "+v"(line));
         u4_t a[4][FM], b[4][FN];
         auto get = [&](int part, int stage, int i) GFR_INLINE {
             const u4_t *tile = lds + stage * kStage;
             if (i < FM)
-                a[part][i] = fragment<WGRAD, kTile>(tile, wm + 32 * i, part, lane);
+                a[part][i] = fragment<WGRAD, kTile>(tile, wm + 32 * i, part, line);
             else
                 b[part][i - FM] =
-                    fragment<WLINE, kTile>(tile + kTile * 8, wn + 32 * (i - FM), part, lane);
+                    fragment<WLINE, kTile>(tile + kTile * 8, wn + 32 * (i - FM), part, line);
         };
         f16_t acc[FM][FN] = {};
         // A part: its MFMAs, and between them `gets` fragments from part `first` on
@@ -636,6 +640,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
 #pragma unroll
         for (int i = 0; i < 3 * kGets; ++i) get(i / kGets, now, i % kGets);
         constexpr int kFirst = (kLoads + 2) / 3, kSecond = kFirst + (kLoads - kFirst + 1) / 2;
+        static_assert(kFirst <= kB, "part 1 begins the same number of loads in every tile");
         for (int step = 0; step < t.steps; ++step) {
             run_part(Int<0>{}, Int<kGets>{}, Int<3>{}, now, Int<0>{}, Int<0>{}, 0);
             lds_wait();
@@ -644,7 +649,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
             db.at(load_step);
             run_part(Int<1>{}, Int<0>{}, Int<0>{}, 0, Int<0>{}, Int<kFirst>{}, now);
             // (the last tile's results may still be on their way)
-            if (stores == 0) direct_wait<kFirst>();
+            if (stores < 16) direct_wait<kFirst>();
             else if (stores < 32) direct_wait<kFirst + 16>();
             else direct_wait<kFirst + 32>();
             stores = 0;
@@ -660,7 +665,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
 #pragma unroll
                 for (int j = 0; j < FN; ++j) {
                     put_block<F16, store>(p, slab, acc[i][j], row0 + wm + 32 * i,
-                                          t.rows - wm - 32 * i, t.n0 + wn + 32 * j, lane);
+                                          t.rows - wm - 32 * i, t.n0 + wn + 32 * j, line);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             stores = FM * FN * block_stores(store);
@@ -694,8 +699,11 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
             clear_tile(t);
             continue;
         }
-        if (t.rows > 128) run_tile(t, Int<4>{}, Int<4>{}, Int<2>{});
-        else run_tile(t, Int<4>{}, Int<2>{}, Int<4>{});
+        if (t.rows > 192) run_tile(t, Int<4>{}, Int<4>{}, Int<2>{});
+        else if (t.rows > 128) run_tile(t, Int<3>{}, Int<4>{}, Int<2>{});
+        else if (t.rows > 64) run_tile(t, Int<4>{}, Int<2>{}, Int<4>{});
+        else if (t.rows > 32) run_tile(t, Int<2>{}, Int<2>{}, Int<4>{});
+        else run_tile(t, Int<1>{}, Int<2>{}, Int<4>{});
     }
     // (no load may be on its way to LDS when the block ends)
     direct_wait<0>();

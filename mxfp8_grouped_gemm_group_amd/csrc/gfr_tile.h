@@ -129,41 +129,38 @@ __device__ __forceinline__ void lds_wait() {
 template <bool LINE, int BX, int WAVES>
 struct Direct {
     static constexpr int kLoads = BX / 8 / WAVES;      // a wave's, per step
-    static_assert(kLoads % 2 == 0, "a wave's loads begin with an even one");
     static constexpr int kRows = LINE ? 512 / BX : 8;  // of the tile in a load
+    static_assert(WAVES % 2 == 0 && (!LINE || kRows >= 2), "a wave's loads share their swizzle");
     const char *base;
     int64_t bytes;                 // from base to the end of what may be read
     rsrc_t r;
     int row_bytes, first;          // first: the wave's first row times row_bytes
-    int offs[2], now[2];           // of even and odd loads; those of the step
-    int piece_k;                   // k-major: first k of the lane's piece in even loads
-    int K, off;
+    int offs, now;                 // the lane's place in a load; in the step's loads
+    int piece_k;                   // k-major: first k of the lane's piece
+    int K, off, loads;             // loads: those that hold any line of the tile
 
-    // Rows of `ld` elements.
+    // Rows of `ld` elements.  Load i takes the tile's rows from (WAVES i + wave) kRows on.
     __device__ __forceinline__ void init(int64_t ld, int wave, int lane) {
         row_bytes = static_cast<int>(2 * ld);
-        first = wave * kLoads * kRows * row_bytes;
+        first = wave * kRows * row_bytes;
         if (LINE) {
             constexpr int kLanes = 64 / kRows;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = lane / kLanes, k = (h * kRows + row) & 3;
-                offs[h] = row * row_bytes + 16 * ((lane % kLanes) ^ (4 * k));
-            }
+            const int row = lane / kLanes, k = (wave * kRows + row) & 3;
+            offs = now = row * row_bytes + 16 * ((lane % kLanes) ^ (4 * k));
         } else {
-            const int piece = (lane & 7) ^ (lane >> 4);        // (odd loads: ^ 4)
+            const int row = lane >> 3, piece = (lane & 7) ^ ((wave * 8 + row) >> 1 & 7);
             piece_k = 8 * piece;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                offs[h] = (lane >> 3) * row_bytes + 16 * (piece ^ (4 * h));
+            offs = row * row_bytes + 16 * piece;
         }
     }
     // The tile whose first line begins at `from` (line-major: at k = 0), with `bytes_`
     // from there to the end of what may be read (0: no tile) and K_ to sum over.
-    __device__ __forceinline__ void tile(const uint16_t *from, int64_t bytes_, int K_) {
+    __device__ __forceinline__ void tile(const uint16_t *from, int64_t bytes_, int K_, int lines) {
         base = reinterpret_cast<const char *>(from);
         bytes = bytes_;
         K = K_;
+        // (of a line-major step every load holds some of the lines)
+        loads = LINE ? kLoads : uniform((lines + 8 * WAVES - 1) / (8 * WAVES));
         if (!LINE) r = uniform_buffer(base, bytes);
     }
     // Ahead of a step's loads.
@@ -172,16 +169,13 @@ struct Direct {
             const int64_t gone = static_cast<int64_t>(step) * 64 * row_bytes;
             r = uniform_buffer(base + gone, bytes > gone ? bytes - gone : 0);
             off = first;
-            now[0] = offs[0];
-            now[1] = offs[kRows == 2];
         } else {
             off = first + 128 * step;
-            now[0] = 64 * step + piece_k < K ? offs[0] : kPast;
-            now[1] = 64 * step + (piece_k ^ 32) < K ? offs[1] : kPast;
+            now = 64 * step + piece_k < K ? offs : kPast;
         }
     }
     __device__ __forceinline__ void load(int i, uint32_t tile, int wave) const {
-        load_lds(r, now[i & 1], off + i * kRows * row_bytes, tile + (wave * kLoads + i) * 1024);
+        load_lds(r, now, off + i * WAVES * kRows * row_bytes, tile + (WAVES * i + wave) * 1024);
     }
 };
 
