@@ -11,10 +11,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 #include "gfr.h"
 #include "gfr_device.h"
+#include "gfr_direct.h"
 #include "gfr_layer.h"
 #include "gfr_tile.h"
 
@@ -296,23 +295,12 @@ __global__ __launch_bounds__(256, 2) void general_kernel(GroupedParams p) {
 // ---------------------------------------------------------------------------
 // Direct kernel: rows of whole pieces
 // ---------------------------------------------------------------------------
-constexpr int kTile = 256, kWaves = 4;
-constexpr int kStage = 2 * kTile * 8;       // pieces: an operand's 256 lines, the other's
 constexpr int kPitch = 36;      // floats of a row of 32 results in LDS: spreads rows over banks
 constexpr int kSlab = 17 * kPitch;
 static_assert(kWaves * kSlab % 4 == 0, "the groups begin at a whole piece");
 constexpr int kDirectLds = 2 * kStage * 16 + kWaves * kSlab * 4 +
                            static_cast<int>(sizeof(Groups));
 static_assert(kDirectLds <= kMaxLds, "as allow_lds allows");
-
-#define GFR_INLINE __attribute__((always_inline))
-template <int N>
-using Int = std::integral_constant<int, N>;
-
-// A tile: `rows` rows of out from row0 on (forward: of x too), columns from n0 on.
-struct TileAt {
-    int e, m0, n0, rows, steps;
-};
 
 // The last of E + 1 experts whose entry is at most u, found by a wave side by side.
 __device__ __forceinline__ int expert_at(const int *from, int E, int u, int lane) {
@@ -322,21 +310,6 @@ __device__ __forceinline__ int expert_at(const int *from, int E, int u, int lane
             __builtin_amdgcn_ballot_w64((e + lane <= E) & (from[min(e + lane, E)] <= u)));
     return uniform(n - 1);
 }
-
-// n / d for 0 <= n < 2^31 by d's reciprocal in FP32 (which is off by less than one for
-// quotients below 2^22, and corrected here).
-struct Divisor {
-    int d;
-    float inverse;
-    __device__ __forceinline__ explicit Divisor(int d_) : d(d_), inverse(1.0f / d_) {}
-    __device__ __forceinline__ int of(int n) const {
-        int q = static_cast<int>(static_cast<float>(n) * inverse);
-        int rest = n - q * d;
-        if (rest < 0) --q, rest += d;
-        if (rest >= d) ++q;
-        return uniform(q);
-    }
-};
 
 // How results are written: FP32 or 16 bits, added to what is there or not; or, for rows
 // that begin anywhere, element by element.
@@ -467,54 +440,40 @@ constexpr int block_stores(int store) {
     return store == k16 || store == k16Add ? 2 : 4;
 }
 
-// 256 x 256 tiles of four waves, one block to a CU, which goes through its tiles'
-// steps (64 of the summed index) as one run: two LDS stages, filled straight from
-// memory two steps ahead, also over the end of a tile.  A step is four parts of 16;
-// each part's fragments have registers of their own, so that a stage is read within
-// three parts and filled in the other five of its two steps:
-//
-//   part 0   reads the step's last fragments; then a barrier: the stage is free
-//   part 1   begins the loads of the step after next; then a barrier: the next stage
-//            has landed
-//   part 2   reads the next step's fragments 0 and 1, goes on loading
-//   part 3   reads fragment 2, goes on loading
-//
-// (One barrier a step, and all loads behind it, took 400 clocks of 2048 more: a CU's
-// loads take 16 clocks each, 64 a step.)  A group's last rows take a tile of fewer:
-// up to 128 split their columns over the waves, up to 192 as the whole tile.
-template <bool F16, bool WGRAD, bool WLINE>
-__global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p) {
-    extern __shared__ u4_t lds[];     // [2][A's 256 lines, B's][8], the waves' results, the groups
-    Groups &s = *reinterpret_cast<Groups *>(lds + 2 * kStage + kWaves * kSlab / 4);
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    float *const slab = reinterpret_cast<float *>(lds + 2 * kStage) + wave * kSlab;
-    // A tile's time: wgrad, its steps and about two more; forward, its rows by the tile
-    // shapes below.
-    find_groups<kTile>(p, s, [](int count) -> uint32_t {
-        if (WGRAD) return (count + 63) / 64 + 2;
-        return 4 * (count / kTile) + (count % kTile + 63) / 64;
-    });
-    const int tiles_n = (p.N + kTile - 1) / kTile, tiles_k = (p.K + kTile - 1) / kTile;
-    const Divisor by_n(tiles_n), by_k(tiles_k), by_band(8 * tiles_n);
-    const int total = tiles_n * (WGRAD ? p.E * tiles_k : uniform(s.units[p.fill ? p.E + 1 : p.E]));
-    // Blocks go round the eight XCDs; each XCD takes a run of tiles, an eighth of the time.
-    const int xcd = blockIdx.x & 7, stride = gridDim.x >> 3;
-    auto run_begin = [&](int x) {
+// The block's run: Blocks go round the eight XCDs; each XCD takes a run of tiles, an eighth
+// of the time.
+template <bool WGRAD, bool WLINE>
+struct GroupedTiles {
+    const GroupedParams &p;
+    const Groups &s;
+    int lane, tiles_n, tiles_k, total;
+    Divisor by_n, by_k, by_band;
+    int begin, end, stride;
+
+    __device__ __forceinline__ GroupedTiles(const GroupedParams &p_, const Groups &s_)
+        : p(p_), s(s_), lane(threadIdx.x & 63), tiles_n((p.N + kTile - 1) / kTile),
+          tiles_k((p.K + kTile - 1) / kTile),
+          total(tiles_n * (WGRAD ? p.E * tiles_k : uniform(s.units[p.fill ? p.E + 1 : p.E]))),
+          by_n(tiles_n), by_k(tiles_k), by_band(8 * tiles_n) {
+        const int xcd = blockIdx.x & 7;
+        stride = gridDim.x >> 3;
+        begin = run_begin(xcd) + (blockIdx.x >> 3);
+        end = run_begin(xcd + 1);
+    }
+    __device__ __forceinline__ int run_begin(int x) const {
         if (x == 0) return 0;
         if (x == 8) return total;
         const int64_t place = static_cast<int64_t>(uniform(s.cost[p.E])) * x;   // in eighths
         const int e = expert_at(s.cost, p.E, static_cast<int>(place >> 3), lane);
         if (e >= p.E) return tiles_n * (WGRAD ? p.E * tiles_k : uniform(s.units[p.E]));
+        // (the cost of the experts before e is at most the place, and that of e too is more)
         const int64_t cost = uniform(s.cost[e + 1]) - uniform(s.cost[e]);
         const int first = WGRAD ? e * tiles_k : uniform(s.units[e]);
         const int units = WGRAD ? tiles_k : uniform(s.units[e + 1]) - first;
-        // (cost of the experts before e is at most the place, and that of e + 1 more)
         const int64_t in = place - 8 * static_cast<int64_t>(uniform(s.cost[e]));
-        return uniform(first * tiles_n +
-                       static_cast<int>(in * units * tiles_n / (8 * cost)));
-    };
-    const int begin = uniform(run_begin(xcd)), end = uniform(run_begin(xcd + 1));
-    auto tile_at = [&](int id) GFR_INLINE {
+        return uniform(first * tiles_n + static_cast<int>(in * units * tiles_n / (8 * cost)));
+    }
+    __device__ __forceinline__ TileAt at(int id) const {
         TileAt t;
         if (WGRAD) {
             const int rest = by_n.of(id);
@@ -538,151 +497,62 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
         t.m0 = uniform(t.m0);
         t.n0 = uniform(t.n0);
         return t;
-    };
-
-    // The loads' place: the operands of a tile, its next step.
-    Direct<WGRAD, kTile, kWaves> da;
-    Direct<WLINE, kTile, kWaves> db;
-    da.init(p.K, wave, lane);
-    db.init(WLINE ? p.N : p.K, wave, lane);
-    int load_id = uniform(begin + (blockIdx.x >> 3) - stride), load_step = 0, load_steps = 0;
-    auto next_loads = [&]() GFR_INLINE {
-        load_step = uniform(load_step + 1);
-        if (load_step < uniform(load_steps)) return;
-        load_step = 0;
-        load_steps = 0x7fffffff;             // no tile left: zeros
-        TileAt t;
-        do {
-            load_id = uniform(load_id + stride);
-            if (load_id >= end) {
-                da.tile(p.x, 0, 0, 0);
-                db.tile(p.w, 0, 0, 0);
-                return;
-            }
-            t = tile_at(load_id);
-        } while (t.steps == 0);
-        load_steps = t.steps;
+    }
+    template <class A, class B>
+    __device__ __forceinline__ void loads(const TileAt &t, A &da, B &db) const {
+        const int64_t k = p.K, n = p.N;
         if (WGRAD) {
             const int first = uniform(s.start[t.e]), count = uniform(s.start[t.e + 1]) - first;
-            const int64_t k = p.K, n = p.N;
             da.tile(p.x + first * k + t.m0, 2 * (count * k - t.m0), count, 0);
             db.tile(p.w + first * n + t.n0, 2 * (count * n - t.n0), count, 0);
         } else {
-            const int64_t k = p.K, n = p.N;
             const uint16_t *w = p.w + t.e * k * n;
             da.tile(p.x + t.m0 * k, 2 * t.rows * k, p.K, t.rows);
             if (WLINE) db.tile(w + t.n0, 2 * (k * n - t.n0), p.K, 0);
             else db.tile(w + t.n0 * k, 2 * min(kTile, p.N - t.n0) * k, p.K, 0);
         }
-    };
-    const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
-        (__attribute__((address_space(3))) void *)lds));
-    constexpr int kB = decltype(db)::kLoads, kLoads = kB + decltype(da)::kLoads;
-    // (B's first: their number does not depend on the tile's rows)
-    auto load = [&](int i, int stage) GFR_INLINE {
-        const uint32_t to = lds0 + stage * kStage * 16;
-        if (i < kB) db.load(i, to + kTile * 128, wave);
-        else if (WGRAD || i - kB < da.loads) da.load(i - kB, to, wave);
-    };
-    int now = 0;                              // the stage of the step that is multiplied
-    int id = load_id + stride;
-    if (id >= end) return;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        next_loads();
-        da.at(load_step);
-        db.at(load_step);
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) load(j, i);
     }
-    direct_wait<kB>();
-    int stores = 0;                           // of this wave, behind its latest loads
+};
 
-    // A tile in waves of 32 FM x 32 FN, kWaves / COLS by COLS of them.
-    auto run_tile = [&](const TileAt &t, auto fm, auto fn, auto cols) GFR_INLINE {
-        constexpr int FM = fm, FN = fn, COLS = cols;
-        constexpr int kGets = FM + FN, kMfmas = FM * FN;
-        const int wm = wave / COLS * (32 * FM), wn = wave % COLS * (32 * FN);
-        // (opaque: the shapes' fragment addresses are not kept over all tiles, which took
-        // the registers that loops then missed)
-        int line = lane;
-        asm volatile("" : "+v"(line));
-        u4_t a[4][FM], b[4][FN];
-        auto get = [&](int part, int stage, int i) GFR_INLINE {
-            const u4_t *tile = lds + stage * kStage;
-            if (i < FM)
-                a[part][i] = fragment<WGRAD, kTile>(tile, wm + 32 * i, part, line);
-            else
-                b[part][i - FM] =
-                    fragment<WLINE, kTile>(tile + kTile * 8, wn + 32 * (i - FM), part, line);
-        };
-        f16_t acc[FM][FN] = {};
-        // A part: its MFMAs, and between them `gets` fragments from part `first` on
-        // of a stage, and loads [from, to).
-        auto run_part = [&](auto part, auto gets, auto first, int stage, auto from, auto to,
-                            int into) GFR_INLINE {
-            constexpr int kG = (gets + kMfmas - 1) / kMfmas;
-            constexpr int kL = (to - from + kMfmas - 1) / kMfmas;
+template <bool F16, bool WGRAD, bool WLINE>
+struct GroupedFinish {
+    const GroupedParams &p;
+    float *slab;
+
+    __device__ __forceinline__ int64_t row0(const TileAt &t) const {
+        return WGRAD ? static_cast<int64_t>(t.e) * p.K + t.m0 : t.m0;
+    }
+    template <int STORE, int FM, int FN>
+    __device__ __forceinline__ int put(const TileAt &t, const f16_t (&acc)[FM][FN], int wm, int wn,
+                                       int lane) const {
 #pragma unroll
-            for (int m = 0; m < kMfmas; ++m) {
+        for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int h = 0; h < kG; ++h)
-                    if (const int i = m * kG + h; i < gets)
-                        get(first + i / kGets, stage, i % kGets);
-#pragma unroll
-                for (int h = 0; h < kL; ++h)
-                    if (const int i = from + m * kL + h; i < to) load(i, into);
-                acc[m / FN][m % FN] = mfma32<F16>(b[part][m % FN], a[part][m / FN],
-                                                  acc[m / FN][m % FN]);
+            for (int j = 0; j < FN; ++j) {
+                put_block<F16, STORE>(p, slab, acc[i][j], row0(t) + wm + 32 * i,
+                                      t.rows - wm - 32 * i, t.n0 + wn + 32 * j, lane);
                 __builtin_amdgcn_sched_barrier(0);
             }
-        };
-#pragma unroll
-        for (int i = 0; i < 3 * kGets; ++i) get(i / kGets, now, i % kGets);
-        constexpr int kFirst = (kLoads + 2) / 3, kSecond = kFirst + (kLoads - kFirst + 1) / 2;
-        static_assert(kFirst <= kB, "part 1 begins the same number of loads in every tile");
-        for (int step = 0; step < t.steps; ++step) {
-            run_part(Int<0>{}, Int<kGets>{}, Int<3>{}, now, Int<0>{}, Int<0>{}, 0);
-            lds_wait();
-            next_loads();
-            da.at(load_step);
-            db.at(load_step);
-            run_part(Int<1>{}, Int<0>{}, Int<0>{}, 0, Int<0>{}, Int<kFirst>{}, now);
-            // (the last tile's results may still be on their way)
-            if (stores < 16) direct_wait<kFirst>();
-            else if (stores < 32) direct_wait<kFirst + 16>();
-            else direct_wait<kFirst + 32>();
-            stores = 0;
-            run_part(Int<2>{}, Int<2 * kGets>{}, Int<0>{}, now ^ 1, Int<kFirst>{}, Int<kSecond>{},
-                     now);
-            run_part(Int<3>{}, Int<kGets>{}, Int<2>{}, now ^ 1, Int<kSecond>{}, Int<kLoads>{}, now);
-            now ^= 1;
-        }
-        const int64_t row0 = WGRAD ? static_cast<int64_t>(t.e) * p.K + t.m0 : t.m0;
-        auto put = [&](auto store) GFR_INLINE {
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    put_block<F16, store>(p, slab, acc[i][j], row0 + wm + 32 * i,
-                                          t.rows - wm - 32 * i, t.n0 + wn + 32 * j, line);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            stores = FM * FN * block_stores(store);
-        };
-        if (!WGRAD && !WLINE && !p.wide) put(Int<kElements>{});
-        else if (WGRAD && p.accumulate) p.out_f32 ? put(Int<kF32Add>{}) : put(Int<k16Add>{});
-        else p.out_f32 ? put(Int<kF32>{}) : put(Int<k16>{});
-    };
-    // A tile without a sum: zeros (in wgrad of an empty group, if they are not added).
-    auto clear_tile = [&](const TileAt &t) GFR_INLINE {
+        return FM * FN * block_stores(STORE);
+    }
+    template <int FM, int FN>
+    __device__ __forceinline__ int tile(const TileAt &t, const f16_t (&acc)[FM][FN], int wm, int wn,
+                                        int lane) const {
+        if (!WGRAD && !WLINE && !p.wide) return put<kElements>(t, acc, wm, wn, lane);
+        if (WGRAD && p.accumulate)
+            return p.out_f32 ? put<kF32Add>(t, acc, wm, wn, lane)
+                             : put<k16Add>(t, acc, wm, wn, lane);
+        return p.out_f32 ? put<kF32>(t, acc, wm, wn, lane) : put<k16>(t, acc, wm, wn, lane);
+    }
+    // Zeros (in wgrad of an empty group, if they are not added).
+    __device__ __forceinline__ void clear(const TileAt &t) const {
         if (WGRAD && p.accumulate) return;
-        const int64_t row0 = WGRAD ? static_cast<int64_t>(t.e) * p.K + t.m0 : t.m0;
+        const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
         const int shift = p.out_f32 ? 2 : 1, row_bytes = p.N << shift;
         const int columns = min(kTile, p.N - t.n0) << shift;
         for (int m = wave; m < t.rows; m += kWaves) {
             char *const to =
-                static_cast<char *>(p.out) + (row0 + m) * row_bytes + (t.n0 << shift);
+                static_cast<char *>(p.out) + (row0(t) + m) * row_bytes + (t.n0 << shift);
             const int skew = reinterpret_cast<uintptr_t>(to) & 2;
             const rsrc_t r = uniform_buffer(to - skew, columns + skew);
             if (p.wide) {
@@ -692,21 +562,23 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
                     __builtin_amdgcn_raw_buffer_store_b16(0, r, skew + i + 2 * lane, 0, 0);
             }
         }
-    };
-    for (; id < end; id += stride) {
-        const TileAt t = tile_at(id);
-        if (t.steps == 0) {
-            clear_tile(t);
-            continue;
-        }
-        if (t.rows > 192) run_tile(t, Int<4>{}, Int<4>{}, Int<2>{});
-        else if (t.rows > 128) run_tile(t, Int<3>{}, Int<4>{}, Int<2>{});
-        else if (t.rows > 64) run_tile(t, Int<4>{}, Int<2>{}, Int<4>{});
-        else if (t.rows > 32) run_tile(t, Int<2>{}, Int<2>{}, Int<4>{});
-        else run_tile(t, Int<1>{}, Int<2>{}, Int<4>{});
     }
-    // (no load may be on its way to LDS when the block ends)
-    direct_wait<0>();
+};
+
+template <bool F16, bool WGRAD, bool WLINE>
+__global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p) {
+    extern __shared__ u4_t lds[];     // [2][A's 256 lines, B's][8], the waves' results, the groups
+    Groups &s = *reinterpret_cast<Groups *>(lds + 2 * kStage + kWaves * kSlab / 4);
+    // A tile's time: wgrad, its steps and about two more; forward, its rows by the tile
+    // shapes there are.
+    find_groups<kTile>(p, s, [](int count) -> uint32_t {
+        if (WGRAD) return (count + 63) / 64 + 2;
+        return 4 * (count / kTile) + (count % kTile + 63) / 64;
+    });
+    float *const slab = reinterpret_cast<float *>(lds + 2 * kStage) + uniform(threadIdx.x >> 6) * kSlab;
+    const GroupedTiles<WGRAD, WLINE> tiles(p, s);
+    const GroupedFinish<F16, WGRAD, WLINE> finish{p, slab};
+    run_tiles<F16, WGRAD, WLINE>(lds, tiles, finish, p.K, WLINE ? p.N : p.K);
 }
 
 template <bool F16, bool WGRAD, bool WLINE>

@@ -120,18 +120,21 @@ struct LoraParams {
     const uint16_t *residual;  // [M, N] or null
     void *out;                 // [M, N]
     int32_t *status;           // may be null
-    float *inner;              // workspace: [M][r], scaled
-    float *dense;              // workspace: [M][N]
-    float *partial;            // workspace of the dense product's K split
+    float *inner;              // workspace, few rows: [M][r], scaled
+    float *dense;              // workspace, few rows: [M][N]
+    float *partial;            // workspace, few rows: of the dense product's K split
+    uint16_t *terms;           // workspace, many rows: [M][2][r], scaled
     LinearChoice choice;
+    int32_t tiles;             // many rows
     int32_t bias_f32, out_f32, f16;
     int32_t M, N, K, L, r;
 };
 
-// Workspace layout of lora_linear (256-byte aligned regions; inner at 0).
+// Workspace layout of lora_linear (256-byte aligned regions; inner or terms at 0).
 struct LoraLayout {
     size_t dense, partial, total;
-    LinearChoice choice;       // of the dense product
+    int32_t tiles;             // many rows: dense tiles that expand in their epilogue
+    LinearChoice choice;       // few rows: of the dense product
 };
 LoraLayout lora_layout(int64_t M, int64_t N, int64_t K, int64_t r);
 hipError_t launch_lora(const LoraParams &p, hipStream_t stream);

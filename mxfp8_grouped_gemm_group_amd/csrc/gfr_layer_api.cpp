@@ -431,6 +431,8 @@ int gfr_lora_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *
     p.out = d.out;
     p.status = opts->status_dev;
     p.inner = reinterpret_cast<float *>(ws);
+    p.terms = reinterpret_cast<uint16_t *>(ws);
+    p.tiles = l.tiles;
     p.dense = reinterpret_cast<float *>(ws + l.dense);
     p.partial = reinterpret_cast<float *>(ws + l.partial);
     p.choice = l.choice;

@@ -103,82 +103,6 @@ __device__ __forceinline__ u4_t eight_first(rsrc_t r, int off, int valid) {
     return s;
 }
 
-// 16 bytes a lane from memory straight to LDS, 1024 consecutive bytes from `lds` on.
-// (Assembly, because behind the builtin the compiler waits for all of them ahead of
-// every later LDS read.  It writes no register; direct_wait is its wait.)
-__device__ __forceinline__ void load_lds(rsrc_t r, int lane_off, int off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(lds), "v"(lane_off), "s"(r), "s"(off) : "memory");
-}
-// All but this wave's N latest loads and stores are through; then the same of the
-// block's other waves.
-template <int N>
-__device__ __forceinline__ void direct_wait() {
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "n"(N) : "memory");
-}
-// This wave's LDS accesses are through, then the other waves' too.
-__device__ __forceinline__ void lds_wait() {
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
-// One operand's loads of a step, straight to LDS, for rows of whole pieces (row
-// lengths multiples of 8).  A load takes 1024 bytes of the tile; its lanes choose
-// their piece by the layout's swizzle.  Pieces behind the summed index's end are
-// zeros (their offsets lie behind the buffer's end), and so is all of a step behind
-// it; what lies behind the last line belongs to lines that are not stored.
-template <bool LINE, int BX, int WAVES>
-struct Direct {
-    static constexpr int kLoads = BX / 8 / WAVES;      // a wave's, per step
-    static constexpr int kRows = LINE ? 512 / BX : 8;  // of the tile in a load
-    static_assert(WAVES % 2 == 0 && (!LINE || kRows >= 2), "a wave's loads share their swizzle");
-    const char *base;
-    int64_t bytes;                 // from base to the end of what may be read
-    rsrc_t r;
-    int row_bytes, first;          // first: the wave's first row times row_bytes
-    int offs, now;                 // the lane's place in a load; in the step's loads
-    int piece_k;                   // k-major: first k of the lane's piece
-    int K, off, loads;             // loads: those that hold any line of the tile
-
-    // Rows of `ld` elements.  Load i takes the tile's rows from (WAVES i + wave) kRows on.
-    __device__ __forceinline__ void init(int64_t ld, int wave, int lane) {
-        row_bytes = static_cast<int>(2 * ld);
-        first = wave * kRows * row_bytes;
-        if (LINE) {
-            constexpr int kLanes = 64 / kRows;
-            const int row = lane / kLanes, k = (wave * kRows + row) & 3;
-            offs = now = row * row_bytes + 16 * ((lane % kLanes) ^ (4 * k));
-        } else {
-            const int row = lane >> 3, piece = (lane & 7) ^ ((wave * 8 + row) >> 1 & 7);
-            piece_k = 8 * piece;
-            offs = row * row_bytes + 16 * piece;
-        }
-    }
-    // The tile whose first line begins at `from` (line-major: at k = 0), with `bytes_`
-    // from there to the end of what may be read (0: no tile) and K_ to sum over.
-    __device__ __forceinline__ void tile(const uint16_t *from, int64_t bytes_, int K_, int lines) {
-        base = reinterpret_cast<const char *>(from);
-        bytes = bytes_;
-        K = K_;
-        // (of a line-major step every load holds some of the lines)
-        loads = LINE ? kLoads : uniform((lines + 8 * WAVES - 1) / (8 * WAVES));
-        if (!LINE) r = uniform_buffer(base, bytes);
-    }
-    // Ahead of a step's loads.
-    __device__ __forceinline__ void at(int step) {
-        if (LINE) {
-            const int64_t gone = static_cast<int64_t>(step) * 64 * row_bytes;
-            r = uniform_buffer(base + gone, bytes > gone ? bytes - gone : 0);
-            off = first;
-        } else {
-            off = first + 128 * step;
-            now = 64 * step + piece_k < K ? offs : kPast;
-        }
-    }
-    __device__ __forceinline__ void load(int i, uint32_t tile, int wave) const {
-        load_lds(r, now, off + i * WAVES * kRows * row_bytes, tile + (WAVES * i + wave) * 1024);
-    }
-};
-
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return F16 ? pack_f16(a, b) : pack_bf16(a, b);
