@@ -28,6 +28,7 @@ struct LinearParams {
     int32_t M, N, K;
     LinearChoice::Kernel kernel;
     int32_t split;             // 1: no partial sums
+    int32_t keep_partial;      // 1: partial sums are the result; nothing joins them
 };
 
 hipError_t launch_linear(const LinearParams &p, hipStream_t stream);
@@ -121,8 +122,7 @@ struct LoraParams {
     void *out;                 // [M, N]
     int32_t *status;           // may be null
     float *inner;              // workspace, few rows: [M][r], scaled
-    float *dense;              // workspace, few rows: [M][N]
-    float *partial;            // workspace, few rows: of the dense product's K split
+    float *dense;              // workspace, few rows: [M][N], or the K splits' sums
     uint16_t *terms;           // workspace, many rows: [M][2][r], scaled
     LinearChoice choice;
     int32_t tiles;             // many rows
@@ -132,7 +132,7 @@ struct LoraParams {
 
 // Workspace layout of lora_linear (256-byte aligned regions; inner or terms at 0).
 struct LoraLayout {
-    size_t dense, partial, total;
+    size_t dense, total;
     int32_t tiles;             // many rows: dense tiles that expand in their epilogue
     LinearChoice choice;       // few rows: of the dense product
 };

@@ -434,7 +434,6 @@ int gfr_lora_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *
     p.terms = reinterpret_cast<uint16_t *>(ws);
     p.tiles = l.tiles;
     p.dense = reinterpret_cast<float *>(ws + l.dense);
-    p.partial = reinterpret_cast<float *>(ws + l.partial);
     p.choice = l.choice;
     p.bias_f32 = d.bias_f32;
     p.out_f32 = d.out_f32;

@@ -729,7 +729,8 @@ hipError_t launch_tiles(const LinearParams &p, hipStream_t stream) {
     const int64_t grid = (static_cast<int64_t>(tm) * tn + 7) / 8 * 8;
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid), p.split),
                        dim3((BM / WM) * (BN / WN) * 64), lds, stream, p, tm, tn);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess || p.split == 1) return e;
+    if (hipError_t e = hipGetLastError(); e != hipSuccess || p.split == 1 || p.keep_partial)
+        return e;
     const int64_t threads = static_cast<int64_t>(p.M) * (p.wide ? (p.N + 7) / 8 : p.N);
     hipLaunchKernelGGL((join_kernel<SWIGLU, F16>),
                        dim3(static_cast<uint32_t>((threads + 255) / 256)), dim3(256), 0, stream, p);

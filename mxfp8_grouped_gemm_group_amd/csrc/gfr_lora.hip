@@ -91,48 +91,63 @@ __global__ __launch_bounds__(256) void shrink_rows_kernel(LoraParams p, int wave
     }
 }
 
+// A result of the dense product: its K splits' sums, in order, and the bias.
+template <bool F16>
+__device__ __forceinline__ float dense_sum(const LoraParams &p, int t, int n, float bias) {
+    const int64_t pitch = p.choice.split > 1 ? (p.N + 7) / 8 * 8 : p.N;
+    const float *at = p.dense + t * pitch + n;
+    float v = 0.0f;
+    for (int s = 0; s < p.choice.split; ++s) v += at[s * p.M * pitch];
+    return v + bias;
+}
+
 // A thread per column, a block's rows in turn; B's row of a column stays in registers
-// while the adapter does (up to 64 ranks).
-template <bool F16, bool ALIGNED>
+// while the adapter does (up to 64 ranks).  B is read V elements at a time.
+template <bool F16, int V>
 __global__ __launch_bounds__(256) void expand_rows_kernel(LoraParams p, int rows) {
     const int n = blockIdx.x * 256 + threadIdx.x, at_n = min(n, p.N - 1);
     const int t0 = blockIdx.y * rows, t1 = min(t0 + rows, p.M);
+    const float bias = p.bias ? element(p.bias, at_n, p.bias_f32, F16) : 0.0f;
     int kept = -1;
-    u4_t b[8];
+    uint32_t b[32];                   // two ranks each
     for (int t = t0; t < t1; ++t) {
         const int64_t at = static_cast<int64_t>(t) * p.N + at_n;
-        const float dense = p.dense[at];
-        const uint16_t res = p.residual ? p.residual[at] : 0;
         const int i = uniform(adapter(p, t));
-        float sum = 0.0f;
+        const uint16_t *row = p.b + (static_cast<int64_t>(max(i, 0)) * p.N + at_n) * p.r;
+        if (V > 1 && p.r <= 64 && i >= 0 && i != kept) {
+            kept = i;
+#pragma unroll
+            for (int j = 0; j < 64; j += V)
+                if (j < p.r) {
+                    if (V == 8) {
+                        const u4_t v = load<u4_t>(row + j);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) b[j / 2 + e] = v[e];
+                    } else {
+                        const u2_t v = load<u2_t>(row + j);
+                        b[j / 2] = v[0];
+                        b[j / 2 + 1] = v[1];
+                    }
+                }
+        }
+        const uint16_t res = p.residual ? p.residual[at] : 0;
+        float y = dense_sum<F16>(p, t, at_n, bias);
         if (i >= 0) {
             const float *s = p.inner + static_cast<int64_t>(t) * p.r;
-            const uint16_t *row = p.b + (static_cast<int64_t>(i) * p.N + at_n) * p.r;
-            if (ALIGNED && p.r <= 64) {
-                if (i != kept)
+            float sum = 0.0f;
+            if (V > 1 && p.r <= 64) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        if (8 * c < p.r) b[c] = load<u4_t>(row + 8 * c);
-                kept = i;
+                for (int j = 0; j < 64; j += V)
+                    if (j < p.r)
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    if (8 * c < p.r)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            sum = fmaf(s[8 * c + e], unpack1<F16>(b[c][e >> 1] >> (16 * (e & 1))),
-                                       sum);
-            } else if (ALIGNED) {
-                for (int j = 0; j < p.r; j += 8) {
-                    const u4_t v = load<u4_t>(row + j);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        sum = fmaf(s[j + e], unpack1<F16>(v[e >> 1] >> (16 * (e & 1))), sum);
-                }
+                        for (int e = 0; e < V; ++e)
+                            sum = fmaf(s[j + e], unpack1<F16>(b[(j + e) / 2] >> (16 * (e & 1))), sum);
             } else {
+#pragma unroll 8
                 for (int j = 0; j < p.r; ++j) sum = fmaf(s[j], unpack1<F16>(row[j]), sum);
             }
+            y += sum;
         }
-        float y = dense + sum;
         if (p.residual) y += unpack1<F16>(res);
         if (n >= p.N) continue;
         if (p.out_f32)
@@ -146,73 +161,94 @@ __global__ __launch_bounds__(256) void expand_rows_kernel(LoraParams p, int rows
 // Many rows
 // ---------------------------------------------------------------------------
 
-// 32 rows a block, its eight waves along K, 32 RF ranks at a time; an adapter after the
-// other where the rows have several.  inner is kept as two 16-bit terms, the value and
-// what its rounding left over: 16 bits of mantissa or more, for the matrix cores.
+// 32 rows by 32 ranks a block, its eight waves along K; an adapter after the other where
+// the rows have several.  A wave's two stages of 64 K are filled straight from memory, in
+// whole lines (fragments loaded from memory took 32 half lines a load: 4096 rows of 4096
+// by rank 64 51 us).  inner is kept as two 16-bit terms, the value and what its
+// rounding left over: 16 bits of mantissa or more, for the matrix cores.
 constexpr int kShrinkWaves = 8;
-template <bool F16, int RF>
+constexpr int kShrinkLds = kShrinkWaves * 2 * 64 * 8 * 16;
+template <bool F16>
 __global__ __launch_bounds__(kShrinkWaves * 64, 2) void shrink_tile_kernel(LoraParams p) {
-    __shared__ float part[kShrinkWaves][32][33];
+    extern __shared__ u4_t lds[];           // [wave][2][x's 32 lines, A's][8]; then the sums
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int c = lane & 31, g = lane >> 5, t0 = blockIdx.x * 32;
+    const int c = lane & 31, g = lane >> 5, t0 = blockIdx.x * 32, j0 = blockIdx.y * 32;
     const int rows = min(32, p.M - t0), row_bytes = 2 * p.K;
     const int id = c < rows ? adapter(p, t0 + c) : -1;
-    if (wave == 0 && lane < rows) check_adapter(p, t0 + lane);
-    const rsrc_t xr = buffer(p.x + static_cast<int64_t>(t0) * p.K,
-                             static_cast<int64_t>(rows) * row_bytes);
+    if (blockIdx.y == 0 && wave == 0 && lane < rows) check_adapter(p, t0 + lane);
+    const rsrc_t xr = uniform_buffer(
+        reinterpret_cast<const char *>(p.x + static_cast<int64_t>(t0) * p.K),
+        static_cast<int64_t>(rows) * row_bytes);
     const int steps = (p.K + 63) / 64;
     const int s0 = steps * wave / kShrinkWaves, s1 = steps * (wave + 1) / kShrinkWaves;
+    // a load takes eight lines; the lane's piece of even and odd ones
+    const int line = lane >> 3;
+    int piece[2], off[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        piece[h] = (lane & 7) ^ ((line >> 1) + 4 * h);
+        off[h] = line * row_bytes + 16 * piece[h];
+    }
+    u4_t *const mine = lds + wave * 2 * 64 * 8;
+    const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+        (__attribute__((address_space(3))) void *)lds)) + wave * 2 * 64 * 128;
     uint64_t todo = __builtin_amdgcn_ballot_w64(id >= 0);
     while (todo) {
         const int i = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
         todo &= ~__builtin_amdgcn_ballot_w64(id == i);
         const float scale = p.scaling ? p.scaling[i] : 1.0f;
-        const rsrc_t ar = buffer(p.a + static_cast<int64_t>(i) * p.r * p.K,
-                                 static_cast<int64_t>(p.r) * row_bytes);
-        for (int j0 = 0; j0 < p.r; j0 += 32 * RF) {
-            f16_t acc[RF] = {};
-#pragma unroll 1
-            for (int s = s0; s < s1; ++s) {
-                u4_t xv[4], av[RF][4];
+        const int64_t rank0 = static_cast<int64_t>(i) * p.r + j0;
+        const rsrc_t ar = uniform_buffer(reinterpret_cast<const char *>(p.a + rank0 * p.K),
+                                         static_cast<int64_t>(min(32, p.r - j0)) * row_bytes);
+        f16_t acc = {};
+        // (behind the wave's last step: zeros)
+        auto fetch = [&](int s) GFR_INLINE {
+            const uint32_t to = lds0 + (s - s0 & 1) * 64 * 128;
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int k = 64 * s + 16 * h + 8 * g;
-                    const int off = k < p.K ? c * row_bytes + 2 * k : kPast;
-                    xv[h] = load16<0>(xr, off, 0);
+            for (int h = 0; h < 4; ++h) {
+                const int o = s < s1 && 64 * s + 8 * piece[h & 1] < p.K ? off[h & 1] : kPast;
+                load_lds(xr, o, 8 * h * row_bytes + 128 * s, to + h * 1024);
+                load_lds(ar, o, 8 * h * row_bytes + 128 * s, to + (4 + h) * 1024);
+            }
+        };
+        fetch(s0);
+        for (int s = s0; s < s1; ++s) {
+            fetch(s + 1);
+            asm volatile("s_waitcnt vmcnt(8)" ::: "memory");       // this step's eight landed
+            const u4_t *stage = mine + (s - s0 & 1) * 64 * 8;
+            u4_t xv[4], av[4];
 #pragma unroll
-                    for (int f = 0; f < RF; ++f)
-                        av[f][h] = load16<0>(ar, off, (j0 + 32 * f) * row_bytes);
-                }
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-#pragma unroll
-                    for (int f = 0; f < RF; ++f) acc[f] = mfma32<F16>(av[f][h], xv[h], acc[f]);
+            for (int h = 0; h < 4; ++h) {
+                xv[h] = fragment<false, 32>(stage, 0, h, lane);
+                av[h] = fragment<false, 32>(stage + 32 * 8, 0, h, lane);
             }
 #pragma unroll
-            for (int f = 0; f < RF; ++f) {
-                // lane (c, g): row c, ranks 8 q + 4 g .. + 3
+            for (int h = 0; h < 4; ++h) acc = mfma32<F16>(av[h], xv[h], acc);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // read, before it is filled
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();                                           // the sums go over the stages
+        float(*part)[32][33] = reinterpret_cast<float(*)[32][33]>(lds);
+        // lane (c, g): row c, ranks 8 q + 4 g .. + 3
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    part[wave][c][8 * (e >> 2) + 4 * g + (e & 3)] = acc[f][e];
-                __syncthreads();
-                const int row = threadIdx.x >> 4, j = threadIdx.x & 15;
+        for (int e = 0; e < 16; ++e) part[wave][c][8 * (e >> 2) + 4 * g + (e & 3)] = acc[e];
+        __syncthreads();
+        const int row = threadIdx.x >> 4;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int rank = j0 + 32 * f + j + 16 * h;
-                    float v = 0.0f;
+        for (int h = 0; h < 2; ++h) {
+            const int j = (threadIdx.x & 15) + 16 * h;
+            float v = 0.0f;
 #pragma unroll
-                    for (int w = 0; w < kShrinkWaves; ++w) v += part[w][row][j + 16 * h];
-                    if (row < rows && rank < p.r && adapter(p, t0 + row) == i) {
-                        v *= scale;
-                        uint16_t *to = p.terms + static_cast<int64_t>(t0 + row) * 2 * p.r + rank;
-                        const uint16_t hi = static_cast<uint16_t>(pack2<F16>(v, 0.0f));
-                        to[0] = hi;
-                        to[p.r] = static_cast<uint16_t>(pack2<F16>(v - unpack1<F16>(hi), 0.0f));
-                    }
-                }
-                __syncthreads();
+            for (int w = 0; w < kShrinkWaves; ++w) v += part[w][row][j];
+            if (row < rows && j0 + j < p.r && adapter(p, t0 + row) == i) {
+                v *= scale;
+                uint16_t *to = p.terms + static_cast<int64_t>(t0 + row) * 2 * p.r + j0 + j;
+                const uint16_t hi = static_cast<uint16_t>(pack2<F16>(v, 0.0f));
+                to[0] = hi;
+                to[p.r] = static_cast<uint16_t>(pack2<F16>(v - unpack1<F16>(hi), 0.0f));
             }
         }
+        __syncthreads();
     }
 }
 
@@ -253,10 +289,11 @@ template <bool F16>
 struct LoraFinish {
     const LoraParams &p;
 
-    // The adapters' part of a wave's results.  Rows with one adapter between them take
-    // its products straight into their sums; where a fragment's 32 rows have several,
-    // each adapter's product is made apart and kept by its own rows alone, so that what
-    // another request's adapter holds (NaN too) reaches nobody else.
+    // The adapters' part of a wave's results, 64 ranks at a time.  A fragment's 32 rows
+    // with one adapter between them take its product straight into their sums; where they
+    // have several, each adapter's product is made apart and kept by its own rows alone, so
+    // that what another request's adapter holds (NaN too) reaches nobody else.  All loads
+    // of a product are issued before its first MFMA (a load at a time took 80 us a tile).
     template <int FM, int FN>
     __device__ __forceinline__ void expand(const TileAt &t, f16_t (&acc)[FM][FN], int wm, int wn,
                                            int lane) const {
@@ -265,68 +302,71 @@ struct LoraFinish {
         int id[FM];
 #pragma unroll
         for (int i = 0; i < FM; ++i) id[i] = adapter(p, row0 + min(32 * i + c, rows - 1));
-        const int one = uniform(id[0]);
-        bool same = true;
-#pragma unroll
-        for (int i = 0; i < FM; ++i) same &= id[i] == one;
-        const int64_t r = p.r;
-        const int s_row = 4 * p.r, b_row = 2 * p.r, parts = (p.r + 15) / 16;
+        const int64_t r = p.r, n = t.n0 + wn;
+        const int s_row = 4 * p.r, b_row = 2 * p.r;
         const rsrc_t sr = uniform_buffer(reinterpret_cast<const char *>(p.terms + row0 * 2 * r),
                                          static_cast<int64_t>(rows) * s_row);
-        auto b_of = [&](int i) {
-            const int64_t n = t.n0 + wn;
-            return uniform_buffer(reinterpret_cast<const char *>(p.b + (i * int64_t{p.N} + n) * r),
-                                  n < p.N ? (p.N - n) * b_row : 0);
-        };
-        if (__builtin_amdgcn_ballot_w64(same) == ~uint64_t{0}) {
-            if (one < 0) return;
-            const rsrc_t br = b_of(one);
-#pragma unroll 1
-            for (int part = 0; part < parts; ++part) {
-                const int k = 16 * part + 8 * g;
-                u4_t bv[FN];
+        u4_t bv[4][FN];
+        for (int k0 = 0; k0 < p.r; k0 += 64) {
+            int held = -1;                        // whose columns bv holds
+            auto hold = [&](int a) GFR_INLINE {
+                if (a == held) return;
+                held = a;
+                const rsrc_t br = uniform_buffer(
+                    reinterpret_cast<const char *>(p.b + (a * int64_t{p.N} + n) * r),
+                    n < p.N ? (p.N - n) * b_row : 0);
 #pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    bv[j] = load16<0>(br, k < p.r ? (32 * j + c) * b_row + 2 * k : kPast, 0);
-#pragma unroll
-                for (int i = 0; i < FM; ++i) {
-                    const int off = k < p.r ? (32 * i + c) * s_row + 2 * k : kPast;
-                    const u4_t hi = load16<0>(sr, off, 0), lo = load16<0>(sr, off, b_row);
+                for (int q = 0; q < 4; ++q)
 #pragma unroll
                     for (int j = 0; j < FN; ++j) {
-                        acc[i][j] = mfma32<F16>(bv[j], hi, acc[i][j]);
-                        acc[i][j] = mfma32<F16>(bv[j], lo, acc[i][j]);
-                    }
-                }
-            }
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            uint64_t todo = __builtin_amdgcn_ballot_w64(id[i] >= 0 && 32 * i + c < rows);
-            while (todo) {
-                const int a = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(todo));
-                const bool mine = id[i] == a;
-                todo &= ~__builtin_amdgcn_ballot_w64(mine);
-                const rsrc_t br = b_of(a);
-                f16_t own[FN] = {};
-#pragma unroll 1
-                for (int part = 0; part < parts; ++part) {
-                    const int k = 16 * part + 8 * g;
-                    const int off = k < p.r ? (32 * i + c) * s_row + 2 * k : kPast;
-                    const u4_t hi = load16<0>(sr, off, 0), lo = load16<0>(sr, off, b_row);
-#pragma unroll
-                    for (int j = 0; j < FN; ++j) {
-                        const u4_t bv =
+                        const int k = k0 + 16 * q + 8 * g;
+                        bv[q][j] =
                             load16<0>(br, k < p.r ? (32 * j + c) * b_row + 2 * k : kPast, 0);
-                        own[j] = mfma32<F16>(bv, hi, own[j]);
-                        own[j] = mfma32<F16>(bv, lo, own[j]);
+                    }
+            };
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                uint64_t todo = __builtin_amdgcn_ballot_w64(id[i] >= 0);
+                if (todo == 0) continue;
+                u4_t sv[4][2];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int k = k0 + 16 * q + 8 * g;
+                    const int off = k < p.r ? (32 * i + c) * s_row + 2 * k : kPast;
+                    sv[q][0] = load16<0>(sr, off, 0);
+                    sv[q][1] = load16<0>(sr, off, b_row);
+                }
+                const int one = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(todo));
+                if (__builtin_amdgcn_ballot_w64(id[i] == one) == ~uint64_t{0}) {
+                    hold(one);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (k0 + 16 * q < p.r)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int j = 0; j < FN; ++j)
+                                    acc[i][j] = mfma32<F16>(bv[q][j], sv[q][h], acc[i][j]);
+                    continue;
+                }
+                while (todo) {
+                    const int a = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(todo));
+                    const bool mine = id[i] == a;
+                    todo &= ~__builtin_amdgcn_ballot_w64(mine);
+                    hold(a);
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) {
+                        f16_t own = {};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (k0 + 16 * q < p.r)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    own = mfma32<F16>(bv[q][j], sv[q][h], own);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) acc[i][j][e] += mine ? own[e] : 0.0f;
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[i][j][e] += mine ? own[j][e] : 0.0f;
             }
         }
     }
@@ -340,8 +380,22 @@ struct LoraFinish {
         // row's other lane for eight, and 16-bit results once more, for runs of 64 bytes.
         const int c = lane & 31, g = lane >> 5, es = p.out_f32 ? 4 : 2;
         const int bias_es = p.bias_f32 ? 4 : 2;
-        const rsrc_t bias = uniform_buffer(static_cast<const char *>(p.bias),
-                                           p.bias ? static_cast<int64_t>(p.N) * bias_es : 0);
+        const rsrc_t from_bias = uniform_buffer(static_cast<const char *>(p.bias),
+                                                p.bias ? static_cast<int64_t>(p.N) * bias_es : 0);
+        float bias[FN][2][8];
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int off = bias_es * (t.n0 + wn + 32 * j + 16 * q + 8 * g);
+                const u4_t b0 = load16<0>(from_bias, off, 0);
+                const u4_t b1 = load16<0>(from_bias, p.bias_f32 ? off : kPast, 16);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    bias[j][q][e] = p.bias_f32
+                                        ? __uint_as_float(e < 4 ? b0[e & 3] : b1[e & 3])
+                                        : unpack1<F16>(b0[e >> 1] >> (16 * (e & 1)));
+            }
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             const int64_t row = t.m0 + wm + 32 * i;
@@ -375,17 +429,8 @@ struct LoraFinish {
                         y[e] = __uint_as_float(w[0]);
                         y[4 + e] = __uint_as_float(w[1]);
                     }
-                    if (p.bias_f32) {
-                        const f4_t b0 = __builtin_bit_cast(f4_t, load16<0>(bias, 4 * n, 0));
-                        const f4_t b1 = __builtin_bit_cast(f4_t, load16<0>(bias, 4 * n, 16));
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) y[e] += b0[e], y[4 + e] += b1[e];
-                    } else if (p.bias) {
-                        const u4_t b = load16<0>(bias, 2 * n, 0);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            y[e] += unpack1<F16>(b[e >> 1] >> (16 * (e & 1)));
-                    }
+                    for (int e = 0; e < 8; ++e) y[e] += bias[j][q][e];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         y[e] += unpack1<F16>(res[j][q][e >> 1] >> (16 * (e & 1)));
@@ -451,8 +496,6 @@ hipError_t launch_rows(const LoraParams &p, hipStream_t stream) {
     LinearParams d{};
     d.x = p.x;
     d.w = p.w;
-    d.bias = p.bias;
-    d.bias_f32 = p.bias_f32;
     d.out = p.dense;
     d.out_f32 = 1;
     d.f16 = p.f16;
@@ -463,35 +506,28 @@ hipError_t launch_rows(const LoraParams &p, hipStream_t stream) {
     d.K = p.K;
     d.kernel = p.choice.kernel;
     d.split = p.choice.split;
-    d.partial = p.partial;
+    d.partial = p.dense;
+    d.keep_partial = 1;
     if (e = launch_linear(d, stream); e != hipSuccess) return e;
-    // about 2048 blocks, of one row or more
+    // a row a block, up to about 16384 blocks
     const int columns = (p.N + 255) / 256;
-    int64_t rows = (static_cast<int64_t>(p.M) * columns + 2047) / 2048;
+    int64_t rows = (static_cast<int64_t>(p.M) * columns + 16383) / 16384;
     if (const int64_t least = (p.M + 65534) / 65535; rows < least) rows = least;
     const dim3 grid(columns, static_cast<uint32_t>((p.M + rows - 1) / rows));
-    if (p.r % 8 == 0)
-        hipLaunchKernelGGL((expand_rows_kernel<F16, true>), grid, dim3(256), 0, stream, p,
-                           static_cast<int>(rows));
-    else
-        hipLaunchKernelGGL((expand_rows_kernel<F16, false>), grid, dim3(256), 0, stream, p,
-                           static_cast<int>(rows));
-    return hipGetLastError();
-}
-
-template <bool F16, int RF>
-hipError_t launch_shrink_tiles(const LoraParams &p, hipStream_t stream) {
-    hipLaunchKernelGGL((shrink_tile_kernel<F16, RF>), dim3((p.M + 31) / 32),
-                       dim3(kShrinkWaves * 64), 0, stream, p);
+    const auto kernel = p.r % 8 == 0   ? &expand_rows_kernel<F16, 8>
+                        : p.r % 4 == 0 ? &expand_rows_kernel<F16, 4>
+                                       : &expand_rows_kernel<F16, 1>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, p, static_cast<int>(rows));
     return hipGetLastError();
 }
 
 template <bool F16>
 hipError_t launch_tiles(const LoraParams &p, hipStream_t stream) {
-    const hipError_t e = p.r <= 32   ? launch_shrink_tiles<F16, 1>(p, stream)
-                         : p.r <= 64 ? launch_shrink_tiles<F16, 2>(p, stream)
-                                     : launch_shrink_tiles<F16, 4>(p, stream);
-    if (e != hipSuccess) return e;
+    constexpr auto shrink = &shrink_tile_kernel<F16>;
+    if (const hipError_t e = allow_lds<shrink>(kShrinkLds); e != hipSuccess) return e;
+    hipLaunchKernelGGL(shrink, dim3((p.M + 31) / 32, (p.r + 31) / 32), dim3(kShrinkWaves * 64),
+                       kShrinkLds, stream, p);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     constexpr int lds = 2 * kStage * 16;
     constexpr auto kernel = &lora_tile_kernel<F16>;
     if (const hipError_t a = allow_lds<kernel>(lds); a != hipSuccess) return a;
@@ -513,10 +549,8 @@ LoraLayout lora_layout(int64_t M, int64_t N, int64_t K, int64_t r) {
     }
     l.choice = linear_choice(M, N, K, GFR_ACT_NONE);
     l.dense = up(sizeof(float) * M * r);
-    l.partial = l.dense + up(sizeof(float) * M * N);
-    l.total = l.partial;
-    if (l.choice.split > 1)
-        l.total += up(sizeof(float) * l.choice.split * M * ((N + 7) / 8 * 8));
+    l.total = l.dense + up(sizeof(float) * l.choice.split * M *
+                           (l.choice.split > 1 ? (N + 7) / 8 * 8 : N));
     return l;
 }
 

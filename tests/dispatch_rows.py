@@ -1,0 +1,21 @@
+"""Which kernels a size of the products chosen by the row takes: the library's own
+host-side choice (csrc/gfr_layer.h: lora_layout), called by its C++ symbol."""
+import ctypes
+
+import mxfp8_grouped_gemm_group_amd as gfr
+
+
+class _Choice(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int32), ("split", ctypes.c_int32)]
+
+
+class _Lora(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in ("dense", "total")] + [
+        ("tiles", ctypes.c_int32), ("choice", _Choice)]
+
+
+def lora(M, N, K, r):
+    """Whether lora_linear takes whole tiles."""
+    f = gfr.load_library()._ZN3gfr11lora_layoutEllll
+    f.restype, f.argtypes = _Lora, [ctypes.c_int64] * 4
+    return bool(f(M, N, K, r).tiles)

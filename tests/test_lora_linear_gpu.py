@@ -291,3 +291,108 @@ def test_two_calls_at_once_on_two_streams():
     torch.cuda.synchronize()
     for y, z in zip(out, want):
         same(y, z)
+
+
+# ---- whole tiles, which expand in their epilogue: 128 of them or more -----------------
+
+
+TILED = dict(M=4300, N=2056, K=72)
+
+
+def test_tiles_are_taken():
+    from tests import dispatch_rows
+    assert dispatch_rows.lora(4300, 2056, 72, 16) and dispatch_rows.lora(4300, 2056, 72, 200)
+    for M, N, K, r in [(4300, 2056, 71, 16), (4300, 2055, 72, 16), (4300, 2056, 72, 12),
+                       (256, 2056, 72, 16)]:
+        assert not dispatch_rows.lora(M, N, K, r)
+
+
+@pytest.mark.parametrize("mix", ["one", "none", "runs", "gaps", "random"])
+@pytest.mark.parametrize("dtype, r", [(BF, 16), (HF, 40)])
+def test_tiles_mixes(mix, dtype, r):
+    check(**TILED, L=9, r=r, dtype=dtype, mix=mix, bias=F32)
+    check(**TILED, L=40, r=r, dtype=dtype, mix=mix, out_dtype=None, residual=True, scaling=False)
+    check(**TILED, L=9, r=r, dtype=dtype, mix=mix, out_dtype=None, residual=True, bias=dtype)
+
+
+@pytest.mark.parametrize("r", [8, 24, 64, 72, 128, 200, 256])
+def test_tiles_ranks(r):
+    check(**TILED, L=3, r=r, mix="runs")
+
+
+@pytest.mark.parametrize("M, N, K", [(4097, 2048, 8), (3900, 2312, 136), (4200, 1800, 520),
+                                     (32800, 264, 64), (100, 32776, 64), (4290, 2056, 264)])
+def test_tiles_shapes(M, N, K):
+    # a last tile of 1, 32, 64, 100 (one), 104 and 192 rows or so; few and many columns
+    check(M, N, K, 5, 16, mix="runs", bias=BF, residual=True, out_dtype=None)
+
+
+def test_tiles_inner_row_keeps_its_bits():
+    a = integers(**TILED, L=3, r=16, dtype=BF, mix="runs")
+    a["a"] = a["a"] * 64
+    a["scaling"][:] = 1
+    same(call(a, out_dtype=F32), definition(a))
+
+
+@pytest.mark.parametrize("mix", ["runs", "random"])
+def test_tiles_nan_stays_with_its_adapter_and_row(mix):
+    L = 4
+    a = integers(**TILED, L=L, r=16, dtype=BF, mix=mix)
+    a["ids"][:4] = torch.tensor([0, 1, 2, 3], dtype=torch.int32)
+    clean = definition(a)
+    for t, i in (("a", 1), ("b", 2)):
+        for bad in (NAN, float("inf")):
+            b = {**a, t: a[t].clone()}
+            b[t][i] = bad
+            y = call(b, out_dtype=F32).cpu()
+            rest = a["ids"] != i
+            same(y[rest], clean[rest], f"{t} {i} {bad}")
+            if bad != bad:
+                assert y[~rest].isnan().all()
+    b = {**a, "x": a["x"].clone()}
+    b["x"][2] = NAN
+    y = call(b, out_dtype=F32).cpu()
+    rest = torch.arange(TILED["M"]) != 2
+    same(y[rest], clean[rest], "row")
+    assert y[2].isnan().all()
+
+
+def test_tiles_in_place_flags_and_nothing_outside_out():
+    M, N, K = TILED.values()
+    a = integers(**TILED, L=4, r=16, dtype=BF, residual=True, mix="random")
+    a["ids"][1], a["ids"][M - 1] = 4, -2
+    want = definition({**a, "ids": torch.where((a["ids"] < 4) & (a["ids"] >= 0), a["ids"], -1)})
+    buf = torch.full((M * N + 128,), 7.0, dtype=BF, device=DEV)
+    out = buf[64:64 + M * N].view(M, N)
+    out.copy_(a["residual"])
+    need = gfr.lora_linear_workspace_size(M, N, K, 16)
+    ws = torch.full((need + 512,), 255, dtype=torch.uint8, device=DEV)       # NaN terms
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    assert call(a, residual=out, out=out, workspace=ws[:need], status=status) is out
+    same(out, want)
+    assert (buf[:64] == 7).all() and (buf[64 + M * N:] == 7).all() and (ws[need:] == 255).all()
+    assert status.item() == gfr.DEV_BAD_ADAPTER
+
+
+def test_tiles_same_bits_twice_and_under_graph():
+    a = integers(**TILED, L=5, r=16, dtype=BF, mix="runs", bias=BF)
+    d = {k: v.to(DEV) for k, v in a.items() if v is not None}
+    run = lambda: gfr.lora_linear(d["x"], d["w"], d["a"], d["b"], d["ids"], scaling=d["scaling"],
+                                  bias=d["bias"], out_dtype=F32)
+    assert torch.equal(run(), run())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = run()
+    torch.cuda.synchronize()
+    for i in range(3):
+        a["ids"] = ids_of(TILED["M"], 5, ["random", "one", "runs"][i], i)
+        d["ids"].copy_(a["ids"])
+        graph.replay()
+        same(y, definition(a), str(i))
+        torch.randn(256, 256, device=DEV).relu_()
