@@ -93,6 +93,16 @@ struct Direct {
     }
 };
 
+// The kernel's first argument, read where this is called: kept over the run of tiles its
+// many words took the scalar registers that the run's loops need.
+template <class Params>
+__device__ __forceinline__ Params fresh() {
+    typedef const __attribute__((address_space(4))) Params *at_t;
+    at_t at = (at_t)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(at));
+    return *(const Params *)at;
+}
+
 // n / d for 0 <= n < 2^31 by d's reciprocal in FP32 (which is off by less than one for
 // quotients below 2^22, and corrected here).
 struct Divisor {
@@ -249,6 +259,13 @@ __device__ __forceinline__ void run_tiles(u4_t *lds, const Tiles &tiles, const F
             run_part(Int<3>{}, Int<kGets>{}, Int<2>{}, now ^ 1, Int<kSecond>{}, Int<kLoads>{}, now);
             now ^= 1;
         }
+        // (two k-major operands: what finish needs registers for is not taken from the
+        // loop's sums, of which one went to memory and back every step)
+        if (!BLINE && FM * FN == 16)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) asm volatile("" : "+a"(acc[i][j]));
         stores = finish.template tile<FM, FN>(t, acc, wm, wn, line);
     };
     for (; id < end; id += stride) {

@@ -254,12 +254,11 @@ __global__ __launch_bounds__(kShrinkWaves * 64, 2) void shrink_tile_kernel(LoraP
 
 // The dense product's tiles: bands of eight by all columns, an eighth of them per XCD.
 struct LoraTiles {
-    const LoraParams &p;
     int tiles_m, tiles_n, begin, end, stride;
     Divisor by_band;
 
-    __device__ __forceinline__ explicit LoraTiles(const LoraParams &p_)
-        : p(p_), tiles_m((p.M + kTile - 1) / kTile), tiles_n((p.N + kTile - 1) / kTile),
+    __device__ __forceinline__ explicit LoraTiles(const LoraParams &p)
+        : tiles_m((p.M + kTile - 1) / kTile), tiles_n((p.N + kTile - 1) / kTile),
           by_band(8 * tiles_n) {
         const int total = tiles_m * tiles_n, per = (total + 7) / 8, xcd = blockIdx.x & 7;
         stride = gridDim.x >> 3;
@@ -269,6 +268,7 @@ struct LoraTiles {
     __device__ __forceinline__ TileAt at(int id) const {
         const int band = by_band.of(id), in_band = id - band * 8 * tiles_n;
         const int depth = min(8, tiles_m - band * 8), column = Divisor(depth).of(in_band);
+        const LoraParams p = fresh<LoraParams>();
         TileAt t;
         t.e = 0;
         t.n0 = uniform(column * kTile);
@@ -279,6 +279,7 @@ struct LoraTiles {
     }
     template <class A, class B>
     __device__ __forceinline__ void loads(const TileAt &t, A &da, B &db) const {
+        const LoraParams p = fresh<LoraParams>();
         const int64_t k = p.K;
         da.tile(p.x + t.m0 * k, 2 * t.rows * k, p.K, t.rows);
         db.tile(p.w + t.n0 * k, 2 * min(kTile, p.N - t.n0) * k, p.K, 0);
@@ -287,84 +288,95 @@ struct LoraTiles {
 
 template <bool F16>
 struct LoraFinish {
-    const LoraParams &p;
-
-    // The adapters' part of a wave's results, 64 ranks at a time.  A fragment's 32 rows
-    // with one adapter between them take its product straight into their sums; where they
-    // have several, each adapter's product is made apart and kept by its own rows alone, so
-    // that what another request's adapter holds (NaN too) reaches nobody else.  All loads
-    // of a product are issued before its first MFMA (a load at a time took 80 us a tile).
+    // The adapters' part of a wave's results, 64 ranks at a time.  Rows with one adapter
+    // between them take its product straight into their sums; where they have several,
+    // each fragment's product with each of its adapters is made apart and kept by that
+    // adapter's rows alone, so that what another request's adapter holds (NaN too) reaches
+    // nobody else.  All loads of a product are issued before its first MFMA (a load at a
+    // time took 80 us a tile).
     template <int FM, int FN>
-    __device__ __forceinline__ void expand(const TileAt &t, f16_t (&acc)[FM][FN], int wm, int wn,
-                                           int lane) const {
+    __device__ __forceinline__ void expand(const LoraParams &p, const TileAt &t,
+                                           f16_t (&acc)[FM][FN], int wm, int wn, int lane) const {
         const int c = lane & 31, g = lane >> 5, row0 = t.m0 + wm, rows = t.rows - wm;
         if (rows <= 0) return;
         int id[FM];
 #pragma unroll
         for (int i = 0; i < FM; ++i) id[i] = adapter(p, row0 + min(32 * i + c, rows - 1));
+        const int one = uniform(id[0]);
+        bool same = true;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) same &= id[i] == one;
+        const bool all = __builtin_amdgcn_ballot_w64(same) == ~uint64_t{0};
+        if (all && one < 0) return;
         const int64_t r = p.r, n = t.n0 + wn;
         const int s_row = 4 * p.r, b_row = 2 * p.r;
         const rsrc_t sr = uniform_buffer(reinterpret_cast<const char *>(p.terms + row0 * 2 * r),
                                          static_cast<int64_t>(rows) * s_row);
-        u4_t bv[4][FN];
-        for (int k0 = 0; k0 < p.r; k0 += 64) {
-            int held = -1;                        // whose columns bv holds
-            auto hold = [&](int a) GFR_INLINE {
-                if (a == held) return;
-                held = a;
-                const rsrc_t br = uniform_buffer(
-                    reinterpret_cast<const char *>(p.b + (a * int64_t{p.N} + n) * r),
-                    n < p.N ? (p.N - n) * b_row : 0);
+        u4_t bv[4][FN], sv[4][2];
+        auto columns = [&](int a, int k0) GFR_INLINE {
+            const rsrc_t br = uniform_buffer(
+                reinterpret_cast<const char *>(p.b + (a * int64_t{p.N} + n) * r),
+                n < p.N ? (p.N - n) * b_row : 0);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int j = 0; j < FN; ++j) {
-                        const int k = k0 + 16 * q + 8 * g;
-                        bv[q][j] =
-                            load16<0>(br, k < p.r ? (32 * j + c) * b_row + 2 * k : kPast, 0);
-                    }
-            };
-#pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                uint64_t todo = __builtin_amdgcn_ballot_w64(id[i] >= 0);
-                if (todo == 0) continue;
-                u4_t sv[4][2];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int j = 0; j < FN; ++j) {
                     const int k = k0 + 16 * q + 8 * g;
-                    const int off = k < p.r ? (32 * i + c) * s_row + 2 * k : kPast;
-                    sv[q][0] = load16<0>(sr, off, 0);
-                    sv[q][1] = load16<0>(sr, off, b_row);
+                    bv[q][j] = load16<0>(br, k < p.r ? (32 * j + c) * b_row + 2 * k : kPast, 0);
                 }
-                const int one = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(todo));
-                if (__builtin_amdgcn_ballot_w64(id[i] == one) == ~uint64_t{0}) {
-                    hold(one);
+        };
+        auto inner = [&](int i, int k0) GFR_INLINE {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int k = k0 + 16 * q + 8 * g;
+                const int off = k < p.r ? (32 * i + c) * s_row + 2 * k : kPast;
+                sv[q][0] = load16<0>(sr, off, 0);
+                sv[q][1] = load16<0>(sr, off, b_row);
+            }
+        };
+        if (all) {
+#pragma unroll 1
+            for (int k0 = 0; k0 < p.r; k0 += 64) {
+                const int parts = (p.r - k0 + 15) / 16;
+                columns(one, k0);
+#pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    inner(i, k0);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        if (k0 + 16 * q < p.r)
+                        if (q < parts)
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
 #pragma unroll
                                 for (int j = 0; j < FN; ++j)
                                     acc[i][j] = mfma32<F16>(bv[q][j], sv[q][h], acc[i][j]);
-                    continue;
                 }
-                while (todo) {
-                    const int a = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(todo));
-                    const bool mine = id[i] == a;
-                    todo &= ~__builtin_amdgcn_ballot_w64(mine);
-                    hold(a);
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            uint64_t todo = __builtin_amdgcn_ballot_w64(id[i] >= 0);
+#pragma unroll 1
+            while (todo) {
+                const int a = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(todo));
+                const bool mine = id[i] == a;
+                todo &= ~__builtin_amdgcn_ballot_w64(mine);
+#pragma unroll 1
+                for (int k0 = 0; k0 < p.r; k0 += 64) {
+                    inner(i, k0);
+                    columns(a, k0);
 #pragma unroll
                     for (int j = 0; j < FN; ++j) {
                         f16_t own = {};
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            if (k0 + 16 * q < p.r)
 #pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    own = mfma32<F16>(bv[q][j], sv[q][h], own);
+                            for (int h = 0; h < 2; ++h)
+                                own = mfma32<F16>(bv[q][j], sv[q][h], own);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) acc[i][j][e] += mine ? own[e] : 0.0f;
+                        __builtin_amdgcn_sched_barrier(0);
                     }
                 }
             }
@@ -374,7 +386,8 @@ struct LoraFinish {
     template <int FM, int FN>
     __device__ __forceinline__ int tile(const TileAt &t, f16_t (&acc)[FM][FN], int wm, int wn,
                                         int lane) const {
-        expand(t, acc, wm, wn, lane);
+        const LoraParams p = fresh<LoraParams>();
+        expand(p, t, acc, wm, wn, lane);
         __builtin_amdgcn_sched_barrier(0);
         // A lane has four columns of row lane % 32 at a time; it trades halves with its
         // row's other lane for eight, and 16-bit results once more, for runs of 64 bytes.
@@ -469,7 +482,7 @@ template <bool F16>
 __global__ __launch_bounds__(kWaves * 64, 1) void lora_tile_kernel(LoraParams p) {
     extern __shared__ u4_t lds[];     // [2][x's 256 rows, w's][8]
     const LoraTiles tiles(p);
-    const LoraFinish<F16> finish{p};
+    const LoraFinish<F16> finish{};
     run_tiles<F16, false, false>(lds, tiles, finish, p.K, p.K);
 }
 
