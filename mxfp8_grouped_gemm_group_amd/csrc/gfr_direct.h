@@ -123,8 +123,14 @@ constexpr int kStage = 2 * kTile * 8;       // pieces: an operand's 256 lines, t
 
 // A tile: `rows` rows from m0 on, columns from n0 on, of the group e's product; steps of
 // the summed index.
+//
+// Tiles of a kernel with kExtra begin with `extra` steps whose products only some of the
+// 32-row fragments take: byte i of `masks` says which ones take the i-th run of
+// `extra_run` steps.
 struct TileAt {
     int e, m0, n0, rows, steps;
+    int extra, extra_run;
+    uint64_t masks;
 };
 
 // 256 x 256 tiles of four waves, one block to a CU, which goes through its tiles'
@@ -143,8 +149,9 @@ struct TileAt {
 // loads take 16 clocks each, 64 a step.)  A tile of fewer rows takes less
 // time: up to 128 of them split their columns over the waves, up to 192 go as 256.
 //
-// Tiles: at(id), the tile; loads(t, da, db), its operands (t null: none); ids begin,
-// begin + stride, ... below end.  Finish: tile<FM, FN>(t, acc, wm, wn, lane) takes a
+// Tiles: at(id), the tile, for ids begin, begin + stride, ... below end; next(cursor, da,
+// db, wave, lane), the operands of the next run of steps and their number, 0 behind the
+// last tile.  Finish: tile<FM, FN>(t, acc, wm, wn, lane) takes a
 // wave's results (32 FM x 32 FN of them from wm, wn on) and returns how many stores it
 // has issued at least; clear(t) a tile without a sum.
 template <bool F16, bool ALINE, bool BLINE, class Tiles, class Finish>
@@ -159,24 +166,18 @@ __device__ __forceinline__ void run_tiles(u4_t *lds, const Tiles &tiles, const F
     const int stride = tiles.stride, end = uniform(tiles.end);
     int id = uniform(tiles.begin);
     if (id >= end) return;
-    int load_id = uniform(id - stride), load_step = 0, load_steps = 0;
+    int load_step = 0, load_steps = 0;
+    typename Tiles::Cursor cursor(id - stride);
     auto next_loads = [&]() GFR_INLINE {
         load_step = uniform(load_step + 1);
         if (load_step < uniform(load_steps)) return;
         load_step = 0;
-        load_steps = 0x7fffffff;             // no tile left: zeros
-        TileAt t;
-        do {
-            load_id = uniform(load_id + stride);
-            if (load_id >= end) {
-                da.tile(nullptr, 0, 0, 0);
-                db.tile(nullptr, 0, 0, 0);
-                return;
-            }
-            t = tiles.at(load_id);
-        } while (t.steps == 0);
-        load_steps = t.steps;
-        tiles.loads(t, da, db);
+        load_steps = tiles.next(cursor, da, db, wave, lane);
+        if (load_steps == 0) {
+            load_steps = 0x7fffffff;             // no tile left: zeros
+            da.tile(nullptr, 0, 0, 0);
+            db.tile(nullptr, 0, 0, 0);
+        }
     };
     const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) void *)lds));
@@ -220,8 +221,8 @@ __device__ __forceinline__ void run_tiles(u4_t *lds, const Tiles &tiles, const F
         f16_t acc[FM][FN] = {};
         // A part: its MFMAs, and between them `gets` fragments from part `first` on
         // of a stage, and loads [from, to).
-        auto run_part = [&](auto part, auto gets, auto first, int stage, auto from, auto to,
-                            int into) GFR_INLINE {
+        auto run_part = [&](auto masked, int mask, auto part, auto gets, auto first, int stage,
+                            auto from, auto to, int into) GFR_INLINE {
             constexpr int kG = (gets + kMfmas - 1) / kMfmas;
             constexpr int kL = (to - from + kMfmas - 1) / kMfmas;
 #pragma unroll
@@ -233,8 +234,9 @@ __device__ __forceinline__ void run_tiles(u4_t *lds, const Tiles &tiles, const F
 #pragma unroll
                 for (int h = 0; h < kL; ++h)
                     if (const int i = from + m * kL + h; i < to) load(i, into);
-                acc[m / FN][m % FN] = mfma32<F16>(b[part][m % FN], a[part][m / FN],
-                                                  acc[m / FN][m % FN]);
+                if (!masked || (mask >> m / FN & 1))
+                    acc[m / FN][m % FN] = mfma32<F16>(b[part][m % FN], a[part][m / FN],
+                                                      acc[m / FN][m % FN]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
@@ -242,23 +244,33 @@ __device__ __forceinline__ void run_tiles(u4_t *lds, const Tiles &tiles, const F
         for (int i = 0; i < 3 * kGets; ++i) get(i / kGets, now, i % kGets);
         constexpr int kFirst = (kLoads + 2) / 3, kSecond = kFirst + (kLoads - kFirst + 1) / 2;
         static_assert(kFirst <= kB, "part 1 begins the same number of loads in every tile");
-        for (int step = 0; step < t.steps; ++step) {
-            run_part(Int<0>{}, Int<kGets>{}, Int<3>{}, now, Int<0>{}, Int<0>{}, 0);
+        auto run_step = [&](auto masked, int mask) GFR_INLINE {
+            run_part(masked, mask, Int<0>{}, Int<kGets>{}, Int<3>{}, now, Int<0>{}, Int<0>{}, 0);
             lds_wait();
             next_loads();
             da.at(load_step);
             db.at(load_step);
-            run_part(Int<1>{}, Int<0>{}, Int<0>{}, 0, Int<0>{}, Int<kFirst>{}, now);
+            run_part(masked, mask, Int<1>{}, Int<0>{}, Int<0>{}, 0, Int<0>{}, Int<kFirst>{}, now);
             // (the last tile's results may still be on their way)
             if (stores < 16) direct_wait<kFirst>();
             else if (stores < 32) direct_wait<kFirst + 16>();
             else direct_wait<kFirst + 32>();
             stores = 0;
-            run_part(Int<2>{}, Int<2 * kGets>{}, Int<0>{}, now ^ 1, Int<kFirst>{}, Int<kSecond>{},
-                     now);
-            run_part(Int<3>{}, Int<kGets>{}, Int<2>{}, now ^ 1, Int<kSecond>{}, Int<kLoads>{}, now);
+            run_part(masked, mask, Int<2>{}, Int<2 * kGets>{}, Int<0>{}, now ^ 1, Int<kFirst>{},
+                     Int<kSecond>{}, now);
+            run_part(masked, mask, Int<3>{}, Int<kGets>{}, Int<2>{}, now ^ 1, Int<kSecond>{},
+                     Int<kLoads>{}, now);
             now ^= 1;
+        };
+        int step = 0;
+        if (Tiles::kExtra) {
+            uint64_t masks = t.masks;
+            for (int run = 0; step < t.extra; ++step) {
+                run_step(Int<1>{}, static_cast<int>(masks & 0xff) >> (wm / 32));
+                if (++run == t.extra_run) run = 0, masks >>= 8;
+            }
         }
+        for (; step < t.steps; ++step) run_step(Int<0>{}, 0);
         // (two k-major operands: what finish needs registers for is not taken from the
         // loop's sums, of which one went to memory and back every step)
         if (!BLINE && FM * FN == 16)

@@ -498,8 +498,19 @@ struct GroupedTiles {
         t.n0 = uniform(t.n0);
         return t;
     }
+    static constexpr bool kExtra = false;
+    struct Cursor {
+        int id;
+        __device__ __forceinline__ explicit Cursor(int first) : id(first) {}
+    };
     template <class A, class B>
-    __device__ __forceinline__ void loads(const TileAt &t, A &da, B &db) const {
+    __device__ __forceinline__ int next(Cursor &c, A &da, B &db, int wave, int lane) const {
+        TileAt t;
+        do {
+            c.id = uniform(c.id + stride);
+            if (c.id >= uniform(end)) return 0;
+            t = at(c.id);
+        } while (t.steps == 0);
         const int64_t k = p.K, n = p.N;
         if (WGRAD) {
             const int first = uniform(s.start[t.e]), count = uniform(s.start[t.e + 1]) - first;
@@ -511,6 +522,7 @@ struct GroupedTiles {
             if (WLINE) db.tile(w + t.n0, 2 * (k * n - t.n0), p.K, 0);
             else db.tile(w + t.n0 * k, 2 * min(kTile, p.N - t.n0) * k, p.K, 0);
         }
+        return t.steps;
     }
 };
 

@@ -122,8 +122,9 @@ struct LoraParams {
     void *out;                 // [M, N]
     int32_t *status;           // may be null
     float *inner;              // workspace, few rows: [M][r], scaled
-    float *dense;              // workspace, few rows: [M][N], or the K splits' sums
+    float *dense;              // workspace: [M][N]; few rows: or the K splits' sums
     uint16_t *terms;           // workspace, many rows: [M][2][r], scaled
+    int32_t *codes;            // workspace, many rows: [M / 32], the adapter of 32 rows
     LinearChoice choice;
     int32_t tiles;             // many rows
     int32_t bias_f32, out_f32, f16;
@@ -132,7 +133,7 @@ struct LoraParams {
 
 // Workspace layout of lora_linear (256-byte aligned regions; inner or terms at 0).
 struct LoraLayout {
-    size_t dense, total;
+    size_t codes, dense, total;
     int32_t tiles;             // many rows: dense tiles that expand in their epilogue
     LinearChoice choice;       // few rows: of the dense product
 };

@@ -432,6 +432,7 @@ int gfr_lora_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *
     p.status = opts->status_dev;
     p.inner = reinterpret_cast<float *>(ws);
     p.terms = reinterpret_cast<uint16_t *>(ws);
+    p.codes = reinterpret_cast<int32_t *>(ws + l.codes);
     p.tiles = l.tiles;
     p.dense = reinterpret_cast<float *>(ws + l.dense);
     p.choice = l.choice;

@@ -6,8 +6,10 @@
 //   expand   + inner[t] B[i]^T + residual[t], rounded once
 //
 // Few rows: shrink, the dense product into FP32 (gfr_linear's kernels), expand.  Many:
-// shrink on the matrix cores, and the expansion in the dense tiles' epilogue, where a
-// wave's results are still in registers.
+// shrink on the matrix cores; the dense tiles, of which 32 rows with one adapter between
+// them take its expansion as a few steps more of their sum; and for the 32 rows that have
+// several, whose sums were kept in FP32, a launch that adds each row its own, so that what
+// another request's adapter holds (NaN too) reaches nobody else.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -166,6 +168,8 @@ __global__ __launch_bounds__(256) void expand_rows_kernel(LoraParams p, int rows
 // whole lines (fragments loaded from memory took 32 half lines a load: 4096 rows of 4096
 // by rank 64 51 us).  inner is kept as two 16-bit terms, the value and what its
 // rounding left over: 16 bits of mantissa or more, for the matrix cores.
+// codes[row / 32]: the adapter of 32 rows, -1 for none, kSeveral.
+constexpr int kSeveral = -2;
 constexpr int kShrinkWaves = 8;
 constexpr int kShrinkLds = kShrinkWaves * 2 * 64 * 8 * 16;
 template <bool F16>
@@ -192,6 +196,11 @@ __global__ __launch_bounds__(kShrinkWaves * 64, 2) void shrink_tile_kernel(LoraP
     u4_t *const mine = lds + wave * 2 * 64 * 8;
     const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) void *)lds)) + wave * 2 * 64 * 128;
+    const int first_id = uniform(id);
+    if (blockIdx.y == 0 && wave == 0) {
+        const bool same = __builtin_amdgcn_ballot_w64(c < rows && id != first_id) == 0;
+        if (lane == 0) p.codes[blockIdx.x] = same ? id : kSeveral;
+    }
     uint64_t todo = __builtin_amdgcn_ballot_w64(id >= 0);
     while (todo) {
         const int i = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
@@ -252,20 +261,24 @@ __global__ __launch_bounds__(kShrinkWaves * 64, 2) void shrink_tile_kernel(LoraP
     }
 }
 
-// The dense product's tiles: bands of eight by all columns, an eighth of them per XCD.
+// The dense product's tiles: bands of eight by all columns, an eighth of them per XCD.  A
+// tile begins with the expansions of its fragments' adapters, each a sum over the ranks of
+// the value's first term, then of its second.
 struct LoraTiles {
-    int tiles_m, tiles_n, begin, end, stride;
+    static constexpr bool kExtra = true;
+    int tiles_m, tiles_n, begin, end, stride, rank_steps;
     Divisor by_band;
 
     __device__ __forceinline__ explicit LoraTiles(const LoraParams &p)
         : tiles_m((p.M + kTile - 1) / kTile), tiles_n((p.N + kTile - 1) / kTile),
-          by_band(8 * tiles_n) {
+          rank_steps((p.r + 63) / 64), by_band(8 * tiles_n) {
         const int total = tiles_m * tiles_n, per = (total + 7) / 8, xcd = blockIdx.x & 7;
         stride = gridDim.x >> 3;
         begin = xcd * per + (blockIdx.x >> 3);
         end = min(total, (xcd + 1) * per);
     }
     __device__ __forceinline__ TileAt at(int id) const {
+        const int lane = threadIdx.x & 63;
         const int band = by_band.of(id), in_band = id - band * 8 * tiles_n;
         const int depth = min(8, tiles_m - band * 8), column = Divisor(depth).of(in_band);
         const LoraParams p = fresh<LoraParams>();
@@ -274,165 +287,131 @@ struct LoraTiles {
         t.n0 = uniform(column * kTile);
         t.m0 = uniform((band * 8 + in_band - column * depth) * kTile);
         t.rows = uniform(min(kTile, p.M - t.m0));
-        t.steps = (p.K + 63) / 64;
+        const int fragments = (t.rows + 31) / 32;
+        const int code = p.codes[t.m0 / 32 + min(lane, fragments - 1)];
+        uint64_t todo = __builtin_amdgcn_ballot_w64((lane < fragments) & (code >= 0));
+        t.extra = 0;
+        t.extra_run = 2 * rank_steps;
+        t.masks = 0;
+        while (todo) {
+            const int a = __builtin_amdgcn_readlane(code, __builtin_ctzll(todo));
+            const uint64_t mine = todo & __builtin_amdgcn_ballot_w64(code == a);
+            todo &= ~mine;
+            t.masks |= mine << (8 * (t.extra / t.extra_run));
+            t.extra += t.extra_run;
+        }
+        t.extra = uniform(t.extra);
+        t.steps = t.extra + (p.K + 63) / 64;
         return t;
     }
+    // The loads' tile, and in it which of an adapter's terms come next (masks: the
+    // adapters left).
+    struct Cursor {
+        int id, term;
+        TileAt t;
+        __device__ __forceinline__ explicit Cursor(int first) : id(first), term(-1) {}
+    };
     template <class A, class B>
-    __device__ __forceinline__ void loads(const TileAt &t, A &da, B &db) const {
+    __device__ __forceinline__ int next(Cursor &c, A &da, B &db, int wave, int lane) const {
         const LoraParams p = fresh<LoraParams>();
+        if (c.term < 0) {                       // a new tile
+            c.id = uniform(c.id + stride);
+            if (c.id >= uniform(end)) return 0;
+            c.t = at(c.id);
+            c.term = 0;
+        }
+        const int64_t columns = min(kTile, p.N - c.t.n0);
+        if (c.t.masks != 0) {
+            const int64_t r = p.r;
+            const int a = uniform(p.codes[c.t.m0 / 32 + __builtin_ctzll(c.t.masks & 0xff)]);
+            da.init(2 * r, wave, lane);
+            db.init(r, wave, lane);
+            // (the second term's rows end with the buffer; the first's, a term ahead)
+            da.tile(p.terms + c.t.m0 * 2 * r + c.term * r, 2 * (c.t.rows * 2 - c.term) * r, p.r,
+                    c.t.rows);
+            db.tile(p.b + (a * int64_t{p.N} + c.t.n0) * r, 2 * columns * r, p.r, 0);
+            if (++c.term == 2) c.term = 0, c.t.masks >>= 8;
+            return rank_steps;
+        }
         const int64_t k = p.K;
-        da.tile(p.x + t.m0 * k, 2 * t.rows * k, p.K, t.rows);
-        db.tile(p.w + t.n0 * k, 2 * min(kTile, p.N - t.n0) * k, p.K, 0);
+        da.init(k, wave, lane);
+        db.init(k, wave, lane);
+        da.tile(p.x + c.t.m0 * k, 2 * c.t.rows * k, p.K, c.t.rows);
+        db.tile(p.w + c.t.n0 * k, 2 * columns * k, p.K, 0);
+        c.term = -1;
+        return (p.K + 63) / 64;
     }
 };
 
 template <bool F16>
 struct LoraFinish {
-    // The adapters' part of a wave's results, 64 ranks at a time.  Rows with one adapter
-    // between them take its product straight into their sums; where they have several,
-    // each fragment's product with each of its adapters is made apart and kept by that
-    // adapter's rows alone, so that what another request's adapter holds (NaN too) reaches
-    // nobody else.  All loads of a product are issued before its first MFMA (a load at a
-    // time took 80 us a tile).
-    template <int FM, int FN>
-    __device__ __forceinline__ void expand(const LoraParams &p, const TileAt &t,
-                                           f16_t (&acc)[FM][FN], int wm, int wn, int lane) const {
-        const int c = lane & 31, g = lane >> 5, row0 = t.m0 + wm, rows = t.rows - wm;
-        if (rows <= 0) return;
-        int id[FM];
-#pragma unroll
-        for (int i = 0; i < FM; ++i) id[i] = adapter(p, row0 + min(32 * i + c, rows - 1));
-        const int one = uniform(id[0]);
-        bool same = true;
-#pragma unroll
-        for (int i = 0; i < FM; ++i) same &= id[i] == one;
-        const bool all = __builtin_amdgcn_ballot_w64(same) == ~uint64_t{0};
-        if (all && one < 0) return;
-        const int64_t r = p.r, n = t.n0 + wn;
-        const int s_row = 4 * p.r, b_row = 2 * p.r;
-        const rsrc_t sr = uniform_buffer(reinterpret_cast<const char *>(p.terms + row0 * 2 * r),
-                                         static_cast<int64_t>(rows) * s_row);
-        u4_t bv[4][FN], sv[4][2];
-        auto columns = [&](int a, int k0) GFR_INLINE {
-            const rsrc_t br = uniform_buffer(
-                reinterpret_cast<const char *>(p.b + (a * int64_t{p.N} + n) * r),
-                n < p.N ? (p.N - n) * b_row : 0);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    const int k = k0 + 16 * q + 8 * g;
-                    bv[q][j] = load16<0>(br, k < p.r ? (32 * j + c) * b_row + 2 * k : kPast, 0);
-                }
-        };
-        auto inner = [&](int i, int k0) GFR_INLINE {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int k = k0 + 16 * q + 8 * g;
-                const int off = k < p.r ? (32 * i + c) * s_row + 2 * k : kPast;
-                sv[q][0] = load16<0>(sr, off, 0);
-                sv[q][1] = load16<0>(sr, off, b_row);
-            }
-        };
-        if (all) {
-#pragma unroll 1
-            for (int k0 = 0; k0 < p.r; k0 += 64) {
-                const int parts = (p.r - k0 + 15) / 16;
-                columns(one, k0);
-#pragma unroll
-                for (int i = 0; i < FM; ++i) {
-                    inner(i, k0);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (q < parts)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                for (int j = 0; j < FN; ++j)
-                                    acc[i][j] = mfma32<F16>(bv[q][j], sv[q][h], acc[i][j]);
-                }
-            }
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            uint64_t todo = __builtin_amdgcn_ballot_w64(id[i] >= 0);
-#pragma unroll 1
-            while (todo) {
-                const int a = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(todo));
-                const bool mine = id[i] == a;
-                todo &= ~__builtin_amdgcn_ballot_w64(mine);
-#pragma unroll 1
-                for (int k0 = 0; k0 < p.r; k0 += 64) {
-                    inner(i, k0);
-                    columns(a, k0);
-#pragma unroll
-                    for (int j = 0; j < FN; ++j) {
-                        f16_t own = {};
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                own = mfma32<F16>(bv[q][j], sv[q][h], own);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) acc[i][j][e] += mine ? own[e] : 0.0f;
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                }
-            }
-        }
-    }
-
     template <int FM, int FN>
     __device__ __forceinline__ int tile(const TileAt &t, f16_t (&acc)[FM][FN], int wm, int wn,
                                         int lane) const {
+        if (t.rows <= wm) return 0;
         const LoraParams p = fresh<LoraParams>();
-        expand(p, t, acc, wm, wn, lane);
-        __builtin_amdgcn_sched_barrier(0);
         // A lane has four columns of row lane % 32 at a time; it trades halves with its
         // row's other lane for eight, and 16-bit results once more, for runs of 64 bytes.
         const int c = lane & 31, g = lane >> 5, es = p.out_f32 ? 4 : 2;
         const int bias_es = p.bias_f32 ? 4 : 2;
         const rsrc_t from_bias = uniform_buffer(static_cast<const char *>(p.bias),
                                                 p.bias ? static_cast<int64_t>(p.N) * bias_es : 0);
-        float bias[FN][2][8];
+        auto column = [&](int j, int q) { return t.n0 + wn + 32 * j + 16 * q + 8 * g; };
+        u4_t bias[FN][2], res[2][FN][2];
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int off = bias_es * (t.n0 + wn + 32 * j + 16 * q + 8 * g);
-                const u4_t b0 = load16<0>(from_bias, off, 0);
-                const u4_t b1 = load16<0>(from_bias, p.bias_f32 ? off : kPast, 16);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    bias[j][q][e] = p.bias_f32
-                                        ? __uint_as_float(e < 4 ? b0[e & 3] : b1[e & 3])
-                                        : unpack1<F16>(b0[e >> 1] >> (16 * (e & 1)));
-            }
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
+            for (int q = 0; q < 2; ++q)
+                bias[j][q] = load16<0>(from_bias, p.bias_f32 ? kPast : 2 * column(j, q), 0);
+        // (a block of 32 rows ahead of its use)
+        auto fetch = [&](int i) GFR_INLINE {
             const int64_t row = t.m0 + wm + 32 * i;
             const int rows = max(0, min(32, t.rows - wm - 32 * i));
-            const rsrc_t to =
-                uniform_buffer(static_cast<char *>(p.out) + row * p.N * es,
-                               static_cast<int64_t>(rows) * p.N * es);
             const rsrc_t from = uniform_buffer(
                 reinterpret_cast<const char *>(p.residual + (p.residual ? row * p.N : 0)),
                 p.residual ? static_cast<int64_t>(rows) * p.N * 2 : 0);
-            u4_t res[FN][2];
 #pragma unroll
             for (int j = 0; j < FN; ++j)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const int n = t.n0 + wn + 32 * j + 16 * q + 8 * g;
-                    res[j][q] = load16<0>(from, n < p.N ? 2 * (c * p.N + n) : kPast, 0);
+                    const int n = column(j, q);
+                    res[i & 1][j][q] = load16<0>(from, n < p.N ? 2 * (c * p.N + n) : kPast, 0);
                 }
+        };
+        fetch(0);
+        // (lane f: fragment f's code)
+        const int codes = p.codes[(t.m0 + wm) / 32 + min(lane, (t.rows - wm - 1) / 32)];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int64_t row = t.m0 + wm + 32 * i;
+            const int rows = max(0, min(32, t.rows - wm - 32 * i));
+            if (i + 1 < FM) fetch(i + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            if (__builtin_amdgcn_readlane(codes, i) == kSeveral) {
+                const rsrc_t to =
+                    uniform_buffer(reinterpret_cast<char *>(p.dense + row * p.N),
+                                   static_cast<int64_t>(rows) * p.N * 4);
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int n = t.n0 + wn + 32 * j + 8 * q + 4 * g;
+                        const f4_t y = {acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                        acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                        store16(to, __builtin_bit_cast(u4_t, y),
+                                n < p.N ? 4 * (c * p.N + n) : kPast);
+                    }
+                continue;
+            }
+            const rsrc_t to =
+                uniform_buffer(static_cast<char *>(p.out) + row * p.N * es,
+                               static_cast<int64_t>(rows) * p.N * es);
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 u4_t h[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const int n = t.n0 + wn + 32 * j + 16 * q + 8 * g;
+                    const int n = column(j, q);
                     float y[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -442,11 +421,20 @@ struct LoraFinish {
                         y[e] = __uint_as_float(w[0]);
                         y[4 + e] = __uint_as_float(w[1]);
                     }
+                    if (p.bias_f32) {
+                        const f4_t b0 = __builtin_bit_cast(f4_t, load16<0>(from_bias, 4 * n, 0));
+                        const f4_t b1 = __builtin_bit_cast(f4_t, load16<0>(from_bias, 4 * n, 16));
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] += bias[j][q][e];
+                        for (int e = 0; e < 4; ++e) y[e] += b0[e], y[4 + e] += b1[e];
+                    } else if (p.bias) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        y[e] += unpack1<F16>(res[j][q][e >> 1] >> (16 * (e & 1)));
+                        for (int e = 0; e < 8; ++e)
+                            y[e] += unpack1<F16>(bias[j][q][e >> 1] >> (16 * (e & 1)));
+                    }
+                    if (p.residual)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            y[e] += unpack1<F16>(res[i & 1][j][q][e >> 1] >> (16 * (e & 1)));
                     if (p.out_f32) {
                         const int off = n < p.N ? 4 * (c * p.N + n) : kPast;
                         store16(to, __builtin_bit_cast(u4_t, f4_t{y[0], y[1], y[2], y[3]}), off);
@@ -477,6 +465,79 @@ struct LoraFinish {
     }
     __device__ __forceinline__ void clear(const TileAt &) const {}
 };
+
+// 32 rows with several adapters, 32 columns a wave: each adapter's product apart, added to
+// its own rows' sums.
+template <bool F16>
+__global__ __launch_bounds__(256) void expand_tile_kernel(LoraParams p) {
+    if (p.codes[blockIdx.y] != kSeveral) return;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int c = lane & 31, g = lane >> 5, t0 = blockIdx.y * 32;
+    const int64_t n0 = blockIdx.x * 128 + wave * 32;
+    if (n0 >= p.N) return;
+    const int rows = min(32, p.M - t0), s_row = 4 * p.r, b_row = 2 * p.r;
+    const int id = c < rows ? adapter(p, t0 + c) : -1;
+    const int64_t row0 = static_cast<int64_t>(t0) * p.N;
+    const rsrc_t from = uniform_buffer(reinterpret_cast<const char *>(p.dense + row0),
+                                       static_cast<int64_t>(rows) * p.N * 4);
+    const rsrc_t sr = uniform_buffer(
+        reinterpret_cast<const char *>(p.terms + static_cast<int64_t>(t0) * 2 * p.r),
+        static_cast<int64_t>(rows) * s_row);
+    f4_t sum[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int n = static_cast<int>(n0) + 8 * q + 4 * g;
+        sum[q] = __builtin_bit_cast(f4_t, load16<0>(from, n < p.N ? 4 * (c * p.N + n) : kPast, 0));
+    }
+    uint64_t todo = __builtin_amdgcn_ballot_w64(id >= 0);
+    while (todo) {
+        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        const bool mine = id == a;
+        todo &= ~__builtin_amdgcn_ballot_w64(mine);
+        const rsrc_t br =
+            uniform_buffer(reinterpret_cast<const char *>(p.b + (a * int64_t{p.N} + n0) * p.r),
+                           (p.N - n0) * b_row);
+        f16_t own = {};
+        for (int k0 = 0; k0 < p.r; k0 += 64) {
+            u4_t b[4], s[4][2];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int k = k0 + 16 * q + 8 * g;
+                const int off = k < p.r ? c * s_row + 2 * k : kPast;
+                b[q] = load16<0>(br, k < p.r ? c * b_row + 2 * k : kPast, 0);
+                s[q][0] = load16<0>(sr, off, 0);
+                s[q][1] = load16<0>(sr, off, b_row);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) own = mfma32<F16>(b[q], s[q][h], own);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum[e >> 2][e & 3] += mine ? own[e] : 0.0f;
+    }
+    if (c >= rows) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int n = static_cast<int>(n0) + 8 * q + 4 * g;
+        if (n >= p.N) continue;                     // (N is a multiple of 8)
+        const int64_t at = row0 + static_cast<int64_t>(c) * p.N + n;
+        f4_t y = sum[q];
+        if (p.bias)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] += element(p.bias, n + e, p.bias_f32, F16);
+        if (p.residual) {
+            const u2_t h = load<u2_t>(p.residual + at);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] += unpack1<F16>(h[e >> 1] >> (16 * (e & 1)));
+        }
+        if (p.out_f32)
+            *reinterpret_cast<f4_t *>(static_cast<float *>(p.out) + at) = y;
+        else
+            *reinterpret_cast<u2_t *>(static_cast<uint16_t *>(p.out) + at) =
+                u2_t{pack2<F16>(y[0], y[1]), pack2<F16>(y[2], y[3])};
+    }
+}
 
 template <bool F16>
 __global__ __launch_bounds__(kWaves * 64, 1) void lora_tile_kernel(LoraParams p) {
@@ -545,6 +606,9 @@ hipError_t launch_tiles(const LoraParams &p, hipStream_t stream) {
     constexpr auto kernel = &lora_tile_kernel<F16>;
     if (const hipError_t a = allow_lds<kernel>(lds); a != hipSuccess) return a;
     hipLaunchKernelGGL(kernel, dim3(256), dim3(kWaves * 64), lds, stream, p);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    hipLaunchKernelGGL((expand_tile_kernel<F16>), dim3((p.N + 127) / 128, (p.M + 31) / 32),
+                       dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -554,10 +618,12 @@ LoraLayout lora_layout(int64_t M, int64_t N, int64_t K, int64_t r) {
     const auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
     LoraLayout l{};
     // Whole tiles where they fill half of the CUs.
-    l.tiles = K % 8 == 0 && N % 8 == 0 && r % 8 == 0 &&
+    l.tiles = K % 8 == 0 && N % 8 == 0 && r % 8 == 0 && M <= 32 * 65535 &&
               ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile) >= 128;
     if (l.tiles) {
-        l.total = up(2 * sizeof(uint16_t) * M * r);
+        l.codes = up(2 * sizeof(uint16_t) * M * r);
+        l.dense = l.codes + up(sizeof(int32_t) * ((M + 31) / 32));
+        l.total = l.dense + up(sizeof(float) * M * N);
         return l;
     }
     l.choice = linear_choice(M, N, K, GFR_ACT_NONE);

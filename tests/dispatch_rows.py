@@ -10,7 +10,7 @@ class _Choice(ctypes.Structure):
 
 
 class _Lora(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_size_t) for n in ("dense", "total")] + [
+    _fields_ = [(n, ctypes.c_size_t) for n in ("codes", "dense", "total")] + [
         ("tiles", ctypes.c_int32), ("choice", _Choice)]
 
 
