@@ -162,17 +162,22 @@ __device__ __forceinline__ void put4(const GroupedParams &p, int64_t row, int n,
 // General kernel: any K and N
 // ---------------------------------------------------------------------------
 
-// One operand's 128 lines of a step, four pieces a thread, through registers.
+// One operand's T lines of a step, T / 32 pieces a thread, through registers.
 // k-major: lines are rows of `ld` = K elements, of which the step's 64 may end
 // early.  line-major: the step's k are rows of `ld` elements, `k_end` of them.
-template <bool LINE>
+template <bool LINE, int T, int D>
 struct Staged {
+    static constexpr int kPieces = T / 32;
     const uint16_t *base;      // k-major: the tile's first line; line-major: its first column at k 0
     int64_t ld, elements;      // of a row; from base to the end of what may be read
     int k_end, lines;
-    u4_t v[4];
+    u4_t v[D][kPieces];
 
-    __device__ __forceinline__ void fetch(int step) {
+    __device__ __forceinline__ void tile(const uint16_t *base_, int64_t ld_, int64_t elements_,
+                                         int k_end_, int lines_) {
+        base = base_, ld = ld_, elements = elements_, k_end = k_end_, lines = lines_;
+    }
+    __device__ __forceinline__ void fetch(u4_t (&to)[kPieces], int step) {
         const bool whole = ld % 8 == 0;
         if (!LINE) {
             const int skew = reinterpret_cast<uintptr_t>(base) & 2;
@@ -180,108 +185,121 @@ struct Staged {
                                     2 * elements + skew);
             const int piece = threadIdx.x & 7, valid = k_end - 64 * step - 8 * piece;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kPieces; ++i) {
                 const int line = (threadIdx.x >> 3) + 32 * i;
                 const int off = line * static_cast<int>(2 * ld) + skew + 128 * step + 16 * piece;
-                v[i] = u4_t{0, 0, 0, 0};
+                to[i] = u4_t{0, 0, 0, 0};
                 if (line < lines && valid > 0)
-                    v[i] = valid >= 8 ? eight_of(r, off, whole) : eight_first(r, off, valid);
+                    to[i] = valid >= 8 ? eight_of(r, off, whole) : eight_first(r, off, valid);
             }
         } else {
             const uint16_t *at = base + 64 * step * ld;
             const int skew = reinterpret_cast<uintptr_t>(at) & 2;
             const rsrc_t r = buffer(reinterpret_cast<const char *>(at) - skew,
                                     2 * (elements - 64 * step * ld) + skew);
+            constexpr int kPer = T / 8;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = (threadIdx.x >> 4) + 16 * i;
-                const int off = k * static_cast<int>(2 * ld) + skew + 16 * (threadIdx.x & 15);
-                v[i] = u4_t{0, 0, 0, 0};
-                if (64 * step + k < k_end) v[i] = eight_of(r, off, whole);
+            for (int i = 0; i < kPieces; ++i) {
+                const int k = threadIdx.x / kPer + 256 / kPer * i;
+                const int off =
+                    k * static_cast<int>(2 * ld) + skew + 16 * (threadIdx.x % kPer);
+                to[i] = u4_t{0, 0, 0, 0};
+                if (64 * step + k < k_end) to[i] = eight_of(r, off, whole);
             }
         }
     }
-    __device__ __forceinline__ void put(u4_t *tile) const {
+    __device__ __forceinline__ void put(u4_t *tile, const u4_t (&from)[kPieces]) const {
+        constexpr int kPer = T / 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            tile[LINE ? piece_line<128>((threadIdx.x >> 4) + 16 * i, threadIdx.x & 15)
-                      : piece_k((threadIdx.x >> 3) + 32 * i, threadIdx.x & 7)] = v[i];
+        for (int i = 0; i < kPieces; ++i)
+            tile[LINE ? piece_line<T>(threadIdx.x / kPer + 256 / kPer * i, threadIdx.x % kPer)
+                      : piece_k((threadIdx.x >> 3) + 32 * i, threadIdx.x & 7)] = from[i];
     }
 };
 
-// 128 x 128 tiles of four waves, one step's loads in flight in registers.
-template <bool F16, bool WGRAD, bool WLINE>
+// T x T tiles of four waves, D steps' loads in flight in registers.
+template <bool F16, bool WGRAD, bool WLINE, int T>
 __global__ __launch_bounds__(256, 2) void general_kernel(GroupedParams p) {
+    constexpr int D = T == 64 ? 4 : 2, F = T / 64;
     __shared__ Groups s;
-    __shared__ u4_t tile[2][128 * 8];
-    find_groups<128>(p, s, [](int) { return 0u; });
+    __shared__ u4_t tile[2][2][T * 8];
+    find_groups<T>(p, s, [](int) { return 0u; });
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int wm = wave / 2 * 64, wn = wave % 2 * 64;
-    const int tiles_n = (p.N + 127) / 128, tiles_k = (p.K + 127) / 128;
+    const int wm = wave / 2 * (T / 2), wn = wave % 2 * (T / 2);
+    const int tiles_n = (p.N + T - 1) / T, tiles_k = (p.K + T - 1) / T;
     const int64_t total = WGRAD ? static_cast<int64_t>(p.E) * tiles_k * tiles_n
                                 : static_cast<int64_t>(s.units[p.fill ? p.E + 1 : p.E]) * tiles_n;
     for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
         int e, m0, rows, steps;
-        const int n0 = static_cast<int>(id % tiles_n) * 128;
-        Staged<WGRAD> a;
-        Staged<WLINE> b;
+        const int n0 = static_cast<int>(id % tiles_n) * T;
+        Staged<WGRAD, T, D> a;
+        Staged<WLINE, T, D> b;
         if (WGRAD) {
             const int64_t rest = id / tiles_n;
             e = static_cast<int>(rest / tiles_k);
-            m0 = static_cast<int>(rest % tiles_k) * 128;
-            rows = min(128, p.K - m0);
+            m0 = static_cast<int>(rest % tiles_k) * T;
+            rows = min(T, p.K - m0);
             const int first = s.start[e], count = s.start[e + 1] - first;
             steps = (count + 63) / 64;
             if (p.accumulate && count == 0) continue;
-            a = {p.x + static_cast<int64_t>(first) * p.K + m0, p.K,
-                 static_cast<int64_t>(count) * p.K - m0, count, 128, {}};
-            b = {p.w + static_cast<int64_t>(first) * p.N + n0, p.N,
-                 static_cast<int64_t>(count) * p.N - n0, count, 128, {}};
+            a.tile(p.x + static_cast<int64_t>(first) * p.K + m0, p.K,
+                   static_cast<int64_t>(count) * p.K - m0, count, T);
+            b.tile(p.w + static_cast<int64_t>(first) * p.N + n0, p.N,
+                   static_cast<int64_t>(count) * p.N - n0, count, T);
         } else {
             const int u = uniform(static_cast<int>(id / tiles_n));
             e = expert_of(s, p.E, u);
-            m0 = s.start[e] + (u - s.units[e]) * 128;
-            rows = min(128, s.start[e + 1] - m0);
+            m0 = s.start[e] + (u - s.units[e]) * T;
+            rows = min(T, s.start[e + 1] - m0);
             steps = e < p.E ? (p.K + 63) / 64 : 0;
             const uint16_t *w = p.w + static_cast<int64_t>(e) * p.K * p.N;
-            a = {p.x + static_cast<int64_t>(m0) * p.K, p.K, static_cast<int64_t>(rows) * p.K, p.K,
-                 rows, {}};
+            a.tile(p.x + static_cast<int64_t>(m0) * p.K, p.K, static_cast<int64_t>(rows) * p.K,
+                   p.K, rows);
             if (WLINE)
-                b = {w + n0, p.N, static_cast<int64_t>(p.K) * p.N - n0, p.K, 128, {}};
+                b.tile(w + n0, p.N, static_cast<int64_t>(p.K) * p.N - n0, p.K, T);
             else
-                b = {w + static_cast<int64_t>(n0) * p.K, p.K,
-                     static_cast<int64_t>(min(128, p.N - n0)) * p.K, p.K, min(128, p.N - n0), {}};
+                b.tile(w + static_cast<int64_t>(n0) * p.K, p.K,
+                       static_cast<int64_t>(min(T, p.N - n0)) * p.K, p.K, min(T, p.N - n0));
         }
-        f16_t acc[2][2] = {};
-        if (steps > 0) a.fetch(0), b.fetch(0);
-        for (int step = 0; step < steps; ++step) {
-            __syncthreads();
-            a.put(tile[0]);
-            b.put(tile[1]);
-            __syncthreads();
-            if (step + 1 < steps) a.fetch(step + 1), b.fetch(step + 1);
+        f16_t acc[F][F] = {};
 #pragma unroll
-            for (int part = 0; part < 4; ++part) {
-                u4_t fa[2], fb[2];
+        for (int d = 0; d < D; ++d)
+            if (d < steps) a.fetch(a.v[d], d), b.fetch(b.v[d], d);
+        for (int first = 0; first < steps; first += D)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    fa[i] = fragment<WGRAD, 128>(tile[0], wm + 32 * i, part, lane);
-                    fb[i] = fragment<WLINE, 128>(tile[1], wn + 32 * i, part, lane);
+            for (int d = 0; d < D; ++d) {
+                const int step = first + d;
+                if (step >= steps) break;
+                // (a stage is written again two steps later: behind the barrier between)
+                u4_t(&to)[2][T * 8] = tile[d & 1];
+                a.put(to[0], a.v[d]);
+                b.put(to[1], b.v[d]);
+                __syncthreads();
+                if (step + D < steps) a.fetch(a.v[d], step + D), b.fetch(b.v[d], step + D);
+#pragma unroll
+                for (int part = 0; part < 4; ++part) {
+                    u4_t fa[F], fb[F];
+#pragma unroll
+                    for (int i = 0; i < F; ++i) {
+                        fa[i] = fragment<WGRAD, T>(to[0], wm + 32 * i, part, lane);
+                        fb[i] = fragment<WLINE, T>(to[1], wn + 32 * i, part, lane);
+                    }
+#pragma unroll
+                    for (int i = 0; i < F; ++i)
+#pragma unroll
+                        for (int j = 0; j < F; ++j)
+                            acc[i][j] = mfma32<F16>(fb[j], fa[i], acc[i][j]);
                 }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<F16>(fb[j], fa[i], acc[i][j]);
             }
-        }
+        __syncthreads();
         // lane l holds line 32 i + l % 32, columns 32 j + 8 r + 4 (l / 32) .. + 3
         const int64_t row0 = WGRAD ? static_cast<int64_t>(e) * p.K + m0 : m0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < F; ++i) {
             const int m = wm + 32 * i + (lane & 31);
             if (m >= rows) continue;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < F; ++j)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float v[4] = {acc[i][j][4 * r], acc[i][j][4 * r + 1],
@@ -593,13 +611,24 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
     run_tiles<F16, WGRAD, WLINE>(lds, tiles, finish, p.K, WLINE ? p.N : p.K);
 }
 
+// Tiles of 64 where those of 128 would leave CUs idle: they are at most that many.
+int64_t general_tiles(const GroupedParams &p, int64_t t) {
+    const int64_t tn = (p.N + t - 1) / t, tk = (p.K + t - 1) / t;
+    return p.wgrad ? p.E * tk * tn : ((p.M + t - 1) / t + (p.E < p.M ? p.E : p.M)) * tn;
+}
+
+template <bool F16, bool WGRAD, bool WLINE, int T>
+hipError_t launch_general_t(const GroupedParams &p, hipStream_t stream) {
+    const int64_t most = general_tiles(p, T), grid = most < 1024 ? most : 1024;
+    hipLaunchKernelGGL((general_kernel<F16, WGRAD, WLINE, T>),
+                       dim3(static_cast<uint32_t>(grid > 0 ? grid : 1)), dim3(256), 0, stream, p);
+    return hipGetLastError();
+}
+
 template <bool F16, bool WGRAD, bool WLINE>
 hipError_t launch_general(const GroupedParams &p, hipStream_t stream) {
-    const int64_t tn = (p.N + 127) / 128, tk = (p.K + 127) / 128;
-    const int64_t most = WGRAD ? p.E * tk * tn : (p.M / 128 + p.E + 1) * tn;
-    const uint32_t grid = static_cast<uint32_t>(most < 1024 ? most : 1024);
-    hipLaunchKernelGGL((general_kernel<F16, WGRAD, WLINE>), dim3(grid), dim3(256), 0, stream, p);
-    return hipGetLastError();
+    return general_tiles(p, 128) < 512 ? launch_general_t<F16, WGRAD, WLINE, 64>(p, stream)
+                                       : launch_general_t<F16, WGRAD, WLINE, 128>(p, stream);
 }
 
 template <bool F16, bool WGRAD, bool WLINE>

@@ -9,8 +9,8 @@
 //               j ^ (r / 2 & 7): sixteen lanes that read one piece of sixteen lines
 //               reach all 64 banks.  (j ^ (r & 7) reaches half of them: 137 of 280
 //               thousand LDS clocks of 16384 x 4096 x 4096 were conflicts.)
-//   line-major  of each k, BX lines in BX / 8 pieces, piece j at j ^ 4 (k & 3).
-//               Fragments come through the transposing LDS read, which gives a
+//   line-major  of each k, BX lines in BX / 8 pieces, piece j at j ^ 4 (k & 3) (of 64
+//               lines at j ^ 4 (k & 1)).  Fragments come through the transposing LDS read, which gives a
 //               lane four k of one line; the 16 lanes that share it read 32 bytes
 //               of four k, and two such groups reach all banks.
 #pragma once
@@ -40,7 +40,7 @@ __device__ __forceinline__ f16_t mfma32(u4_t a, u4_t b, f16_t c) {
 __device__ __forceinline__ int piece_k(int r, int j) { return r * 8 + (j ^ (r >> 1 & 7)); }
 template <int BX>
 __device__ __forceinline__ int piece_line(int k, int j) {
-    return k * (BX / 8) + (j ^ (4 * (k & 3)));
+    return k * (BX / 8) + (j ^ (4 * (k & 3) & (BX / 8 - 1)));
 }
 
 // The fragment of lines [line, line + 32), k in [16 part, 16 part + 16): lane l
