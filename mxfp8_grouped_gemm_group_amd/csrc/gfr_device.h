@@ -105,10 +105,9 @@ __device__ __forceinline__ float silu(float v) {
     return v * __builtin_amdgcn_rcpf(1.0f + exp_f32(-v));
 }
 
-// Lets kernel K have up to 159 KB of dynamic LDS (a CU has 160); the runtime is asked
-// once per device.
-constexpr int kMaxLds = 159 << 10;
-template <auto K>
+// Lets kernel K have up to MOST bytes of dynamic LDS (with its static LDS they have to fit
+// a CU's 160 KB); the runtime is asked once per device.
+template <auto K, int MOST = 146 << 10>
 hipError_t allow_lds(int bytes) {
     if (bytes <= (32 << 10)) return hipSuccess;
     static std::atomic<bool> done[64];
@@ -116,7 +115,7 @@ hipError_t allow_lds(int bytes) {
     if (hipError_t e = hipGetDevice(&dev); e != hipSuccess) return e;
     if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_relaxed)) return hipSuccess;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(K),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, MOST);
     if (e == hipSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_relaxed);
     return e;
 }

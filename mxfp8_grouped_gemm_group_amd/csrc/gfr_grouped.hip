@@ -634,7 +634,7 @@ hipError_t launch_general(const GroupedParams &p, hipStream_t stream) {
 template <bool F16, bool WGRAD, bool WLINE>
 hipError_t launch_direct(const GroupedParams &p, hipStream_t stream) {
     constexpr auto kernel = &direct_kernel<F16, WGRAD, WLINE>;
-    if (hipError_t e = allow_lds<kernel>(kDirectLds); e != hipSuccess) return e;
+    if (hipError_t e = allow_lds<kernel, kMaxLds>(kDirectLds); e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, dim3(256), dim3(kWaves * 64), kDirectLds, stream, p);
     return hipGetLastError();
 }

@@ -598,13 +598,13 @@ hipError_t launch_rows(const LoraParams &p, hipStream_t stream) {
 template <bool F16>
 hipError_t launch_tiles(const LoraParams &p, hipStream_t stream) {
     constexpr auto shrink = &shrink_tile_kernel<F16>;
-    if (const hipError_t e = allow_lds<shrink>(kShrinkLds); e != hipSuccess) return e;
+    if (const hipError_t e = allow_lds<shrink, kMaxLds>(kShrinkLds); e != hipSuccess) return e;
     hipLaunchKernelGGL(shrink, dim3((p.M + 31) / 32, (p.r + 31) / 32), dim3(kShrinkWaves * 64),
                        kShrinkLds, stream, p);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     constexpr int lds = 2 * kStage * 16;
     constexpr auto kernel = &lora_tile_kernel<F16>;
-    if (const hipError_t a = allow_lds<kernel>(lds); a != hipSuccess) return a;
+    if (const hipError_t a = allow_lds<kernel, kMaxLds>(lds); a != hipSuccess) return a;
     hipLaunchKernelGGL(kernel, dim3(256), dim3(kWaves * 64), lds, stream, p);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     hipLaunchKernelGGL((expand_tile_kernel<F16>), dim3((p.N + 127) / 128, (p.M + 31) / 32),
