@@ -623,7 +623,7 @@ int gfr_grouped_linear_wgrad(const gfr_tensor *x, const gfr_tensor *dy,
  * that overlap in time need workspaces of their own.  With F16, inner and its products
  * are to stay within F16's range, as an F16 layer's own intermediate row.  Errors as
  * gfr_linear, and GFR_ERR_UNSUPPORTED for r outside [1, GFR_MAX_RANK], L outside
- * [1, 2^20] or M > 2^26; lora_a, lora_b 16-byte, adapter_ids and scaling 4-byte aligned.
+ * [1, 2^20], M > 2^26 or M r > 2^27; lora_a, lora_b 16-byte, adapter_ids and scaling 4-byte aligned.
  */
 int gfr_lora_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *bias,
                     const gfr_tensor *residual, const gfr_tensor *lora_a,

@@ -103,8 +103,8 @@ __device__ __forceinline__ Params fresh() {
     return *(const Params *)at;
 }
 
-// n / d for 0 <= n < 2^31 by d's reciprocal in FP32 (which is off by less than one for
-// quotients below 2^22, and corrected here).
+// n / d for 0 <= n < 2^31 by d's reciprocal in FP32, which is off by a few for the largest
+// quotients, and corrected.
 struct Divisor {
     int d;
     float inverse;
@@ -112,8 +112,8 @@ struct Divisor {
     __device__ __forceinline__ int of(int n) const {
         int q = static_cast<int>(static_cast<float>(n) * inverse);
         int rest = n - q * d;
-        if (rest < 0) --q, rest += d;
-        if (rest >= d) ++q;
+        while (uniform(rest) < 0) --q, rest += d;
+        while (uniform(rest) >= d) ++q, rest -= d;
         return uniform(q);
     }
 };

@@ -471,7 +471,7 @@ struct GroupedTiles {
     __device__ __forceinline__ GroupedTiles(const GroupedParams &p_, const Groups &s_)
         : p(p_), s(s_), lane(threadIdx.x & 63), tiles_n((p.N + kTile - 1) / kTile),
           tiles_k((p.K + kTile - 1) / kTile),
-          total(tiles_n * (WGRAD ? p.E * tiles_k : uniform(s.units[p.fill ? p.E + 1 : p.E]))),
+          total(tiles_n * (WGRAD ? p.E * tiles_k : uniform(s.units[p.E]))),
           by_n(tiles_n), by_k(tiles_k), by_band(8 * tiles_n) {
         const int xcd = blockIdx.x & 7;
         stride = gridDim.x >> 3;
@@ -483,7 +483,7 @@ struct GroupedTiles {
         if (x == 8) return total;
         const int64_t place = static_cast<int64_t>(uniform(s.cost[p.E])) * x;   // in eighths
         const int e = expert_at(s.cost, p.E, static_cast<int>(place >> 3), lane);
-        if (e >= p.E) return tiles_n * (WGRAD ? p.E * tiles_k : uniform(s.units[p.E]));
+        if (e >= p.E) return total;
         // (the cost of the experts before e is at most the place, and that of e too is more)
         const int64_t cost = uniform(s.cost[e + 1]) - uniform(s.cost[e]);
         const int first = WGRAD ? e * tiles_k : uniform(s.units[e]);
@@ -609,6 +609,12 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
     const GroupedTiles<WGRAD, WLINE> tiles(p, s);
     const GroupedFinish<F16, WGRAD, WLINE> finish{p, slab};
     run_tiles<F16, WGRAD, WLINE>(lds, tiles, finish, p.K, WLINE ? p.N : p.K);
+    // the rows behind the last group, by all blocks
+    if (!WGRAD && p.fill) {
+        const int all = tiles.tiles_n * uniform(s.units[p.E + 1]);
+        for (int id = tiles.total + blockIdx.x; id < all; id += gridDim.x)
+            finish.clear(tiles.at(id));
+    }
 }
 
 // Tiles of 64 where those of 128 would leave CUs idle: they are at most that many.

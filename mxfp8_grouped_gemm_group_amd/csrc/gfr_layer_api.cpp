@@ -135,6 +135,8 @@ int check_lora_sizes(int64_t M, int64_t N, int64_t K, int64_t r) {
     if (r < 1 || r > GFR_MAX_RANK || M > int64_t{1} << 26 || N > int64_t{1} << 30 ||
         K > int64_t{1} << 21)
         return GFR_ERR_UNSUPPORTED;
+    // (a grid has at most 2^32 threads, here a wave for four of a row's ranks)
+    if (M * ((r + 3) / 4) > int64_t{1} << 25) return GFR_ERR_UNSUPPORTED;
     return gfr::linear_choice(M, N, K, GFR_ACT_NONE).split > 0 ? GFR_OK : GFR_ERR_UNSUPPORTED;
 }
 

@@ -52,8 +52,9 @@ __device__ __forceinline__ float wave_sum(float v) {
 template <bool F16, bool ALIGNED, int R>
 __global__ __launch_bounds__(256) void shrink_rows_kernel(LoraParams p, int waves_per_row) {
     const int lane = threadIdx.x & 63;
-    const int id = uniform(static_cast<int>(blockIdx.x) * 4 + (threadIdx.x >> 6));
-    const int t = id / waves_per_row, j0 = id % waves_per_row * R;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + uniform(threadIdx.x >> 6);
+    const int t = static_cast<int>(id / waves_per_row);
+    const int j0 = static_cast<int>(id % waves_per_row) * R;
     if (t >= p.M) return;
     if (j0 == 0 && lane == 0) check_adapter(p, t);
     const int i = adapter(p, t);
@@ -618,7 +619,7 @@ LoraLayout lora_layout(int64_t M, int64_t N, int64_t K, int64_t r) {
     const auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
     LoraLayout l{};
     // Whole tiles where they fill half of the CUs.
-    l.tiles = K % 8 == 0 && N % 8 == 0 && r % 8 == 0 && M <= 32 * 65535 &&
+    l.tiles = K % 8 == 0 && N % 8 == 0 && r % 8 == 0 && M <= 32 * 65535 && N <= 1 << 21 &&
               ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile) >= 128;
     if (l.tiles) {
         l.codes = up(2 * sizeof(uint16_t) * M * r);
