@@ -502,13 +502,17 @@ struct GroupedTiles {
             t.steps = uniform((s.start[t.e + 1] - s.start[t.e] + 63) / 64);
         } else {
             t.e = expert_at(s.units, p.E, by_n.of(id), lane);
-            // within an expert, bands of eight units by all columns
+            // within an expert, bands of eight units by all columns; a column's units begin
+            // one further every 32 tiles, or a block would meet the same unit each time,
+            // and the last one is cheaper
             const int u0 = uniform(s.units[t.e]), units = uniform(s.units[t.e + 1]) - u0;
             const int at = id - u0 * tiles_n;
             const int band = by_band.of(at), in_band = at - band * 8 * tiles_n;
             const int depth = min(8, units - band * 8), column = Divisor(depth).of(in_band);
+            int unit = in_band - column * depth + (column * depth / 32) % depth;
+            if (unit >= depth) unit -= depth;
             t.n0 = column * kTile;
-            t.m0 = uniform(s.start[t.e]) + (band * 8 + in_band - column * depth) * kTile;
+            t.m0 = uniform(s.start[t.e]) + (band * 8 + unit) * kTile;
             t.rows = uniform(min(kTile, uniform(s.start[t.e + 1]) - t.m0));
             t.steps = uniform(t.e < p.E ? (p.K + 63) / 64 : 0);
         }
@@ -617,24 +621,11 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
     }
 }
 
-// Tiles of 64 where those of 128 would leave CUs idle: they are at most that many.
-int64_t general_tiles(const GroupedParams &p, int64_t t) {
-    const int64_t tn = (p.N + t - 1) / t, tk = (p.K + t - 1) / t;
-    return p.wgrad ? p.E * tk * tn : ((p.M + t - 1) / t + (p.E < p.M ? p.E : p.M)) * tn;
-}
-
 template <bool F16, bool WGRAD, bool WLINE, int T>
 hipError_t launch_general_t(const GroupedParams &p, hipStream_t stream) {
-    const int64_t most = general_tiles(p, T), grid = most < 1024 ? most : 1024;
-    hipLaunchKernelGGL((general_kernel<F16, WGRAD, WLINE, T>),
-                       dim3(static_cast<uint32_t>(grid > 0 ? grid : 1)), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((general_kernel<F16, WGRAD, WLINE, T>), dim3(T == 64 ? 1024 : 512),
+                       dim3(256), 0, stream, p);
     return hipGetLastError();
-}
-
-template <bool F16, bool WGRAD, bool WLINE>
-hipError_t launch_general(const GroupedParams &p, hipStream_t stream) {
-    return general_tiles(p, 128) < 512 ? launch_general_t<F16, WGRAD, WLINE, 64>(p, stream)
-                                       : launch_general_t<F16, WGRAD, WLINE, 128>(p, stream);
 }
 
 template <bool F16, bool WGRAD, bool WLINE>
@@ -645,20 +636,50 @@ hipError_t launch_direct(const GroupedParams &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <bool F16, bool WGRAD, bool WLINE>
+hipError_t launch_kernel(const GroupedParams &p, hipStream_t stream) {
+    switch (p.kernel) {
+    case GroupedKernel::kDirect: return launch_direct<F16, WGRAD, WLINE>(p, stream);
+    case GroupedKernel::k128: return launch_general_t<F16, WGRAD, WLINE, 128>(p, stream);
+    default: return launch_general_t<F16, WGRAD, WLINE, 64>(p, stream);
+    }
+}
+
 template <bool F16>
 hipError_t launch_grouped_t(const GroupedParams &p, hipStream_t stream) {
-    // rows of whole pieces, of every operand that is loaded
-    if (p.K % 8 == 0 && (p.N % 8 == 0 || (!p.wgrad && p.transpose))) {
-        if (p.wgrad) return launch_direct<F16, true, true>(p, stream);
-        return p.transpose ? launch_direct<F16, false, false>(p, stream)
-                           : launch_direct<F16, false, true>(p, stream);
-    }
-    if (p.wgrad) return launch_general<F16, true, true>(p, stream);
-    return p.transpose ? launch_general<F16, false, false>(p, stream)
-                       : launch_general<F16, false, true>(p, stream);
+    if (p.wgrad) return launch_kernel<F16, true, true>(p, stream);
+    return p.transpose ? launch_kernel<F16, false, false>(p, stream)
+                       : launch_kernel<F16, false, true>(p, stream);
 }
 
 }  // namespace
+
+// The kernel for a size, by estimated time; groups are taken as equal, an expert as
+// having a row if there is one for it.  A block's time per 64-step of the direct kernel
+// by its tile's rows, with the CUs one round after the other; of the general kernel with
+// two blocks to a CU.  (Direct against general, us: 8 rows over 256 experts of 2048 x
+// 1024 23 and 26; 64 over 64 27 and 45; 512 of one 46 and 25; 2048 of one of 4096 x 2048
+// 85 and 100; wgrad of 1024 rows of one of 1024 x 1024 29 and 17, of 2048 rows of one of
+// 4096 x 2048 52 and 59.)
+GroupedKernel grouped_kernel(int wgrad, int transpose, int64_t M, int64_t E, int64_t K, int64_t N) {
+    const auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
+    const auto most = [](double a, double b) { return a > b ? a : b; };
+    const int64_t experts = E < M ? E : M, rows = experts > 0 ? up(M, experts) : 0;
+    const auto tiles = [&](int64_t t) {
+        return wgrad ? static_cast<double>(E * up(K, t)) * static_cast<double>(up(N, t))
+                     : static_cast<double>(experts * up(rows, t)) * static_cast<double>(up(N, t));
+    };
+    const double steps = static_cast<double>(up(wgrad ? rows : K, 64));
+    const GroupedKernel general = tiles(128) < 512 ? GroupedKernel::k64 : GroupedKernel::k128;
+    // rows of whole pieces, of every operand that is loaded
+    if (K % 8 != 0 || (N % 8 != 0 && (wgrad || !transpose))) return general;
+    const double rounds = static_cast<double>(static_cast<int64_t>(tiles(256) / 256.0 + 0.999));
+    const double step = wgrad || rows > 192 ? 1.2 : rows > 128 ? 1.0 : rows > 64 ? 0.8 : rows > 32 ? 0.56 : 0.47;
+    const double direct = 8.0 + rounds * (steps * step + (wgrad ? 3.0 : 0.0));
+    const double fill = tiles(64) / 512.0;
+    const double other = 5.0 + most(1.0, fill) * (steps * (fill > 1.0 ? 0.75 : 0.65) + wgrad);
+    return direct <= other ? GroupedKernel::kDirect : general;
+}
 
 hipError_t launch_grouped(const GroupedParams &p, hipStream_t stream) {
     return p.f16 ? launch_grouped_t<true>(p, stream) : launch_grouped_t<false>(p, stream);

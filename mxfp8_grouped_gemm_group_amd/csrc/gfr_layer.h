@@ -94,6 +94,11 @@ struct RouteParams {
 size_t route_workspace(int64_t T, int64_t E, int64_t k);
 hipError_t launch_route(const RouteParams &p, hipStream_t stream);
 
+// The kernel for a size of the 16-bit grouped products: whole rows of pieces straight to
+// LDS, or the general one by its tile.
+enum class GroupedKernel : int32_t { kDirect, k128, k64 };
+GroupedKernel grouped_kernel(int wgrad, int transpose, int64_t M, int64_t E, int64_t K, int64_t N);
+
 struct GroupedParams {
     const uint16_t *x;         // [M, K]
     const uint16_t *w;         // forward: [E, K, N] ([E, N, K] transposed); wgrad: [M, N]
@@ -105,6 +110,7 @@ struct GroupedParams {
     int32_t accumulate;        // wgrad: out is added to
     int32_t f16, out_f32;
     int32_t wide;              // rows of out are whole, aligned 16 bytes
+    GroupedKernel kernel;
     int32_t M, E, K, N;
 };
 

@@ -349,6 +349,7 @@ int gfr_grouped_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tenso
     p.K = static_cast<int32_t>(K);
     p.N = static_cast<int32_t>(N);
     p.transpose = transpose_w;
+    p.kernel = gfr::grouped_kernel(0, transpose_w, M, E, K, N);
     p.fill = fill;
     p.wide = N % 8 == 0;
     // (tiles are counted in 32 bits)
@@ -381,6 +382,7 @@ int gfr_grouped_linear_wgrad(const gfr_tensor *x, const gfr_tensor *dy,
     p.N = static_cast<int32_t>(columns->shape[1]);
     p.wgrad = 1;
     p.accumulate = accumulate;
+    p.kernel = gfr::grouped_kernel(1, 0, M, E, p.K, p.N);
     p.wide = p.N % 8 == 0;
     if (E * ((K + 63) / 64) * ((N + 63) / 64) > kMaxRows) return GFR_ERR_UNSUPPORTED;
     return gfr::launch_grouped(p, static_cast<hipStream_t>(stream)) == hipSuccess ? GFR_OK

@@ -1,5 +1,6 @@
 """Which kernels a size of the products chosen by the row takes: the library's own
-host-side choice (csrc/gfr_layer.h: lora_layout), called by its C++ symbol."""
+host-side choice (csrc/gfr_layer.h: grouped_kernel, lora_layout), called by its C++
+symbols."""
 import ctypes
 
 import mxfp8_grouped_gemm_group_amd as gfr
@@ -19,3 +20,10 @@ def lora(M, N, K, r):
     f = gfr.load_library()._ZN3gfr11lora_layoutEllll
     f.restype, f.argtypes = _Lora, [ctypes.c_int64] * 4
     return bool(f(M, N, K, r).tiles)
+
+
+def grouped(M, E, K, N, wgrad=False, transpose=False):
+    """"direct", "128" or "64"."""
+    f = gfr.load_library()._ZN3gfr14grouped_kernelEiillll
+    f.restype, f.argtypes = ctypes.c_int32, [ctypes.c_int] * 2 + [ctypes.c_int64] * 4
+    return ("direct", "128", "64")[f(int(wgrad), int(transpose), M, E, K, N)]
