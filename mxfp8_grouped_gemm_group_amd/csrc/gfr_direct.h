@@ -52,6 +52,7 @@ struct Direct {
     int offs, now;                 // the lane's place in a load; in the step's loads
     int piece_k;                   // k-major: first k of the lane's piece
     int K, off, loads;             // loads: those that hold any line of the tile
+    int turn;                      // k-major: the step of K that comes first
 
     // Rows of `ld` elements.  Load i takes the tile's rows from (WAVES i + wave) kRows on.
     __device__ __forceinline__ void init(int64_t ld, int wave, int lane) {
@@ -69,7 +70,9 @@ struct Direct {
     }
     // The tile whose first line begins at `from` (line-major: at k = 0), with `bytes_`
     // from there to the end of what may be read (0: no tile) and K_ to sum over.
-    __device__ __forceinline__ void tile(const uint16_t *from, int64_t bytes_, int K_, int lines) {
+    __device__ __forceinline__ void tile(const uint16_t *from, int64_t bytes_, int K_, int lines,
+                                         int turn_ = 0) {
+        turn = turn_;
         base = reinterpret_cast<const char *>(from);
         bytes = bytes_;
         K = K_;
@@ -84,6 +87,8 @@ struct Direct {
             r = uniform_buffer(base + gone, bytes > gone ? bytes - gone : 0);
             off = first;
         } else {
+            step += turn;
+            if (64 * step >= K && turn > 0) step -= (K + 63) / 64;
             off = first + 128 * step;
             now = 64 * step + piece_k < K ? offs : kPast;
         }

@@ -110,6 +110,7 @@ struct GroupedParams {
     int32_t accumulate;        // wgrad: out is added to
     int32_t f16, out_f32;
     int32_t wide;              // rows of out are whole, aligned 16 bytes
+    int32_t turn;              // forward, [E, N, K]: column tiles begin at different steps of K
     GroupedKernel kernel;
     int32_t M, E, K, N;
 };

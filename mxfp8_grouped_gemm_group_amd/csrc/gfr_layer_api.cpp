@@ -350,6 +350,7 @@ int gfr_grouped_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tenso
     p.N = static_cast<int32_t>(N);
     p.transpose = transpose_w;
     p.kernel = gfr::grouped_kernel(0, transpose_w, M, E, K, N);
+    p.turn = transpose_w && M <= 128 * E;
     p.fill = fill;
     p.wide = N % 8 == 0;
     // (tiles are counted in 32 bits)
