@@ -120,44 +120,6 @@ __device__ __forceinline__ int expert_of(const Groups &s, int E, int u) {
     return lo;
 }
 
-// Four neighbouring results of a row, columns n .. n + 3 of N.
-template <bool F16>
-__device__ __forceinline__ void put4(const GroupedParams &p, int64_t row, int n, const float (&v)[4]) {
-    const int64_t at = row * p.N + n;
-    if (p.wide) {
-        if (n >= p.N) return;
-        float y[4] = {v[0], v[1], v[2], v[3]};
-        if (p.out_f32) {
-            f4_t *to = reinterpret_cast<f4_t *>(static_cast<float *>(p.out) + at);
-            f4_t o = {y[0], y[1], y[2], y[3]};
-            if (p.accumulate) o += *to;
-            *to = o;
-            return;
-        }
-        u2_t *to = reinterpret_cast<u2_t *>(static_cast<uint16_t *>(p.out) + at);
-        if (p.accumulate) {
-            const u2_t old = *to;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] += unpack1<F16>(old[j >> 1] >> (16 * (j & 1)));
-        }
-        *to = u2_t{pack2<F16>(y[0], y[1]), pack2<F16>(y[2], y[3])};
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (n + j >= p.N) return;
-        float y = v[j];
-        if (p.out_f32) {
-            float *to = static_cast<float *>(p.out) + at + j;
-            *to = p.accumulate ? *to + y : y;
-        } else {
-            uint16_t *to = static_cast<uint16_t *>(p.out) + at + j;
-            if (p.accumulate) y += unpack1<F16>(*to);
-            *to = static_cast<uint16_t>(pack2<F16>(y, 0.0f));
-        }
-    }
-}
-
 // ---------------------------------------------------------------------------
 // General kernel: any K and N
 // ---------------------------------------------------------------------------
@@ -292,21 +254,66 @@ __global__ __launch_bounds__(256, 2) void general_kernel(GroupedParams p) {
                 }
             }
         __syncthreads();
-        // lane l holds line 32 i + l % 32, columns 32 j + 8 r + 4 (l / 32) .. + 3
-        const int64_t row0 = WGRAD ? static_cast<int64_t>(e) * p.K + m0 : m0;
+        // Lane l holds line 32 i + l % 32, columns 32 j + 8 r + 4 (l / 32) .. + 3.  A wave's
+        // results go through its part of the stages, four columns of row m at piece j ^
+        // m, so that rows are written in runs (straight from here a store took 64
+        // places: zeros for 105 empty experts of 676 x 3588 0.7 ms).
+        constexpr int W = T / 2, kRow = W / 4;          // a wave's rows and columns; pieces
+        f4_t *const slab = reinterpret_cast<f4_t *>(tile) + wave * W * kRow;
 #pragma unroll
-        for (int i = 0; i < F; ++i) {
-            const int m = wm + 32 * i + (lane & 31);
-            if (m >= rows) continue;
+        for (int i = 0; i < F; ++i)
 #pragma unroll
             for (int j = 0; j < F; ++j)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float v[4] = {acc[i][j][4 * r], acc[i][j][4 * r + 1],
-                                        acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
-                    put4<F16>(p, row0 + m, n0 + wn + 32 * j + 8 * r + 4 * (lane >> 5), v);
+                    const int m = 32 * i + (lane & 31), piece = 8 * j + 2 * r + (lane >> 5);
+                    slab[m * kRow + (piece ^ (m & (kRow - 1)))] =
+                        f4_t{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2],
+                             acc[i][j][4 * r + 3]};
                 }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const int64_t row0 = (WGRAD ? static_cast<int64_t>(e) * p.K : 0) + m0 + wm;
+        if (p.N % 4 == 0) {
+            // four columns a lane
+            for (int k = lane; k < W * kRow; k += 64) {
+                const int m = k / kRow, n = n0 + wn + 4 * (k % kRow);
+                if (wm + m >= rows || n >= p.N) continue;
+                const int64_t at = (row0 + m) * p.N + n;
+                f4_t y = slab[m * kRow + (k % kRow ^ (m & (kRow - 1)))];
+                if (p.out_f32) {
+                    f4_t *to = reinterpret_cast<f4_t *>(static_cast<float *>(p.out) + at);
+                    if (p.accumulate) y += *to;
+                    *to = y;
+                } else {
+                    u2_t *to = reinterpret_cast<u2_t *>(static_cast<uint16_t *>(p.out) + at);
+                    if (p.accumulate) {
+                        const u2_t old = *to;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            y[q] += unpack1<F16>(old[q >> 1] >> (16 * (q & 1)));
+                    }
+                    *to = u2_t{pack2<F16>(y[0], y[1]), pack2<F16>(y[2], y[3])};
+                }
+            }
+        } else {
+            // a column a lane
+            for (int k = lane; k < W * W; k += 64) {
+                const int m = k / W, c = k % W, n = n0 + wn + c;
+                if (wm + m >= rows || n >= p.N) continue;
+                const int64_t at = (row0 + m) * p.N + n;
+                float y = slab[m * kRow + (c / 4 ^ (m & (kRow - 1)))][c % 4];
+                if (p.out_f32) {
+                    float *to = static_cast<float *>(p.out) + at;
+                    *to = p.accumulate ? *to + y : y;
+                } else {
+                    uint16_t *to = static_cast<uint16_t *>(p.out) + at;
+                    if (p.accumulate) y += unpack1<F16>(*to);
+                    *to = static_cast<uint16_t>(pack2<F16>(y, 0.0f));
+                }
+            }
         }
+        __syncthreads();
     }
 }
 

@@ -396,3 +396,13 @@ def test_tiles_same_bits_twice_and_under_graph():
         graph.replay()
         same(y, definition(a), str(i))
         torch.randn(256, 256, device=DEV).relu_()
+
+
+# few columns or ranks in fours alone, many rows: the shrink by tiles ahead of rows' expansion
+@pytest.mark.parametrize("M, N, K, r", [(4400, 72, 2056, 128), (4000, 71, 1096, 36),
+                                        (3000, 75, 2056, 20)])
+@pytest.mark.parametrize("mix", ["runs", "gaps"])
+def test_shrink_by_tiles_and_rows_expanded(M, N, K, r, mix):
+    assert 2 * M * r * K > 2e8
+    check(M, N, K, 5, r, mix=mix, bias=BF)
+    check(M, N, K, 5, r, dtype=HF, mix=mix, residual=True, out_dtype=None)
