@@ -600,8 +600,8 @@ int gfr_grouped_linear_wgrad(const gfr_tensor *x, const gfr_tensor *dy,
  *   inner[m, j] = scaling[i] * sum_k x[m, k] * lora_a[i, j, k]     i = adapter_ids[m]
  *
  * accumulated in FP32, rounded once to out's type; inner keeps at least 16 bits of
- * mantissa.  Rows of any order and mix of adapters; what a row gets depends on
- * its own adapter alone, whatever the others' hold.
+ * mantissa (with F16, down to 2^-25).  Rows of any order and mix of adapters; what a
+ * row gets depends on its own adapter alone, whatever the others' hold.
  *
  *  x            BF16 or F16 [M, K].
  *  w            x's dtype [N, K].

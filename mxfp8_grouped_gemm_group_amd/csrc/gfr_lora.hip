@@ -11,6 +11,7 @@
 // several, whose sums were kept in FP32, a launch that adds each row its own, so that what
 // another request's adapter holds (NaN too) reaches nobody else.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "gfr.h"
@@ -39,13 +40,16 @@ __device__ __forceinline__ void check_adapter(const LoraParams &p, int t) {
 }
 
 // inner as two 16-bit terms: the value rounded, and what that left over (16 bits of
-// mantissa or more), the ranks' first terms ahead of their second ones.
+// mantissa or more; nothing of an infinity), the ranks' first terms ahead of their second
+// ones.
 template <bool F16>
 __device__ __forceinline__ void put_terms(const LoraParams &p, int64_t t, int rank, float v) {
     uint16_t *to = p.terms + t * 2 * p.r + rank;
     const uint16_t hi = static_cast<uint16_t>(pack2<F16>(v, 0.0f));
     to[0] = hi;
-    to[p.r] = static_cast<uint16_t>(pack2<F16>(v - unpack1<F16>(hi), 0.0f));
+    const float first = unpack1<F16>(hi);
+    to[p.r] = static_cast<uint16_t>(
+        pack2<F16>(fabsf(first) == INFINITY ? 0.0f : v - first, 0.0f));
 }
 
 // a.x b.x + a.y b.y + c
@@ -199,8 +203,8 @@ __global__ __launch_bounds__(256) void expand_rows_kernel(LoraParams p, int rows
 // 32 rows by 32 ranks a block, its eight waves along K; an adapter after the other where
 // the rows have several.  A wave's two stages of 64 K are filled straight from memory, in
 // whole lines (fragments loaded from memory took 32 half lines a load: 4096 rows of 4096
-// by rank 64 51 us).  inner is kept as two 16-bit terms, the value and what its
-// rounding left over: 16 bits of mantissa or more, for the matrix cores.
+// by rank 64 51 us, so 18).
+//
 // codes[row / 32]: the adapter of 32 rows, -1 for none, kSeveral.
 constexpr int kSeveral = -2;
 constexpr int kShrinkWaves = 8;

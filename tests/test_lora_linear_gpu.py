@@ -406,3 +406,23 @@ def test_shrink_by_tiles_and_rows_expanded(M, N, K, r, mix):
     assert 2 * M * r * K > 2e8
     check(M, N, K, 5, r, mix=mix, bias=BF)
     check(M, N, K, 5, r, dtype=HF, mix=mix, residual=True, out_dtype=None)
+
+
+@pytest.mark.parametrize("M, N, K", [(5, 136, 72), (300, 136, 264), (4300, 2056, 72)])
+@pytest.mark.parametrize("r", [8, 5])
+def test_infinities_as_the_definition_has_them(M, N, K, r):
+    """An infinite inner value gives infinities (and NaN for a zero beside it), not NaN all
+    over: x, an adapter's row and a scaling that are infinite."""
+    a = integers(M, N, K, 3, r, BF, mix="random")
+    a["ids"][:3] = torch.tensor([0, 1, 2], dtype=torch.int32)
+    a["b"][a["b"] == 0] = 1
+    for change in ("x", "a", "scaling"):
+        b = {**a, change: a[change].clone()}
+        if change == "x":
+            b["x"][1, K - 1] = float("inf")
+        elif change == "a":
+            b["a"][1, r - 1, 3] = float("-inf")
+            b["x"][:, 3] = 2
+        else:
+            b["scaling"][2] = float("inf")
+        same(call(b, out_dtype=F32), definition(b), change)
