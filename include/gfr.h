@@ -557,8 +557,8 @@ int gfr_moe_route_workspace_size(int64_t T, int64_t E, int64_t k, size_t *bytes)
  * row, whatever group sizes surround it: two calls give the same bits.  Errors:
  * GFR_ERR_NULL_ARG, GFR_ERR_BAD_DTYPE, GFR_ERR_BAD_RANK, GFR_ERR_BAD_SHAPE,
  * GFR_ERR_BAD_ARG, GFR_ERR_UNSUPPORTED (E outside [1, GFR_MAX_EXPERTS], M > 2^30, K or
- * N > 2^21, more than 2^31 tiles of 64 x 64 results), GFR_ERR_BAD_ALIGNMENT (x, w or out not 16-byte, group_list not 8-byte
- * aligned), GFR_ERR_HIP.
+ * N > 2^21, more than 2^31 tiles of 64 x 64 results), GFR_ERR_BAD_ALIGNMENT (x, w or out
+ * not 16-byte, group_list not 8-byte aligned), GFR_ERR_HIP.
  */
 int gfr_grouped_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *group_list,
                        int group_list_type, int transpose_w, int fill, const gfr_tensor *out,

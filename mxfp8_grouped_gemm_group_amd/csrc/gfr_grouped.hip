@@ -29,10 +29,11 @@ struct Groups {
     int start[GFR_MAX_EXPERTS + 2];
     int units[GFR_MAX_EXPERTS + 2];
     int cost[GFR_MAX_EXPERTS + 1];
-    uint32_t waves[2][4];
+    uint32_t waves[2][16];
 };
 
-// Exclusive prefix sum over a block of 256 threads.
+// Exclusive prefix sum over a block of THREADS threads.
+template <int THREADS>
 __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *waves, uint32_t &total) {
     const int wave = threadIdx.x >> 6;
     const uint32_t upto = wave_prefix(v);
@@ -41,7 +42,7 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *waves, ui
     uint32_t before = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < THREADS / 64; ++w) {
         if (w < wave) before += waves[w];
         total += waves[w];
     }
@@ -50,8 +51,8 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *waves, ui
 }
 
 // Counts below zero or beyond M are clamped into [0, M], and the ranges, one behind
-// another, into [0, M); either is a bad list.  256 threads; ends with a barrier.
-template <int UNIT, class Cost>
+// another, into [0, M); either is a bad list.  256 threads take part; ends with a barrier.
+template <int UNIT, int THREADS, class Cost>
 __device__ __forceinline__ void find_groups(const GroupedParams &p, Groups &s, Cost cost_of) {
     constexpr int kPer = GFR_MAX_EXPERTS / 256;
     const int e0 = threadIdx.x * kPer;
@@ -71,8 +72,10 @@ __device__ __forceinline__ void find_groups(const GroupedParams &p, Groups &s, C
     }
     // (two scans of 16 bits and the rest: 1024 counts of 31 bits do not fit one)
     uint32_t low_total, high_total, total;
-    const uint32_t low = block_prefix(static_cast<uint32_t>(sum & 0xffff), s.waves[0], low_total);
-    const uint32_t high = block_prefix(static_cast<uint32_t>(sum >> 16), s.waves[1], high_total);
+    const uint32_t low =
+        block_prefix<THREADS>(static_cast<uint32_t>(sum & 0xffff), s.waves[0], low_total);
+    const uint32_t high =
+        block_prefix<THREADS>(static_cast<uint32_t>(sum >> 16), s.waves[1], high_total);
     int64_t run = static_cast<int64_t>(low) + (static_cast<int64_t>(high) << 16);
     bad |= static_cast<int64_t>(low_total) + (static_cast<int64_t>(high_total) << 16) > p.M;
     uint32_t n = 0, cost = 0, cost_total;
@@ -87,8 +90,8 @@ __device__ __forceinline__ void find_groups(const GroupedParams &p, Groups &s, C
         n += static_cast<uint32_t>((count[i] + UNIT - 1) / UNIT);
         if (e0 + i < p.E) cost += cost_of(static_cast<int>(count[i]));
     }
-    uint32_t at = block_prefix(n, s.waves[0], total);
-    cost = block_prefix(cost, s.waves[1], cost_total);
+    uint32_t at = block_prefix<THREADS>(n, s.waves[0], total);
+    cost = block_prefix<THREADS>(cost, s.waves[1], cost_total);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         if (e0 + i < p.E) {
@@ -132,12 +135,13 @@ struct Staged {
     static constexpr int kPieces = T / 32;
     const uint16_t *base;      // k-major: the tile's first line; line-major: its first column at k 0
     int64_t ld, elements;      // of a row; from base to the end of what may be read
-    int k_end, lines;
+    int k_end, lines, tid;     // tid: of the 256 threads that take the tile
     u4_t v[D][kPieces];
 
     __device__ __forceinline__ void tile(const uint16_t *base_, int64_t ld_, int64_t elements_,
                                          int k_end_, int lines_) {
         base = base_, ld = ld_, elements = elements_, k_end = k_end_, lines = lines_;
+        tid = threadIdx.x & 255;
     }
     __device__ __forceinline__ void fetch(u4_t (&to)[kPieces], int step) {
         const bool whole = ld % 8 == 0;
@@ -145,10 +149,10 @@ struct Staged {
             const int skew = reinterpret_cast<uintptr_t>(base) & 2;
             const rsrc_t r = buffer(reinterpret_cast<const char *>(base) - skew,
                                     2 * elements + skew);
-            const int piece = threadIdx.x & 7, valid = k_end - 64 * step - 8 * piece;
+            const int piece = tid & 7, valid = k_end - 64 * step - 8 * piece;
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-                const int line = (threadIdx.x >> 3) + 32 * i;
+                const int line = (tid >> 3) + 32 * i;
                 const int off = line * static_cast<int>(2 * ld) + skew + 128 * step + 16 * piece;
                 to[i] = u4_t{0, 0, 0, 0};
                 if (line < lines && valid > 0)
@@ -162,9 +166,9 @@ struct Staged {
             constexpr int kPer = T / 8;
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-                const int k = threadIdx.x / kPer + 256 / kPer * i;
+                const int k = tid / kPer + 256 / kPer * i;
                 const int off =
-                    k * static_cast<int>(2 * ld) + skew + 16 * (threadIdx.x % kPer);
+                    k * static_cast<int>(2 * ld) + skew + 16 * (tid % kPer);
                 to[i] = u4_t{0, 0, 0, 0};
                 if (64 * step + k < k_end) to[i] = eight_of(r, off, whole);
             }
@@ -174,19 +178,24 @@ struct Staged {
         constexpr int kPer = T / 8;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
-            tile[LINE ? piece_line<T>(threadIdx.x / kPer + 256 / kPer * i, threadIdx.x % kPer)
-                      : piece_k((threadIdx.x >> 3) + 32 * i, threadIdx.x & 7)] = from[i];
+            tile[LINE ? piece_line<T>(tid / kPer + 256 / kPer * i, tid % kPer)
+                      : piece_k((tid >> 3) + 32 * i, tid & 7)] = from[i];
     }
 };
 
-// T x T tiles of four waves, D steps' loads in flight in registers.
-template <bool F16, bool WGRAD, bool WLINE, int T>
-__global__ __launch_bounds__(256, 2) void general_kernel(GroupedParams p) {
-    constexpr int D = T == 64 ? 4 : 2, F = T / 64;
+// T x T tiles of G groups of four waves, each with the loads of two of its steps in flight
+// in registers.  The groups take steps in turn and add up what they have in LDS: what
+// bounds a step of few tiles is its loads' latency, and G groups have G steps on their way
+// (512 rows of one expert of 2048 x 1024: 26.0 us with one group, which had four steps in
+// flight, 18.8 with two, 17.2 with four; 64 rows over 8 experts of 4096 x 1024 31.6 and 25.6).
+template <bool F16, bool WGRAD, bool WLINE, int T, int G>
+__global__ __launch_bounds__(G * 256, G == 1 ? 2 : 4) void general_kernel(GroupedParams p) {
+    constexpr int D = 2, F = T / 64;
     __shared__ Groups s;
-    __shared__ u4_t tile[2][2][T * 8];
-    find_groups<T>(p, s, [](int) { return 0u; });
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    __shared__ u4_t tile[G][2][2][T * 8];
+    find_groups<T, G * 256>(p, s, [](int) { return 0u; });
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6 & 3);
+    const int half = G == 1 ? 0 : uniform(threadIdx.x >> 8);
     const int wm = wave / 2 * (T / 2), wn = wave % 2 * (T / 2);
     const int tiles_n = (p.N + T - 1) / T, tiles_k = (p.K + T - 1) / T;
     const int64_t total = WGRAD ? static_cast<int64_t>(p.E) * tiles_k * tiles_n
@@ -224,20 +233,28 @@ __global__ __launch_bounds__(256, 2) void general_kernel(GroupedParams p) {
                        static_cast<int64_t>(min(T, p.N - n0)) * p.K, p.K, min(T, p.N - n0));
         }
         f16_t acc[F][F] = {};
+        // this group's steps: half, half + G, ...
+        const int mine = (steps - half + G - 1) / G, rounds = (steps + G - 1) / G;
 #pragma unroll
         for (int d = 0; d < D; ++d)
-            if (d < steps) a.fetch(a.v[d], d), b.fetch(b.v[d], d);
-        for (int first = 0; first < steps; first += D)
+            if (d < mine) a.fetch(a.v[d], half + G * d), b.fetch(b.v[d], half + G * d);
+        for (int first = 0; first < rounds; first += D)
 #pragma unroll
             for (int d = 0; d < D; ++d) {
-                const int step = first + d;
-                if (step >= steps) break;
-                // (a stage is written again two steps later: behind the barrier between)
-                u4_t(&to)[2][T * 8] = tile[d & 1];
-                a.put(to[0], a.v[d]);
-                b.put(to[1], b.v[d]);
+                const int n = first + d;
+                if (n >= rounds) break;
+                // (a stage is written again two rounds later: behind the barrier between)
+                u4_t(&to)[2][T * 8] = tile[half][d & 1];
+                if (n < mine) {
+                    a.put(to[0], a.v[d]);
+                    b.put(to[1], b.v[d]);
+                }
                 __syncthreads();
-                if (step + D < steps) a.fetch(a.v[d], step + D), b.fetch(b.v[d], step + D);
+                if (n >= mine) continue;
+                if (n + D < mine) {
+                    a.fetch(a.v[d], half + G * (n + D));
+                    b.fetch(b.v[d], half + G * (n + D));
+                }
 #pragma unroll
                 for (int part = 0; part < 4; ++part) {
                     u4_t fa[F], fb[F];
@@ -260,6 +277,7 @@ __global__ __launch_bounds__(256, 2) void general_kernel(GroupedParams p) {
         // places: zeros for 105 empty experts of 676 x 3588 0.7 ms).
         constexpr int W = T / 2, kRow = W / 4;          // a wave's rows and columns; pieces
         f4_t *const slab = reinterpret_cast<f4_t *>(tile) + wave * W * kRow;
+        constexpr int kGroup = 4 * W * kRow;            // pieces of a group's results
 #pragma unroll
         for (int i = 0; i < F; ++i)
 #pragma unroll
@@ -267,20 +285,22 @@ __global__ __launch_bounds__(256, 2) void general_kernel(GroupedParams p) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int m = 32 * i + (lane & 31), piece = 8 * j + 2 * r + (lane >> 5);
-                    slab[m * kRow + (piece ^ (m & (kRow - 1)))] =
+                    slab[half * kGroup + m * kRow + (piece ^ (m & (kRow - 1)))] =
                         f4_t{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2],
                              acc[i][j][4 * r + 3]};
                 }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+        __syncthreads();
         const int64_t row0 = (WGRAD ? static_cast<int64_t>(e) * p.K : 0) + m0 + wm;
         if (p.N % 4 == 0) {
             // four columns a lane
-            for (int k = lane; k < W * kRow; k += 64) {
+            for (int k = lane + 64 * half; k < W * kRow; k += 64 * G) {
                 const int m = k / kRow, n = n0 + wn + 4 * (k % kRow);
                 if (wm + m >= rows || n >= p.N) continue;
                 const int64_t at = (row0 + m) * p.N + n;
-                f4_t y = slab[m * kRow + (k % kRow ^ (m & (kRow - 1)))];
+                const f4_t *from = slab + m * kRow + (k % kRow ^ (m & (kRow - 1)));
+                f4_t y = from[0];
+#pragma unroll
+                for (int g = 1; g < G; ++g) y += from[g * kGroup];
                 if (p.out_f32) {
                     f4_t *to = reinterpret_cast<f4_t *>(static_cast<float *>(p.out) + at);
                     if (p.accumulate) y += *to;
@@ -298,11 +318,14 @@ __global__ __launch_bounds__(256, 2) void general_kernel(GroupedParams p) {
             }
         } else {
             // a column a lane
-            for (int k = lane; k < W * W; k += 64) {
+            for (int k = lane + 64 * half; k < W * W; k += 64 * G) {
                 const int m = k / W, c = k % W, n = n0 + wn + c;
                 if (wm + m >= rows || n >= p.N) continue;
                 const int64_t at = (row0 + m) * p.N + n;
-                float y = slab[m * kRow + (c / 4 ^ (m & (kRow - 1)))][c % 4];
+                const f4_t *from = slab + m * kRow + (c / 4 ^ (m & (kRow - 1)));
+                float y = from[0][c % 4];
+#pragma unroll
+                for (int g = 1; g < G; ++g) y += from[g * kGroup][c % 4];
                 if (p.out_f32) {
                     float *to = static_cast<float *>(p.out) + at;
                     *to = p.accumulate ? *to + y : y;
@@ -617,11 +640,12 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
     Groups &s = *reinterpret_cast<Groups *>(lds + 2 * kStage + kWaves * kSlab / 4);
     // A tile's time: wgrad, its steps and about two more; forward, its rows by the tile
     // shapes there are.
-    find_groups<kTile>(p, s, [](int count) -> uint32_t {
+    find_groups<kTile, kWaves * 64>(p, s, [](int count) -> uint32_t {
         if (WGRAD) return (count + 63) / 64 + 2;
         return 4 * (count / kTile) + (count % kTile + 63) / 64;
     });
-    float *const slab = reinterpret_cast<float *>(lds + 2 * kStage) + uniform(threadIdx.x >> 6) * kSlab;
+    float *const slab =
+        reinterpret_cast<float *>(lds + 2 * kStage) + uniform(threadIdx.x >> 6) * kSlab;
     const GroupedTiles<WGRAD, WLINE> tiles(p, s);
     const GroupedFinish<F16, WGRAD, WLINE> finish{p, slab};
     run_tiles<F16, WGRAD, WLINE>(lds, tiles, finish, p.K, WLINE ? p.N : p.K);
@@ -633,10 +657,10 @@ __global__ __launch_bounds__(kWaves * 64, 1) void direct_kernel(GroupedParams p)
     }
 }
 
-template <bool F16, bool WGRAD, bool WLINE, int T>
+template <bool F16, bool WGRAD, bool WLINE, int T, int G>
 hipError_t launch_general_t(const GroupedParams &p, hipStream_t stream) {
-    hipLaunchKernelGGL((general_kernel<F16, WGRAD, WLINE, T>), dim3(T == 64 ? 1024 : 512),
-                       dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((general_kernel<F16, WGRAD, WLINE, T, G>), dim3(G == 4 ? 256 : 512),
+                       dim3(G * 256), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -652,8 +676,9 @@ template <bool F16, bool WGRAD, bool WLINE>
 hipError_t launch_kernel(const GroupedParams &p, hipStream_t stream) {
     switch (p.kernel) {
     case GroupedKernel::kDirect: return launch_direct<F16, WGRAD, WLINE>(p, stream);
-    case GroupedKernel::k128: return launch_general_t<F16, WGRAD, WLINE, 128>(p, stream);
-    default: return launch_general_t<F16, WGRAD, WLINE, 64>(p, stream);
+    case GroupedKernel::k128: return launch_general_t<F16, WGRAD, WLINE, 128, 1>(p, stream);
+    case GroupedKernel::k64Long: return launch_general_t<F16, WGRAD, WLINE, 64, 4>(p, stream);
+    default: return launch_general_t<F16, WGRAD, WLINE, 64, 2>(p, stream);
     }
 }
 
@@ -668,11 +693,13 @@ hipError_t launch_grouped_t(const GroupedParams &p, hipStream_t stream) {
 
 // The kernel for a size, by estimated time; groups are taken as equal, an expert as
 // having a row if there is one for it.  A block's time per 64-step of the direct kernel
-// by its tile's rows, with the CUs one round after the other; of the general kernel with
-// two blocks to a CU.  (Direct against general, us: 8 rows over 256 experts of 2048 x
-// 1024 23 and 26; 64 over 64 27 and 45; 512 of one 46 and 25; 2048 of one of 4096 x 2048
-// 85 and 100; wgrad of 1024 rows of one of 1024 x 1024 29 and 17, of 2048 rows of one of
-// 4096 x 2048 52 and 59.)
+// by its tile's rows, with the CUs one round after the other; of the general kernel by the
+// tiles a CU has.  Four groups of waves begin later than two and end sooner from 20 steps
+// on, as long as the tiles fill no more than the CUs (16 steps of 256 tiles 13.1 us and
+// 12.5, 32 steps of 512 40.6 and 36.7).  (Direct against general, us: 8 rows over 256
+// experts of 2048 x 1024 24 and 17.6; 64 over 64 27 and 45; 64 over 8 of 4096 x 1024 38.5
+// and 25.6; 512 of one 46 and 17.2; 2048 of one of 4096 x 2048 85 and 100; wgrad of 1024
+// rows of one of 1024 x 1024 29 and 13, of 2048 rows of one of 4096 x 2048 52 and 59.)
 GroupedKernel grouped_kernel(int wgrad, int transpose, int64_t M, int64_t E, int64_t K, int64_t N) {
     const auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
     const auto most = [](double a, double b) { return a > b ? a : b; };
@@ -682,14 +709,23 @@ GroupedKernel grouped_kernel(int wgrad, int transpose, int64_t M, int64_t E, int
                      : static_cast<double>(experts * up(rows, t)) * static_cast<double>(up(N, t));
     };
     const double steps = static_cast<double>(up(wgrad ? rows : K, 64));
-    const GroupedKernel general = tiles(128) < 512 ? GroupedKernel::k64 : GroupedKernel::k128;
+    const bool by_groups = tiles(64) <= 256.0 && steps >= 20.0;
+    const GroupedKernel general = by_groups            ? GroupedKernel::k64Long
+                                  : tiles(128) < 512.0 ? GroupedKernel::k64
+                                                       : GroupedKernel::k128;
     // rows of whole pieces, of every operand that is loaded
     if (K % 8 != 0 || (N % 8 != 0 && (wgrad || !transpose))) return general;
     const double rounds = static_cast<double>(static_cast<int64_t>(tiles(256) / 256.0 + 0.999));
-    const double step = wgrad || rows > 192 ? 1.2 : rows > 128 ? 1.0 : rows > 64 ? 0.8 : rows > 32 ? 0.56 : 0.47;
+    const double step = wgrad || rows > 192 ? 1.2
+                        : rows > 128        ? 1.0
+                        : rows > 64         ? 0.8
+                        : rows > 32         ? 0.56
+                                            : 0.47;
     const double direct = 8.0 + rounds * (steps * step + (wgrad ? 3.0 : 0.0));
-    const double fill = tiles(64) / 512.0;
-    const double other = 5.0 + most(1.0, fill) * (steps * (fill > 1.0 ? 0.75 : 0.65) + wgrad);
+    const double fill = most(1.0, tiles(64) / 256.0);
+    const double step64 = general == GroupedKernel::k64 ? 0.46 : 0.375;
+    const double other = by_groups ? 8.9 + steps * 0.26
+                                   : 5.0 + fill * (steps * step64 + (wgrad ? 0.5 : 0.0));
     return direct <= other ? GroupedKernel::kDirect : general;
 }
 

@@ -96,7 +96,7 @@ hipError_t launch_route(const RouteParams &p, hipStream_t stream);
 
 // The kernel for a size of the 16-bit grouped products: whole rows of pieces straight to
 // LDS, or the general one by its tile.
-enum class GroupedKernel : int32_t { kDirect, k128, k64 };
+enum class GroupedKernel : int32_t { kDirect, k128, k64, k64Long };
 GroupedKernel grouped_kernel(int wgrad, int transpose, int64_t M, int64_t E, int64_t K, int64_t N);
 
 struct GroupedParams {

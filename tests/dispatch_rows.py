@@ -22,8 +22,8 @@ def lora(M, N, K, r):
     return bool(f(M, N, K, r).tiles)
 
 
-def grouped(M, E, K, N, wgrad=False, transpose=False):
-    """"direct", "128" or "64"."""
+def grouped(M, E, K, N, wgrad=False, transpose=False, long=False):
+    """"direct", "128" or "64" (`long`: "64 long" for its form of four groups of waves)."""
     f = gfr.load_library()._ZN3gfr14grouped_kernelEiillll
     f.restype, f.argtypes = ctypes.c_int32, [ctypes.c_int] * 2 + [ctypes.c_int64] * 4
-    return ("direct", "128", "64")[f(int(wgrad), int(transpose), M, E, K, N)]
+    return ("direct", "128", "64", "64 long" if long else "64")[f(int(wgrad), int(transpose), M, E, K, N)]

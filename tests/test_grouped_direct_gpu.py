@@ -12,7 +12,8 @@ from tests.test_grouped_linear_gpu import BF, DEV, F32, HF, NAN, check, dev, gro
 # each of their ends.
 RESTS = [300, 520, 700, 33, 65, 0, 97, 161, 225, 1, 32, 64, 129, 193, 256]
 # (counts, K, N): steps that end early, columns that do, few rows of a long sum
-FORWARD = [([5, 0, 40, 64, 1], 4104, 264), ([1], 5000, 1032), ([100, 128, 0, 90], 392, 8200),
+FEW = [([5, 0, 40, 64, 1], 4104, 264), ([1], 5000, 1032)]      # (the general kernel's)
+FORWARD = [([5, 0, 40, 64, 1], 4104, 8200), ([1], 5000, 40008), ([100, 128, 0, 90], 392, 8200),
            (RESTS, 136, 4104), (RESTS, 200, 2568), ([2000], 1096, 2056), ([7] * 200, 72, 1032),
            ([3, 0] * 300, 1000, 264)]
 WGRAD = [(RESTS, 520, 4104), (RESTS, 1032, 1544), ([5, 0, 40, 64, 1] * 4, 1000, 648),
@@ -39,7 +40,7 @@ def test_the_other_kernels_are_taken_too():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("counts, K, N", FORWARD)
+@pytest.mark.parametrize("counts, K, N", FEW + FORWARD)
 @pytest.mark.parametrize("transpose", [False, True])
 def test_forward(counts, K, N, transpose):
     check(counts, K, N, BF, transpose, ops="f")
@@ -66,6 +67,65 @@ def test_general_tiles_of_128():
     check([5000, 0, 3000, 8384], 131, 1032, BF, True, ops="f")
     check([1000, 0, 1000, 1], 1097, 2056, BF, False, ops="w")
     check([2001], 2056, 4107, HF, True, out_dtype=None, ops="w")
+
+
+# Long sums of few tiles: steps that do not share out evenly among four groups of waves,
+# rows that begin anywhere, more tiles than CUs (groups of one row), groups without steps.
+LONG = [([5, 0, 40, 64, 1], 1281, 99), ([70], 2051, 515), ([1, 0, 3], 1344, 64),
+        ([1] * 39 + [2521], 1288, 384), ([300, 7], 5000, 1032)]
+LONG_WGRAD = [([1300, 0, 1, 4000], 130, 259), ([4097], 72, 1032), ([9, 1281, 2600], 64, 64),
+              ([30, 0] * 8 + [8000, 9000, 12000], 136, 200)]
+
+
+def test_long_sums_of_few_tiles_take_four_groups():
+    for counts, K, N in LONG + FEW:
+        for t in (False, True):
+            assert dispatch_rows.grouped(sum(counts), len(counts), K, N, False, t,
+                                         long=True) == "64 long"
+    for counts, K, N in LONG_WGRAD:
+        assert dispatch_rows.grouped(sum(counts), len(counts), K, N, True, long=True) == "64 long"
+    # the same steps of more tiles; fewer steps
+    assert dispatch_rows.grouped(1024, 2, 2048, 2048, long=True) == "64"
+    assert dispatch_rows.grouped(1024, 1, 1024, 1024, long=True) == "64"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts, K, N", LONG)
+@pytest.mark.parametrize("transpose", [False, True])
+def test_long_sums(counts, K, N, transpose):
+    check(counts, K, N, BF, transpose, ops="f")
+    check(counts, K, N, HF, transpose, out_dtype=None, kind=0, rest=70, ops="f")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts, K, N", LONG_WGRAD)
+@pytest.mark.parametrize("transpose", [False, True])
+def test_long_sums_of_wgrad(counts, K, N, transpose):
+    check(counts, K, N, BF, transpose, ops="w")
+    check(counts, K, N, HF, transpose, out_dtype=None, kind=0, rest=70, ops="w")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_long_sums_add_up_keep_their_bits_and_their_place(dtype):
+    counts, K, N = [1300, 0, 1, 4000], 130, 259
+    M = sum(counts) + 5
+    x, w, dy = gi.integers(counts, M, K, N, BF, False)
+    want = gi.wgrad(x, dy, gi.ranges(counts, 1, M), False)
+    old = torch.randint(-100, 100, want.shape).to(dtype)
+    buf = torch.full((want.numel() + 128,), -5.0, dtype=dtype, device=DEV)
+    out = buf[64:64 + want.numel()].view(want.shape)
+    out.copy_(old)
+    gfr.grouped_linear_wgrad(*dev(x, dy), groups(counts, 1), 1, out=out, accumulate=True)
+    same(out, (old.double() + want).to(dtype), "accumulate")
+    assert (buf[:64] == -5).all() and (buf[64 + want.numel():] == -5).all()
+    x = torch.randn(300, 2051, device=DEV).bfloat16()
+    w = torch.randn(3, 2051, 515, device=DEV).bfloat16()
+    call = lambda c: gfr.grouped_linear(x, w, groups(c, 1), 1, out_dtype=dtype)
+    one, two, three = call([100] * 3), call([100] * 3), call([30, 170, 100])
+    assert torch.equal(one, two)
+    for a, b in [(0, 30), (100, 300)]:
+        assert torch.equal(one[a:b], three[a:b])
 
 
 @pytest.mark.gpu
