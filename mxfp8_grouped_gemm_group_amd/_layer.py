@@ -362,9 +362,9 @@ class _GroupedLinear(torch.autograd.Function):
         away = _elsewhere(x.get_device(), None)
         with away if away is not None else contextlib.nullcontext():
             dx = dw = None
-            if ctx.needs_input_grad[0]:
-                dx = _grouped(dy, w, group_list, group_list_type, not transpose_w, x.dtype, None,
-                              None)
+            if ctx.needs_input_grad[0]:      # (no columns: a product has to sum over some)
+                dx = torch.zeros_like(x) if dy.shape[1] == 0 else _grouped(
+                    dy, w, group_list, group_list_type, not transpose_w, x.dtype, None, None)
             if ctx.needs_input_grad[1]:
                 dw = _wgrad(x, dy, group_list, group_list_type, transpose_w, w.dtype, None, False,
                             None)

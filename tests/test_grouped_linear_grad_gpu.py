@@ -145,3 +145,18 @@ def test_training_step_under_graph(K, N):
         assert torch.equal(dx.cpu(), gi.forward(dy, w, rng, True).bfloat16())
         assert torch.equal(dw.cpu(), gi.wgrad(x, dy, rng, False).bfloat16())
         torch.randn(256, 256, device=DEV).relu_()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("M, N", [(0, 24), (5, 0), (0, 0)])
+def test_gradients_without_rows_or_columns(M, N, transpose):
+    x = torch.ones(M, 16, dtype=torch.bfloat16, device="cuda:0", requires_grad=True)
+    w = torch.ones(2, *((N, 16) if transpose else (16, N)), dtype=torch.bfloat16, device="cuda:0",
+                   requires_grad=True)
+    counts = torch.tensor([M, 0], device="cuda:0")
+    y = gfr.grouped_linear(x, w, counts, 1, transpose_w=transpose)
+    assert y.shape == (M, N)
+    y.backward(torch.ones_like(y))
+    assert x.grad.shape == x.shape and not x.grad.any()
+    assert w.grad.shape == w.shape and not w.grad.any()
