@@ -133,7 +133,7 @@ __device__ __forceinline__ int expert_of(const Groups &s, int E, int u) {
 template <bool LINE, int T, int D>
 struct Staged {
     static constexpr int kPieces = T / 32;
-    const uint16_t *base;      // k-major: the tile's first line; line-major: its first column at k 0
+    const uint16_t *base;      // k-major: the tile's first line; else its first column at k 0
     int64_t ld, elements;      // of a row; from base to the end of what may be read
     int k_end, lines, tid;     // tid: of the 256 threads that take the tile
     u4_t v[D][kPieces];
@@ -369,7 +369,9 @@ enum Store { kF32, kF32Add, k16, k16Add, kElements };
 template <bool F16, int STORE>
 __device__ __forceinline__ void put_block(const GroupedParams &p, float *slab, const f16_t &v,
                                           int64_t row, int rows, int n0, int lane) {
-    const int shift = STORE == kF32 || STORE == kF32Add ? 2 : STORE == kElements ? p.out_f32 + 1 : 1;
+    const int shift = STORE == kF32 || STORE == kF32Add ? 2
+                      : STORE == kElements              ? p.out_f32 + 1
+                                                        : 1;
     const int row_bytes = p.N << shift, g = lane >> 5;
     char *const out = static_cast<char *>(p.out) + row * row_bytes;
     // (a buffer over the rows: what is behind the last one is not written)
