@@ -19,9 +19,13 @@ using Int = std::integral_constant<int, N>;
 
 // 16 bytes a lane from memory straight to LDS, 1024 consecutive bytes from `lds` on.
 // (Assembly, because behind the builtin the compiler waits for all of them ahead of
-// every later LDS read.  It writes no register; direct_wait is its wait.)
+// every later LDS read.  It writes no register but m0, which the compiler keeps for single
+// instructions and does not take as a clobber; direct_wait is its wait.  A vector access has
+// to be five wait states behind a vector instruction that wrote a scalar register it reads,
+// which the compiler does not see to in here: the buffer's size and `off` come by
+// v_readfirstlane, or by v_readlane where they were spilled.)
 __device__ __forceinline__ void load_lds(rsrc_t r, int lane_off, int off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :: "s"(lds), "v"(lane_off), "s"(r), "s"(off) : "memory");
 }
 // All but this wave's N latest loads and stores are through; then the same of the
