@@ -128,9 +128,9 @@ struct LoraParams {
     const uint16_t *residual;  // [M, N] or null
     void *out;                 // [M, N]
     int32_t *status;           // may be null
-    float *inner;              // workspace, ranks not in fours: [M][r], scaled
+    float *inner;              // workspace, few rows: [M][r], scaled
     float *dense;              // workspace: [M][N]; few rows: or the K splits' sums
-    uint16_t *terms;           // workspace, ranks in fours: [M][2][r], scaled
+    uint16_t *terms;           // workspace, many rows: [M][2][r], scaled
     int32_t *codes;            // workspace, many rows: [M / 32], the adapter of 32 rows
     LinearChoice choice;
     int32_t tiles;             // many rows

@@ -52,16 +52,6 @@ __device__ __forceinline__ void put_terms(const LoraParams &p, int64_t t, int ra
         pack2<F16>(fabsf(first) == INFINITY ? 0.0f : v - first, 0.0f));
 }
 
-// a.x b.x + a.y b.y + c
-template <bool F16>
-__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
-    if (F16)
-        return __builtin_amdgcn_fdot2(__builtin_bit_cast(h2_t, a), __builtin_bit_cast(h2_t, b), c,
-                                      false);
-    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf2_t, a),
-                                           __builtin_bit_cast(bf2_t, b), c, false);
-}
-
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
@@ -114,10 +104,7 @@ __global__ __launch_bounds__(256) void shrink_rows_kernel(LoraParams p, int wave
 #pragma unroll
     for (int q = 0; q < R; ++q) {
         const float v = wave_sum(sum[q]) * scale;
-        if (lane == 0 && j0 + q < p.r) {
-            if (p.r % 4 == 0) put_terms<F16>(p, t, j0 + q, v);
-            else p.inner[static_cast<int64_t>(t) * p.r + j0 + q] = v;
-        }
+        if (lane == 0 && j0 + q < p.r) p.inner[static_cast<int64_t>(t) * p.r + j0 + q] = v;
     }
 }
 
@@ -132,13 +119,11 @@ __device__ __forceinline__ float dense_sum(const LoraParams &p, int t, int n, fl
 }
 
 // A thread per column, a block's rows in turn; B's row of a column stays in registers
-// while the adapter does (up to 64 ranks).  Ranks in fours (V: 16 or 8 bytes of B at a
-// time) are summed in pairs with inner's two terms, which are the same in all lanes and
-// come through scalar loads (one rank at a time, B unpacked: 512 rows of 4096 by rank 64
-// 58 us); other ranks one by one with inner in FP32.
+// while the adapter does (up to 64 ranks; V of them come at a time).  inner, in FP32, is the
+// same in all lanes and comes through scalar loads.
 template <bool F16, int V>
 __global__ __launch_bounds__(256) void expand_rows_kernel(LoraParams p, int rows) {
-    typedef const __attribute__((address_space(4))) uint32_t *scalar_t;
+    typedef const __attribute__((address_space(4))) float *scalar_t;
     const int n = blockIdx.x * 256 + threadIdx.x, at_n = min(n, p.N - 1);
     const int t0 = blockIdx.y * rows, t1 = min(t0 + rows, p.M);
     const float bias = p.bias ? element(p.bias, at_n, p.bias_f32, F16) : 0.0f;
@@ -150,9 +135,9 @@ __global__ __launch_bounds__(256) void expand_rows_kernel(LoraParams p, int rows
         const uint16_t *row = p.b + (static_cast<int64_t>(max(i, 0)) * p.N + at_n) * p.r;
         const uint16_t res = p.residual ? p.residual[at] : 0;
         float y = dense_sum<F16>(p, t, at_n, bias);
+        const scalar_t s = (scalar_t)(p.inner + static_cast<int64_t>(t) * p.r);
+        float sum = 0.0f;
         if (i >= 0 && V > 1) {
-            const scalar_t s = (scalar_t)(p.terms + static_cast<int64_t>(t) * 2 * p.r);
-            float sum = 0.0f;
             for (int k0 = 0; k0 < p.r; k0 += 64) {
                 const int ranks = min(64, p.r - k0);
                 if (i != kept || p.r > 64)
@@ -173,16 +158,12 @@ __global__ __launch_bounds__(256) void expand_rows_kernel(LoraParams p, int rows
                 for (int j = 0; j < 64; j += V)
                     if (j < ranks)
 #pragma unroll
-                        for (int e = j / 2; e < (j + V) / 2; ++e) {
-                            sum = dot2<F16>(b[e], s[k0 / 2 + e], sum);
-                            sum = dot2<F16>(b[e], s[(p.r + k0) / 2 + e], sum);
-                        }
+                        for (int e = j; e < j + V; ++e)
+                            sum = fmaf(s[k0 + e], unpack1<F16>(b[e / 2] >> (16 * (e & 1))), sum);
             }
             kept = i;
             y += sum;
         } else if (i >= 0) {
-            const float *s = p.inner + static_cast<int64_t>(t) * p.r;
-            float sum = 0.0f;
 #pragma unroll 8
             for (int j = 0; j < p.r; ++j) sum = fmaf(s[j], unpack1<F16>(row[j]), sum);
             y += sum;
@@ -286,8 +267,10 @@ __global__ __launch_bounds__(kShrinkWaves * 64, 2) void shrink_tile_kernel(LoraP
             float v = 0.0f;
 #pragma unroll
             for (int w = 0; w < kShrinkWaves; ++w) v += part[w][row][j];
-            if (row < rows && j0 + j < p.r && adapter(p, t0 + row) == i)
-                put_terms<F16>(p, t0 + row, j0 + j, v * scale);
+            if (row < rows && j0 + j < p.r && adapter(p, t0 + row) == i) {
+                if (p.tiles) put_terms<F16>(p, t0 + row, j0 + j, v * scale);
+                else p.inner[static_cast<int64_t>(t0 + row) * p.r + j0 + j] = v * scale;
+            }
         }
         __syncthreads();
     }

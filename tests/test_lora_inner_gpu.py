@@ -1,0 +1,92 @@
+"""lora_linear keeps its inner row in 32 bits: integer inputs whose inner values need up to
+21 bits (and lie beyond F16's range), while every sum stays exact in FP32; infinities in
+lora_b as the definition has them, whatever the rank."""
+import pytest
+import torch
+
+from tests.test_lora_linear_gpu import BF, F32, HF, call, definition, ids_of, integers, same
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+FEW = [(5, 136, 264), (64, 72, 520), (300, 264, 136), (331, 67, 133)]
+MANY = [(4300, 2056, 136)]
+
+
+def wide(M, N, K, L, r, dtype, mix):
+    """CPU arguments: |inner| up to about 2^20, each column of an adapter's B with two
+    non-zeros."""
+    g = torch.Generator().manual_seed(M + 31 * N + K + r)
+
+    def signed(low, high, *s):
+        return torch.randint(low, high + 1, s, generator=g) * \
+            (2 * torch.randint(0, 2, s, generator=g) - 1)
+
+    a = integers(M, N, K, L, r, dtype, mix=mix)
+    a["x"] = signed(64, 127, M, K).to(dtype)
+    low = signed(128, 255, L, r, K)
+    low[..., 128:] = 0
+    a["a"] = low.to(dtype)
+    b = torch.zeros(L, N, r)
+    b.scatter_(2, torch.randint(0, r, (L, N, 2), generator=g), signed(1, 1, L, N, 2).float())
+    a["b"] = b.to(dtype)
+    a["scaling"][:] = 1
+    return a
+
+
+def inner_of(a):
+    """All adapters' inner rows in 64 bits, and the most that a sum of the call can reach."""
+    x, low = a["x"].double(), a["a"].double()
+    inner = torch.einsum("mk,lrk->lmr", x, low)
+    most = max((torch.einsum("mk,lrk->lmr", x.abs(), low.abs())).max().item(),
+               torch.bmm(inner.abs(), a["b"].double().abs().transpose(1, 2)).max().item())
+    return inner, most + (x.abs() @ a["w"].double().abs().T).max().item()
+
+
+def check(M, N, K, L, r, dtype, mix):
+    print(M, N, K, L, r, dtype, mix, flush=True)
+    a = wide(M, N, K, L, r, dtype, mix)
+    inner, most = inner_of(a)
+    # (sums of halves and quarters of them are exact too)
+    assert most < 2 ** 22
+    high = inner.to(BF).double()
+    lost = high + (inner - high).to(BF).double() != inner
+    assert lost.double().mean() > 0.03 and inner.abs().max() > 65504
+    same(call(a, out_dtype=F32), definition(a))
+    same(call(a, out_dtype=BF if dtype == BF else F32), definition(a))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("mix", ["one", "runs", "gaps"])
+@pytest.mark.parametrize("r", [3, 4, 16, 24, 65, 72, 256])
+@pytest.mark.parametrize("M, N, K", FEW)
+def test_few_rows_keep_the_inner_row(M, N, K, r, mix, dtype):
+    check(M, N, K, 5, r, dtype, mix)
+
+
+@pytest.mark.parametrize("M, N, K, r", [(4400, 72, 1032, 128), (3000, 75, 2056, 20)])
+def test_a_shrink_by_tiles_keeps_the_inner_row(M, N, K, r):
+    assert 2 * M * r * K > 2e8
+    check(M, N, K, 5, r, BF, "runs")
+    check(M, N, K, 5, r, HF, "gaps")
+
+
+def infinities(M, N, K, r, dtype):
+    """One infinity of either sign in an adapter's B, and inner values of every kind
+    beside it: large, of few bits, zero."""
+    a = integers(M, N, K, 4, r, dtype, mix="random")
+    a["ids"][:4] = torch.tensor([0, 1, 2, 3], dtype=torch.int32)
+    for i, bad in ((1, INF), (2, -INF)):
+        b = {**a, "b": a["b"].clone()}
+        b["b"][i, N - 1, r - 1] = bad
+        b["b"][i, 2, 0] = bad
+        want = definition(b)
+        assert want.isinf().any()
+        same(call(b, out_dtype=F32), want, f"{r} {bad}")
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("r", [5, 8, 12, 16, 72])
+@pytest.mark.parametrize("M, N, K", FEW)
+def test_infinities_in_b(M, N, K, r, dtype):
+    infinities(M, N, K, r, dtype)
