@@ -599,11 +599,10 @@ int gfr_grouped_linear_wgrad(const gfr_tensor *x, const gfr_tensor *dy,
  *               + sum_j inner[m, j] * lora_b[i, n, j] + residual[m, n]
  *   inner[m, j] = scaling[i] * sum_k x[m, k] * lora_a[i, j, k]     i = adapter_ids[m]
  *
- * accumulated in FP32, rounded once to out's type; inner keeps at least 16 bits of
- * mantissa (with F16, down to 2^-25).  Rows of any order and mix of adapters; what a
- * row gets depends on its own adapter alone, whatever the others' hold.  An infinity in
- * x, w, lora_a or scaling comes out as the sums have it; one in lora_b may come out NaN,
- * for inner is kept as two terms, of which one can be zero or of the other sign.
+ * accumulated in FP32, inner too, rounded once to out's type.  Rows of any order and mix of
+ * adapters; what a row gets depends on its own adapter alone, whatever the others' hold.
+ * Infinities come out as the sums have them (one in lora_b beside an inner value below
+ * 2^-110, which is as good as 0, may come out NaN).
  *
  *  x            BF16 or F16 [M, K].
  *  w            x's dtype [N, K].
@@ -622,11 +621,9 @@ int gfr_grouped_linear_wgrad(const gfr_tensor *x, const gfr_tensor *dy,
  *
  * Any M, N >= 0 and K >= 1 (K and r multiples of 8 are the fast path).  M = 0 or N = 0
  * is a no-op.  The sizes fix the summation order: two calls give the same bits.  Calls
- * that overlap in time need workspaces of their own.  With F16, inner and its products
- * are to stay within F16's range, as an F16 layer's own intermediate row.  Errors as
- * gfr_linear, and GFR_ERR_UNSUPPORTED for r outside [1, GFR_MAX_RANK], L outside
- * [1, 2^20], M > 2^26 or M r > 2^27; lora_a, lora_b 16-byte, adapter_ids and scaling
- * 4-byte aligned.
+ * that overlap in time need workspaces of their own.  Errors as gfr_linear, and
+ * GFR_ERR_UNSUPPORTED for r outside [1, GFR_MAX_RANK], L outside [1, 2^20], M > 2^26 or
+ * M r > 2^27; lora_a, lora_b 16-byte, adapter_ids and scaling 4-byte aligned.
  */
 int gfr_lora_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *bias,
                     const gfr_tensor *residual, const gfr_tensor *lora_a,

@@ -57,6 +57,7 @@ struct Direct {
     int piece_k;                   // k-major: first k of the lane's piece
     int K, off, loads;             // loads: those that hold any line of the tile
     int turn;                      // k-major: the step of K that comes first
+    int thrice;                    // k-major: pieces of a row whose pairs come three times
 
     // Rows of `ld` elements.  Load i takes the tile's rows from (WAVES i + wave) kRows on.
     __device__ __forceinline__ void init(int64_t ld, int wave, int lane) {
@@ -75,8 +76,9 @@ struct Direct {
     // The tile whose first line begins at `from` (line-major: at k = 0), with `bytes_`
     // from there to the end of what may be read (0: no tile) and K_ to sum over.
     __device__ __forceinline__ void tile(const uint16_t *from, int64_t bytes_, int K_, int lines,
-                                         int turn_ = 0) {
+                                         int turn_ = 0, int thrice_ = 0) {
         turn = turn_;
+        thrice = thrice_;
         base = reinterpret_cast<const char *>(from);
         bytes = bytes_;
         K = K_;
@@ -84,7 +86,8 @@ struct Direct {
         loads = LINE ? kLoads : uniform((lines + 8 * WAVES - 1) / (8 * WAVES));
         if (!LINE) r = uniform_buffer(base, bytes);
     }
-    // Ahead of a step's loads.
+    // Ahead of a step's loads (THRICE: of tiles that may have it; up to 96 pieces in all).
+    template <bool THRICE>
     __device__ __forceinline__ void at(int step) {
         if (LINE) {
             const int64_t gone = static_cast<int64_t>(step) * 64 * row_bytes;
@@ -94,7 +97,14 @@ struct Direct {
             step += turn;
             if (64 * step >= K && turn > 0) step -= (K + 63) / 64;
             off = first + 128 * step;
-            now = 64 * step + piece_k < K ? offs : kPast;
+            now = offs;
+            if (THRICE && thrice > 0) {
+                const int p = 8 * step + (piece_k >> 3), pair = p * 43 >> 8;       // p / 6
+                const int second = 2 * pair + 1 < thrice ? p - 6 * pair & 1 : 0;
+                off = first;
+                now += 16 * (2 * pair + second) - 2 * piece_k;
+            }
+            if (64 * step + piece_k >= K) now = kPast;
         }
     }
     __device__ __forceinline__ void load(int i, uint32_t tile, int wave) const {
@@ -163,7 +173,7 @@ struct TileAt {
 // db, wave, lane), the operands of the next run of steps and their number, 0 behind the
 // last tile.  Finish: tile<FM, FN>(t, acc, wm, wn, lane) takes a
 // wave's results (32 FM x 32 FN of them from wm, wn on) and returns how many stores it
-// has issued at least; clear(t) a tile without a sum.
+// has issued at least (kLong: it needs many registers); clear(t) a tile without a sum.
 template <bool F16, bool ALINE, bool BLINE, class Tiles, class Finish>
 __device__ __forceinline__ void run_tiles(u4_t *lds, const Tiles &tiles, const Finish &finish,
                                           int64_t lda, int64_t ldb) {
@@ -202,8 +212,8 @@ __device__ __forceinline__ void run_tiles(u4_t *lds, const Tiles &tiles, const F
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         next_loads();
-        da.at(load_step);
-        db.at(load_step);
+        da.template at<false>(load_step);
+        db.template at<Tiles::kExtra>(load_step);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) load(j, i);
     }
@@ -258,8 +268,8 @@ __device__ __forceinline__ void run_tiles(u4_t *lds, const Tiles &tiles, const F
             run_part(masked, mask, Int<0>{}, Int<kGets>{}, Int<3>{}, now, Int<0>{}, Int<0>{}, 0);
             lds_wait();
             next_loads();
-            da.at(load_step);
-            db.at(load_step);
+            da.template at<false>(load_step);
+            db.template at<Tiles::kExtra>(load_step);
             run_part(masked, mask, Int<1>{}, Int<0>{}, Int<0>{}, 0, Int<0>{}, Int<kFirst>{}, now);
             // (the last tile's results may still be on their way)
             if (stores < 16) direct_wait<kFirst>();
@@ -284,7 +294,7 @@ __device__ __forceinline__ void run_tiles(u4_t *lds, const Tiles &tiles, const F
         // (what a long finish needs registers for is not taken from the loop's sums, of which
         // one went to memory and back every step; a short one is better off without: 8192
         // rows over 64 experts of 2048 x 1536 145 us with it, 132 without)
-        if (Tiles::kExtra && FM * FN == 16)
+        if (Finish::kLong && FM * FN == 16)
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll

@@ -587,6 +587,7 @@ struct GroupedTiles {
 
 template <bool F16, bool WGRAD, bool WLINE>
 struct GroupedFinish {
+    static constexpr bool kLong = false;
     const GroupedParams &p;
     float *slab;
 

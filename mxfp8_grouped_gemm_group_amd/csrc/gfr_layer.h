@@ -128,9 +128,10 @@ struct LoraParams {
     const uint16_t *residual;  // [M, N] or null
     void *out;                 // [M, N]
     int32_t *status;           // may be null
-    float *inner;              // workspace, few rows: [M][r], scaled
-    float *dense;              // workspace: [M][N]; few rows: or the K splits' sums
-    uint16_t *terms;           // workspace, many rows: [M][2][r], scaled
+    float *inner;              // workspace, few rows or F16: [M][r], scaled
+    float *dense;              // workspace, many rows: [M / 32][N / 32] of 32 x 32 sums as
+                               // lanes have them; few rows: [M][N], or the K splits' sums
+    uint16_t *terms;           // workspace, many rows of bf16: [M][3][r], scaled
     int32_t *codes;            // workspace, many rows: [M / 32], the adapter of 32 rows
     LinearChoice choice;
     int32_t tiles;             // many rows

@@ -7,9 +7,12 @@
 //
 // Few rows: shrink, the dense product into FP32 (gfr_linear's kernels), expand.  Many:
 // shrink on the matrix cores; the dense tiles, of which 32 rows with one adapter between
-// them take its expansion as a few steps more of their sum; and for the 32 rows that have
-// several, whose sums were kept in FP32, a launch that adds each row its own, so that what
-// another request's adapter holds (NaN too) reaches nobody else.
+// them take its expansion as a few steps more of their sum (bf16: inner as three terms); and
+// for the 32 rows that have several, whose sums were kept in FP32, a launch that adds each
+// row its own, so that what another request's adapter holds (NaN too) reaches nobody else.
+// With F16 that launch expands all rows, on the FP32 matrix instructions: F16 terms do not
+// have inner's range (4096 rows of 4096 x 7168 by rank 64: tiles 236 us and it 76, in bf16
+// 250 and 15; by rank 16 221 and 33).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -39,17 +42,25 @@ __device__ __forceinline__ void check_adapter(const LoraParams &p, int t) {
     if (p.status && (i < -1 || i >= p.L)) atomicOr(p.status, GFR_DEV_BAD_ADAPTER);
 }
 
-// inner as two 16-bit terms: the value rounded, and what that left over (16 bits of
-// mantissa or more; nothing of an infinity), the ranks' first terms ahead of their second
-// ones.
-template <bool F16>
+// inner as three bf16 terms whose sum it is: of 16 ranks (or the last 8) the smallest terms,
+// then the middle ones, then the largest, which so join in FP32 without loss.  All have its
+// sign, and none is zero unless it is: their products with an infinity of B, and those of an
+// infinite inner, are what the one product would be.  (A bf16 value goes as its half and two
+// quarters.)
 __device__ __forceinline__ void put_terms(const LoraParams &p, int64_t t, int rank, float v) {
-    uint16_t *to = p.terms + t * 2 * p.r + rank;
-    const uint16_t hi = static_cast<uint16_t>(pack2<F16>(v, 0.0f));
-    to[0] = hi;
-    const float first = unpack1<F16>(hi);
-    to[p.r] = static_cast<uint16_t>(
-        pack2<F16>(fabsf(first) == INFINITY ? 0.0f : v - first, 0.0f));
+    const auto cut = [](float f) { return __uint_as_float(__float_as_uint(f) & 0xffff0000u); };
+    float first = cut(v);
+    const float rest = v - first;                        // up to 16 bits
+    float second = cut(rest), third = rest - second;     // up to 8
+    if (rest == 0.0f) first = 0.5f * v, second = third = 0.25f * v;
+    else if (third == 0.0f) second = third = 0.5f * rest;
+    // (a NaN may have all its payload below)
+    if (!(fabsf(v) < INFINITY)) first = second = third = v != v ? NAN : v;
+    const int group = rank & ~15, width = group + 16 <= p.r ? 16 : 8;
+    uint16_t *to = p.terms + t * 3 * p.r + 3 * group + (rank - group);
+    to[0] = static_cast<uint16_t>(__float_as_uint(third) >> 16);
+    to[width] = static_cast<uint16_t>(__float_as_uint(second) >> 16);
+    to[2 * width] = static_cast<uint16_t>(__float_as_uint(first) >> 16);
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -186,8 +197,9 @@ __global__ __launch_bounds__(256) void expand_rows_kernel(LoraParams p, int rows
 // whole lines (fragments loaded from memory took 32 half lines a load: 4096 rows of 4096
 // by rank 64 51 us, so 18).
 //
-// codes[row / 32]: the adapter of 32 rows, -1 for none, kSeveral.
-constexpr int kSeveral = -2;
+// codes[row / 32]: the adapter of 32 rows, -1 for none, kApart where the dense tiles leave
+// the expansion to a launch of its own: of several adapters, and with F16 of any.
+constexpr int kApart = -2;
 constexpr int kShrinkWaves = 8;
 constexpr int kShrinkLds = kShrinkWaves * 2 * 64 * 8 * 16;
 template <bool F16>
@@ -217,7 +229,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64, 2) void shrink_tile_kernel(LoraP
     const int first_id = uniform(id);
     if (blockIdx.y == 0 && wave == 0) {
         const bool same = __builtin_amdgcn_ballot_w64(c < rows && id != first_id) == 0;
-        if (lane == 0) p.codes[blockIdx.x] = same ? id : kSeveral;
+        if (lane == 0) p.codes[blockIdx.x] = same && (!F16 || id < 0) ? id : kApart;
     }
     uint64_t todo = __builtin_amdgcn_ballot_w64(id >= 0);
     while (todo) {
@@ -268,7 +280,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64, 2) void shrink_tile_kernel(LoraP
 #pragma unroll
             for (int w = 0; w < kShrinkWaves; ++w) v += part[w][row][j];
             if (row < rows && j0 + j < p.r && adapter(p, t0 + row) == i) {
-                if (p.tiles) put_terms<F16>(p, t0 + row, j0 + j, v * scale);
+                if (!F16 && p.tiles) put_terms(p, t0 + row, j0 + j, v * scale);
                 else p.inner[static_cast<int64_t>(t0 + row) * p.r + j0 + j] = v * scale;
             }
         }
@@ -277,16 +289,17 @@ __global__ __launch_bounds__(kShrinkWaves * 64, 2) void shrink_tile_kernel(LoraP
 }
 
 // The dense product's tiles: bands of eight by all columns, an eighth of them per XCD.  A
-// tile begins with the expansions of its fragments' adapters, each a sum over the ranks of
-// the value's first term, then of its second.
+// tile of bf16 begins with the expansions of its fragments' adapters, each one run of steps
+// over inner's terms, B's ranks three times.
+template <bool F16>
 struct LoraTiles {
-    static constexpr bool kExtra = true;
-    int tiles_m, tiles_n, begin, end, stride, rank_steps;
+    static constexpr bool kExtra = !F16;
+    int tiles_m, tiles_n, begin, end, stride;
     Divisor by_band;
 
     __device__ __forceinline__ explicit LoraTiles(const LoraParams &p)
         : tiles_m((p.M + kTile - 1) / kTile), tiles_n((p.N + kTile - 1) / kTile),
-          rank_steps((p.r + 63) / 64), by_band(8 * tiles_n) {
+          by_band(8 * tiles_n) {
         const int total = tiles_m * tiles_n, per = (total + 7) / 8, xcd = blockIdx.x & 7;
         stride = gridDim.x >> 3;
         begin = xcd * per + (blockIdx.x >> 3);
@@ -302,12 +315,14 @@ struct LoraTiles {
         t.n0 = uniform(column * kTile);
         t.m0 = uniform((band * 8 + in_band - column * depth) * kTile);
         t.rows = uniform(min(kTile, p.M - t.m0));
+        t.extra = 0;
+        t.masks = 0;
+        t.steps = (p.K + 63) / 64;
+        if (F16) return t;
         const int fragments = (t.rows + 31) / 32;
         const int code = p.codes[t.m0 / 32 + min(lane, fragments - 1)];
         uint64_t todo = __builtin_amdgcn_ballot_w64((lane < fragments) & (code >= 0));
-        t.extra = 0;
-        t.extra_run = 2 * rank_steps;
-        t.masks = 0;
+        t.extra_run = (3 * p.r + 63) / 64;
         while (todo) {
             const int a = __builtin_amdgcn_readlane(code, __builtin_ctzll(todo));
             const uint64_t mine = todo & __builtin_amdgcn_ballot_w64(code == a);
@@ -316,80 +331,152 @@ struct LoraTiles {
             t.extra += t.extra_run;
         }
         t.extra = uniform(t.extra);
-        t.steps = t.extra + (p.K + 63) / 64;
+        t.steps += t.extra;
         return t;
     }
-    // The loads' tile, and in it which of an adapter's terms come next (masks: the
-    // adapters left).
+    // The loads' tile, whose dense steps are still to come, and the adapters left in it
+    // (masks).
     struct Cursor {
-        int id, term;
+        int id;
+        bool open;
         TileAt t;
-        __device__ __forceinline__ explicit Cursor(int first) : id(first), term(-1) {}
+        __device__ __forceinline__ explicit Cursor(int first) : id(first), open(false) {}
     };
     template <class A, class B>
     __device__ __forceinline__ int next(Cursor &c, A &da, B &db, int wave, int lane) const {
         const LoraParams p = fresh<LoraParams>();
-        if (c.term < 0) {                       // a new tile
+        if (!c.open) {
             c.id = uniform(c.id + stride);
             if (c.id >= uniform(end)) return 0;
             c.t = at(c.id);
-            c.term = 0;
+            c.open = true;
         }
         const int64_t columns = min(kTile, p.N - c.t.n0);
-        if (c.t.masks != 0) {
+        if (!F16 && c.t.masks != 0) {
             const int64_t r = p.r;
             const int a = uniform(p.codes[c.t.m0 / 32 + __builtin_ctzll(c.t.masks & 0xff)]);
-            da.init(2 * r, wave, lane);
+            da.init(3 * r, wave, lane);
             db.init(r, wave, lane);
-            // (the second term's rows end with the buffer; the first's, a term ahead)
-            da.tile(p.terms + c.t.m0 * 2 * r + c.term * r, 2 * (c.t.rows * 2 - c.term) * r, p.r,
-                    c.t.rows);
-            db.tile(p.b + (a * int64_t{p.N} + c.t.n0) * r, 2 * columns * r, p.r, 0);
-            if (++c.term == 2) c.term = 0, c.t.masks >>= 8;
-            return rank_steps;
+            da.tile(p.terms + c.t.m0 * 3 * r, 2 * c.t.rows * 3 * r, 3 * p.r, c.t.rows);
+            db.tile(p.b + (a * int64_t{p.N} + c.t.n0) * r, 2 * columns * r, 3 * p.r, 0, 0, p.r / 8);
+            c.t.masks >>= 8;
+            return c.t.extra_run;
         }
         const int64_t k = p.K;
         da.init(k, wave, lane);
         db.init(k, wave, lane);
         da.tile(p.x + c.t.m0 * k, 2 * c.t.rows * k, p.K, c.t.rows);
         db.tile(p.w + c.t.n0 * k, 2 * columns * k, p.K, 0);
-        c.term = -1;
+        c.open = false;
         return (p.K + 63) / 64;
     }
 };
 
+// The 32 x 32 sums of which FP32 memory holds a copy, in the order that lanes have them: at
+// fragment (row / 32, column / 32), four sums of all lanes after another.
+__device__ __forceinline__ rsrc_t apart(const LoraParams &p, int row, int n) {
+    const int64_t fragment = row / 32 * static_cast<int64_t>((p.N + 31) / 32) + n / 32;
+    return uniform_buffer(reinterpret_cast<char *>(p.dense + 1024 * fragment), 4096);
+}
+
+// A lane's places in 32 rows of 32 columns from n0 on: lane (c, g) has columns n0 + 16 q +
+// 8 g .. + 7 of row c once it has traded halves with its row's other lane.
+struct Columns {
+    int n0, g;
+    __device__ __forceinline__ int of(int q) const { return n0 + 16 * q + 8 * g; }
+};
+
+__device__ __forceinline__ rsrc_t residual_rows(const LoraParams &p, int64_t row, int rows) {
+    return uniform_buffer(reinterpret_cast<const char *>(p.residual + (p.residual ? row * p.N : 0)),
+                          p.residual ? static_cast<int64_t>(rows) * p.N * 2 : 0);
+}
+__device__ __forceinline__ rsrc_t bias_row(const LoraParams &p) {
+    return uniform_buffer(static_cast<const char *>(p.bias),
+                          p.bias ? static_cast<int64_t>(p.N) * (p.bias_f32 ? 4 : 2) : 0);
+}
+
+// 32 x 32 sums with their bias (16-bit: `bias`) and residual (`res`), rounded and written to
+// `rows` rows from `row` on: a lane trades halves for eight columns, and 16-bit results once
+// more, for runs of 64 bytes.  Two stores or more.
+template <bool F16>
+__device__ __forceinline__ void put_sums(const LoraParams &p, const f16_t &acc, int64_t row,
+                                         int rows, Columns at, rsrc_t from_bias,
+                                         const u4_t (&bias)[2], const u4_t (&res)[2], int lane) {
+    const int c = lane & 31, es = p.out_f32 ? 4 : 2;
+    const rsrc_t to = uniform_buffer(static_cast<char *>(p.out) + row * p.N * es,
+                                     static_cast<int64_t>(rows) * p.N * es);
+    u4_t h[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int n = at.of(q);
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[8 * q + e]),
+                                                            __float_as_uint(acc[8 * q + 4 + e]),
+                                                            false, false);
+            y[e] = __uint_as_float(w[0]);
+            y[4 + e] = __uint_as_float(w[1]);
+        }
+        if (p.bias_f32) {
+            const f4_t b0 = __builtin_bit_cast(f4_t, load16<0>(from_bias, 4 * n, 0));
+            const f4_t b1 = __builtin_bit_cast(f4_t, load16<0>(from_bias, 4 * n, 16));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] += b0[e], y[4 + e] += b1[e];
+        } else if (p.bias) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] += unpack1<F16>(bias[q][e >> 1] >> (16 * (e & 1)));
+        }
+        if (p.residual)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] += unpack1<F16>(res[q][e >> 1] >> (16 * (e & 1)));
+        if (p.out_f32) {
+            const int off = n < p.N ? 4 * (c * p.N + n) : kPast;
+            store16(to, __builtin_bit_cast(u4_t, f4_t{y[0], y[1], y[2], y[3]}), off);
+            store16(to, __builtin_bit_cast(u4_t, f4_t{y[4], y[5], y[6], y[7]}), off + 16);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[q][e] = pack2<F16>(y[2 * e], y[2 * e + 1]);
+    }
+    if (p.out_f32) return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const auto w = __builtin_amdgcn_permlane16_swap(h[0][e], h[1][e], false, false);
+        h[0][e] = w[0];
+        h[1][e] = w[1];
+    }
+    const int n = at.n0 + 16 * (lane >> 4 & 1) + 8 * at.g;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        store16(to, h[q], n < p.N ? 2 * (((lane & 15) + 16 * q) * p.N + n) : kPast);
+}
+
 template <bool F16>
 struct LoraFinish {
+    static constexpr bool kLong = true;
     template <int FM, int FN>
     __device__ __forceinline__ int tile(const TileAt &t, f16_t (&acc)[FM][FN], int wm, int wn,
                                         int lane) const {
         if (t.rows <= wm) return 0;
         const LoraParams p = fresh<LoraParams>();
-        // A lane has four columns of row lane % 32 at a time; it trades halves with its
-        // row's other lane for eight, and 16-bit results once more, for runs of 64 bytes.
-        const int c = lane & 31, g = lane >> 5, es = p.out_f32 ? 4 : 2;
-        const int bias_es = p.bias_f32 ? 4 : 2;
-        const rsrc_t from_bias = uniform_buffer(static_cast<const char *>(p.bias),
-                                                p.bias ? static_cast<int64_t>(p.N) * bias_es : 0);
-        auto column = [&](int j, int q) { return t.n0 + wn + 32 * j + 16 * q + 8 * g; };
+        const int c = lane & 31, g = lane >> 5;
+        const rsrc_t from_bias = bias_row(p);
+        auto columns = [&](int j) { return Columns{t.n0 + wn + 32 * j, g}; };
         u4_t bias[FN][2], res[2][FN][2];
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-                bias[j][q] = load16<0>(from_bias, p.bias_f32 ? kPast : 2 * column(j, q), 0);
+                bias[j][q] = load16<0>(from_bias, p.bias_f32 ? kPast : 2 * columns(j).of(q), 0);
         // (a block of 32 rows ahead of its use)
         auto fetch = [&](int i) GFR_INLINE {
-            const int64_t row = t.m0 + wm + 32 * i;
-            const int rows = max(0, min(32, t.rows - wm - 32 * i));
-            const rsrc_t from = uniform_buffer(
-                reinterpret_cast<const char *>(p.residual + (p.residual ? row * p.N : 0)),
-                p.residual ? static_cast<int64_t>(rows) * p.N * 2 : 0);
+            const rsrc_t from = residual_rows(p, t.m0 + wm + 32 * i,
+                                              max(0, min(32, t.rows - wm - 32 * i)));
 #pragma unroll
             for (int j = 0; j < FN; ++j)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const int n = column(j, q);
+                    const int n = columns(j).of(q);
                     res[i & 1][j][q] = load16<0>(from, n < p.N ? 2 * (c * p.N + n) : kPast, 0);
                 }
         };
@@ -398,80 +485,25 @@ struct LoraFinish {
         const int codes = p.codes[(t.m0 + wm) / 32 + min(lane, (t.rows - wm - 1) / 32)];
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
-            const int64_t row = t.m0 + wm + 32 * i;
-            const int rows = max(0, min(32, t.rows - wm - 32 * i));
+            const int row = t.m0 + wm + 32 * i, rows = max(0, min(32, t.rows - wm - 32 * i));
             if (i + 1 < FM) fetch(i + 1);
             __builtin_amdgcn_sched_barrier(0);
-            if (__builtin_amdgcn_readlane(codes, i) == kSeveral) {
-                const rsrc_t to =
-                    uniform_buffer(reinterpret_cast<char *>(p.dense + row * p.N),
-                                   static_cast<int64_t>(rows) * p.N * 4);
+            const bool later = __builtin_amdgcn_readlane(codes, i) == kApart;
 #pragma unroll
-                for (int j = 0; j < FN; ++j)
+            for (int j = 0; j < FN; ++j) {
+                const int n0 = columns(j).n0;
+                if (later) {
+                    const rsrc_t to = apart(p, row, n0);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const int n = t.n0 + wn + 32 * j + 8 * q + 4 * g;
                         const f4_t y = {acc[i][j][4 * q], acc[i][j][4 * q + 1],
                                         acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
                         store16(to, __builtin_bit_cast(u4_t, y),
-                                n < p.N ? 4 * (c * p.N + n) : kPast);
+                                rows > 0 && n0 < p.N ? 1024 * q + 16 * lane : kPast);
                     }
-                continue;
-            }
-            const rsrc_t to =
-                uniform_buffer(static_cast<char *>(p.out) + row * p.N * es,
-                               static_cast<int64_t>(rows) * p.N * es);
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                u4_t h[2];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int n = column(j, q);
-                    float y[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const auto w = __builtin_amdgcn_permlane32_swap(
-                            __float_as_uint(acc[i][j][8 * q + e]),
-                            __float_as_uint(acc[i][j][8 * q + 4 + e]), false, false);
-                        y[e] = __uint_as_float(w[0]);
-                        y[4 + e] = __uint_as_float(w[1]);
-                    }
-                    if (p.bias_f32) {
-                        const f4_t b0 = __builtin_bit_cast(f4_t, load16<0>(from_bias, 4 * n, 0));
-                        const f4_t b1 = __builtin_bit_cast(f4_t, load16<0>(from_bias, 4 * n, 16));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) y[e] += b0[e], y[4 + e] += b1[e];
-                    } else if (p.bias) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            y[e] += unpack1<F16>(bias[j][q][e >> 1] >> (16 * (e & 1)));
-                    }
-                    if (p.residual)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            y[e] += unpack1<F16>(res[i & 1][j][q][e >> 1] >> (16 * (e & 1)));
-                    if (p.out_f32) {
-                        const int off = n < p.N ? 4 * (c * p.N + n) : kPast;
-                        store16(to, __builtin_bit_cast(u4_t, f4_t{y[0], y[1], y[2], y[3]}), off);
-                        store16(to, __builtin_bit_cast(u4_t, f4_t{y[4], y[5], y[6], y[7]}),
-                                off + 16);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) h[q][e] = pack2<F16>(y[2 * e], y[2 * e + 1]);
-                }
-                if (!p.out_f32) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const auto w =
-                            __builtin_amdgcn_permlane16_swap(h[0][e], h[1][e], false, false);
-                        h[0][e] = w[0];
-                        h[1][e] = w[1];
-                    }
-                    const int n = t.n0 + wn + 32 * j + 16 * (lane >> 4 & 1) + 8 * g;
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        store16(to, h[q],
-                                n < p.N ? 2 * (((lane & 15) + 16 * q) * p.N + n) : kPast);
+                } else {
+                    put_sums<F16>(p, acc[i][j], row, rows, columns(j), from_bias, bias[j],
+                                  res[i & 1][j], lane);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -481,83 +513,102 @@ struct LoraFinish {
     __device__ __forceinline__ void clear(const TileAt &) const {}
 };
 
-// 32 rows with several adapters, 32 columns a wave: each adapter's product apart, added to
-// its own rows' sums.
+// The 32 rows left to it, 32 columns a wave: each adapter's product apart, added to its own
+// rows' sums; the ranks in the dense tiles' order.  With F16 the products are in FP32.
 template <bool F16>
 __global__ __launch_bounds__(256) void expand_tile_kernel(LoraParams p) {
-    if (p.codes[blockIdx.y] != kSeveral) return;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int c = lane & 31, g = lane >> 5, t0 = blockIdx.y * 32;
-    const int64_t n0 = blockIdx.x * 128 + wave * 32;
-    if (n0 >= p.N) return;
-    const int rows = min(32, p.M - t0), s_row = 4 * p.r, b_row = 2 * p.r;
+    const int n0 = blockIdx.x * 128 + wave * 32;
+    const int rows = min(32, p.M - t0), b_row = 2 * p.r, s_row = F16 ? 4 * p.r : 6 * p.r;
     const int id = c < rows ? adapter(p, t0 + c) : -1;
-    const int64_t row0 = static_cast<int64_t>(t0) * p.N;
-    const rsrc_t from = uniform_buffer(reinterpret_cast<const char *>(p.dense + row0),
-                                       static_cast<int64_t>(rows) * p.N * 4);
-    const rsrc_t sr = uniform_buffer(
-        reinterpret_cast<const char *>(p.terms + static_cast<int64_t>(t0) * 2 * p.r),
-        static_cast<int64_t>(rows) * s_row);
-    f4_t sum[4];
+    if (p.codes[blockIdx.y] != kApart || n0 >= p.N) return;
+    const rsrc_t from = apart(p, t0, n0), from_bias = bias_row(p);
+    const rsrc_t from_res = residual_rows(p, t0, rows);
+    const Columns columns{n0, g};
+    f16_t sum;
+    u4_t bias[2], res[2];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const int n = static_cast<int>(n0) + 8 * q + 4 * g;
-        sum[q] = __builtin_bit_cast(f4_t, load16<0>(from, n < p.N ? 4 * (c * p.N + n) : kPast, 0));
+        const f4_t v = __builtin_bit_cast(f4_t, load16<0>(from, 1024 * q + 16 * lane, 0));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[4 * q + e] = v[e];
     }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int n = columns.of(q);
+        bias[q] = load16<0>(from_bias, p.bias_f32 ? kPast : 2 * n, 0);
+        res[q] = load16<0>(from_res, n < p.N ? 2 * (c * p.N + n) : kPast, 0);
+    }
+    const rsrc_t sr = uniform_buffer((F16 ? reinterpret_cast<const char *>(p.inner)
+                                          : reinterpret_cast<const char *>(p.terms)) +
+                                         static_cast<int64_t>(t0) * s_row,
+                                     static_cast<int64_t>(rows) * s_row);
+    // Ranks [64 i, 64 i + 64) in groups of 16: lane (c, g) has ranks 8 g .. + 7 of each, of B's
+    // column c and of inner's row c (bf16: of its three terms; of the last 8 ranks alone the
+    // terms are side by side).
+    struct Ranks {
+        u4_t b[4], s[4][F16 ? 2 : 3];
+    };
+    const auto fetch = [&](rsrc_t br, int i, Ranks &v) GFR_INLINE {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int k0 = 64 * i + 16 * q;
+            if (k0 >= p.r) break;
+            const int width = k0 + 16 <= p.r ? 16 : 8, k = k0 + (8 * g & width - 1);
+            const bool live = !F16 || 8 * g < width;
+            v.b[q] = load16<0>(br, live ? c * b_row + 2 * k : kPast, 0);
+#pragma unroll
+            for (int j = 0; j < (F16 ? 2 : 3); ++j) {
+                const int at = F16 ? 4 * (k + 4 * j) : 2 * (3 * k0 + 16 * j + 8 * g);
+                v.s[q][j] = load16<0>(
+                    sr, F16 ? (live ? c * s_row + at : kPast)
+                            : (16 * j + 8 * g < 3 * width ? c * s_row + at : kPast), 0);
+            }
+        }
+    };
     uint64_t todo = __builtin_amdgcn_ballot_w64(id >= 0);
     while (todo) {
         const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
         const bool mine = id == a;
         todo &= ~__builtin_amdgcn_ballot_w64(mine);
-        const rsrc_t br =
-            uniform_buffer(reinterpret_cast<const char *>(p.b + (a * int64_t{p.N} + n0) * p.r),
-                           (p.N - n0) * b_row);
+        const rsrc_t br = uniform_buffer(
+            reinterpret_cast<const char *>(p.b + (a * int64_t{p.N} + n0) * p.r),
+            static_cast<int64_t>(p.N - n0) * b_row);
         f16_t own = {};
-        for (int k0 = 0; k0 < p.r; k0 += 64) {
-            u4_t b[4], s[4][2];
+        for (int i = 0; 64 * i < p.r; ++i) {
+            Ranks v;
+            fetch(br, i, v);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int k = k0 + 16 * q + 8 * g;
-                const int off = k < p.r ? c * s_row + 2 * k : kPast;
-                b[q] = load16<0>(br, k < p.r ? c * b_row + 2 * k : kPast, 0);
-                s[q][0] = load16<0>(sr, off, 0);
-                s[q][1] = load16<0>(sr, off, b_row);
+                if (64 * i + 16 * q >= p.r) break;
+                if (F16)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        own = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                            unpack1<F16>(v.b[q][e >> 1] >> (16 * (e & 1))),
+                            __uint_as_float(v.s[q][e >> 2][e & 3]), own, 0, 0, 0);
+                else
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) {
+                        // (8 ranks alone: 16 terms, then 8)
+                        const bool alone = 64 * i + 16 * q + 16 > p.r;
+                        if (alone && j == 2) break;
+                        const u4_t b = alone && j == 1 && g == 1 ? u4_t{0, 0, 0, 0} : v.b[q];
+                        own = mfma32<F16>(b, v.s[q][j], own);
+                    }
             }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) own = mfma32<F16>(b[q], s[q][h], own);
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sum[e >> 2][e & 3] += mine ? own[e] : 0.0f;
+        for (int e = 0; e < 16; ++e) sum[e] += mine ? own[e] : 0.0f;
     }
-    if (c >= rows) return;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int n = static_cast<int>(n0) + 8 * q + 4 * g;
-        if (n >= p.N) continue;                     // (N is a multiple of 8)
-        const int64_t at = row0 + static_cast<int64_t>(c) * p.N + n;
-        f4_t y = sum[q];
-        if (p.bias)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] += element(p.bias, n + e, p.bias_f32, F16);
-        if (p.residual) {
-            const u2_t h = load<u2_t>(p.residual + at);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] += unpack1<F16>(h[e >> 1] >> (16 * (e & 1)));
-        }
-        if (p.out_f32)
-            *reinterpret_cast<f4_t *>(static_cast<float *>(p.out) + at) = y;
-        else
-            *reinterpret_cast<u2_t *>(static_cast<uint16_t *>(p.out) + at) =
-                u2_t{pack2<F16>(y[0], y[1]), pack2<F16>(y[2], y[3])};
-    }
+    put_sums<F16>(p, sum, t0, rows, columns, from_bias, bias, res, lane);
 }
 
 template <bool F16>
 __global__ __launch_bounds__(kWaves * 64, 1) void lora_tile_kernel(LoraParams p) {
     extern __shared__ u4_t lds[];     // [2][x's 256 rows, w's][8]
-    const LoraTiles tiles(p);
+    const LoraTiles<F16> tiles(p);
     const LoraFinish<F16> finish{};
     run_tiles<F16, false, false>(lds, tiles, finish, p.K, p.K);
 }
@@ -650,9 +701,9 @@ LoraLayout lora_layout(int64_t M, int64_t N, int64_t K, int64_t r) {
     l.tiles = K % 8 == 0 && N % 8 == 0 && r % 8 == 0 && M <= 32 * 65535 && N <= 1 << 21 &&
               ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile) >= 128;
     if (l.tiles) {
-        l.codes = up(2 * sizeof(uint16_t) * M * r);
+        l.codes = up(3 * sizeof(uint16_t) * M * r);       // (or M r floats)
         l.dense = l.codes + up(sizeof(int32_t) * ((M + 31) / 32));
-        l.total = l.dense + up(sizeof(float) * M * N);
+        l.total = l.dense + up(sizeof(float) * 1024 * ((M + 31) / 32) * ((N + 31) / 32));
         return l;
     }
     l.choice = linear_choice(M, N, K, GFR_ACT_NONE);

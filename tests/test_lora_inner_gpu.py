@@ -4,6 +4,7 @@ lora_b as the definition has them, whatever the rank."""
 import pytest
 import torch
 
+from tests import dispatch_rows
 from tests.test_lora_linear_gpu import BF, F32, HF, call, definition, ids_of, integers, same
 
 pytestmark = pytest.mark.gpu
@@ -39,7 +40,7 @@ def inner_of(a):
     x, low = a["x"].double(), a["a"].double()
     inner = torch.einsum("mk,lrk->lmr", x, low)
     most = max((torch.einsum("mk,lrk->lmr", x.abs(), low.abs())).max().item(),
-               torch.bmm(inner.abs(), a["b"].double().abs().transpose(1, 2)).max().item())
+               2 * inner.abs().max().item())
     return inner, most + (x.abs() @ a["w"].double().abs().T).max().item()
 
 
@@ -71,10 +72,19 @@ def test_a_shrink_by_tiles_keeps_the_inner_row(M, N, K, r):
     check(M, N, K, 5, r, HF, "gaps")
 
 
-def infinities(M, N, K, r, dtype):
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("mix", ["one", "runs", "gaps"])
+@pytest.mark.parametrize("r", [8, 16, 72, 256])
+@pytest.mark.parametrize("M, N, K", MANY)
+def test_whole_tiles_keep_the_inner_row(M, N, K, r, mix, dtype):
+    assert dispatch_rows.lora(M, N, K, r)
+    check(M, N, K, 3, r, dtype, mix)
+
+
+def infinities(M, N, K, r, dtype, mix="random"):
     """One infinity of either sign in an adapter's B, and inner values of every kind
     beside it: large, of few bits, zero."""
-    a = integers(M, N, K, 4, r, dtype, mix="random")
+    a = integers(M, N, K, 4, r, dtype, mix=mix)
     a["ids"][:4] = torch.tensor([0, 1, 2, 3], dtype=torch.int32)
     for i, bad in ((1, INF), (2, -INF)):
         b = {**a, "b": a["b"].clone()}
@@ -90,3 +100,33 @@ def infinities(M, N, K, r, dtype):
 @pytest.mark.parametrize("M, N, K", FEW)
 def test_infinities_in_b(M, N, K, r, dtype):
     infinities(M, N, K, r, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("r", [8, 72])
+@pytest.mark.parametrize("mix", ["random", "runs"])
+@pytest.mark.parametrize("M, N, K", MANY)
+def test_infinities_in_b_of_whole_tiles(M, N, K, mix, r, dtype):
+    infinities(M, N, K, r, dtype, mix)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("mix", ["one", "random"])
+def test_whole_tiles_of_all_kinds_of_inner_values(mix, dtype):
+    """A rank's inner value of 24 bits or few, of either sign, large, small or zero: its
+    product with a power of two of B is exact."""
+    M, N, K = MANY[0]
+    a = integers(M, N, K, 3, 8, dtype, mix=mix)
+    a["x"] = torch.zeros(M, K).to(dtype)
+    a["w"][:, 0] = 0
+    a["a"], a["b"] = torch.zeros(3, 8, K).to(dtype), torch.zeros(3, N, 8).to(dtype)
+    power = torch.arange(M) % 26 - 12                      # 2^-12 .. 2^13, of either sign
+    a["x"][:, 0] = (2.0 ** power * torch.where(torch.arange(M) % 2 == 0, 1, -1)).to(dtype)
+    a["b"][:, :, 3] = (2.0 ** (torch.arange(N) % 20 - 8)).to(dtype)
+    for scale in (1.0, 1.0 + 2.0 ** -23, 2.0 ** 60, 2.0 ** -60, 0.0):
+        a["scaling"][:] = scale
+        factors = [1.0, 2.0, 0.125] if scale % 2.0 ** -20 else [1.0, 3.0, 255.0]
+        a["a"][:, 3, 0] = torch.tensor(factors).to(dtype)
+        want = definition(a)
+        assert torch.equal(want.float().double(), want)
+        same(call(a, out_dtype=F32), want, str(scale))
