@@ -620,8 +620,9 @@ int gfr_grouped_linear_wgrad(const gfr_tensor *x, const gfr_tensor *dy,
  *               status_dev; the other fields are ignored.
  *
  * Any M, N >= 0 and K >= 1 (K and r multiples of 8 are the fast path).  M = 0 or N = 0
- * is a no-op.  The sizes fix the summation order: two calls give the same bits.  Calls
- * that overlap in time need workspaces of their own.  Errors as gfr_linear, and
+ * is a no-op.  The sizes fix the summation order: two calls give the same bits, and a row
+ * its own whatever its neighbours' ids.  Calls that overlap in time need workspaces of
+ * their own.  Errors as gfr_linear, and
  * GFR_ERR_UNSUPPORTED for r outside [1, GFR_MAX_RANK], L outside [1, 2^20], M > 2^26 or
  * M r > 2^27; lora_a, lora_b 16-byte, adapter_ids and scaling 4-byte aligned.
  */

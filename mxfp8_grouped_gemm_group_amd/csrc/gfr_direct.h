@@ -144,7 +144,7 @@ constexpr int kStage = 2 * kTile * 8;       // pieces: an operand's 256 lines, t
 // A tile: `rows` rows from m0 on, columns from n0 on, of the group e's product; steps of
 // the summed index.
 //
-// Tiles of a kernel with kExtra begin with `extra` steps whose products only some of the
+// Tiles of a kernel with kExtra end with `extra` steps whose products only some of the
 // 32-row fragments take: byte i of `masks` says which ones take the i-th run of
 // `extra_run` steps.
 struct TileAt {
@@ -282,15 +282,15 @@ __device__ __forceinline__ void run_tiles(u4_t *lds, const Tiles &tiles, const F
                      Int<kLoads>{}, now);
             now ^= 1;
         };
-        int step = 0;
+        const int all = Tiles::kExtra ? t.steps - t.extra : t.steps;
+        for (int step = 0; step < all; ++step) run_step(Int<0>{}, 0);
         if (Tiles::kExtra) {
             uint64_t masks = t.masks;
-            for (int run = 0; step < t.extra; ++step) {
+            for (int step = 0, run = 0; step < t.extra; ++step) {
                 run_step(Int<1>{}, static_cast<int>(masks & 0xff) >> (wm / 32));
                 if (++run == t.extra_run) run = 0, masks >>= 8;
             }
         }
-        for (; step < t.steps; ++step) run_step(Int<0>{}, 0);
         // (what a long finish needs registers for is not taken from the loop's sums, of which
         // one went to memory and back every step; a short one is better off without: 8192
         // rows over 64 experts of 2048 x 1536 145 us with it, 132 without)

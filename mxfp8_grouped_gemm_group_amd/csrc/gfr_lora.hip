@@ -8,8 +8,8 @@
 // Few rows: shrink, the dense product into FP32 (gfr_linear's kernels), expand.  Many:
 // shrink on the matrix cores; the dense tiles, of which 32 rows with one adapter between
 // them take its expansion as a few steps more of their sum (bf16: inner as three terms); and
-// for the 32 rows that have several, whose sums were kept in FP32, a launch that adds each
-// row its own, so that what another request's adapter holds (NaN too) reaches nobody else.
+// for the 32 rows that have several, whose sums were kept in FP32, a launch that goes on with
+// each row's own, so that what another request's adapter holds (NaN too) reaches nobody else.
 // With F16 that launch expands all rows, on the FP32 matrix instructions: F16 terms do not
 // have inner's range (4096 rows of 4096 x 7168 by rank 64: tiles 236 us and it 76, in bf16
 // 250 and 15; by rank 16 221 and 33).
@@ -289,7 +289,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64, 2) void shrink_tile_kernel(LoraP
 }
 
 // The dense product's tiles: bands of eight by all columns, an eighth of them per XCD.  A
-// tile of bf16 begins with the expansions of its fragments' adapters, each one run of steps
+// tile of bf16 ends with the expansions of its fragments' adapters, each one run of steps
 // over inner's terms, B's ranks three times.
 template <bool F16>
 struct LoraTiles {
@@ -334,26 +334,17 @@ struct LoraTiles {
         t.steps += t.extra;
         return t;
     }
-    // The loads' tile, whose dense steps are still to come, and the adapters left in it
-    // (masks).
+    // The loads' tile and the adapters left in it (masks).
     struct Cursor {
         int id;
-        bool open;
         TileAt t;
-        __device__ __forceinline__ explicit Cursor(int first) : id(first), open(false) {}
+        __device__ __forceinline__ explicit Cursor(int first) : id(first) { t.masks = 0; }
     };
     template <class A, class B>
     __device__ __forceinline__ int next(Cursor &c, A &da, B &db, int wave, int lane) const {
         const LoraParams p = fresh<LoraParams>();
-        if (!c.open) {
-            c.id = uniform(c.id + stride);
-            if (c.id >= uniform(end)) return 0;
-            c.t = at(c.id);
-            c.open = true;
-        }
-        const int64_t columns = min(kTile, p.N - c.t.n0);
         if (!F16 && c.t.masks != 0) {
-            const int64_t r = p.r;
+            const int64_t r = p.r, columns = min(kTile, p.N - c.t.n0);
             const int a = uniform(p.codes[c.t.m0 / 32 + __builtin_ctzll(c.t.masks & 0xff)]);
             da.init(3 * r, wave, lane);
             db.init(r, wave, lane);
@@ -362,12 +353,14 @@ struct LoraTiles {
             c.t.masks >>= 8;
             return c.t.extra_run;
         }
-        const int64_t k = p.K;
+        c.id = uniform(c.id + stride);
+        if (c.id >= uniform(end)) return 0;
+        c.t = at(c.id);
+        const int64_t k = p.K, columns = min(kTile, p.N - c.t.n0);
         da.init(k, wave, lane);
         db.init(k, wave, lane);
         da.tile(p.x + c.t.m0 * k, 2 * c.t.rows * k, p.K, c.t.rows);
         db.tile(p.w + c.t.n0 * k, 2 * columns * k, p.K, 0);
-        c.open = false;
         return (p.K + 63) / 64;
     }
 };
@@ -513,8 +506,9 @@ struct LoraFinish {
     __device__ __forceinline__ void clear(const TileAt &) const {}
 };
 
-// The 32 rows left to it, 32 columns a wave: each adapter's product apart, added to its own
-// rows' sums; the ranks in the dense tiles' order.  With F16 the products are in FP32.
+// The 32 rows left to it, 32 columns a wave: each adapter's product goes on from all rows'
+// dense sums and is kept by its own, the ranks in the dense tiles' order, so that a row gets
+// the same bits there and here.  With F16 the products are in FP32.
 template <bool F16>
 __global__ __launch_bounds__(256) void expand_tile_kernel(LoraParams p) {
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -575,7 +569,7 @@ __global__ __launch_bounds__(256) void expand_tile_kernel(LoraParams p) {
         const rsrc_t br = uniform_buffer(
             reinterpret_cast<const char *>(p.b + (a * int64_t{p.N} + n0) * p.r),
             static_cast<int64_t>(p.N - n0) * b_row);
-        f16_t own = {};
+        f16_t own = sum;
         for (int i = 0; 64 * i < p.r; ++i) {
             Ranks v;
             fetch(br, i, v);
@@ -600,7 +594,7 @@ __global__ __launch_bounds__(256) void expand_tile_kernel(LoraParams p) {
             }
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sum[e] += mine ? own[e] : 0.0f;
+        for (int e = 0; e < 16; ++e) sum[e] = mine ? own[e] : sum[e];
     }
     put_sums<F16>(p, sum, t0, rows, columns, from_bias, bias, res, lane);
 }

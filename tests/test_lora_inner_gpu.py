@@ -1,6 +1,6 @@
 """lora_linear keeps its inner row in 32 bits: integer inputs whose inner values need up to
 21 bits (and lie beyond F16's range), while every sum stays exact in FP32; infinities in
-lora_b as the definition has them, whatever the rank."""
+lora_b as the definition has them, whatever the rank; a row's bits are its own."""
 import pytest
 import torch
 
@@ -130,3 +130,24 @@ def test_whole_tiles_of_all_kinds_of_inner_values(mix, dtype):
         want = definition(a)
         assert torch.equal(want.float().double(), want)
         same(call(a, out_dtype=F32), want, str(scale))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("r", [8, 16, 40, 64, 200])
+@pytest.mark.parametrize("M, N, K", [(40, 136, 264), (300, 264, 520), *MANY])
+def test_a_row_keeps_its_bits_whatever_its_neighbours_ids(M, N, K, r, dtype):
+    """One id changes in blocks of one adapter, another's in blocks of none."""
+    g = torch.Generator().manual_seed(r + M)
+    f = lambda *s: torch.randn(*s, generator=g)
+    ids = torch.arange(M, dtype=torch.int32) // 128 % 4 - 1
+    a = dict(x=f(M, K).to(dtype), w=(f(N, K) / K ** 0.5).to(dtype),
+             a=(f(3, r, K) / K ** 0.5).to(dtype), b=f(3, N, r).to(dtype), ids=ids,
+             scaling=0.5 + f(3).abs(), bias=f(N).to(dtype), residual=f(M, N).to(dtype))
+    other = ids.clone()
+    other[5::64] = (other[5::64] + 2) % 3
+    same_id = other == ids
+    assert 0 < (~same_id).sum() <= M / 32
+    one, two = (call({**a, "ids": i}, out_dtype=F32) for i in (ids, other))
+    torch.cuda.synchronize()
+    assert torch.equal(one.cpu()[same_id], two.cpu()[same_id])
+    assert not torch.equal(one, two)
