@@ -359,6 +359,8 @@ class _GroupedLinear(torch.autograd.Function):
         group_list_type, transpose_w = ctx.args
         # (an FP32 result's gradient comes in FP32: the products take x's type)
         dy = dy.to(x.dtype).contiguous()
+        if dy.data_ptr() % 16:               # (a view that begins anywhere, as cat hands on)
+            dy = dy.clone()
         away = _elsewhere(x.get_device(), None)
         with away if away is not None else contextlib.nullcontext():
             dx = dw = None

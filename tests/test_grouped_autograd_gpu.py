@@ -1,0 +1,61 @@
+"""grouped_linear under autograd, as torch's other functions hand it gradients and as its
+results are asked for derivatives."""
+import pytest
+import torch
+
+import mxfp8_grouped_gemm_group_amd as gfr
+from tests import grouped_inputs as gi
+from tests.test_grouped_linear_grad_gpu import COUNTS, DEV, setup
+
+pytestmark = pytest.mark.gpu
+
+
+def gradients_are(xd, wd, x, w, dy, rng, transpose):
+    torch.cuda.synchronize()
+    assert torch.equal(xd.grad.cpu(), gi.forward(dy, w, rng, not transpose).to(x.dtype))
+    assert torch.equal(wd.grad.cpu(), gi.wgrad(x, dy, rng, transpose).to(x.dtype))
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("K, N, ahead", [(67, 33, 3), (72, 136, 1), (264, 40, 0)])
+def test_gradients_that_begin_anywhere(K, N, ahead, transpose):
+    """Behind other rows (cat along rows) and behind other elements (a flat cat)."""
+    x, w, dy, xd, wd, dyd, gl, rng = setup(K, N, transpose)
+    y = gfr.grouped_linear(xd, wd, gl, 1, transpose_w=transpose)
+    z = torch.zeros(ahead, N, dtype=y.dtype, device=DEV)
+    torch.cat([z, y]).backward(torch.cat([z, dyd]))
+    gradients_are(xd, wd, x, w, dy, rng, transpose)
+    xd.grad = wd.grad = None
+    y = gfr.grouped_linear(xd, wd, gl, 1, transpose_w=transpose)
+    five = torch.zeros(5, dtype=y.dtype, device=DEV)
+    torch.cat([five, y.flatten()]).backward(torch.cat([five, dyd.flatten()]))
+    gradients_are(xd, wd, x, w, dy, rng, transpose)
+
+
+def test_a_captured_gradient_that_begins_anywhere():
+    x, w, dy, xd, wd, dyd, gl, rng = setup(67, 33, False)
+    five = torch.zeros(5, dtype=dyd.dtype, device=DEV)
+
+    def step():
+        y = torch.cat([five, gfr.grouped_linear(xd, wd, gl, 1).flatten()])
+        return torch.autograd.grad(y, (xd, wd), torch.cat([five, dyd.flatten()]))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dx, dw = step()
+    torch.cuda.synchronize()
+    for i in range(4):
+        x, w, dy = gi.integers(COUNTS, x.shape[0], 67, 33, torch.bfloat16, seed=i)
+        with torch.no_grad():
+            xd.copy_(x), wd.copy_(w), dyd.copy_(dy)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dx.cpu(), gi.forward(dy, w, rng, True).bfloat16())
+        assert torch.equal(dw.cpu(), gi.wgrad(x, dy, rng, False).bfloat16())
+        torch.randn(256, 256, device=DEV).relu_()
