@@ -15,6 +15,7 @@ import functools
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _binding as b
 from ._binding import GfrError, _need
@@ -127,6 +128,15 @@ def _elsewhere(index: int, stream: Optional[int]):
         return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=index) if stream
                                  else torch.cuda.default_stream(index))
     return None if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+
+def _tracked(*tensors) -> bool:
+    """Whether a result made from the tensors owes autograd a derivative: a gradient, or
+    the tangent of a forward-mode level."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        return True
+    return forward_ad._current_level >= 0 and any(
+        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 def _device(t, name: str) -> int:
@@ -386,9 +396,9 @@ def grouped_linear(x, w, group_list, group_list_type, *, transpose_w=False, out_
 
     Differentiable by x and w (then ``out`` has to be None): their gradients have
     their dtypes; dy is rounded to x's dtype first where out_dtype is float32.
-    Gradients kept in float32 take grouped_linear_wgrad.  A step that is captured
-    into a graph needs leaves of which no eager graph is alive, as every autograd
-    function does.
+    Gradients kept in float32 take grouped_linear_wgrad.  Forward-mode derivatives are
+    refused (NotImplementedError).  A step that is captured into a graph needs leaves of
+    which no eager graph is alive, as every autograd function does.
     """
     index = _device(x, "x")
     _need(out is None or out_dtype is None or out.dtype == out_dtype, "out must have out_dtype")
@@ -397,7 +407,7 @@ def grouped_linear(x, w, group_list, group_list_type, *, transpose_w=False, out_
         with away:
             return grouped_linear(x, w, group_list, group_list_type, transpose_w=transpose_w,
                                   out_dtype=out_dtype, out=out, status=status)
-    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
+    if _tracked(x, w):
         _need(out is None, "out must be None where a gradient is wanted")
         return _GroupedLinear.apply(x, w, group_list, int(group_list_type), bool(transpose_w),
                                     out_dtype, status)
@@ -411,7 +421,8 @@ def grouped_linear_wgrad(x, dy, group_list, group_list_type, *, transpose_w=Fals
     transpose with transpose_w; returns out.
 
     x bfloat16 or float16 [M, K], dy x's dtype [M, N]; out_dtype x's (default) or
-    float32; ``accumulate`` adds to ``out`` (which must be given).
+    float32; ``accumulate`` adds to ``out`` (which must be given).  Not differentiable
+    itself: autograd does not see the call.
     """
     index = _device(x, "x")
     _need(out is None or out_dtype is None or out.dtype == out_dtype, "out must have out_dtype")

@@ -2,6 +2,7 @@
 results are asked for derivatives."""
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 import mxfp8_grouped_gemm_group_amd as gfr
 from tests import grouped_inputs as gi
@@ -59,3 +60,21 @@ def test_a_captured_gradient_that_begins_anywhere():
         assert torch.equal(dx.cpu(), gi.forward(dy, w, rng, True).bfloat16())
         assert torch.equal(dw.cpu(), gi.wgrad(x, dy, rng, False).bfloat16())
         torch.randn(256, 256, device=DEV).relu_()
+
+
+def test_forward_mode_is_refused():
+    """A tangent is not dropped; without one the call is as ever."""
+    *_, xd, wd, dyd, gl, _ = setup(72, 136, False, requires=False)
+    plain = gfr.grouped_linear(xd, wd, gl, 1)
+    with forward_ad.dual_level():
+        for args in [(forward_ad.make_dual(xd, torch.ones_like(xd)), wd),
+                     (xd, forward_ad.make_dual(wd, torch.ones_like(wd)))]:
+            with pytest.raises(NotImplementedError):
+                gfr.grouped_linear(*args, gl, 1)
+            with torch.no_grad(), pytest.raises(NotImplementedError):
+                gfr.grouped_linear(*args, gl, 1)
+            with pytest.raises(ValueError):
+                gfr.grouped_linear(*args, gl, 1, out=torch.empty_like(plain))
+        assert torch.equal(gfr.grouped_linear(xd, wd, gl, 1), plain)
+    with pytest.raises(Exception):
+        torch.func.jvp(lambda a: gfr.grouped_linear(a, wd, gl, 1), (xd,), (torch.ones_like(xd),))
