@@ -460,8 +460,11 @@ def lora_linear(x, w, lora_a, lora_b, adapter_ids, *, scaling=None, bias=None, r
     element) receives DEV_BAD_ADAPTER if an id is out of range.  ``workspace``
     (uint8, lora_linear_workspace_size bytes) is allocated here if none is given;
     calls that overlap in time need one each.
+
+    Has no gradients: where autograd wants one, the result can be used (``out`` has to be
+    None), but its backward pass raises RuntimeError.  Adapters are trained over rows sorted
+    by adapter, with grouped_linear.
     """
-    lib = _lib()
     index = _device(x, "x")
     _need(x.dim() == 2 and w.dim() == 2 and lora_a.dim() == 3,
           "x must be [M, K], w [N, K] and lora_a [L, r, K]")
@@ -472,8 +475,18 @@ def lora_linear(x, w, lora_a, lora_b, adapter_ids, *, scaling=None, bias=None, r
             return lora_linear(x, w, lora_a, lora_b, adapter_ids, scaling=scaling, bias=bias,
                                residual=residual, out_dtype=out_dtype, out=out,
                                workspace=workspace, status=status)
+    operands = (x, w, bias, residual, lora_a, lora_b, adapter_ids, scaling)
+    if _tracked(*operands):
+        _need(out is None, "out must be None where a gradient is wanted")
+        return _LoraLinear.apply(out_dtype, workspace, status, *operands)
+    return _lora(operands, out_dtype, out, workspace, status)
+
+
+def _lora(operands, out_dtype, out, workspace, status):
+    x, w, lora_a = operands[0], operands[1], operands[4]
+    index = x.get_device()
     M, N = x.shape[0], w.shape[0]
-    tensors, made = (x, w, bias, residual, lora_a, lora_b, adapter_ids, scaling), ()
+    tensors, made = operands, ()
     if out is None:
         out = x.new_empty((M, N), dtype=out_dtype or x.dtype)
         made = (out,)
@@ -483,5 +496,17 @@ def lora_linear(x, w, lora_a, lora_b, adapter_ids, *, scaling=None, bias=None, r
         workspace = x.new_empty(lora_linear_workspace_size(M, N, x.shape[1], lora_a.shape[1]),
                                 dtype=torch.uint8)
     words, at, opts = _pack(index, tensors, made, workspace, status)
-    _check(lib.gfr_lora_linear(*at, _raw_stream(index), opts))
+    _check(_lib().gfr_lora_linear(*at, _raw_stream(index), opts))
     return out
+
+
+class _LoraLinear(torch.autograd.Function):
+    """lora_linear for autograd: a result whose gradient is refused, not lost."""
+
+    @staticmethod
+    def forward(ctx, out_dtype, workspace, status, *operands):
+        return _lora(operands, out_dtype, None, workspace, status)
+
+    @staticmethod
+    def backward(ctx, dy):
+        raise RuntimeError("lora_linear has no gradients: train adapters with grouped_linear")
