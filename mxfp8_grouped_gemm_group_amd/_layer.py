@@ -358,27 +358,29 @@ class _GroupedLinear(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w, group_list, group_list_type, transpose_w, out_dtype, status):
-        ctx.save_for_backward(x, w, group_list)
-        ctx.args = group_list_type, transpose_w
+        # (each gradient's product takes the other operand)
+        dx, dw = ctx.needs_input_grad[:2]
+        ctx.save_for_backward(x if dw else None, w if dx else None, group_list)
+        ctx.args = group_list_type, transpose_w, x.shape, x.dtype
         return _grouped(x, w, group_list, group_list_type, transpose_w, out_dtype, None, status)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, w, group_list = ctx.saved_tensors
-        group_list_type, transpose_w = ctx.args
+        group_list_type, transpose_w, shape, dtype = ctx.args
         # (an FP32 result's gradient comes in FP32: the products take x's type)
-        dy = dy.to(x.dtype).contiguous()
+        dy = dy.to(dtype).contiguous()
         if dy.data_ptr() % 16:               # (a view that begins anywhere, as cat hands on)
             dy = dy.clone()
-        away = _elsewhere(x.get_device(), None)
+        away = _elsewhere(dy.get_device(), None)
         with away if away is not None else contextlib.nullcontext():
             dx = dw = None
             if ctx.needs_input_grad[0]:      # (no columns: a product has to sum over some)
-                dx = torch.zeros_like(x) if dy.shape[1] == 0 else _grouped(
-                    dy, w, group_list, group_list_type, not transpose_w, x.dtype, None, None)
+                dx = dy.new_zeros(shape) if dy.shape[1] == 0 else _grouped(
+                    dy, w, group_list, group_list_type, not transpose_w, dtype, None, None)
             if ctx.needs_input_grad[1]:
-                dw = _wgrad(x, dy, group_list, group_list_type, transpose_w, w.dtype, None, False,
+                dw = _wgrad(x, dy, group_list, group_list_type, transpose_w, dtype, None, False,
                             None)
         return dx, dw, None, None, None, None, None
 

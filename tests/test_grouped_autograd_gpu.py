@@ -78,3 +78,31 @@ def test_forward_mode_is_refused():
         assert torch.equal(gfr.grouped_linear(xd, wd, gl, 1), plain)
     with pytest.raises(Exception):
         torch.func.jvp(lambda a: gfr.grouped_linear(a, wd, gl, 1), (xd,), (torch.ones_like(xd),))
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_only_what_a_gradient_takes_is_kept(transpose):
+    """With frozen weights x may change, and is freed, before the backward pass; with
+    frozen rows the weights may."""
+    x, w, dy, xd, wd, dyd, gl, rng = setup(72, 136, transpose, requires=False)
+    xd.requires_grad_(True)
+    rows = xd * 1
+    before = torch.cuda.memory_allocated()
+    y = gfr.grouped_linear(rows, wd, gl, 1, transpose_w=transpose)
+    rows.zero_()
+    del rows
+    assert torch.cuda.memory_allocated() < before + y.numel() * y.element_size()
+    y.backward(dyd)
+    assert torch.equal(xd.grad.cpu(), gi.forward(dy, w, rng, not transpose).bfloat16())
+    xd, wd = xd.detach(), wd.requires_grad_(True)
+    copy = wd * 1
+    y = gfr.grouped_linear(xd, copy, gl, 1, transpose_w=transpose)
+    copy.zero_()
+    y.backward(dyd)
+    assert torch.equal(wd.grad.cpu(), gi.wgrad(x, dy, rng, transpose).bfloat16())
+    # what it takes is guarded
+    wd = wd.detach()
+    y = gfr.grouped_linear(xd.requires_grad_(True), wd, gl, 1, transpose_w=transpose)
+    wd.zero_()
+    with pytest.raises(RuntimeError):
+        y.backward(dyd)
