@@ -624,7 +624,8 @@ int gfr_grouped_linear_wgrad(const gfr_tensor *x, const gfr_tensor *dy,
  * its own whatever its neighbours' ids.  Calls that overlap in time need workspaces of
  * their own.  Errors as gfr_linear, and
  * GFR_ERR_UNSUPPORTED for r outside [1, GFR_MAX_RANK], L outside [1, 2^20], M > 2^26 or
- * M r > 2^27; lora_a, lora_b 16-byte, adapter_ids and scaling 4-byte aligned.
+ * M times r, rounded up to a multiple of 4, above 2^27; lora_a, lora_b 16-byte, adapter_ids
+ * and scaling 4-byte aligned.
  */
 int gfr_lora_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tensor *bias,
                     const gfr_tensor *residual, const gfr_tensor *lora_a,
