@@ -580,7 +580,8 @@ int gfr_grouped_linear(const gfr_tensor *x, const gfr_tensor *w, const gfr_tenso
  *  out         x's dtype or F32; must not overlap the inputs.
  *
  * Any M, K, N >= 0 (K and N multiples of 8 are the fast path); rows of no range do
- * not take part.  The sizes of a range fix its summation order.  Errors as
+ * not take part.  M, E, K, N and a range's own size fix its summation order, whatever the
+ * other ranges' sizes; rows behind the last range count in M.  Errors as
  * gfr_grouped_linear.
  */
 int gfr_grouped_linear_wgrad(const gfr_tensor *x, const gfr_tensor *dy,
