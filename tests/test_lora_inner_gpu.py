@@ -151,3 +151,16 @@ def test_a_row_keeps_its_bits_whatever_its_neighbours_ids(M, N, K, r, dtype):
     torch.cuda.synchronize()
     assert torch.equal(one.cpu()[same_id], two.cpu()[same_id])
     assert not torch.equal(one, two)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_offsets_beyond_32_bits(dtype):
+    """Sums that wait beyond 4 GiB, results beyond 2 GiB: the first and last rows are right."""
+    M, N, K, L, r = 300000, 4096, 64, 3, 64
+    assert dispatch_rows.lora(M, N, K, r)
+    a = integers(M, N, K, L, r, dtype, mix="runs")
+    ends = torch.cat([torch.arange(300), torch.arange(M - 300, M)])
+    a["ids"][ends] = torch.arange(600, dtype=torch.int32) // 40 % 4 - 1
+    y = call(a)
+    part = {**a, "x": a["x"][ends], "ids": a["ids"][ends]}
+    same(y[ends.to(y.device)], definition(part).to(dtype))
