@@ -52,7 +52,8 @@ struct Direct {
     const char *base;
     int64_t bytes;                 // from base to the end of what may be read
     rsrc_t r;
-    int row_bytes, first;          // first: the wave's first row times row_bytes
+    int row_bytes, stride;         // stride: bytes between a wave's loads
+    int first;                     // the wave's first row times row_bytes, less one stride
     int offs, now;                 // the lane's place in a load; in the step's loads
     int piece_k;                   // k-major: first k of the lane's piece
     int K, off, loads;             // loads: those that hold any line of the tile
@@ -62,7 +63,8 @@ struct Direct {
     // Rows of `ld` elements.  Load i takes the tile's rows from (WAVES i + wave) kRows on.
     __device__ __forceinline__ void init(int64_t ld, int wave, int lane) {
         row_bytes = static_cast<int>(2 * ld);
-        first = wave * kRows * row_bytes;
+        stride = WAVES * kRows * row_bytes;
+        first = wave * kRows * row_bytes - stride;
         if (LINE) {
             constexpr int kLanes = 64 / kRows;
             const int row = lane / kLanes, k = (wave * kRows + row) & 3;
@@ -107,8 +109,15 @@ struct Direct {
             if (64 * step + piece_k >= K) now = kPast;
         }
     }
-    __device__ __forceinline__ void load(int i, uint32_t tile, int wave) const {
-        load_lds(r, now, off + i * WAVES * kRows * row_bytes, tile + (WAVES * i + wave) * 1024);
+    // Load i, all in turn.  `off` goes on to it in two of load_lds's five states, all of which
+    // cost 1 % where the matrix cores bound it (32768 rows over 32 experts of 4096 x 7168 1787
+    // -> 1810 us; 1816 with the sums ahead of load_lds, and twice the scalar spills).
+    __device__ __forceinline__ void load(int i, uint32_t tile) {
+        asm volatile("s_add_u32 %0, %0, %3\n\ts_add_u32 m0, %4, %5\n\ts_nop 2\n\t"
+                     "buffer_load_dwordx4 %1, %2, %0 offen lds"
+                     : "+&s"(off)
+                     : "v"(now), "s"(r), "s"(stride), "s"(tile), "i"(WAVES * 1024 * i)
+                     : "memory", "scc");
     }
 };
 
@@ -200,13 +209,13 @@ __device__ __forceinline__ void run_tiles(u4_t *lds, const Tiles &tiles, const F
         }
     };
     const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
-        (__attribute__((address_space(3))) void *)lds));
+        (__attribute__((address_space(3))) void *)lds)) + wave * 1024;
     constexpr int kB = decltype(db)::kLoads, kLoads = kB + decltype(da)::kLoads;
     // (B's first: their number does not depend on the tile's rows)
     auto load = [&](int i, int stage) GFR_INLINE {
         const uint32_t to = lds0 + stage * kStage * 16;
-        if (i < kB) db.load(i, to + kTile * 128, wave);
-        else if (ALINE || i - kB < da.loads) da.load(i - kB, to, wave);
+        if (i < kB) db.load(i, to + kTile * 128);
+        else if (ALINE || i - kB < da.loads) da.load(i - kB, to);
     };
     int now = 0;                              // the stage of the step that is multiplied
 #pragma unroll
