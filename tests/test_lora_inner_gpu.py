@@ -4,8 +4,9 @@ lora_b as the definition has them, whatever the rank; a row's bits are its own."
 import pytest
 import torch
 
+import mxfp8_grouped_gemm_group_amd as gfr
 from tests import dispatch_rows
-from tests.test_lora_linear_gpu import BF, F32, HF, call, definition, ids_of, integers, same
+from tests.test_lora_linear_gpu import BF, DEV, F32, HF, call, definition, ids_of, integers, same
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +165,74 @@ def test_offsets_beyond_32_bits(dtype):
     y = call(a)
     part = {**a, "x": a["x"][ends], "ids": a["ids"][ends]}
     same(y[ends.to(y.device)], definition(part).to(dtype))
+
+
+def tiled_f16(mix, **kw):
+    assert dispatch_rows.lora(*MANY[0], 16)
+    return integers(*MANY[0], 4, 16, HF, mix=mix, **kw)
+
+
+@pytest.mark.parametrize("mix", ["one", "runs", "random"])
+def test_f16_tiles_keep_nan_with_its_adapter_and_row(mix):
+    a = tiled_f16(mix)
+    a["ids"][:4] = torch.tensor([0, 1, 2, 3], dtype=torch.int32)
+    clean = definition(a)
+    nan = float("nan")
+    for t, i, value in (("a", 1, nan), ("b", 2, nan), ("b", 3, INF), ("scaling", 0, nan)):
+        b = {**a, t: a[t].clone()}
+        b[t][i] = value
+        y, rest = call(b, out_dtype=F32).cpu(), a["ids"] != i
+        same(y[rest], clean[rest], f"{t} {i}")
+        if value != value:
+            assert y[~rest].isnan().all()
+    b = {**a, "x": a["x"].clone()}
+    b["x"][2] = nan
+    y, rest = call(b, out_dtype=F32).cpu(), torch.arange(a["x"].shape[0]) != 2
+    same(y[rest], clean[rest], "row")
+    assert y[2].isnan().all()
+
+
+def test_f16_tiles_in_place_flags_and_nothing_outside():
+    M, N, K = MANY[0]
+    a = tiled_f16("random", residual=True)
+    a["ids"][1], a["ids"][M - 1] = 4, -2
+    want = definition({**a, "ids": torch.where((a["ids"] < 4) & (a["ids"] >= 0), a["ids"], -1)})
+    buf = torch.full((M * N + 128,), 7.0, dtype=HF, device=DEV)
+    out = buf[64:64 + M * N].view(M, N)
+    out.copy_(a["residual"])
+    need = gfr.lora_linear_workspace_size(M, N, K, 16)
+    ws = torch.full((need + 512,), 255, dtype=torch.uint8, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    assert call(a, residual=out, out=out, workspace=ws[:need], status=status) is out
+    same(out, want)
+    assert (buf[:64] == 7).all() and (buf[64 + M * N:] == 7).all() and (ws[need:] == 255).all()
+    assert status.item() == gfr.DEV_BAD_ADAPTER
+
+
+def test_f16_tiles_under_graph_and_on_two_streams():
+    a = tiled_f16("runs", bias=HF)
+    d = {k: v.to(DEV) for k, v in a.items() if v is not None}
+    run = lambda **kw: gfr.lora_linear(d["x"], d["w"], d["a"], d["b"], d["ids"],
+                                       scaling=d["scaling"], bias=d["bias"], out_dtype=F32, **kw)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = run()
+    torch.cuda.synchronize()
+    for i, mix in enumerate(["random", "none", "one", "runs"]):
+        a["ids"] = ids_of(MANY[0][0], 4, mix, i)
+        d["ids"].copy_(a["ids"])
+        graph.replay()
+        same(y, definition(a), mix)
+        torch.randn(256, 256, device=DEV).relu_()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(3):
+        out = [run(stream=s.cuda_stream) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, out[0]) for o in out)
+    same(out[0], definition(a))
