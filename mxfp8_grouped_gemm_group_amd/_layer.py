@@ -133,8 +133,10 @@ def _elsewhere(index: int, stream: Optional[int]):
 def _tracked(*tensors) -> bool:
     """Whether a result made from the tensors owes autograd a derivative: a gradient, or
     the tangent of a forward-mode level."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        return True
+    if torch.is_grad_enabled():
+        for t in tensors:               # (any() takes half a microsecond more)
+            if t is not None and t.requires_grad:
+                return True
     return forward_ad._current_level >= 0 and any(
         t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
@@ -478,15 +480,14 @@ def lora_linear(x, w, lora_a, lora_b, adapter_ids, *, scaling=None, bias=None, r
                                residual=residual, out_dtype=out_dtype, out=out,
                                workspace=workspace, status=status)
     operands = (x, w, bias, residual, lora_a, lora_b, adapter_ids, scaling)
-    if _tracked(*operands):
+    if _tracked(x, w, bias, residual, lora_a, lora_b, scaling):
         _need(out is None, "out must be None where a gradient is wanted")
         return _LoraLinear.apply(out_dtype, workspace, status, *operands)
-    return _lora(operands, out_dtype, out, workspace, status)
+    return _lora(index, operands, out_dtype, out, workspace, status)
 
 
-def _lora(operands, out_dtype, out, workspace, status):
-    x, w, lora_a = operands[0], operands[1], operands[4]
-    index = x.get_device()
+def _lora(index, operands, out_dtype, out, workspace, status):
+    x, w, _, _, lora_a = operands[:5]
     M, N = x.shape[0], w.shape[0]
     tensors, made = operands, ()
     if out is None:
@@ -507,7 +508,7 @@ class _LoraLinear(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, out_dtype, workspace, status, *operands):
-        return _lora(operands, out_dtype, None, workspace, status)
+        return _lora(operands[0].get_device(), operands, out_dtype, None, workspace, status)
 
     @staticmethod
     def backward(ctx, dy):
