@@ -142,7 +142,7 @@ struct LoraParams {
 // Workspace layout of lora_linear (256-byte aligned regions; inner or terms at 0).
 struct LoraLayout {
     size_t codes, dense, total;
-    int32_t tiles;             // many rows: dense tiles that expand in their epilogue
+    int32_t tiles;             // many rows: dense tiles that take expansions in their sum
     LinearChoice choice;       // few rows: of the dense product
 };
 LoraLayout lora_layout(int64_t M, int64_t N, int64_t K, int64_t r);
