@@ -506,52 +506,64 @@ struct LoraFinish {
     __device__ __forceinline__ void clear(const TileAt &) const {}
 };
 
-// The 32 rows left to it, 32 columns a wave: each adapter's product goes on from all rows'
+// The 32 rows left to it, 32 W columns a wave: each adapter's product goes on from all rows'
 // dense sums and is kept by its own, the ranks in the dense tiles' order, so that a row gets
 // the same bits there and here.  With F16 the products are in FP32.
-template <bool F16>
+//
+// Bound by its loads, 32 lines each.  bf16 takes two fragments of columns from 24 ranks on,
+// which read inner once for both (2048 rows in random order over 64 adapters of 4096 columns,
+// us: rank 64 384 and 267, 32 110 and 85, 16 46 and 57); F16, with more rows, one, 32 ranks
+// at a time, for more waves (4096 rows of 7168 columns, rank 64: 61, with two 73, with 64
+// ranks at a time 65).
+template <bool F16, int W>
 __global__ __launch_bounds__(256) void expand_tile_kernel(LoraParams p) {
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int c = lane & 31, g = lane >> 5, t0 = blockIdx.y * 32;
-    const int n0 = blockIdx.x * 128 + wave * 32;
+    const int n0 = (blockIdx.x * 4 + wave) * 32 * W;
     const int rows = min(32, p.M - t0), b_row = 2 * p.r, s_row = F16 ? 4 * p.r : 6 * p.r;
     const int id = c < rows ? adapter(p, t0 + c) : -1;
     if (p.codes[blockIdx.y] != kApart || n0 >= p.N) return;
-    const rsrc_t from = apart(p, t0, n0), from_bias = bias_row(p);
-    const rsrc_t from_res = residual_rows(p, t0, rows);
-    const Columns columns{n0, g};
-    f16_t sum;
-    u4_t bias[2], res[2];
+    const rsrc_t from_bias = bias_row(p), from_res = residual_rows(p, t0, rows);
+    f16_t sum[W];
+    u4_t bias[W][2], res[W][2];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const f4_t v = __builtin_bit_cast(f4_t, load16<0>(from, 1024 * q + 16 * lane, 0));
+    for (int w = 0; w < W; ++w) {
+        const rsrc_t from = apart(p, t0, n0 + 32 * w);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum[4 * q + e] = v[e];
-    }
+        for (int q = 0; q < 4; ++q) {
+            const int off = n0 + 32 * w < p.N ? 1024 * q + 16 * lane : kPast;
+            const f4_t v = __builtin_bit_cast(f4_t, load16<0>(from, off, 0));
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int n = columns.of(q);
-        bias[q] = load16<0>(from_bias, p.bias_f32 ? kPast : 2 * n, 0);
-        res[q] = load16<0>(from_res, n < p.N ? 2 * (c * p.N + n) : kPast, 0);
+            for (int e = 0; e < 4; ++e) sum[w][4 * q + e] = v[e];
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int n = Columns{n0 + 32 * w, g}.of(q);
+            bias[w][q] = load16<0>(from_bias, p.bias_f32 ? kPast : 2 * n, 0);
+            res[w][q] = load16<0>(from_res, n < p.N ? 2 * (c * p.N + n) : kPast, 0);
+        }
     }
     const rsrc_t sr = uniform_buffer((F16 ? reinterpret_cast<const char *>(p.inner)
                                           : reinterpret_cast<const char *>(p.terms)) +
                                          static_cast<int64_t>(t0) * s_row,
                                      static_cast<int64_t>(rows) * s_row);
-    // Ranks [64 i, 64 i + 64) in groups of 16: lane (c, g) has ranks 8 g .. + 7 of each, of B's
-    // column c and of inner's row c (bf16: of its three terms; of the last 8 ranks alone the
-    // terms are side by side).
+    // Ranks [16 Q i, 16 Q (i + 1)) in groups of 16: lane (c, g) has ranks 8 g .. + 7 of each,
+    // of B's columns c and of inner's row c (bf16: of its three terms; of the last 8 ranks
+    // alone the terms are side by side).
+    constexpr int Q = F16 ? 2 : 4;
     struct Ranks {
-        u4_t b[4], s[4][F16 ? 2 : 3];
+        u4_t b[Q][W], s[Q][F16 ? 2 : 3];
     };
     const auto fetch = [&](rsrc_t br, int i, Ranks &v) GFR_INLINE {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int k0 = 64 * i + 16 * q;
+        for (int q = 0; q < Q; ++q) {
+            const int k0 = 16 * (Q * i + q);
             if (k0 >= p.r) break;
             const int width = k0 + 16 <= p.r ? 16 : 8, k = k0 + (8 * g & width - 1);
             const bool live = !F16 || 8 * g < width;
-            v.b[q] = load16<0>(br, live ? c * b_row + 2 * k : kPast, 0);
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                v.b[q][w] = load16<0>(br, live ? (c + 32 * w) * b_row + 2 * k : kPast, 0);
 #pragma unroll
             for (int j = 0; j < (F16 ? 2 : 3); ++j) {
                 const int at = F16 ? 4 * (k + 4 * j) : 2 * (3 * k0 + 16 * j + 8 * g);
@@ -569,34 +581,45 @@ __global__ __launch_bounds__(256) void expand_tile_kernel(LoraParams p) {
         const rsrc_t br = uniform_buffer(
             reinterpret_cast<const char *>(p.b + (a * int64_t{p.N} + n0) * p.r),
             static_cast<int64_t>(p.N - n0) * b_row);
-        f16_t own = sum;
-        for (int i = 0; 64 * i < p.r; ++i) {
+        f16_t own[W];
+#pragma unroll
+        for (int w = 0; w < W; ++w) own[w] = sum[w];
+        for (int i = 0; 16 * Q * i < p.r; ++i) {
             Ranks v;
             fetch(br, i, v);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (64 * i + 16 * q >= p.r) break;
-                if (F16)
+            for (int q = 0; q < Q; ++q) {
+                const int k0 = 16 * (Q * i + q);
+                if (k0 >= p.r) break;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        own = __builtin_amdgcn_mfma_f32_32x32x2f32(
-                            unpack1<F16>(v.b[q][e >> 1] >> (16 * (e & 1))),
-                            __uint_as_float(v.s[q][e >> 2][e & 3]), own, 0, 0, 0);
-                else
+                for (int w = 0; w < W; ++w)
+                    if (F16)
 #pragma unroll
-                    for (int j = 0; j < 3; ++j) {
-                        // (8 ranks alone: 16 terms, then 8)
-                        const bool alone = 64 * i + 16 * q + 16 > p.r;
-                        if (alone && j == 2) break;
-                        const u4_t b = alone && j == 1 && g == 1 ? u4_t{0, 0, 0, 0} : v.b[q];
-                        own = mfma32<F16>(b, v.s[q][j], own);
-                    }
+                        for (int e = 0; e < 8; ++e)
+                            own[w] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                                unpack1<F16>(v.b[q][w][e >> 1] >> (16 * (e & 1))),
+                                __uint_as_float(v.s[q][e >> 2][e & 3]), own[w], 0, 0, 0);
+                    else
+#pragma unroll
+                        for (int j = 0; j < 3; ++j) {
+                            // (8 ranks alone: 16 terms, then 8)
+                            const bool alone = k0 + 16 > p.r;
+                            if (alone && j == 2) break;
+                            const u4_t b =
+                                alone && j == 1 && g == 1 ? u4_t{0, 0, 0, 0} : v.b[q][w];
+                            own[w] = mfma32<F16>(b, v.s[q][j], own[w]);
+                        }
             }
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sum[e] = mine ? own[e] : sum[e];
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum[w][e] = mine ? own[w][e] : sum[w][e];
     }
-    put_sums<F16>(p, sum, t0, rows, columns, from_bias, bias, res, lane);
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+        put_sums<F16>(p, sum[w], t0, rows, Columns{n0 + 32 * w, g}, from_bias, bias[w], res[w],
+                      lane);
 }
 
 template <bool F16>
@@ -681,8 +704,12 @@ hipError_t launch_tiles(const LoraParams &p, hipStream_t stream) {
     if (const hipError_t a = allow_lds<kernel, kMaxLds>(lds); a != hipSuccess) return a;
     hipLaunchKernelGGL(kernel, dim3(256), dim3(kWaves * 64), lds, stream, p);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    hipLaunchKernelGGL((expand_tile_kernel<F16>), dim3((p.N + 127) / 128, (p.M + 31) / 32),
-                       dim3(256), 0, stream, p);
+    const auto expand = [&](auto kernel, int columns) {
+        hipLaunchKernelGGL(kernel, dim3((p.N + columns - 1) / columns, (p.M + 31) / 32), dim3(256),
+                           0, stream, p);
+    };
+    if (!F16 && p.r > 16) expand(&expand_tile_kernel<F16, F16 ? 1 : 2>, 256);
+    else expand(&expand_tile_kernel<F16, 1>, 128);
     return hipGetLastError();
 }
 
