@@ -11,8 +11,8 @@
 // for the 32 rows that have several, whose sums were kept in FP32, a launch that goes on with
 // each row's own, so that what another request's adapter holds (NaN too) reaches nobody else.
 // With F16 that launch expands all rows, on the FP32 matrix instructions: F16 terms do not
-// have inner's range (4096 rows of 4096 x 7168 by rank 64: tiles 227 us and it 76, in bf16
-// 242 and 15; whole calls by rank 16 254 and 228).
+// have inner's range (4096 rows of 4096 x 7168 by rank 64: tiles 237 us and it 78, in bf16
+// 239 and 16; whole calls by rank 16 254 and 228).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
